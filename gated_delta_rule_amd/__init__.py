@@ -12,6 +12,10 @@ calls raise; there is no fallback.
                       commit=True)                     # up to 64 tokens per request
     q, k, v, log_alpha, beta = prologue(q_raw, k_raw, v_raw, conv_w, a, b, conv_cache)
     out = epilogue(o, g, w)                            # gated RMSNorm of the output
+
+The state space scan, its short convolution and the draft verification
+(include/kda_ssm.h, include/kda_spec.h) are in the same library; their calls
+(ssm_*, verify_drafts) are in gated_delta_rule_amd.ssm and re-exported here.
 """
 from __future__ import annotations
 
@@ -20,7 +24,10 @@ import os
 
 __all__ = ["chunk_fwd", "decode_step", "recurrent_fwd", "prologue", "epilogue",
            "chunk_fwd_workspace_bytes",
-           "library_path", "load_library", "KDAError", "KDA_BF16", "KDA_F32", "HEAD_DIM"]
+           "library_path", "load_library", "KDAError", "KDA_BF16", "KDA_F32", "HEAD_DIM",
+           "ssm_conv_fwd", "ssm_conv_step", "ssm_conv_bwd", "ssm_chunk_fwd", "ssm_chunk_bwd",
+           "ssm_recurrent_fwd", "ssm_chunk_fwd_workspace_bytes", "ssm_chunk_bwd_workspace_bytes",
+           "verify_drafts"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -78,6 +85,29 @@ def load_library():
     lib.kda_chunk_bwd.argtypes = [vp, vp, vp, ctypes.c_int, fp, fp, fp, ip, i32, i64, i32, i32,
                                   i32, fp, fp, fp, fp, fp, fp, fp, fp, vp, sz, vp]
     lib.kda_chunk_bwd.restype = ctypes.c_int
+    ci = ctypes.c_int
+    for name, args in {
+            "kda_ssm_conv_fwd": [vp, i64, ci, fp, fp, fp, ip, i32, i64, i32, i32, ci, vp, vp],
+            "kda_ssm_conv_step": [vp, i64, ci, fp, fp, fp, vp, i64, ip, i32, i32, i32, i32, i32, ci, ci, vp, vp],
+            "kda_ssm_conv_bwd": [vp, i64, ci, fp, fp, fp, ip, i32, i64, i32, i32, ci, vp, i64, vp, fp, fp, fp,
+                                 vp, sz, vp],
+            "kda_ssm_chunk_fwd": [vp, i64, vp, i64, vp, i64, ci, fp, fp, ci, fp, fp, fp, ip, i32, i64, i32,
+                                  i32, i32, i32, vp, fp, vp, sz, vp],
+            "kda_ssm_chunk_bwd": [vp, i64, vp, i64, vp, i64, ci, fp, fp, ci, fp, fp, fp, ip, i32, i64, i32,
+                                  i32, i32, i32, vp, fp, vp, i64, vp, i64, vp, i64, fp, fp, fp, fp, fp, vp,
+                                  sz, vp],
+            "kda_ssm_recurrent_fwd": [vp, i64, vp, i64, vp, i64, ci, fp, fp, ci, fp, fp, vp, i64, vp, i64, fp,
+                                      ip, fp, i32, i32, i32, i32, i32, i32, i32, ci, vp, vp],
+            "kda_verify_drafts": [vp, vp, ci, ip, ip, fp, fp, i32, i32, i64, ip, ip, vp, sz, vp]}.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ci
+    for name, args in {
+            "kda_ssm_conv_bwd_workspace_bytes": [i64, i32, i32],
+            "kda_ssm_chunk_fwd_workspace_bytes": [i32, i64, i32, i32, i32, i32, ci],
+            "kda_ssm_chunk_bwd_workspace_bytes": [ci, i32, i64, i32, i32, i32, i32, ci, i32],
+            "kda_verify_drafts_workspace_bytes": [i32, i32, i64]}.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = sz
     _lib = lib
     return lib
 
@@ -416,3 +446,8 @@ def epilogue(o, g, w, *, out=None):
                           ctypes.c_void_p(stream))
     _status(rc, "kda_epilogue")
     return out
+
+
+from .ssm import (ssm_chunk_bwd, ssm_chunk_bwd_workspace_bytes, ssm_chunk_fwd,  # noqa: E402
+                  ssm_chunk_fwd_workspace_bytes, ssm_conv_bwd, ssm_conv_fwd, ssm_conv_step,
+                  ssm_recurrent_fwd, verify_drafts)

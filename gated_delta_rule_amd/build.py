@@ -13,8 +13,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_abi.hip", "kda_noalloc.hip", "kda_prefill.hip", "kda_prefill_pipe.hip", "kda_segment.hip", "kda_recurrent.hip",
-           "kda_layer.hip", "kda_backward.hip"]
-HEADERS = ["kda_device.h", "kda_launch.h", "kda_chunk.h"]
+           "kda_layer.hip", "kda_backward.hip", "kda_ssm_abi.hip", "kda_ssm_conv.hip", "kda_ssm_scan.hip",
+           "kda_ssm_bwd.hip", "kda_ssm_recurrent.hip", "kda_spec.hip"]
+HEADERS = ["kda_device.h", "kda_launch.h", "kda_chunk.h", "kda_ssm_launch.h", "kda_ssm_tile.h"]
 ARCH = "gfx950"
 
 FLAGS = [

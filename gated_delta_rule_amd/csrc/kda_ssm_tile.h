@@ -1,0 +1,242 @@
+// Device-side pieces shared by the scan's forward and backward kernels
+// (gfx950 only): the sequence table, the decay sums of a chunk, and operand
+// tiles in LDS.
+//
+// Operands of the bf16 16x16x32 matrix instruction: lane l supplies row (A)
+// or column (B) l & 15 and k = 8 (l >> 4) .. + 7; it receives column l & 15,
+// rows 4 (l >> 4) .. + 3 of the product.  The two operands have the same
+// form, so swapping them transposes the product.
+//
+// A tile is [rows][columns] of bf16 in LDS, in 16-byte units of 8 columns
+// whose place in the row is exclusive-ored with the row number, so that 16
+// rows' units of one column block fall into different banks.  A fragment
+// whose k runs along the tile's columns is one 16-byte read per lane; one
+// whose k runs along its rows takes two transposing reads.
+//
+// A float32 value enters a product as the sum of bf16 parts (8 significant
+// bits each): parts i and j of the two operands are multiplied while
+// i + j < 3, the rest is below 2^-24 of the product.  bf16 inputs have one
+// part, float32 inputs three (three planes of the tile).
+#pragma once
+
+#include "kda_device.h"
+#include "kda_ssm_launch.h"
+
+namespace kda {
+
+constexpr int SS_THREADS = 256;
+
+__device__ __forceinline__ float ss_softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+// Token rows [start, end) of sequence n, clamped into [0, rows].
+struct SsmRange {
+    int64_t start, end;
+};
+__device__ __forceinline__ SsmRange ssm_range(const int32_t* cu, int64_t rows, int64_t T, int64_t n) {
+    if (!cu) return SsmRange{n * T, n * T + T};
+    int64_t a = cu[n], b = cu[n + 1];
+    a = a < 0 ? 0 : (a > rows ? rows : a);
+    b = b < a ? a : (b > rows ? rows : b);
+    return SsmRange{a, b};
+}
+// The sequence and the piece of `len` tokens that a slot stands for (see
+// SsmScanParams); piece -1: an unused slot.  Its rows are [r0, r1).
+struct SsmPiece {
+    int64_t n, piece, r0, r1, start, end;   // start, end: the sequence's
+};
+__device__ __forceinline__ SsmPiece ssm_piece(const int32_t* cu, int64_t rows, int64_t T, int32_t n_seqs,
+                                              int64_t len, int64_t slot) {
+    SsmPiece s;
+    if (!cu) {
+        const int64_t per = (T + len - 1) / len;
+        s.n = slot / per;
+        s.piece = slot - s.n * per;
+    } else {
+        int lo = 0, hi = n_seqs;   // largest n with cu[n] / len + n <= slot
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (ssm_range(cu, rows, T, mid).start / len + mid <= slot) lo = mid;
+            else hi = mid;
+        }
+        s.n = lo;
+        s.piece = slot - (ssm_range(cu, rows, T, lo).start / len + lo);
+    }
+    const SsmRange r = ssm_range(cu, rows, T, s.n);
+    s.start = r.start;
+    s.end = r.end;
+    if (s.piece < 0 || s.piece * len >= r.end - r.start) {
+        s.piece = -1;
+        s.r0 = s.r1 = r.end;
+        return s;
+    }
+    s.r0 = r.start + s.piece * len;
+    s.r1 = s.r0 + len < r.end ? s.r0 + len : r.end;
+    return s;
+}
+
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Place of unit u (8 columns) of a row in a tile with U units per row.
+template <int U>
+__device__ __forceinline__ int ss_unit(int row, int u) {
+    return row * U + (u ^ ((row / (16 / U)) & (U - 1)));
+}
+
+// Fragment with k along the columns: row r0 + (l & 15), columns 32 ks + 8 (l >> 4) .. + 7.
+template <int COLS>
+__device__ __forceinline__ bf16x8 frag_row(const __bf16* tile, int r0, int ks) {
+    const int l = threadIdx.x & 63;
+    return *reinterpret_cast<const bf16x8*>(tile + 8 * ss_unit<COLS / 8>(r0 + (l & 15), 4 * ks + (l >> 4)));
+}
+// Fragment with k along the rows: lane i = l & 15 receives column
+// c0 + step (i >> 2) + (i & 3), rows 32 ks + 8 (l >> 4) .. + 7.  step 4: 16
+// neighbouring columns; step 8: the pair of calls with c0 and c0 + 4 covers 32
+// columns so that a lane's four rows of each of the two products (rows
+// 4 (l >> 4) .. + 3) are eight neighbouring columns 8 (l >> 4) .. + 7 of the
+// 32.
+template <int COLS, int STEP>
+__device__ __forceinline__ bf16x8 frag_col(const __bf16* tile, int c0, int ks) {
+    const int l = threadIdx.x & 63, i = l & 15;
+    const int c = c0 + STEP * (i & 3);
+    const int r = 32 * ks + 8 * (l >> 4) + (i >> 2);
+    const __bf16* a = tile + 8 * ss_unit<COLS / 8>(r, c >> 3) + (c & 7);
+    const __bf16* b = tile + 8 * ss_unit<COLS / 8>(r + 4, c >> 3) + (c & 7);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)b);
+    bf16x8 f;
+    __builtin_memcpy(&f, &lo, 8);
+    __builtin_memcpy(reinterpret_cast<char*>(&f) + 8, &hi, 8);
+    return f;
+}
+
+// NP bf16 parts of 8 float32 values; the last part is rounded, so the sum is
+// off by at most 2^-8NP of the value.
+template <int NP>
+__device__ __forceinline__ void parts8(const float (&x)[8], bf16x8 (&p)[NP]) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = pack_bf2(r[2 * i], r[2 * i + 1]);
+            if (k + 1 < NP) {
+                r[2 * i] -= bf2_first(w[i]);
+                r[2 * i + 1] -= bf2_second(w[i]);
+            }
+        }
+        p[k] = __builtin_bit_cast(bf16x8, w);
+    }
+}
+// c += sum over parts i of a, j of b with i + j < 3, smallest first.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma_parts(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c) {
+#pragma unroll
+    for (int s = NA + NB - 2; s >= 0; --s) {
+        if (s > 2) continue;
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = s - i;
+            if (j >= 0 && j < NB) c = mfma32(a[i], b[j], c);
+        }
+    }
+    return c;
+}
+
+// Global memory -> registers -> LDS of a tile of L rows by COLS columns:
+// PER 16-byte pieces per thread, rows past `valid` as zeros.
+template <typename InT, int L, int COLS>
+struct Stager {
+    static constexpr int EV = 16 / (int)sizeof(InT);      // elements per piece
+    static constexpr int PPR = COLS / EV;                 // pieces per row
+    static constexpr int PER = L * PPR / SS_THREADS;
+    static constexpr int PARTS = sizeof(InT) == 2 ? 1 : 3;
+    static_assert(L * PPR % SS_THREADS == 0, "whole pieces per thread");
+    u32x4 r[PER];
+
+    // base: first row's first column; cols: columns that exist (the others read as zero)
+    __device__ __forceinline__ void load(const InT* base, int64_t stride, int valid, int cols) {
+        const int bytes = valid > 0 ? (int)((valid - 1) * stride + cols) * (int)sizeof(InT) : 0;
+        const auto rs = make_rsrc(base, bytes);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int idx = (int)threadIdx.x + SS_THREADS * j;
+            const int row = idx / PPR, c = (idx - row * PPR) * EV;
+            const uint32_t off = row < valid && c < cols ? (uint32_t)(row * (int)stride + c) * (uint32_t)sizeof(InT)
+                                                         : 0x80000000u;
+            r[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+        }
+    }
+    // planes of L * COLS bf16 each
+    __device__ __forceinline__ void put(__bf16* tile) const {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int idx = (int)threadIdx.x + SS_THREADS * j;
+            const int row = idx / PPR, c = (idx - row * PPR) * EV;
+            __bf16* at = tile + 8 * ss_unit<COLS / 8>(row, c >> 3) + (c & 7);
+            if constexpr (PARTS == 1) {
+                *reinterpret_cast<u32x4*>(at) = r[j];
+            } else {
+                float f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[j][i]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    u32x2 w = {pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3])};
+                    *reinterpret_cast<u32x2*>(at + k * L * COLS) = w;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        f[2 * i] -= bf2_first(w[i]);
+                        f[2 * i + 1] -= bf2_second(w[i]);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// Decay sums of one head's chunk, one token per lane (lanes >= L idle):
+// g_t = sum_{s<=t} a_s in float64, kept as hi + lo floats, so that g_t - g_s
+// is good to float32 rounding of the difference itself however far both are
+// from the chunk's start.
+template <int L>
+struct ChunkDecay {
+    float gh[L], gl[L];   // g_t
+    float dt[L];          // after softplus; 0 past the end
+    float eg[L];          // e^{g_t}
+    float w[L];           // e^{g_end - g_t} dt_t
+    float eL;             // e^{g_end}
+};
+// dt_raw: this lane's token, `valid` whether it exists.  Returns g_end.
+template <int L>
+__device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bool valid, float bias, int softplus,
+                                              float A) {
+    const int lane = threadIdx.x & 63;
+    float dt = 0.f;
+    if (valid) {
+        dt = dt_raw + bias;
+        if (softplus) dt = ss_softplus(dt);
+    }
+    double g = (double)(dt * A);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+        const double y = __shfl_up(g, o);
+        if (lane >= o) g += y;
+    }
+    const double end = __shfl(g, L - 1);
+    if (lane < L) {
+        const float h = (float)g;
+        d.gh[lane] = h;
+        d.gl[lane] = (float)(g - (double)h);
+        d.dt[lane] = dt;
+        d.eg[lane] = expf(h);
+        d.w[lane] = expf((float)(end - g)) * dt;
+        if (lane == 0) d.eL = expf((float)end);
+    }
+    return end;
+}
+
+}  // namespace kda
