@@ -160,8 +160,8 @@ int kda_ssm_conv_fwd(const void* x, int64_t x_stride, int in_dtype, const float*
     int64_t rows = 0;
     if ((rc = count_rows(cu_seqlens, n_seqs, T, &rows))) return rc;
     if (n_seqs == 0) return KDA_OK;
-    if (ceil_div(rows, 128) * ceil_div(channels, 128) > kMaxWorkgroups ||
-        ceil_div((int64_t)n_seqs * channels, 1024) > kMaxWorkgroups)
+    if (ceil_div(rows, 32) * ceil_div(channels, 256) > kMaxWorkgroups ||
+        ceil_div((int64_t)n_seqs * channels, 256) > kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
     if ((rows > 0 && (!x || !w || !y))) return KDA_ERR_NULL_POINTER;
     const int64_t es = elem_size(in_dtype);
@@ -244,7 +244,7 @@ int kda_ssm_conv_step(const void* x, int64_t x_stride, int in_dtype, const float
 
 size_t kda_ssm_conv_bwd_workspace_bytes(int64_t rows, int32_t channels, int32_t width) {
     if (rows < 0 || rows > ((int64_t)1 << 38) || conv_shape(KDA_BF16, 0, 0, channels, width)) return 0;
-    const int64_t parts = ceil_div(rows, kda::kConvBwdRows);
+    const int64_t parts = kda::conv_bwd_parts(rows, channels);
     int64_t n = 0;
     if (!mul_ok(parts, (int64_t)(width + 1) * channels * 4, &n)) return 0;
     return (size_t)(n < 16 ? 16 : n);
@@ -261,8 +261,8 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
     int64_t rows = 0;
     if ((rc = count_rows(cu_seqlens, n_seqs, T, &rows))) return rc;
     if (n_seqs == 0) rows = 0;
-    if (ceil_div(rows, kda::kConvBwdRows) * ceil_div(channels, 128) > kMaxWorkgroups ||
-        ceil_div((int64_t)n_seqs * channels, 1024) > kMaxWorkgroups)
+    if (ceil_div(rows, 32) * ceil_div(channels, 256) > kMaxWorkgroups ||
+        ceil_div((int64_t)n_seqs * channels, 256) > kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
     if (!w || !grad_w || (rows > 0 && (!x || !grad_y || !grad_x))) return KDA_ERR_NULL_POINTER;
     const int64_t es = elem_size(in_dtype);
@@ -309,6 +309,7 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
     q.gcache = grad_cache;
     q.partial = (float*)workspace;
     q.gy_stride = grad_y_stride;
+    q.rows_per_wave = (int32_t)kda::conv_rows_per_wave(rows, channels);
     return kda::launch_conv_bwd(q, in_dtype == KDA_BF16, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 

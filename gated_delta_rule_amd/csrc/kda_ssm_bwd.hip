@@ -52,9 +52,11 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
     __shared__ float sR[TT][L], sQ[TT][L], sU[4][L], sV[4][L], sW[L], sE[L], sZ[4];
 
     const SsmScanParams& p = q.f;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l15 = lane & 15, lg = lane >> 4;
+    int lane = tid & 63;
+    int rN = lane_row<N>(lane), rP = lane_row<P>(lane), rL = lane_row<L>(lane);
+    int2 cN = lane_col<N, 4>(lane), cP = lane_col<P, 4>(lane), cL = lane_col<L, 4>(lane);
     const int hpg = p.H / p.G;
     const int64_t heads = (int64_t)p.gn * hpg;
     const int per_slot = p.gn * q.blocks;
@@ -77,7 +79,7 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
         reinterpret_cast<u32x4*>(tK)[i] = u32x4{0, 0, 0, 0};
         reinterpret_cast<u32x4*>(tM)[i] = u32x4{0, 0, 0, 0};
     }
-    Stager<InT, L, P> gX, gY;
+    Stager<InT, L, P, SS_THREADS> gX, gY;
     float gdt = 0.f;
     auto fetch = [&](int hw) {
         const int64_t h = hfirst + hw;
@@ -86,7 +88,7 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
         if (wave == 0) gdt = lane < valid ? p.dt[(row0 + lane) * p.H + h] : 0.f;
     };
     {
-        Stager<InT, L, N> g;
+        Stager<InT, L, N, SS_THREADS> g;
         g.load((const InT*)p.B + row0 * p.B_stride + grp * N, p.B_stride, valid, N);
         g.put(tB);
         g.load((const InT*)p.C + row0 * p.C_stride + grp * N, p.C_stride, valid, N);
@@ -111,8 +113,8 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
             bf16x8 fb[XP], fc[XP];
 #pragma unroll
             for (int i = 0; i < XP; ++i) {
-                fb[i] = frag_row<N>(tB + i * L * N, 16 * g_st[k], ks);
-                fc[i] = frag_row<N>(tC + i * L * N, 16 * g_tt[k], ks);
+                fb[i] = frag_row<N>(tB + i * L * N, 16 * g_st[k], ks, rN);
+                fc[i] = frag_row<N>(tC + i * L * N, 16 * g_tt[k], ks, rN);
             }
             G[k] = mma_parts<XP, XP>(fb, fc, G[k]);
         }
@@ -140,6 +142,8 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
 
     for (int hw = hw0; hw < hw0 + hwn; ++hw) {
         const int h = hfirst + hw;
+        hide(lane), hide(rN), hide(rP), hide(rL), hide(cN), hide(cP), hide(cL);
+        const int l15 = lane & 15, lg = lane >> 4;
         const float* S = q.states + (slot * heads + hw) * (N * P);
         const float* R = q.dstates + (slot * heads + hw) * (N * P);
         const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
@@ -148,8 +152,21 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
         gX.put(tX);
         gY.put(tY);
         if (wave == 0) chunk_decay<L>(dec, gdt, lane < valid, bias, p.softplus, A);
-        __syncthreads();
-        if (hw + 1 < hw0 + hwn) fetch(hw + 1);
+        lds_barrier();
+        // S and R rows of this wave, in flight during the chunk matrices
+        f32x4 fS[MT][P / 32][2], fR[MT][P / 32][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int ks = 0; ks < P / 32; ++ks) {
+                const int at = ((N / 4) * wave + 16 * m + l15) * P + 32 * ks + 8 * lg;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    fS[m][ks][k] = *reinterpret_cast<const f32x4*>(S + at + 4 * k);
+                    fR[m][ks][k] = *reinterpret_cast<const f32x4*>(R + at + 4 * k);
+                }
+            }
+        __builtin_amdgcn_sched_barrier(0);
 
         // chunk matrices, a lane holding four neighbouring s of one t
 #pragma unroll
@@ -162,8 +179,8 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
                 bf16x8 fx[XP], fy[XP];
 #pragma unroll
                 for (int i = 0; i < XP; ++i) {
-                    fx[i] = frag_row<P>(tX + i * L * P, 16 * st, ks);
-                    fy[i] = frag_row<P>(tY + i * L * P, 16 * tt, ks);
+                    fx[i] = frag_row<P>(tX + i * L * P, 16 * st, ks, rP);
+                    fy[i] = frag_row<P>(tY + i * L * P, 16 * tt, ks, rP);
                 }
                 E = mma_parts<XP, XP>(fx, fy, E);
             }
@@ -182,7 +199,7 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
                 const float w = sr <= t ? G[k][r] * l * E[r] : 0.f;
                 col[r] = sr < t ? w : 0.f;
                 row += col[r] * ds[r];
-                if (sr == t) {
+                if (tt == st && sr == t) {
                     M[r] += D;
                     sW[t] = w;
                     sE[t] = E[r];
@@ -219,6 +236,7 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
         }
 
         // products with S and R: rows n = (N / 4) wave + 16 m + .., columns token
+        __builtin_amdgcn_sched_barrier(0);
         float z = 0.f, u[TT], v[TT];
 #pragma unroll
         for (int t = 0; t < TT; ++t) u[t] = v[t] = 0.f;
@@ -230,28 +248,28 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
             for (int t = 0; t < TT; ++t) aC[t] = aB[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < P / 32; ++ks) {
-                const int64_t at = (n0 + l15) * P + 32 * ks + 8 * lg;
-                float fS[8], fR[8];
-                *reinterpret_cast<f32x4*>(fS) = *reinterpret_cast<const f32x4*>(S + at);
-                *reinterpret_cast<f32x4*>(fS + 4) = *reinterpret_cast<const f32x4*>(S + at + 4);
-                *reinterpret_cast<f32x4*>(fR) = *reinterpret_cast<const f32x4*>(R + at);
-                *reinterpret_cast<f32x4*>(fR + 4) = *reinterpret_cast<const f32x4*>(R + at + 4);
+                float vS[8], vR[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z = fmaf(fS[e], fR[e], z);
+                for (int e = 0; e < 8; ++e) {
+                    vS[e] = fS[m][ks][e / 4][e % 4];
+                    vR[e] = fR[m][ks][e / 4][e % 4];
+                    z = fmaf(vS[e], vR[e], z);
+                }
                 bf16x8 pS[SP], pR[SP];
-                parts8<SP>(fS, pS);
-                parts8<SP>(fR, pR);
+                parts8<SP>(vS, pS);
+                parts8<SP>(vR, pR);
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     bf16x8 fy[XP], fx[XP];
 #pragma unroll
                     for (int i = 0; i < XP; ++i) {
-                        fy[i] = frag_row<P>(tY + i * L * P, 16 * t, ks);
-                        fx[i] = frag_row<P>(tX + i * L * P, 16 * t, ks);
+                        fy[i] = frag_row<P>(tY + i * L * P, 16 * t, ks, rP);
+                        fx[i] = frag_row<P>(tX + i * L * P, 16 * t, ks, rP);
                     }
                     aC[t] = mma_parts<SP, XP>(pS, fy, aC[t]);
                     aB[t] = mma_parts<SP, XP>(pR, fx, aB[t]);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
@@ -267,6 +285,7 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
                     dB[m][t][r] = fmaf(w, aB[t][r], dB[m][t][r]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         z = wave_sum_dpp(z);
         if (lane == 0) sZ[wave] = z;
@@ -278,7 +297,8 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
                 sV[wave][16 * t + l15] = b;
             }
         }
-        __syncthreads();   // the chunk matrices and the partial sums are whole
+        lds_barrier();   // the chunk matrices and the partial sums are whole
+        if (hw + 1 < hw0 + hwn) fetch(hw + 1);
 
         // products with the chunk matrices
 #pragma unroll
@@ -289,25 +309,26 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
                 bf16x8 fb[XP], fc[XP];
 #pragma unroll
                 for (int i = 0; i < XP; ++i) {
-                    fb[i] = frag_col<N, 4>(tB + i * L * N, n0, ks);
-                    fc[i] = frag_col<N, 4>(tC + i * L * N, n0, ks);
+                    fb[i] = frag_col<N>(tB + i * L * N, n0, ks, cN);
+                    fc[i] = frag_col<N>(tC + i * L * N, n0, ks, cN);
                 }
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     if (ks <= t / 2) {
                         bf16x8 fk[KP];
 #pragma unroll
-                        for (int i = 0; i < KP; ++i) fk[i] = frag_row<L>(tK + i * L * L, 16 * t, ks);
+                        for (int i = 0; i < KP; ++i) fk[i] = frag_row<L>(tK + i * L * L, 16 * t, ks, rL);
                         dC[m][t] = mma_parts<XP, KP>(fb, fk, dC[m][t]);
                     }
                     if (ks >= t / 2) {
                         bf16x8 fk[KP];
 #pragma unroll
-                        for (int i = 0; i < KP; ++i) fk[i] = frag_col<L, 4>(tK + i * L * L, 16 * t, ks);
+                        for (int i = 0; i < KP; ++i) fk[i] = frag_col<L>(tK + i * L * L, 16 * t, ks, cL);
                         dB[m][t] = mma_parts<XP, KP>(fc, fk, dB[m][t]);
                     }
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int c = 0; c < PT; ++c) {
@@ -326,7 +347,7 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
                 for (int t = 0; t < TT; ++t) {
                     bf16x8 fb[XP];
 #pragma unroll
-                    for (int i = 0; i < XP; ++i) fb[i] = frag_row<N>(tB + i * L * N, 16 * t, ks);
+                    for (int i = 0; i < XP; ++i) fb[i] = frag_row<N>(tB + i * L * N, 16 * t, ks, rN);
                     dX[t] = mma_parts<RP, XP>(pR, fb, dX[t]);
                 }
             }
@@ -336,13 +357,13 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
             for (int ks = 0; ks < L / 32; ++ks) {
                 bf16x8 fy[XP];
 #pragma unroll
-                for (int i = 0; i < XP; ++i) fy[i] = frag_col<P, 4>(tY + i * L * P, p0, ks);
+                for (int i = 0; i < XP; ++i) fy[i] = frag_col<P>(tY + i * L * P, p0, ks, cP);
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     if (ks < t / 2) continue;
                     bf16x8 fm[KP];
 #pragma unroll
-                    for (int i = 0; i < KP; ++i) fm[i] = frag_col<L, 4>(tM + i * L * L, 16 * t, ks);
+                    for (int i = 0; i < KP; ++i) fm[i] = frag_col<L>(tM + i * L * L, 16 * t, ks, cL);
                     dX[t] = mma_parts<XP, KP>(fy, fm, dX[t]);
                 }
             }
@@ -398,10 +419,11 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
                 to[2] = b;
             }
         }
-        __syncthreads();   // the tiles are consumed
+        lds_barrier();   // the tiles are consumed (rows and stores stay in flight)
     }
 
     // dB and dC of these heads: the gradients themselves, or a partial sum
+    const int l15 = lane & 15, lg = lane >> 4;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll

@@ -3,57 +3,66 @@
 // include/kda_ssm.h.
 //
 // Every form moves each element once and does about 2 W + 10 flops on it, so
-// all are bound by HBM.  A lane owns 16 bytes of neighbouring channels (8 of
-// bf16, 4 of float32) of a block of consecutive token rows, so that every
-// access of a wave is a run of 512 contiguous bytes per row, and slides the
-// last W - 1 inputs through registers: each input is read once per block plus
-// the W - 1 rows before it.
+// all are bound by HBM.  A wave owns 256 neighbouring channels, four per lane
+// (512 contiguous bytes of bf16 per row, 1 KB of float32), of a block of
+// consecutive token rows, requests CV_AHEAD rows while it computes the
+// CV_AHEAD before them and slides the last W - 1 inputs through registers:
+// each input is read once per block plus the W - 1 rows before it.  Rows are
+// the same for all lanes, so sequence boundaries cost scalar instructions
+// only.  Eight channels per lane and all rows requested at once, the first
+// form, needs 180 to 400 registers: 42 us forward and 121 us backward at 8192
+// rows of 4352 channels.
 #include "kda_device.h"
 #include "kda_ssm_launch.h"
 
 namespace kda {
 
-constexpr int CV_LANES = 32;    // channel vectors per workgroup
-constexpr int CV_BLOCKS = 8;    // row blocks per workgroup
-constexpr int CV_THREADS = CV_LANES * CV_BLOCKS;
-constexpr int CV_TOK = 16;      // rows per lane, forward
+constexpr int CV_WAVES = (int)kConvWaves;       // row blocks per workgroup, one per wave
+constexpr int CV_THREADS = 64 * CV_WAVES;
+constexpr int CV_AHEAD = 8;       // rows per request, forward
+constexpr int CB_AHEAD = 4;       // ... backward (more registers per row)
+constexpr int CV_CH = 256;        // channels per wave
 
-// 16 bytes of channels as floats, and back.
+// Four channels as floats, and back (stores that leave no copy in the L2,
+// which is far smaller than any large output: forward 33 against 40 us).
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__bf16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const void* base, int64_t e, float (&f)[8]) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>((const __bf16*)base + e);
+    typedef u32x2 raw;
+    static __device__ __forceinline__ raw fetch(const void* base, int64_t e) {
+        return *reinterpret_cast<const u32x2*>((const __bf16*)base + e);
+    }
+    static __device__ __forceinline__ void open(raw u, float (&f)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             f[2 * i] = bf2_first(u[i]);
             f[2 * i + 1] = bf2_second(u[i]);
         }
     }
-    static __device__ __forceinline__ void store(void* base, int64_t e, const float (&f)[8]) {
-        u32x4 u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = pack_bf2(f[2 * i], f[2 * i + 1]);
-        *reinterpret_cast<u32x4*>((__bf16*)base + e) = u;
+    static __device__ __forceinline__ void store(void* base, int64_t e, const float (&f)[4]) {
+        __builtin_nontemporal_store(u32x2{pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3])},
+                                    reinterpret_cast<u32x2*>((__bf16*)base + e));
     }
 };
 template <>
 struct Vec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const void* base, int64_t e, float (&f)[4]) {
-        const f32x4 u = *reinterpret_cast<const f32x4*>((const float*)base + e);
+    typedef f32x4 raw;
+    static __device__ __forceinline__ raw fetch(const void* base, int64_t e) {
+        return *reinterpret_cast<const f32x4*>((const float*)base + e);
+    }
+    static __device__ __forceinline__ void open(raw u, float (&f)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = u[i];
     }
     static __device__ __forceinline__ void store(void* base, int64_t e, const float (&f)[4]) {
-        f32x4 u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = f[i];
-        *reinterpret_cast<f32x4*>((float*)base + e) = u;
+        __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4*>((float*)base + e));
     }
 };
+template <typename T>
+__device__ __forceinline__ void load4(const void* base, int64_t e, float (&f)[4]) {
+    Vec<T>::open(Vec<T>::fetch(base, e), f);
+}
 // N floats from a 16-byte aligned float array.
 template <int N>
 __device__ __forceinline__ void load_f(const float* p, float (&f)[N]) {
@@ -103,107 +112,109 @@ __device__ __forceinline__ Seq seq_of_row(const ConvParams& p, int64_t row) {
 }
 
 // x at position pos of sequence s (pos < 0: the cache's entry, or zero) for
-// N channels from c0.
-template <typename InT, int W, int N>
-__device__ __forceinline__ void input_at(const ConvParams& p, const Seq& s, int64_t pos, int64_t c0,
-                                         float (&f)[N]) {
+// four channels from c0.
+template <typename InT, int W>
+__device__ __forceinline__ void input_at(const ConvParams& p, const Seq& s, int64_t pos, int64_t c0, float (&f)[4]) {
     if (pos >= 0) {
-        Vec<InT>::load(p.x, (s.start + pos) * p.x_stride + c0, f);
+        load4<InT>(p.x, (s.start + pos) * p.x_stride + c0, f);
     } else if (p.cache && pos >= 1 - W) {
-        load_f<N>(p.cache + (s.n * (W - 1) + (W - 1 + pos)) * p.channels + c0, f);
+        load4<float>(p.cache, (s.n * (W - 1) + (W - 1 + pos)) * p.channels + c0, f);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = 0.f;
+        for (int i = 0; i < 4; ++i) f[i] = 0.f;
     }
 }
 
-// Channel tiles of a row; a launch's workgroups run through them first, so
+// Channel strips of a row; a launch's workgroups run through them first, so
 // that whole rows are in flight together.
-template <int N>
-__host__ __device__ __forceinline__ int64_t cv_tiles(int64_t channels) {
-    return (channels + CV_LANES * N - 1) / (CV_LANES * N);
-}
+__host__ __device__ __forceinline__ int64_t cv_strips(int64_t channels) { return (channels + CV_CH - 1) / CV_CH; }
+
+// The rows of a walk, one after the other, all wave-uniform.
+struct Walk {
+    Seq s;
+    int64_t r;
+    __device__ __forceinline__ Walk(const ConvParams& p, int64_t row) : s(seq_of_row(p, row)), r(row) {}
+    // moves to row r; whether it belongs to a sequence (then s is that one)
+    __device__ __forceinline__ bool at(const ConvParams& p, int64_t row) {
+        r = row;
+        while (r >= s.end && s.n + 1 < p.n_seqs) s = seq_range(p, s.n + 1);
+        return r >= s.start && r < s.end;
+    }
+};
 
 template <typename InT, int W>
-__global__ __launch_bounds__(CV_THREADS) void conv_fwd_kernel(ConvParams p) {
-    constexpr int N = Vec<InT>::N;
-    const uint32_t tiles = (uint32_t)cv_tiles<N>(p.channels);
-    const uint32_t rb = blockIdx.x / tiles;
-    const int64_t c0 = ((int64_t)(blockIdx.x - rb * tiles) * CV_LANES + (threadIdx.x & (CV_LANES - 1))) * N;
+__global__ __launch_bounds__(CV_THREADS) void conv_fwd_kernel(ConvParams p, int32_t rows_per_wave) {
+    const uint32_t strips = (uint32_t)cv_strips(p.channels);
+    const uint32_t rb = blockIdx.x / strips;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t c0 = (int64_t)(blockIdx.x - rb * strips) * CV_CH + 4 * (threadIdx.x & 63);
     if (c0 >= p.channels) return;
-    const int64_t r0 = ((int64_t)rb * CV_BLOCKS + threadIdx.x / CV_LANES) * CV_TOK;
+    const int64_t r0 = ((int64_t)rb * CV_WAVES + wave) * rows_per_wave;
     if (r0 >= p.rows) return;
-    const int64_t r1 = r0 + CV_TOK < p.rows ? r0 + CV_TOK : p.rows;
-    // all rows first: one round trip to memory
-    float cur[CV_TOK][N];
+    const int64_t r1 = r0 + rows_per_wave < p.rows ? r0 + rows_per_wave : p.rows;
+    typename Vec<InT>::raw ahead[CV_AHEAD], now[CV_AHEAD];
+    auto request = [&](int64_t r) {
 #pragma unroll
-    for (int i = 0; i < CV_TOK; ++i) {
-        const int64_t r = r0 + i < r1 ? r0 + i : r1 - 1;
-        Vec<InT>::load(p.x, r * p.x_stride + c0, cur[i]);
-    }
-    float w[W][N], b[N];
-    load_w<W, N>(p.w, c0, w);
-#pragma unroll
-    for (int c = 0; c < N; ++c) b[c] = 0.f;
+        for (int i = 0; i < CV_AHEAD; ++i) {
+            const int64_t k = r + i < p.rows ? r + i : p.rows - 1;
+            ahead[i] = Vec<InT>::fetch(p.x, k * p.x_stride + c0);
+        }
+    };
+    request(r0);
+    float w[W][4], b[4] = {0.f, 0.f, 0.f, 0.f};
+    load_w<W, 4>(p.w, c0, w);
     if (p.bias) {
 #pragma unroll
-        for (int c = 0; c < N; ++c) b[c] = p.bias[c0 + c];
+        for (int c = 0; c < 4; ++c) b[c] = p.bias[c0 + c];
     }
-    Seq s = seq_of_row(p, r0);
-    float win[W - 1][N];
-    bool fresh = true;
+    Walk k(p, r0);
+    float win[W - 1][4];
 #pragma unroll
-    for (int i = 0; i < CV_TOK; ++i) {
-        const int64_t r = r0 + i;
-        if (r >= r1) break;
-        while (r >= s.end && s.n + 1 < p.n_seqs) {
-            s = seq_range(p, s.n + 1);
-            fresh = true;
+    for (int j = 0; j < W - 1; ++j) input_at<InT, W>(p, k.s, r0 >= k.s.start && r0 < k.s.end ? r0 - k.s.start - (W - 1) + j : -W, c0, win[j]);
+    for (int64_t r = r0; r < r1; r += CV_AHEAD) {
+#pragma unroll
+        for (int i = 0; i < CV_AHEAD; ++i) now[i] = ahead[i];
+        if (r + CV_AHEAD < r1) request(r + CV_AHEAD);
+#pragma unroll
+        for (int i = 0; i < CV_AHEAD; ++i) {
+            if (r + i >= r1) break;
+            const bool in = k.at(p, r + i);
+            if (in && r + i == k.s.start) {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) input_at<InT, W>(p, k.s, j - (W - 1), c0, win[j]);
+            }
+            float x[4], y[4];
+            Vec<InT>::open(now[i], x);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float z = b[c];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
+                z = fmaf(w[W - 1][c], x[c], z);
+                y[c] = p.activation ? z * cv_sigm(z) : z;
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) win[j][c] = win[j + 1][c];
+                win[W - 2][c] = x[c];
+            }
+            if (in) Vec<InT>::store(p.y, (r + i) * p.channels + c0, y);
         }
-        if (r < s.start || r >= s.end) continue;   // outside every sequence
-        if (fresh || r == s.start) {
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) input_at<InT, W, N>(p, s, r - s.start - (W - 1) + j, c0, win[j]);
-            fresh = false;
-        }
-        float y[N];
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-            float z = b[c];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
-            z = fmaf(w[W - 1][c], cur[i][c], z);
-            y[c] = p.activation ? z * cv_sigm(z) : z;
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) win[j][c] = win[j + 1][c];
-            win[W - 2][c] = cur[i][c];
-        }
-        Vec<InT>::store(p.y, r * p.channels + c0, y);
     }
 }
 
 // The cache after the call, as a launch of its own: no lane of the
 // convolution reads an entry that another has replaced.
 template <typename InT, int W>
-__global__ __launch_bounds__(CV_THREADS) void conv_cache_update_kernel(ConvParams p) {
-    constexpr int N = Vec<InT>::N;
-    const int64_t nv = p.channels / N;
-    const int64_t idx = (int64_t)blockIdx.x * CV_THREADS + threadIdx.x;
+__global__ __launch_bounds__(64) void conv_cache_update_kernel(ConvParams p) {
+    const int64_t nv = p.channels / 4;
+    const int64_t idx = (int64_t)blockIdx.x * 64 + threadIdx.x;
     if (idx >= nv * p.n_seqs) return;
-    const int64_t n = idx / nv, c0 = (idx - n * nv) * N;
+    const int64_t n = idx / nv, c0 = (idx - n * nv) * 4;
     const Seq s = seq_range(p, n);
-    float f[W - 1][N];
+    float f[W - 1][4];
 #pragma unroll
-    for (int m = 0; m < W - 1; ++m) input_at<InT, W, N>(p, s, s.end - s.start - (W - 1) + m, c0, f[m]);
+    for (int m = 0; m < W - 1; ++m) input_at<InT, W>(p, s, s.end - s.start - (W - 1) + m, c0, f[m]);
 #pragma unroll
-    for (int m = 0; m < W - 1; ++m)
-        Vec<float>::store(p.cache, (n * (W - 1) + m) * p.channels + c0, *reinterpret_cast<float(*)[4]>(f[m]));
-    if constexpr (N == 8) {
-#pragma unroll
-        for (int m = 0; m < W - 1; ++m)
-            Vec<float>::store(p.cache, (n * (W - 1) + m) * p.channels + c0 + 4,
-                              *reinterpret_cast<float(*)[4]>(f[m] + 4));
-    }
+    for (int m = 0; m < W - 1; ++m) Vec<float>::store(p.cache, (n * (W - 1) + m) * p.channels + c0, f[m]);
 }
 
 // A few tokens per request: a lane owns 4 channels of one request from its
@@ -215,20 +226,9 @@ __global__ __launch_bounds__(64) void conv_step_kernel(ConvParams p) {
     const int64_t idx = (int64_t)blockIdx.x * 64 + threadIdx.x;
     if (idx >= nv * p.n_seqs) return;
     const int64_t n = idx / nv, c0 = (idx - n * nv) * 4;
-    auto load = [&](const void* base, int64_t e, float (&f)[4]) {
-        if constexpr (sizeof(InT) == 4) {
-            Vec<float>::load(base, e, f);
-        } else {
-            const u32x2 u = *reinterpret_cast<const u32x2*>((const __bf16*)base + e);
-            f[0] = bf2_first(u[0]);
-            f[1] = bf2_second(u[0]);
-            f[2] = bf2_first(u[1]);
-            f[3] = bf2_second(u[1]);
-        }
-    };
     float win[W - 1][4];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) Vec<float>::load(p.cache, (n * (W - 1) + j) * p.channels + c0, win[j]);
+    for (int j = 0; j < W - 1; ++j) load4<float>(p.cache, (n * (W - 1) + j) * p.channels + c0, win[j]);
     auto push = [&](const float (&f)[4]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -241,40 +241,43 @@ __global__ __launch_bounds__(64) void conv_step_kernel(ConvParams p) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) Vec<float>::store(p.cache, (n * (W - 1) + j) * p.channels + c0, win[j]);
     };
-    if (p.Tr > 0) {
-        int k = p.n_replay ? p.n_replay[n] : p.Tr;
-        k = k < 0 ? 0 : (k > p.Tr ? p.Tr : k);
-        for (int t = k > W - 1 ? k - (W - 1) : 0; t < k; ++t) {   // only the last W - 1 stay
-            float f[4];
-            load(p.rx, (n * p.Tr + t) * p.rx_stride + c0, f);
-            push(f);
-        }
-    }
-    if (!p.commit) keep();
     float w[W][4], b[4] = {0.f, 0.f, 0.f, 0.f};
     load_w<W, 4>(p.w, c0, w);
     if (p.bias) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) b[c] = p.bias[c0 + c];
     }
-    for (int t = 0; t < (int)p.T; ++t) {
-        const int64_t r = n * p.T + t;
-        float f[4], y[4];
-        load(p.x, r * p.x_stride + c0, f);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float z = b[c];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
-            z = fmaf(w[W - 1][c], f[c], z);
-            y[c] = p.activation ? z / (1.f + expf(-z)) : z;
+    if (p.Tr > 0) {
+        int k = p.n_replay ? p.n_replay[n] : p.Tr;
+        k = k < 0 ? 0 : (k > p.Tr ? p.Tr : k);
+        for (int t = k > W - 1 ? k - (W - 1) : 0; t < k; ++t) {   // only the last W - 1 stay
+            float f[4];
+            load4<InT>(p.rx, (n * p.Tr + t) * p.rx_stride + c0, f);
+            push(f);
         }
-        push(f);
-        if constexpr (sizeof(InT) == 4) {
-            Vec<float>::store(p.y, r * p.channels + c0, y);
-        } else {
-            u32x2 u = {pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
-            *reinterpret_cast<u32x2*>((__bf16*)p.y + r * p.channels + c0) = u;
+    }
+    if (!p.commit) keep();
+    const int T = (int)p.T;
+    for (int t0 = 0; t0 < T; t0 += CV_AHEAD) {
+        typename Vec<InT>::raw xr[CV_AHEAD];
+#pragma unroll
+        for (int i = 0; i < CV_AHEAD; ++i)
+            xr[i] = Vec<InT>::fetch(p.x, (n * T + (t0 + i < T ? t0 + i : T - 1)) * p.x_stride + c0);
+#pragma unroll
+        for (int i = 0; i < CV_AHEAD; ++i) {
+            if (t0 + i >= T) break;
+            float f[4], y[4];
+            Vec<InT>::open(xr[i], f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float z = b[c];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
+                z = fmaf(w[W - 1][c], f[c], z);
+                y[c] = p.activation ? z / (1.f + expf(-z)) : z;
+            }
+            push(f);
+            Vec<InT>::store(p.y, (n * T + t0 + i) * p.channels + c0, y);
         }
     }
     if (p.commit) keep();
@@ -282,129 +285,130 @@ __global__ __launch_bounds__(64) void conv_step_kernel(ConvParams p) {
 
 // Backward.  With dz = dy silu'(z):
 //   dx_t = sum_d w_{W-1-d} dz_{t+d},  dw_j = sum_t dz_t x_{t-W+1+j},  db = sum_t dz_t.
-// A lane walks CB_TOK rows and the W - 1 rows after them (recomputing their
-// dz, so that no dz goes through memory), with the W - 1 unfinished dx in
+// A wave walks its rows and the W - 1 rows after them (recomputing their dz,
+// so that no dz goes through memory), with the W - 1 unfinished dx in
 // registers; its part of dw and db is summed over the workgroup's row blocks
 // in LDS and written as one partial sum per workgroup, which a second launch
 // adds up in a fixed order.
-constexpr int CB_TOK = (int)(kConvBwdRows / CV_BLOCKS);
-
 template <typename InT, int W>
 __global__ __launch_bounds__(CV_THREADS) void conv_bwd_kernel(ConvBwdParams q) {
-    constexpr int N = Vec<InT>::N;
     const ConvParams& p = q.f;
-    const int lane = threadIdx.x & (CV_LANES - 1), blk = threadIdx.x / CV_LANES;
-    const uint32_t tiles = (uint32_t)cv_tiles<N>(p.channels);
-    const uint32_t rb = blockIdx.x / tiles;
-    const int64_t c0 = ((int64_t)(blockIdx.x - rb * tiles) * CV_LANES + lane) * N;
+    const uint32_t strips = (uint32_t)cv_strips(p.channels);
+    const uint32_t rb = blockIdx.x / strips;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t c0 = (int64_t)(blockIdx.x - rb * strips) * CV_CH + 4 * lane;
     const bool live = c0 < p.channels;
-    const int64_t r0 = ((int64_t)rb * CV_BLOCKS + blk) * CB_TOK;
-    float gw[W + 1][N];
+    const int64_t r0 = ((int64_t)rb * CV_WAVES + wave) * q.rows_per_wave;
+    float gw[W + 1][4];
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int c = 0; c < N; ++c) gw[j][c] = 0.f;
+        for (int c = 0; c < 4; ++c) gw[j][c] = 0.f;
     if (live && r0 < p.rows) {
-        const int64_t r1 = r0 + CB_TOK < p.rows ? r0 + CB_TOK : p.rows;
-        const int64_t r2 = r1 + W - 1 < p.rows ? r1 + W - 1 : p.rows;
-        float w[W][N], b[N];
-        load_w<W, N>(p.w, c0, w);
+        const int64_t r1 = r0 + q.rows_per_wave < p.rows ? r0 + q.rows_per_wave : p.rows;
+        const int64_t r2 = r1 + W - 1;
+        typename Vec<InT>::raw xa[CB_AHEAD], ga[CB_AHEAD], xn[CB_AHEAD], gn[CB_AHEAD];
+        auto request = [&](int64_t r) {
 #pragma unroll
-        for (int c = 0; c < N; ++c) b[c] = p.bias ? p.bias[c0 + c] : 0.f;
-        Seq s = seq_of_row(p, r0);
-        float win[W - 1][N], dx[W][N];   // dx[d]: the row d before the current one
+            for (int i = 0; i < CB_AHEAD; ++i) {
+                const int64_t k = r + i < p.rows ? r + i : p.rows - 1;
+                xa[i] = Vec<InT>::fetch(p.x, k * p.x_stride + c0);
+                ga[i] = Vec<InT>::fetch(q.gy, k * q.gy_stride + c0);
+            }
+        };
+        request(r0);
+        float w[W][4], b[4];
+        load_w<W, 4>(p.w, c0, w);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[c] = p.bias ? p.bias[c0 + c] : 0.f;
+        Walk k(p, r0);
+        float win[W - 1][4], dx[W][4];   // dx[d]: of the row d before the current one
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) input_at<InT, W>(p, k.s, r0 >= k.s.start && r0 < k.s.end ? r0 - k.s.start - (W - 1) + j : -W, c0, win[j]);
 #pragma unroll
         for (int d = 0; d < W; ++d)
 #pragma unroll
-            for (int c = 0; c < N; ++c) dx[d][c] = 0.f;
-        // rows [lo, ...) of this walk belong to a sequence and are this lane's
-        bool fresh = true;
-        int64_t first = r0;   // first row of the current sequence in this walk
-        auto finish = [&](int64_t r, const float (&f)[N]) {
-            if (r >= first && r < r1) Vec<InT>::store(q.gx, r * p.channels + c0, f);
-        };
-        int64_t r = r0;
-        for (; r < r2; ++r) {
-            if (r >= s.end) {
-                // the sequence ends: its last rows are complete
-                if (!fresh) {
+            for (int c = 0; c < 4; ++c) dx[d][c] = 0.f;
+        uint32_t mine = 0;   // bit d: the row d before the current one is of a sequence and this wave's
+        for (int64_t r = r0; r < r2; r += CB_AHEAD) {
 #pragma unroll
-                    for (int d = 1; d < W; ++d) finish(r - d, dx[d - 1]);
-                }
-                while (r >= s.end && s.n + 1 < p.n_seqs) s = seq_range(p, s.n + 1);
-                fresh = true;
+            for (int i = 0; i < CB_AHEAD; ++i) {
+                xn[i] = xa[i];
+                gn[i] = ga[i];
             }
-            if (r < s.start || r >= s.end) continue;
-            if (fresh) {
-                if (r >= r1) break;   // the next sequence's rows are another lane's
-                first = r;
+            if (r + CB_AHEAD < r2) request(r + CB_AHEAD);
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) input_at<InT, W, N>(p, s, r - s.start - (W - 1) + j, c0, win[j]);
+            for (int i = 0; i < CB_AHEAD; ++i) {
+                const int64_t row = r + i;
+                if (row >= r2) break;
+                const bool in = row < p.rows && k.at(p, row);
+                if (in && row == k.s.start) {
 #pragma unroll
-                for (int d = 0; d < W; ++d)
-#pragma unroll
-                    for (int c = 0; c < N; ++c) dx[d][c] = 0.f;
-                fresh = false;
-            }
-            float x[N], g[N];
-            Vec<InT>::load(p.x, r * p.x_stride + c0, x);
-            Vec<InT>::load(q.gy, r * q.gy_stride + c0, g);
-            const bool own = r < r1;
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-                float dz = g[c];
-                if (p.activation) {
-                    float z = b[c];
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
-                    z = fmaf(w[W - 1][c], x[c], z);
-                    const float sg = cv_sigm(z);
-                    dz = g[c] * sg * fmaf(z, 1.f - sg, 1.f);
+                    for (int j = 0; j < W - 1; ++j) input_at<InT, W>(p, k.s, j - (W - 1), c0, win[j]);
                 }
+                mine = mine << 1 | (in && row < r1 ? 1u : 0u);
+                // rows before this one that this row's z reaches (none outside its sequence)
+                const int reach = in ? (row - k.s.start < W - 1 ? (int)(row - k.s.start) : W - 1) : -1;
+                float x[4], g[4];
+                Vec<InT>::open(xn[i], x);
+                Vec<InT>::open(gn[i], g);
 #pragma unroll
-                for (int d = W - 1; d >= 1; --d) dx[d][c] = fmaf(w[W - 1 - d][c], dz, dx[d - 1][c]);
-                dx[0][c] = w[W - 1][c] * dz;
-                if (own) {
+                for (int c = 0; c < 4; ++c) {
+                    float dz = g[c];
+                    if (p.activation) {
+                        float z = b[c];
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) gw[j][c] = fmaf(dz, win[j][c], gw[j][c]);
-                    gw[W - 1][c] = fmaf(dz, x[c], gw[W - 1][c]);
-                    gw[W][c] += dz;
+                        for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
+                        z = fmaf(w[W - 1][c], x[c], z);
+                        const float sg = cv_sigm(z);
+                        dz = g[c] * sg * fmaf(z, 1.f - sg, 1.f);
+                    }
+                    if (reach == W - 1) {
+#pragma unroll
+                        for (int d = W - 1; d >= 1; --d) dx[d][c] = fmaf(w[W - 1 - d][c], dz, dx[d - 1][c]);
+                    } else {
+#pragma unroll
+                        for (int d = W - 1; d >= 1; --d)
+                            dx[d][c] = d <= reach ? fmaf(w[W - 1 - d][c], dz, dx[d - 1][c]) : dx[d - 1][c];
+                    }
+                    dx[0][c] = w[W - 1][c] * dz;
+                    if (mine & 1) {
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) gw[j][c] = fmaf(dz, win[j][c], gw[j][c]);
+                        gw[W - 1][c] = fmaf(dz, x[c], gw[W - 1][c]);
+                        gw[W][c] += dz;
+                    }
+#pragma unroll
+                    for (int j = 0; j + 1 < W - 1; ++j) win[j][c] = win[j + 1][c];
+                    win[W - 2][c] = x[c];
                 }
-#pragma unroll
-                for (int j = 0; j + 1 < W - 1; ++j) win[j][c] = win[j + 1][c];
-                win[W - 2][c] = x[c];
+                if (mine >> (W - 1) & 1) Vec<InT>::store(q.gx, (row - (W - 1)) * p.channels + c0, dx[W - 1]);
             }
-            finish(r - (W - 1), dx[W - 1]);
-        }
-        if (!fresh) {   // the walk ended inside a sequence, or at its end with the rows
-#pragma unroll
-            for (int d = 1; d < W; ++d) finish(r - d, dx[d - 1]);
         }
     }
-    __shared__ float sum[CV_BLOCKS / 2][W + 1][CV_LANES * N];
+    __shared__ float sum[CV_WAVES / 2][W + 1][4][64];
 #pragma unroll
-    for (int half = CV_BLOCKS / 2; half >= 1; half /= 2) {
-        if (blk >= half && blk < 2 * half) {
+    for (int half = CV_WAVES / 2; half >= 1; half /= 2) {
+        if (wave >= half && wave < 2 * half) {
 #pragma unroll
             for (int j = 0; j <= W; ++j)
 #pragma unroll
-                for (int c = 0; c < N; ++c) sum[blk - half][j][lane * N + c] = gw[j][c];
+                for (int c = 0; c < 4; ++c) sum[wave - half][j][c][lane] = gw[j][c];
         }
         __syncthreads();
-        if (blk < half) {
+        if (wave < half) {
 #pragma unroll
             for (int j = 0; j <= W; ++j)
 #pragma unroll
-                for (int c = 0; c < N; ++c) gw[j][c] += sum[blk][j][lane * N + c];
+                for (int c = 0; c < 4; ++c) gw[j][c] += sum[wave][j][c][lane];
         }
         __syncthreads();
     }
-    if (blk == 0 && live) {
+    if (wave == 0 && live) {
 #pragma unroll
         for (int j = 0; j <= W; ++j)
-#pragma unroll
-            for (int c = 0; c < N; ++c)
-                q.partial[((int64_t)rb * (W + 1) + j) * p.channels + c0 + c] = gw[j][c];
+            Vec<float>::store(q.partial, ((int64_t)rb * (W + 1) + j) * p.channels + c0, gw[j]);
     }
 }
 
@@ -416,7 +420,13 @@ __global__ __launch_bounds__(256) void conv_bwd_reduce_kernel(ConvBwdParams q, i
     const int k = threadIdx.x >> 6;
     float a = 0.f;
     if (col < cols)
-        for (int64_t i = k; i < n_part; i += 4) a += q.partial[i * cols + col];
+        for (int64_t i = k; i < n_part; i += 32) {   // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = i + 4 * j < n_part ? q.partial[(i + 4 * j) * cols + col] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a += v[j];
+        }
     __shared__ float s[4][64];
     s[k][threadIdx.x & 63] = a;
     __syncthreads();
@@ -432,11 +442,11 @@ __global__ __launch_bounds__(256) void conv_bwd_reduce_kernel(ConvBwdParams q, i
 // Gradient of the cache: its entry m (position m - W + 1) is read by the
 // positions t < W - 1 with t - (W - 1 - j) = m - W + 1, that is tap j = m - t.
 template <typename InT, int W>
-__global__ __launch_bounds__(CV_THREADS) void conv_bwd_cache_kernel(ConvBwdParams q) {
-    constexpr int N = Vec<InT>::N;
+__global__ __launch_bounds__(64) void conv_bwd_cache_kernel(ConvBwdParams q) {
+    constexpr int N = 4;
     const ConvParams& p = q.f;
     const int64_t nv = p.channels / N;
-    const int64_t idx = (int64_t)blockIdx.x * CV_THREADS + threadIdx.x;
+    const int64_t idx = (int64_t)blockIdx.x * 64 + threadIdx.x;
     if (idx >= nv * p.n_seqs) return;
     const int64_t n = idx / nv, c0 = (idx - n * nv) * N;
     const Seq s = seq_range(p, n);
@@ -446,7 +456,7 @@ __global__ __launch_bounds__(CV_THREADS) void conv_bwd_cache_kernel(ConvBwdParam
 #pragma unroll
     for (int j = 0; j < 2 * (W - 1); ++j) {   // positions 1 - W .. W - 2
         const int64_t pos = j - (W - 1);
-        if (pos < len) input_at<InT, W, N>(p, s, pos, c0, in[j]);
+        if (pos < len) input_at<InT, W>(p, s, pos, c0, in[j]);
         else
             for (int c = 0; c < N; ++c) in[j][c] = 0.f;
     }
@@ -458,7 +468,7 @@ __global__ __launch_bounds__(CV_THREADS) void conv_bwd_cache_kernel(ConvBwdParam
     for (int t = 0; t < W - 1; ++t) {
         if (t >= len) break;
         float g[N];
-        Vec<InT>::load(q.gy, (s.start + t) * q.gy_stride + c0, g);
+        load4<InT>(q.gy, (s.start + t) * q.gy_stride + c0, g);
 #pragma unroll
         for (int c = 0; c < N; ++c) {
             float dz = g[c];
@@ -481,15 +491,14 @@ __global__ __launch_bounds__(CV_THREADS) void conv_bwd_cache_kernel(ConvBwdParam
 
 template <typename InT, int W>
 static hipError_t run_conv_fwd(const ConvParams& p, hipStream_t stream) {
-    constexpr int N = Vec<InT>::N;
     if (p.rows > 0) {
-        const dim3 grid((unsigned)(cv_tiles<N>(p.channels) * ((p.rows + CV_BLOCKS * CV_TOK - 1) / (CV_BLOCKS * CV_TOK))));
-        hipLaunchKernelGGL((conv_fwd_kernel<InT, W>), grid, dim3(CV_THREADS), 0, stream, p);
+        const int32_t rpw = (int32_t)conv_rows_per_wave(p.rows, p.channels);
+        const dim3 grid((unsigned)(cv_strips(p.channels) * ((p.rows + CV_WAVES * rpw - 1) / (CV_WAVES * rpw))));
+        hipLaunchKernelGGL((conv_fwd_kernel<InT, W>), grid, dim3(CV_THREADS), 0, stream, p, rpw);
     }
     if (p.cache) {
-        const int64_t n = (int64_t)p.n_seqs * (p.channels / N);
-        hipLaunchKernelGGL((conv_cache_update_kernel<InT, W>), dim3((unsigned)((n + CV_THREADS - 1) / CV_THREADS)),
-                           dim3(CV_THREADS), 0, stream, p);
+        const int64_t n = (int64_t)p.n_seqs * (p.channels / 4);
+        hipLaunchKernelGGL((conv_cache_update_kernel<InT, W>), dim3((unsigned)((n + 63) / 64)), dim3(64), 0, stream, p);
     }
     return hipGetLastError();
 }
@@ -501,19 +510,17 @@ static hipError_t run_conv_step(const ConvParams& p, hipStream_t stream) {
 }
 template <typename InT, int W>
 static hipError_t run_conv_bwd(const ConvBwdParams& q, hipStream_t stream) {
-    constexpr int N = Vec<InT>::N;
     const ConvParams& p = q.f;
-    const int64_t parts = (p.rows + kConvBwdRows - 1) / kConvBwdRows;
+    const int64_t parts = conv_bwd_parts(p.rows, p.channels);
     if (parts > 0) {
-        const dim3 grid((unsigned)(cv_tiles<N>(p.channels) * parts));
+        const dim3 grid((unsigned)(cv_strips(p.channels) * parts));
         hipLaunchKernelGGL((conv_bwd_kernel<InT, W>), grid, dim3(CV_THREADS), 0, stream, q);
     }
     const int64_t cols = (int64_t)(W + 1) * p.channels;
     hipLaunchKernelGGL((conv_bwd_reduce_kernel<W>), dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream, q, parts);
     if (q.gcache && p.n_seqs > 0) {
-        const int64_t n = (int64_t)p.n_seqs * (p.channels / N);
-        hipLaunchKernelGGL((conv_bwd_cache_kernel<InT, W>), dim3((unsigned)((n + CV_THREADS - 1) / CV_THREADS)),
-                           dim3(CV_THREADS), 0, stream, q);
+        const int64_t n = (int64_t)p.n_seqs * (p.channels / 4);
+        hipLaunchKernelGGL((conv_bwd_cache_kernel<InT, W>), dim3((unsigned)((n + 63) / 64)), dim3(64), 0, stream, q);
     }
     return hipGetLastError();
 }

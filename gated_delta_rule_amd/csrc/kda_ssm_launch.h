@@ -24,9 +24,22 @@ struct ConvParams {
 hipError_t launch_conv_fwd(const ConvParams& p, bool bf16_in, hipStream_t stream);
 hipError_t launch_conv_step(const ConvParams& p, bool bf16_in, hipStream_t stream);
 
-// Token rows per partial sum of the weight gradient (see kda_ssm_conv.hip):
-// the workspace holds [ceil(rows / this), width + 1, channels] floats.
-constexpr int64_t kConvBwdRows = 256;
+// Token rows per wave (a wave takes 256 channels of them): whole rounds of
+// the 4096 waves that run at once (16 per compute unit), with 32 to 64 rows
+// per wave where there are that many, at least 8.  A workgroup's waves share
+// a partial sum of the weight gradient: the backward workspace holds
+// [conv_bwd_parts, width + 1, channels] floats.
+constexpr int64_t kConvWaves = 4;
+constexpr int64_t conv_rows_per_wave(int64_t rows, int64_t channels) {
+    const int64_t units = rows * ((channels + 255) / 256);
+    const int64_t rounds = units / (4096 * 32) > 0 ? units / (4096 * 32) : 1;
+    const int64_t r = (units + 4096 * rounds - 1) / (4096 * rounds);
+    return r < 8 ? 8 : (r + 3) / 4 * 4;
+}
+constexpr int64_t conv_bwd_parts(int64_t rows, int64_t channels) {
+    const int64_t per = kConvWaves * conv_rows_per_wave(rows, channels);
+    return (rows + per - 1) / per;
+}
 struct ConvBwdParams {
     ConvParams f;            // x, w, bias, cache (before the forward call), cu, sizes
     const void* gy;          // rows of gy_stride elements
@@ -36,6 +49,7 @@ struct ConvBwdParams {
     float* gcache;           // [n_seqs, width - 1, channels] or nullptr
     float* partial;
     int64_t gy_stride;
+    int32_t rows_per_wave;
 };
 hipError_t launch_conv_bwd(const ConvBwdParams& p, bool bf16_in, hipStream_t stream);
 

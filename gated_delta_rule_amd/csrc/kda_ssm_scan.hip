@@ -33,9 +33,11 @@ struct ScanCfg {
     static constexpr int XP = BF ? 1 : 3;      // bf16 parts of an input
     static constexpr int MP = BF ? 1 : 3;      // ... of M
     static constexpr int SP = BF ? 1 : 3;      // ... of S in S^T C
-    static constexpr int WP = 3;               // ... of w x in the state update
+    static constexpr int WP = 3;               // ... of w x in the state update (two: S_T off by up to 2e-6, a tenth faster)
     static constexpr int HPW = 128 / P;        // heads per workgroup
 };
+// Eight waves of 16 columns each.
+constexpr int SC_WAVES = 8, SC_THREADS = 64 * SC_WAVES, SC_COLS = 128 / SC_WAVES, SC_CT = SC_COLS / 16;
 
 // What a launch computes along its chains.
 enum ScanMode {
@@ -47,21 +49,26 @@ enum ScanMode {
 //   dS' = e^{g_end} dS + sum_t C_t (e^{g_t} dy_t)^T
 // (C takes B's place, dy takes x's).
 template <typename InT, int N, int P, int MODE, bool REV>
-__global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p, int32_t hblocks) {
+__global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p, int32_t hblocks) {
     constexpr bool OUT = MODE == kOut;
     static_assert(!(OUT && REV), "outputs run forward");
     using Cfg = ScanCfg<InT, N, P>;
     constexpr int L = Cfg::L, XP = Cfg::XP, MP = Cfg::MP, SP = Cfg::SP, WP = Cfg::WP, HPW = Cfg::HPW;
     constexpr int TT = L / 16, NT = N / 16;
+    constexpr int TILES = TT * (TT + 1) / 2;   // 16 x 16 tiles of M up to the diagonal
     __shared__ __attribute__((aligned(16))) __bf16 tB[XP * L * N];
     __shared__ __attribute__((aligned(16))) __bf16 tC[OUT ? XP * L * N : 8];
     __shared__ __attribute__((aligned(16))) __bf16 tX[XP * L * 128];
     __shared__ __attribute__((aligned(16))) __bf16 tM[OUT ? HPW * MP * L * L : 8];
-    __shared__ ChunkDecay<L> dec[HPW];
+    // decay sums of DB chunks at a time, one chunk and head per wave
+    constexpr int DB = SC_WAVES / HPW;
+    __shared__ ChunkDecay<L> dec[DB][HPW];
 
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l15 = lane & 15, lg = lane >> 4;
+    int lane = tid & 63;
+    int rN = lane_row<N>(lane), rL = lane_row<L>(lane);
+    int2 cB = lane_col<N, OUT ? 8 : 4>(lane), cX = lane_col<128, 4>(lane);
     const int64_t slot = blockIdx.x / (uint32_t)hblocks;
     const int hb = (int)(blockIdx.x - (uint32_t)slot * hblocks);
     const int hpg = p.H / p.G, bpg = (hpg + HPW - 1) / HPW;
@@ -70,10 +77,10 @@ __global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p
     const int64_t heads = (int64_t)p.gn * hpg;    // of the seg, seg_decay and states arrays
     const int hfirst = p.g0 * hpg;
     const int nh = (grp + 1) * hpg - h0 < HPW ? (grp + 1) * hpg - h0 : HPW;
-    const int wh = wave * 32 / P;                 // this wave's head of the workgroup's
+    const int wh = wave * SC_COLS / P;                 // this wave's head of the workgroup's
     const bool live = wh < nh;
     const int h = h0 + (live ? wh : 0);
-    const int pc = (wave * 32) % P;               // first column within the head
+    const int pc = (wave * SC_COLS) % P;               // first column within the head
     SsmPiece s;
     if (p.cut) {
         s = ssm_piece(p.cu, p.rows, p.T, p.n_seqs, p.seg_len, slot);
@@ -91,14 +98,15 @@ __global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p
     // columns pc + 16 c + 4 lg + r, the order in which a lane's four registers
     // are neighbours in memory.
     auto state_at = [&](int c, int m, int r) {
+        const int l15 = lane & 15, lg = lane >> 4;
         return OUT ? (32 * (m >> 1) + 8 * lg + 4 * (m & 1) + r) * P + pc + 16 * c + l15
                    : (16 * m + l15) * P + pc + 16 * c + 4 * lg + r;
     };
-    f32x4 S[2][NT];
+    f32x4 S[SC_CT][NT];
     const int64_t seg_at = (slot * heads + h - hfirst) * (N * P), seq_at = (s.n * p.H + h) * (N * P);
     const float* init = MODE == kLocal ? nullptr : p.cut ? p.seg + seg_at : p.S0 ? p.S0 + seq_at : nullptr;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < SC_CT; ++c)
 #pragma unroll
         for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -106,7 +114,7 @@ __global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p
     auto save = [&](float* to) {
         if (!live) return;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < SC_CT; ++c)
 #pragma unroll
             for (int m = 0; m < NT; ++m) {
                 if constexpr (OUT) {
@@ -119,105 +127,143 @@ __global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p
     };
 
     if constexpr (OUT) {   // tiles above the diagonal that a 32-token slab reaches
-        for (int i = tid; i < HPW * MP * L * L / 8; i += SS_THREADS)
+        for (int i = tid; i < HPW * MP * L * L / 8; i += SC_THREADS)
             reinterpret_cast<u32x4*>(tM)[i] = u32x4{0, 0, 0, 0};
     }
 
+    const int64_t chunks = (s.r1 - s.r0 + L - 1) / L;
     // requests for a chunk's rows, one chunk ahead
-    Stager<InT, L, N> gB, gC;
-    Stager<InT, L, 128> gX;
-    float gdt = 0.f;
-    auto fetch = [&](int64_t row0) {
+    Stager<InT, L, N, SC_THREADS> gB, gC;
+    Stager<InT, L, 128, SC_THREADS> gX;
+    auto fetch = [&](int64_t row0, int what) {
         const int valid = s.r1 - row0 < L ? (s.r1 > row0 ? (int)(s.r1 - row0) : 0) : L;
         const int64_t r = valid > 0 ? row0 : s.r0;
-        gB.load((const InT*)p.B + r * p.B_stride + grp * N, p.B_stride, valid, N);
-        if constexpr (OUT) gC.load((const InT*)p.C + r * p.C_stride + grp * N, p.C_stride, valid, N);
-        gX.load((const InT*)p.x + r * p.x_stride + (int64_t)h0 * P, p.x_stride, valid, nh * P);
-        if (wave < nh) gdt = lane < valid ? p.dt[(r + lane) * p.H + h0 + wave] : 0.f;
+        if (what & 1) gB.load((const InT*)p.B + r * p.B_stride + grp * N, p.B_stride, valid, N);
+        if constexpr (OUT)
+            if (what & 2) gC.load((const InT*)p.C + r * p.C_stride + grp * N, p.C_stride, valid, N);
+        if (what & 4) gX.load((const InT*)p.x + r * p.x_stride + (int64_t)h0 * P, p.x_stride, valid, nh * P);
     };
-    const float bias = p.dt_bias && wave < nh ? p.dt_bias[h0 + wave] : 0.f;
-    const float Ah = wave < nh ? p.A[h0 + wave] : 0.f;
+    const int dh = wave % HPW, dk = wave / HPW;   // the head and, within a block, the chunk
+    const bool dec_live = dh < nh;
+    const float bias = p.dt_bias && dec_live ? p.dt_bias[h0 + dh] : 0.f;
+    const float Ah = dec_live ? p.A[h0 + dh] : 0.f;
+    float gdt = 0.f;
+    auto dt_there = [&](int64_t k, int64_t& row) {   // this lane's token of the k-th chunk of the walk
+        row = s.r0 + (REV ? chunks - 1 - k : k) * L + lane;
+        return dec_live && k < chunks && lane < L && row < s.r1;
+    };
+    auto fetch_dt = [&](int64_t k) {
+        int64_t row;
+        gdt = dt_there(k, row) ? p.dt[row * p.H + h0 + dh] : 0.f;
+    };
+    const float D0 = OUT && p.D ? p.D[h0] : 0.f, D1 = OUT && p.D && nh > 1 ? p.D[h0 + 1] : 0.f;
     double total = 0.0;
-    const int64_t chunks = (s.r1 - s.r0 + L - 1) / L;
     // this chain's first chunk among the slots of the states array
     const int64_t chunk0 = (p.cu ? s.start / L + s.n : s.n * ((p.T + L - 1) / L)) + (s.r0 - s.start) / L;
-    fetch(chunks == 0 ? s.r1 : REV ? s.r0 + (chunks - 1) * L : s.r0);   // (an empty sequence: no row)
+    const int64_t first = chunks == 0 ? s.r1 : REV ? s.r0 + (chunks - 1) * L : s.r0;   // (an empty sequence: no row)
+    fetch(first, 7);
+    fetch_dt(dk);
 
     for (int64_t i = 0; i < chunks; ++i) {
         const int64_t ch = REV ? chunks - 1 - i : i;
         const int64_t row0 = s.r0 + ch * L;
         const int valid = s.r1 - row0 < L ? (int)(s.r1 - row0) : L;
+        hide(lane), hide(rN), hide(rL), hide(cB), hide(cX);
+        const int l15 = lane & 15, lg = lane >> 4;
         gB.put(tB);
         if constexpr (OUT) gC.put(tC);
         gX.put(tX);
-        if (wave < HPW) total += chunk_decay<L>(dec[wave], gdt, wave < nh && lane < valid, bias, p.softplus, Ah);
-        __syncthreads();
-        fetch(REV ? (ch > 0 ? row0 - L : s.r1) : row0 + L);
-        const ChunkDecay<L>& d = dec[wh];
+        if (i % DB == 0) {
+            int64_t row;
+            const bool there = dt_there(i + dk, row);
+            total += chunk_decay<L>(dec[dk][dh], gdt, there, bias, p.softplus, Ah);
+            fetch_dt(i + DB + dk);
+        }
+        const ChunkDecay<L>* dc = dec[i % DB];
+        lds_barrier();
+        // the next chunk's rows, a tile at a time between the products: a
+        // wave would stand at a burst of requests
+        const int64_t next = REV ? (ch > 0 ? row0 - L : s.r1) : row0 + L;
+        fetch(next, 4);
+        const ChunkDecay<L>& d = dc[wh];
         if constexpr (MODE == kWalk) save(p.states + ((chunk0 + ch) * heads + h - hfirst) * (N * P));
 
-        f32x4 Y[2][TT];
+        f32x4 Y[SC_CT][TT];
         if constexpr (OUT) {
             // M tiles: rows s (B), columns t (C) of the transposed product, so
             // that a lane holds four neighbouring s of one t
-#pragma unroll
-            for (int k = 0; k < (TT * (TT + 1) / 2 + 3) / 4; ++k) {
-                const int idx = wave + 4 * k;
-                if (idx >= TT * (TT + 1) / 2) break;
-                int tt = 0;
-                while ((tt + 1) * (tt + 2) / 2 <= idx) ++tt;
-                const int st = idx - tt * (tt + 1) / 2;
+            auto tile_of = [&](int idx, int& tt, int& st) {
+                tt = (idx >= 1) + (idx >= 3) + (idx >= 6);
+                st = idx - tt * (tt + 1) / 2;
+            };
+            auto raw_tile = [&](int tt, int st) {
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < N / 32; ++ks) {
                     bf16x8 fb[XP], fc[XP];
 #pragma unroll
                     for (int i = 0; i < XP; ++i) {
-                        fb[i] = frag_row<N>(tB + i * L * N, 16 * st, ks);
-                        fc[i] = frag_row<N>(tC + i * L * N, 16 * tt, ks);
+                        fb[i] = frag_row<N>(tB + i * L * N, 16 * st, ks, rN);
+                        fc[i] = frag_row<N>(tC + i * L * N, 16 * tt, ks, rN);
                     }
                     acc = mma_parts<XP, XP>(fb, fc, acc);
                 }
+                return acc;
+            };
+            auto weigh = [&](const f32x4& acc, int tt, int st, int hh) {
                 const int t = 16 * tt + l15, s0 = 16 * st + 4 * lg;
+                const ChunkDecay<L>& dm = dc[hh];
+                const float ht = dm.gh[t], lt = dm.gl[t];
+                const f32x4 hs = *reinterpret_cast<const f32x4*>(&dm.gh[s0]);
+                const f32x4 ls = *reinterpret_cast<const f32x4*>(&dm.gl[s0]);
+                const f32x4 ds = *reinterpret_cast<const f32x4*>(&dm.dt[s0]);
+                float m[4];
 #pragma unroll
-                for (int hh = 0; hh < HPW; ++hh) {
-                    const ChunkDecay<L>& dh = dec[hh];
-                    const float ht = dh.gh[t], lt = dh.gl[t];
-                    const f32x4 hs = *reinterpret_cast<const f32x4*>(&dh.gh[s0]);
-                    const f32x4 ls = *reinterpret_cast<const f32x4*>(&dh.gl[s0]);
-                    const f32x4 ds = *reinterpret_cast<const f32x4*>(&dh.dt[s0]);
-                    const float Dh = p.D && hh < nh ? p.D[h0 + hh] : 0.f;
-                    float m[4];
+                for (int r = 0; r < 4; ++r) m[r] = acc[r] * (__expf((ht - hs[r]) + (lt - ls[r])) * ds[r]);
+                if (tt == st) {   // the diagonal tile: nothing above the diagonal, D on it
+                    const float Dh = hh == 0 ? D0 : D1;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        m[r] = s0 + r <= t ? acc[r] * (__expf((ht - hs[r]) + (lt - ls[r])) * ds[r]) : 0.f;
-                        if (s0 + r == t) m[r] += Dh;
-                    }
-                    __bf16* at = tM + hh * MP * L * L + 8 * ss_unit<L / 8>(t, s0 >> 3) + (s0 & 7);
+                    for (int r = 0; r < 4; ++r) m[r] = s0 + r < t ? m[r] : s0 + r == t ? m[r] + Dh : 0.f;
+                }
+                __bf16* at = tM + hh * MP * L * L + 8 * ss_unit<L / 8>(t, s0 >> 3) + (s0 & 7);
 #pragma unroll
-                    for (int i = 0; i < MP; ++i) {
-                        const u32x2 w = {pack_bf2(m[0], m[1]), pack_bf2(m[2], m[3])};
-                        *reinterpret_cast<u32x2*>(at + i * L * L) = w;
-                        if (i + 1 < MP) {
+                for (int i = 0; i < MP; ++i) {
+                    const u32x2 w = {pack_bf2(m[0], m[1]), pack_bf2(m[2], m[3])};
+                    *reinterpret_cast<u32x2*>(at + i * L * L) = w;
+                    if (i + 1 < MP) {
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                m[2 * r] -= bf2_first(w[r]);
-                                m[2 * r + 1] -= bf2_second(w[r]);
-                            }
+                        for (int r = 0; r < 2; ++r) {
+                            m[2 * r] -= bf2_first(w[r]);
+                            m[2 * r + 1] -= bf2_second(w[r]);
                         }
                     }
                 }
+            };
+            // a tile for both heads per wave, then the rest one head at a time
+            int tt, st;
+            if (wave < TILES) {
+                tile_of(wave, tt, st);
+                const f32x4 acc = raw_tile(tt, st);
+#pragma unroll
+                for (int hh = 0; hh < HPW; ++hh) weigh(acc, tt, st, hh);
             }
+            if constexpr (TILES > SC_WAVES) {
+                if (wave < (TILES - SC_WAVES) * HPW) {
+                    tile_of(SC_WAVES + wave / HPW, tt, st);
+                    weigh(raw_tile(tt, st), tt, st, wave % HPW);
+                }
+            }
+            fetch(next, 1);
             // Y^T = S^T C^T, rows p, columns t
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < SC_CT; ++c)
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) Y[c][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < N / 32; ++j) {
-                bf16x8 fs[2][SP];
+                bf16x8 fs[SC_CT][SP];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < SC_CT; ++c) {
                     float v[8];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -230,29 +276,30 @@ __global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p
                 for (int tt = 0; tt < TT; ++tt) {
                     bf16x8 fc[XP];
 #pragma unroll
-                    for (int i = 0; i < XP; ++i) fc[i] = frag_row<N>(tC + i * L * N, 16 * tt, j);
+                    for (int i = 0; i < XP; ++i) fc[i] = frag_row<N>(tC + i * L * N, 16 * tt, j, rN);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) Y[c][tt] = mma_parts<SP, XP>(fs[c], fc, Y[c][tt]);
+                    for (int c = 0; c < SC_CT; ++c) Y[c][tt] = mma_parts<SP, XP>(fs[c], fc, Y[c][tt]);
                 }
             }
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt) {
                 const float e = d.eg[16 * tt + l15];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) Y[c][tt] *= e;
+                for (int c = 0; c < SC_CT; ++c) Y[c][tt] *= e;
             }
-            __syncthreads();   // M is whole
+            lds_barrier();   // M is whole
         }
 
+        fetch(next, OUT ? 2 : 1);
         // x columns as operands: k runs over the tokens
-        bf16x8 fx[2][L / 32][XP];
+        bf16x8 fx[SC_CT][L / 32][XP];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < SC_CT; ++c)
 #pragma unroll
             for (int ks = 0; ks < L / 32; ++ks)
 #pragma unroll
                 for (int i = 0; i < XP; ++i)
-                    fx[c][ks][i] = frag_col<128, 4>(tX + i * L * 128, 32 * wave + 16 * c, ks);
+                    fx[c][ks][i] = frag_col<128>(tX + i * L * 128, SC_COLS * wave + 16 * c, ks, cX);
 
         if constexpr (OUT) {
             const __bf16* M = tM + wh * MP * L * L;
@@ -262,9 +309,9 @@ __global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p
                 for (int ks = 0; ks <= tt / 2; ++ks) {
                     bf16x8 fm[MP];
 #pragma unroll
-                    for (int i = 0; i < MP; ++i) fm[i] = frag_row<L>(M + i * L * L, 16 * tt, ks);
+                    for (int i = 0; i < MP; ++i) fm[i] = frag_row<L>(M + i * L * L, 16 * tt, ks, rL);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) Y[c][tt] = mma_parts<XP, MP>(fx[c][ks], fm, Y[c][tt]);
+                    for (int c = 0; c < SC_CT; ++c) Y[c][tt] = mma_parts<XP, MP>(fx[c][ks], fm, Y[c][tt]);
                 }
             // a lane stores four neighbouring columns of token 16 tt + l15
 #pragma unroll
@@ -273,7 +320,7 @@ __global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p
                 if (live && t < valid) {
                     const int64_t at = ((row0 + t) * p.H + h) * P + pc + 4 * lg;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < SC_CT; ++c) {
                         if constexpr (Cfg::BF) {
                             *reinterpret_cast<u32x2*>((__bf16*)p.y + at + 16 * c) =
                                 u32x2{pack_bf2(Y[c][tt][0], Y[c][tt][1]), pack_bf2(Y[c][tt][2], Y[c][tt][3])};
@@ -285,48 +332,68 @@ __global__ __launch_bounds__(SS_THREADS, 2) void ssm_scan_kernel(SsmScanParams p
             }
         }
 
-        // state update
+        // State update, four row tiles at a time: each part of w x runs over
+        // the four before the next part, so that no product waits for its own
+        // result.
         const float eL = d.eL;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < SC_CT; ++c)
 #pragma unroll
             for (int m = 0; m < NT; ++m) S[c][m] *= eL;
 #pragma unroll
         for (int ks = 0; ks < L / 32; ++ks) {
-            bf16x8 fw[2][WP];
+            bf16x8 fw[SC_CT][WP];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < SC_CT; ++c) {
                 float v[8];
+                const f32x4* ws = reinterpret_cast<const f32x4*>(&(REV ? d.eg : d.w)[32 * ks + 8 * lg]);
+                const f32x4 w0 = ws[0], w1 = ws[1];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     float x = (float)fx[c][ks][XP - 1][e];
 #pragma unroll
                     for (int i = XP - 2; i >= 0; --i) x += (float)fx[c][ks][i][e];
-                    v[e] = x * (REV ? d.eg : d.w)[32 * ks + 8 * lg + e];
+                    v[e] = x * (e < 4 ? w0[e & 3] : w1[e & 3]);
                 }
                 parts8<WP>(v, fw[c]);
             }
 #pragma unroll
-            for (int j = 0; j < N / 32; ++j)
+            for (int m0 = 0; m0 < NT; m0 += 4) {
+                bf16x8 fb[4][XP];
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    bf16x8 fb[XP];
+                for (int m = 0; m < 4; ++m)
 #pragma unroll
                     for (int i = 0; i < XP; ++i)
-                        fb[i] = OUT ? frag_col<N, 8>(tB + i * L * N, 32 * j + 4 * o, ks)
-                                    : frag_col<N, 4>(tB + i * L * N, 32 * j + 16 * o, ks);
+                        fb[m][i] = frag_col<N>(tB + i * L * N,
+                                               OUT ? 32 * ((m0 + m) >> 1) + 4 * (m & 1) : 16 * (m0 + m), ks, cB);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        S[c][2 * j + o] = OUT ? mma_parts<XP, WP>(fb, fw[c], S[c][2 * j + o])
-                                              : mma_parts<WP, XP>(fw[c], fb, S[c][2 * j + o]);
-                }
+                for (int c = 0; c < SC_CT; ++c)
+#pragma unroll
+                    for (int k = 2; k >= 0; --k)   // parts i + j = k, smallest first
+#pragma unroll
+                        for (int i = 0; i < XP; ++i) {
+                            const int j = k - i;
+                            if (j < 0 || j >= WP) continue;
+#pragma unroll
+                            for (int m = 0; m < 4; ++m)
+                                S[c][m0 + m] = OUT ? mfma32(fb[m][i], fw[c][j], S[c][m0 + m])
+                                                   : mfma32(fw[c][j], fb[m][i], S[c][m0 + m]);
+                        }
+            }
         }
-        __syncthreads();   // the tiles are consumed
+        lds_barrier();   // the tiles are consumed (rows and stores stay in flight)
     }
 
     if constexpr (MODE == kLocal) {
         save(p.seg + seg_at);
-        if (wave < nh && lane == 0) p.seg_decay[slot * heads + h0 - hfirst + wave] = expf((float)total);
+        __shared__ double sums[SC_WAVES];
+        if (lane == 0) sums[wave] = total;
+        __syncthreads();
+        if (tid < nh) {
+            double g = 0.0;
+            for (int k = 0; k < DB; ++k) g += sums[k * HPW + tid];
+            p.seg_decay[slot * heads + h0 - hfirst + tid] = expf((float)g);
+        }
     } else {
         if (p.S_T && (REV ? s.r0 == s.start : s.r1 == s.end)) save(p.S_T + seq_at);
     }
@@ -371,12 +438,12 @@ static hipError_t run_scan(const SsmScanParams& p, hipStream_t stream) {
     constexpr int HPW = 128 / P;
     const int hpg = p.H / p.G;
     const int32_t hblocks = p.gn * ((hpg + HPW - 1) / HPW);
-    const dim3 grid((unsigned)(p.slots * hblocks)), block(SS_THREADS);
+    const dim3 grid((unsigned)(p.slots * hblocks)), block(SC_THREADS);
     if (p.cut) {
         hipLaunchKernelGGL((ssm_scan_kernel<InT, N, P, kLocal, REV>), grid, block, 0, stream, p, hblocks);
         const int64_t n = (int64_t)p.n_seqs * p.gn * hpg * N * P / 4;
-        hipLaunchKernelGGL((ssm_merge_kernel<REV>), dim3((unsigned)((n + SS_THREADS - 1) / SS_THREADS)), block, 0,
-                           stream, p);
+        hipLaunchKernelGGL((ssm_merge_kernel<REV>), dim3((unsigned)((n + SS_THREADS - 1) / SS_THREADS)),
+                           dim3(SS_THREADS), 0, stream, p);
     }
     hipLaunchKernelGGL((ssm_scan_kernel<InT, N, P, MODE, REV>), grid, block, 0, stream, p, hblocks);
     return hipGetLastError();

@@ -83,27 +83,47 @@ __device__ __forceinline__ int ss_unit(int row, int u) {
     return row * U + (u ^ ((row / (16 / U)) & (U - 1)));
 }
 
-// Fragment with k along the columns: row r0 + (l & 15), columns 32 ks + 8 (l >> 4) .. + 7.
+// Where a lane reads its fragments: byte offsets within a tile, for row 0 and
+// column 0.  Every other fragment of the tile is that offset with the bytes
+// of its first column exclusive-ored in (the columns of a row are whole
+// powers of two, and the row's own exclusive-or commutes with it) plus the
+// bytes of its first row, so that a fragment costs one instruction of
+// address at most.  The kernels hide these offsets from the compiler once per
+// chunk: it would otherwise keep all of a loop's addresses in registers, more
+// than there are.
+//
+// k along the columns: row l & 15, columns 8 (l >> 4) .. + 7.
 template <int COLS>
-__device__ __forceinline__ bf16x8 frag_row(const __bf16* tile, int r0, int ks) {
-    const int l = threadIdx.x & 63;
-    return *reinterpret_cast<const bf16x8*>(tile + 8 * ss_unit<COLS / 8>(r0 + (l & 15), 4 * ks + (l >> 4)));
+__device__ __forceinline__ int lane_row(int l) {
+    return 16 * ss_unit<COLS / 8>(l & 15, l >> 4);
 }
-// Fragment with k along the rows: lane i = l & 15 receives column
-// c0 + step (i >> 2) + (i & 3), rows 32 ks + 8 (l >> 4) .. + 7.  step 4: 16
-// neighbouring columns; step 8: the pair of calls with c0 and c0 + 4 covers 32
-// columns so that a lane's four rows of each of the two products (rows
-// 4 (l >> 4) .. + 3) are eight neighbouring columns 8 (l >> 4) .. + 7 of the
-// 32.
+// k along the rows: lane i = l & 15 supplies rows 8 (l >> 4) + (i >> 2) and 4
+// more (x, y), columns STEP (i & 3) .. + 3.
 template <int COLS, int STEP>
-__device__ __forceinline__ bf16x8 frag_col(const __bf16* tile, int c0, int ks) {
-    const int l = threadIdx.x & 63, i = l & 15;
-    const int c = c0 + STEP * (i & 3);
-    const int r = 32 * ks + 8 * (l >> 4) + (i >> 2);
-    const __bf16* a = tile + 8 * ss_unit<COLS / 8>(r, c >> 3) + (c & 7);
-    const __bf16* b = tile + 8 * ss_unit<COLS / 8>(r + 4, c >> 3) + (c & 7);
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)b);
+__device__ __forceinline__ int2 lane_col(int l) {
+    const int i = l & 15, c = STEP * (i & 3), r = 8 * (l >> 4) + (i >> 2);
+    return make_int2(16 * ss_unit<COLS / 8>(r, c >> 3) + 2 * (c & 7), 16 * ss_unit<COLS / 8>(r + 4, c >> 3) + 2 * (c & 7));
+}
+__device__ __forceinline__ void hide(int& x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void hide(int2& x) { asm volatile("" : "+v"(x.x), "+v"(x.y)); }
+
+// Fragment with k along the columns: lane l gets row r0 + (l & 15) (r0 a
+// multiple of 16), columns 32 ks + 8 (l >> 4) .. + 7.
+template <int COLS>
+__device__ __forceinline__ bf16x8 frag_row(const __bf16* tile, int r0, int ks, int at) {
+    return *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(tile) + r0 * COLS * 2 + (at ^ (64 * ks)));
+}
+// Fragment with k along the rows: lane i = l & 15 gets column
+// c0 + STEP (i >> 2) + (i & 3), rows 32 ks + 8 (l >> 4) .. + 7.  STEP 4 (c0 a
+// multiple of 16): 16 neighbouring columns; STEP 8: the pair of calls with c0
+// and c0 + 4 (c0 a multiple of 32) covers 32 columns so that a lane's four
+// rows of each of the two products (rows 4 (l >> 4) .. + 3) are eight
+// neighbouring columns 8 (l >> 4) .. + 7 of the 32.
+template <int COLS>
+__device__ __forceinline__ bf16x8 frag_col(const __bf16* tile, int c0, int ks, int2 at) {
+    const char* t = reinterpret_cast<const char*>(tile) + 32 * ks * COLS * 2;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(t + (at.x ^ (2 * c0))));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(t + (at.y ^ (2 * c0))));
     bf16x8 f;
     __builtin_memcpy(&f, &lo, 8);
     __builtin_memcpy(reinterpret_cast<char*>(&f) + 8, &hi, 8);
@@ -148,13 +168,13 @@ __device__ __forceinline__ f32x4 mma_parts(const bf16x8 (&a)[NA], const bf16x8 (
 
 // Global memory -> registers -> LDS of a tile of L rows by COLS columns:
 // PER 16-byte pieces per thread, rows past `valid` as zeros.
-template <typename InT, int L, int COLS>
+template <typename InT, int L, int COLS, int THREADS>
 struct Stager {
     static constexpr int EV = 16 / (int)sizeof(InT);      // elements per piece
     static constexpr int PPR = COLS / EV;                 // pieces per row
-    static constexpr int PER = L * PPR / SS_THREADS;
+    static constexpr int PER = L * PPR / THREADS;
     static constexpr int PARTS = sizeof(InT) == 2 ? 1 : 3;
-    static_assert(L * PPR % SS_THREADS == 0, "whole pieces per thread");
+    static_assert(L * PPR % THREADS == 0, "whole pieces per thread");
     u32x4 r[PER];
 
     // base: first row's first column; cols: columns that exist (the others read as zero)
@@ -163,7 +183,7 @@ struct Stager {
         const auto rs = make_rsrc(base, bytes);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int idx = (int)threadIdx.x + SS_THREADS * j;
+            const int idx = (int)threadIdx.x + THREADS * j;
             const int row = idx / PPR, c = (idx - row * PPR) * EV;
             const uint32_t off = row < valid && c < cols ? (uint32_t)(row * (int)stride + c) * (uint32_t)sizeof(InT)
                                                          : 0x80000000u;
@@ -174,7 +194,7 @@ struct Stager {
     __device__ __forceinline__ void put(__bf16* tile) const {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int idx = (int)threadIdx.x + SS_THREADS * j;
+            const int idx = (int)threadIdx.x + THREADS * j;
             const int row = idx / PPR, c = (idx - row * PPR) * EV;
             __bf16* at = tile + 8 * ss_unit<COLS / 8>(row, c >> 3) + (c & 7);
             if constexpr (PARTS == 1) {
@@ -203,13 +223,31 @@ struct Stager {
 // is good to float32 rounding of the difference itself however far both are
 // from the chunk's start.
 template <int L>
-struct ChunkDecay {
+struct __attribute__((aligned(16))) ChunkDecay {
     float gh[L], gl[L];   // g_t
     float dt[L];          // after softplus; 0 past the end
     float eg[L];          // e^{g_t}
     float w[L];           // e^{g_end - g_t} dt_t
     float eL;             // e^{g_end}
 };
+// Inclusive sum over the wave's lanes up to each one, by DPP row shifts and
+// row broadcasts (no LDS round trips).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add_f64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return x + __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+__device__ __forceinline__ double wave_scan_f64(double x) {
+    x = dpp_add_f64<0x111, 0xf>(x);   // row_shr:1
+    x = dpp_add_f64<0x112, 0xf>(x);   // row_shr:2
+    x = dpp_add_f64<0x114, 0xf>(x);   // row_shr:4
+    x = dpp_add_f64<0x118, 0xf>(x);   // row_shr:8
+    x = dpp_add_f64<0x142, 0xa>(x);   // row_bcast:15 into rows 1 and 3
+    x = dpp_add_f64<0x143, 0xc>(x);   // row_bcast:31 into rows 2 and 3
+    return x;
+}
 // dt_raw: this lane's token, `valid` whether it exists.  Returns g_end.
 template <int L>
 __device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bool valid, float bias, int softplus,
@@ -220,13 +258,11 @@ __device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bo
         dt = dt_raw + bias;
         if (softplus) dt = ss_softplus(dt);
     }
-    double g = (double)(dt * A);
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-        const double y = __shfl_up(g, o);
-        if (lane >= o) g += y;
-    }
-    const double end = __shfl(g, L - 1);
+    const double g = wave_scan_f64((double)(dt * A));
+    const uint64_t gu = __builtin_bit_cast(uint64_t, g);
+    const double end = __builtin_bit_cast(
+        double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)gu, L - 1) |
+                    ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(gu >> 32), L - 1) << 32));
     if (lane < L) {
         const float h = (float)g;
         d.gh[lane] = h;
