@@ -15,7 +15,8 @@ namespace {
 constexpr int64_t kMaxWorkgroups = (1 << 24) - 1;
 constexpr int32_t kMaxTokens = 64;        // tokens per request in the step forms
 constexpr int64_t kScanFill = 512;        // chains that fill the 256 compute units (two each)
-constexpr int64_t kScanMinSeg = 512;      // shortest segment worth its state traffic
+constexpr int64_t kScanMinSeg = 256;      // shortest segment worth its state's traffic
+constexpr int64_t kScanMinCut = 3;        // segments from which two passes are shorter than one chain
 constexpr int64_t kScanAlign = 64;
 constexpr int64_t kGradFill = 512;        // workgroups of the gradient kernel that fill the GPU
 
@@ -106,7 +107,7 @@ ScanPlan scan_plan(int32_t n_seqs, int64_t T, int64_t blocks, bool varlen) {
     int64_t len = ceil_div(rows * blocks, kScanFill);
     if (len < kScanMinSeg) len = kScanMinSeg;
     const int64_t segs = ceil_div(T, len);
-    if (segs < 2) return whole;
+    if (segs < kScanMinCut) return whole;
     if (!varlen) len = ceil_div(T, segs);
     len = ceil_div(len, kScanAlign) * kScanAlign;
     return ScanPlan{true, len, varlen ? T / len + n_seqs : n_seqs * ceil_div(T, len)};

@@ -12,8 +12,8 @@
 //   da_t  = sum_{s<t<=u} W_us + sum_{u>=t} U_u + sum_{s<t} V_s + Z
 //   W_us  = L_us G_us E_us dt_s,  U_u = e^{g_u} C_u . S dy_u,
 //   V_s   = e^{g_end - g_s} dt_s B_s . R x_s,  Z = e^{g_end} <S, R>,
-// (the first sum by differences of row and column sums of W without its
-// diagonal, over one chunk only), and
+// (the first sum from row and column sums of W's 16 x 16 tiles; differences
+// of them only within a tile), and
 //   ddt_s = sum_u W_us / dt_s + V_s / dt_s + A da_s,  dA = sum_t dt_t da_t,
 //   dD    = sum_t E_tt,
 // with the divisions left out of the sums in the first place.
@@ -21,8 +21,7 @@
 // A workgroup runs one chunk for several heads of a group in turn: B, C and
 // the tiles of G stay on chip, and dB and dC are summed over the heads in
 // registers, so that only one partial sum per workgroup goes through memory.
-// Wave w owns a quarter of the state's rows (for dB, dC, U, V, Z) and of x's
-// columns (for dx).  S and R come straight from memory into operand
+// S and R come straight from memory into operand
 // registers, each row once.  Bound by the traffic of S and R, which the walks
 // wrote: 16 N P bytes per chunk and head against 6 L P of x, dy and dx.
 #include "kda_ssm_tile.h"
@@ -30,26 +29,41 @@
 namespace kda {
 
 __device__ __forceinline__ float sum_lane_groups(float v) {   // over lanes with equal l & 15
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    return v;
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v += __uint_as_float((threadIdx.x & 16) ? r[0] : r[1]);
+    return v + swap_halves(v);
 }
 
+// Eight waves.  For the products with S, R and the chunk matrices towards dB
+// and dC a wave owns one 16-row tile of the state (and, with N = 64, every
+// second 16-token tile); towards dx one 16-column tile of x (with P = 64,
+// every second token tile).
+constexpr int SG_WAVES = 8, SG_THREADS = 64 * SG_WAVES;
+constexpr int SG_HEADS = 4;   // heads whose decay sums are computed together, one per wave
+
 template <typename InT, int N, int P>
-__global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) void ssm_grad_kernel(SsmGradParams q) {
+__global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q) {
     constexpr bool BF = sizeof(InT) == 2;
     constexpr int L = BF ? 64 : 32;
     constexpr int XP = BF ? 1 : 3;      // bf16 parts of an input
     constexpr int KP = BF ? 1 : 3;      // ... of the chunk matrices (their products are rounded to the input type)
     constexpr int RP = BF ? 1 : 3;      // ... of R in dx
     constexpr int SP = 3;               // ... of S and R where U and V come from (float32 results)
-    constexpr int TT = L / 16, NTILE = TT * (TT + 1) / 2, TPW = (NTILE + 3) / 4;
-    constexpr int MT = N / 64, PT = P / 64;   // row tiles of the state, column tiles of x per wave
+    constexpr int TT = L / 16, NTILE = TT * (TT + 1) / 2, EW = SG_WAVES - 1, TPW = (NTILE + EW - 1) / EW;   // (the last wave has no tile)
+    constexpr int RW = N / 16, RS = SG_WAVES / RW, RT = TT / RS;   // row tiles; waves per row tile; its token tiles per wave
+    constexpr int CW = P / 16, CS = SG_WAVES / CW, CT = TT / CS;   // column tiles of x, likewise
     __shared__ __attribute__((aligned(16))) __bf16 tB[XP * L * N], tC[XP * L * N];
     __shared__ __attribute__((aligned(16))) __bf16 tX[XP * L * P], tY[XP * L * P];
     __shared__ __attribute__((aligned(16))) __bf16 tK[KP * L * L], tM[KP * L * L];
-    __shared__ ChunkDecay<L> dec;
-    __shared__ float sR[TT][L], sQ[TT][L], sU[4][L], sV[4][L], sW[L], sE[L], sZ[4];
+    __shared__ ChunkDecay<L> decs[2 * SG_HEADS];
+    // R in bf16, for its columns (float32: they come from memory, three planes being too large)
+    __shared__ __attribute__((aligned(16))) __bf16 tR[BF ? N * P : 8];
+    // a head's sums, read while the next head's are written
+    struct __attribute__((aligned(16))) Sums {
+        float R[TT][L], Q[TT][L], U[RW][L], V[RW][L], W[L], E[L], Z[RW];
+    };
+    __shared__ Sums sums[2];
+    __shared__ float sRaw[2 * SG_HEADS][L];
 
     const SsmScanParams& p = q.f;
     const int tid = threadIdx.x;
@@ -57,6 +71,9 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
     int lane = tid & 63;
     int rN = lane_row<N>(lane), rP = lane_row<P>(lane), rL = lane_row<L>(lane);
     int2 cN = lane_col<N, 4>(lane), cP = lane_col<P, 4>(lane), cL = lane_col<L, 4>(lane);
+    const int rt = wave % RW, rh = wave / RW;      // this wave's row tile and its share of the token tiles
+    const int ct = wave % CW, ch = wave / CW;      // ... column tile ...
+    const int n0 = 16 * rt, p0 = 16 * ct;
     const int hpg = p.H / p.G;
     const int64_t heads = (int64_t)p.gn * hpg;
     const int per_slot = p.gn * q.blocks;
@@ -69,52 +86,73 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
     const int hfirst = p.g0 * hpg;
     const SsmPiece s = ssm_piece(p.cu, p.rows, p.T, p.n_seqs, L, slot);
     if (s.piece < 0) {
-        for (int i = tid; i < 3 * hwn; i += SS_THREADS) q.sums[(slot * heads + hw0) * 3 + i] = 0.f;
+        for (int i = tid; i < 3 * hwn; i += SG_THREADS) q.sums[(slot * heads + hw0) * 3 + i] = 0.f;
         return;
     }
     const int64_t row0 = s.r0;
     const int valid = (int)(s.r1 - s.r0);
 
-    for (int i = tid; i < KP * L * L / 8; i += SS_THREADS) {
+    for (int i = tid; i < KP * L * L / 8; i += SG_THREADS) {
         reinterpret_cast<u32x4*>(tK)[i] = u32x4{0, 0, 0, 0};
         reinterpret_cast<u32x4*>(tM)[i] = u32x4{0, 0, 0, 0};
     }
-    Stager<InT, L, P, SS_THREADS> gX, gY;
-    float gdt = 0.f;
+    Stager<InT, L, P, SG_THREADS> gX, gY;
     auto fetch = [&](int hw) {
         const int64_t h = hfirst + hw;
         gX.load((const InT*)p.x + row0 * p.x_stride + h * P, p.x_stride, valid, P);
         gY.load((const InT*)q.gy + (row0 * p.H + h) * P, (int64_t)p.H * P, valid, P);
-        if (wave == 0) gdt = lane < valid ? p.dt[(row0 + lane) * p.H + h] : 0.f;
+    };
+    // this lane's raw dt of head hw0 + k
+    auto raw_dt = [&](int k) {
+        const int64_t h = hfirst + hw0 + k;
+        return k < hwn && lane < valid ? p.dt[(row0 + lane) * p.H + h] + (p.dt_bias ? p.dt_bias[h] : 0.f) : 0.f;
     };
     {
-        Stager<InT, L, N, SS_THREADS> g;
+        Stager<InT, L, N, SG_THREADS> g, c;
         g.load((const InT*)p.B + row0 * p.B_stride + grp * N, p.B_stride, valid, N);
+        c.load((const InT*)p.C + row0 * p.C_stride + grp * N, p.C_stride, valid, N);
         g.put(tB);
-        g.load((const InT*)p.C + row0 * p.C_stride + grp * N, p.C_stride, valid, N);
-        g.put(tC);
+        c.put(tC);
     }
+    // this wave's rows of a head's S and R, one head ahead
+    f32x4 fS[P / 32][2], fR[P / 32][2];
+    auto fetch_states = [&](int hw) {
+        const f32x4* S = reinterpret_cast<const f32x4*>(q.states + (slot * heads + hw) * (N * P));
+        const f32x4* R = reinterpret_cast<const f32x4*>(q.dstates + (slot * heads + hw) * (N * P));
+        const int l15 = lane & 15, lg = lane >> 4;
+#pragma unroll
+        for (int ks = 0; ks < P / 32; ++ks)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {   // columns 32 ks + 8 lg + 4 k .. + 3 of row n0 + l15
+                const int at = walk_at<N>(2 * ks + (lg >> 1), rt, l15 + 16 * (2 * (lg & 1) + k));
+                fS[ks][k] = S[at];
+                fR[ks][k] = R[at];
+            }
+    };
     fetch(hw0);
+    fetch_states(hw0);
+    float raw_next = wave < SG_HEADS ? raw_dt(wave) : 0.f;
     __syncthreads();
 
     // tiles of G^T (rows s, columns t), kept for all heads
     f32x4 G[TPW];
-    int g_tt[TPW], g_st[TPW];
+    auto tile_of = [&](int k, int& tt, int& st) {
+        const int idx = wave + EW * k < NTILE ? wave + EW * k : NTILE - 1;
+        tt = (idx >= 1) + (idx >= 3) + (idx >= 6);
+        st = idx - tt * (tt + 1) / 2;
+    };
 #pragma unroll
     for (int k = 0; k < TPW; ++k) {
-        const int idx = wave + 4 * k < NTILE ? wave + 4 * k : NTILE - 1;
-        int tt = 0;
-        while ((tt + 1) * (tt + 2) / 2 <= idx) ++tt;
-        g_tt[k] = tt;
-        g_st[k] = idx - tt * (tt + 1) / 2;
+        int tt, st;
+        tile_of(k, tt, st);
         G[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < N / 32; ++ks) {
             bf16x8 fb[XP], fc[XP];
 #pragma unroll
             for (int i = 0; i < XP; ++i) {
-                fb[i] = frag_row<N>(tB + i * L * N, 16 * g_st[k], ks, rN);
-                fc[i] = frag_row<N>(tC + i * L * N, 16 * g_tt[k], ks, rN);
+                fb[i] = frag_row<N>(tB + i * L * N, 16 * st, ks, rN);
+                fc[i] = frag_row<N>(tC + i * L * N, 16 * tt, ks, rN);
             }
             G[k] = mma_parts<XP, XP>(fb, fc, G[k]);
         }
@@ -134,45 +172,111 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
         }
     };
 
-    f32x4 dB[MT][TT], dC[MT][TT];   // rows n, columns token, of all heads so far
+    // gradients of the decay and of dt of a head whose sums are whole: one
+    // token per lane of the last wave
+    auto finish = [&](int hk) {
+        const int hw = hw0 + hk, h = hfirst + hw, at = hk % (2 * SG_HEADS);
+        const Sums& o = sums[hk & 1];
+        const ChunkDecay<L>& dec = decs[at];
+        const int t = lane < L ? lane : L - 1;
+        const bool on = lane < valid;
+        const float raw = sRaw[at][t], A = p.A[h];
+        // W across token t: tiles (u's tile a, s's tile b) around t's tile k.
+        // Whole tiles and whole rows or columns of them only add up; just
+        // within the tile on the diagonal do row and column sums cancel.
+        const float dt = dec.dt[t];
+        const int k = t / 16;
+        float Q = 0.f, rows = 0.f, cols = 0.f;
+        double whole = 0.0;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int b = 0; b < TT; ++b) {
+            const float r = o.R[b][t], c = o.Q[b][t];
+            if (b < k) rows += r;         // (a = k, b < k)
+            if (b > k) cols += c;         // (a = b > k, b = k)
+            if (b >= k) Q += c;
+        }
 #pragma unroll
-        for (int t = 0; t < TT; ++t) dB[m][t] = dC[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 1; j + 1 < TT; ++j) {   // tiles a > j, b < j
+            float r = 0.f;
+#pragma unroll
+            for (int b = 0; b < j; ++b) r += o.R[b][t];
+            const double all = wave_last_f64(wave_scan_f64(lane < L && k > j ? (double)r : 0.0));
+            if (k == j) whole = all;
+        }
+        const double diag = (double)o.R[k][t] - (double)(o.Q[k][t] * dt);
+        const double own = lane < L ? (double)(cols * dt) : 0.0;
+        const double X = whole + row_suffix_f64(lane < L ? (double)rows + diag : 0.0) + (row_prefix_f64(own) - own);
+        float U = 0.f, V = 0.f, Z = 0.f;
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+            U += o.U[j][t];
+            V += o.V[j][t];
+            Z += o.Z[j];
+        }
+        U *= dec.eg[t];
+        V *= expf((dec.gh[L - 1] - dec.gh[t]) + (dec.gl[L - 1] - dec.gl[t]));   // without dt
+        Z *= dec.eL;
+        // U of this token and the later ones, V of the earlier ones
+        const double x = lane < L ? (double)U : 0.0, y = lane < L ? (double)(V * dt) : 0.0;
+        const double sx = wave_scan_f64(x), sy = wave_scan_f64(y);
+        const float da = (float)(X + (wave_last_f64(sx) - sx + x) + (sy - y) + (double)Z);
+        float ddt = (Q + o.W[t]) + V + A * da;
+        if (p.softplus) ddt *= 1.f / (1.f + expf(-raw));
+        if (on) q.gdt[(row0 + lane) * p.H + h] = ddt;
+        const float a = wave_sum_dpp(on ? dt * da : 0.f);
+        const float d = wave_sum_dpp(on ? o.E[t] : 0.f);
+        const float b = wave_sum_dpp(on ? ddt : 0.f);
+        if (lane == 0) {
+            float* to = q.sums + (slot * heads + hw) * 3;
+            to[0] = a;
+            to[1] = d;
+            to[2] = b;
+        }
+    };
 
-    for (int hw = hw0; hw < hw0 + hwn; ++hw) {
-        const int h = hfirst + hw;
+    f32x4 dB[RT], dC[RT];   // rows n, columns token, of all heads so far
+#pragma unroll
+    for (int k = 0; k < RT; ++k) dB[k] = dC[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int hk = 0; hk < hwn; ++hk) {
+        const int hw = hw0 + hk, h = hfirst + hw;
         hide(lane), hide(rN), hide(rP), hide(rL), hide(cN), hide(cP), hide(cL);
         const int l15 = lane & 15, lg = lane >> 4;
-        const float* S = q.states + (slot * heads + hw) * (N * P);
         const float* R = q.dstates + (slot * heads + hw) * (N * P);
-        const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-        const float raw = gdt + bias;          // wave 0
-        const float A = p.A[h], D = p.D ? p.D[h] : 0.f;
+        const float D = p.D ? p.D[h] : 0.f;
         gX.put(tX);
         gY.put(tY);
-        if (wave == 0) chunk_decay<L>(dec, gdt, lane < valid, bias, p.softplus, A);
+        if (hk % SG_HEADS == 0 && wave < SG_HEADS) {   // (the last four heads' stay for the sums that are still open)
+            const int k = hk + wave, at = k % (2 * SG_HEADS);
+            const float a = k < hwn ? p.A[hfirst + hw0 + k] : 0.f;
+            chunk_decay<L>(decs[at], raw_next, k < hwn && lane < valid, 0.f, p.softplus, a);
+            if (lane < L) sRaw[at][lane] = raw_next;
+            raw_next = raw_dt(k + SG_HEADS);
+        }
+        const ChunkDecay<L>& dec = decs[hk % (2 * SG_HEADS)];
+        Sums& now = sums[hk & 1];
         lds_barrier();
-        // S and R rows of this wave, in flight during the chunk matrices
-        f32x4 fS[MT][P / 32][2], fR[MT][P / 32][2];
+        // R by columns, for dx (float32): out of cache, its rows having come for fR
+        float fRc[BF ? 1 : N / 32][8];
+        if constexpr (!BF) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int ks = 0; ks < N / 32; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < P / 32; ++ks) {
-                const int at = ((N / 4) * wave + 16 * m + l15) * P + 32 * ks + 8 * lg;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    fS[m][ks][k] = *reinterpret_cast<const f32x4*>(S + at + 4 * k);
-                    fR[m][ks][k] = *reinterpret_cast<const f32x4*>(R + at + 4 * k);
+                for (int e = 0; e < 8; ++e) {
+                    const int n = 32 * ks + 8 * lg + e;
+                    fRc[ks][e] = R[4 * walk_at<N>(ct, n >> 4, (n & 15) + 16 * (l15 >> 2)) + (l15 & 3)];
                 }
-            }
-        __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // the last wave ends the previous head while the others start this one
+        if (wave == SG_WAVES - 1 && hk > 0) finish(hk - 1);
 
         // chunk matrices, a lane holding four neighbouring s of one t
 #pragma unroll
         for (int k = 0; k < TPW; ++k) {
-            if (wave + 4 * k >= NTILE) break;
-            const int tt = g_tt[k], st = g_st[k];
+            if (wave == EW || wave + EW * k >= NTILE) break;
+            int tt, st;
+            tile_of(k, tt, st);
             f32x4 E = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < P / 32; ++ks) {
@@ -190,32 +294,42 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
             const f32x4 ls = *reinterpret_cast<const f32x4*>(&dec.gl[s0]);
             const f32x4 ds = *reinterpret_cast<const f32x4*>(&dec.dt[s0]);
             float K[4], M[4], row = 0.f, col[4];
+            if (tt != st) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int sr = s0 + r;
-                const float l = sr <= t ? __expf((ht - hs[r]) + (lt - ls[r])) : 0.f;
-                K[r] = sr <= t ? E[r] * l * ds[r] : 0.f;
-                M[r] = sr <= t ? G[k][r] * l * ds[r] : 0.f;
-                const float w = sr <= t ? G[k][r] * l * E[r] : 0.f;
-                col[r] = sr < t ? w : 0.f;
-                row += col[r] * ds[r];
-                if (tt == st && sr == t) {
-                    M[r] += D;
-                    sW[t] = w;
-                    sE[t] = E[r];
+                for (int r = 0; r < 4; ++r) {
+                    const float l = __expf((ht - hs[r]) + (lt - ls[r]));
+                    K[r] = E[r] * l * ds[r];
+                    M[r] = G[k][r] * l * ds[r];
+                    col[r] = G[k][r] * l * E[r];
+                    row = fmaf(col[r], ds[r], row);
+                }
+            } else {   // the diagonal tile: nothing above the diagonal, D on it, and W's diagonal apart
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int sr = s0 + r;
+                    const float l = sr <= t ? __expf((ht - hs[r]) + (lt - ls[r])) : 0.f;
+                    K[r] = sr <= t ? E[r] * l * ds[r] : 0.f;
+                    M[r] = sr <= t ? G[k][r] * l * ds[r] : 0.f;
+                    const float w = sr <= t ? G[k][r] * l * E[r] : 0.f;
+                    col[r] = sr < t ? w : 0.f;
+                    row = fmaf(col[r], ds[r], row);
+                    if (sr == t) {
+                        M[r] += D;
+                        now.W[t] = w;
+                        now.E[t] = E[r];
+                    }
                 }
             }
             row = sum_lane_groups(row);
-            if (lg == 0) sR[st][t] = row;
+            if (lg == 0) now.R[st][t] = row;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                float v = col[r];
-                v += dpp_mov<0xB1>(v);
-                v += dpp_mov<0x4E>(v);
-                v += dpp_mov<0x124>(v);
-                v += dpp_mov<0x128>(v);
-                if (l15 == 0) sQ[tt][s0 + r] = v;
+                col[r] += dpp_mov<0xB1>(col[r]);
+                col[r] += dpp_mov<0x4E>(col[r]);
+                col[r] += dpp_mov<0x124>(col[r]);
+                col[r] += dpp_mov<0x128>(col[r]);
             }
+            if (l15 == 0) *reinterpret_cast<f32x4*>(&now.Q[tt][s0]) = f32x4{col[0], col[1], col[2], col[3]};
             const int at = 8 * ss_unit<L / 8>(t, s0 >> 3) + (s0 & 7);
 #pragma unroll
             for (int i = 0; i < KP; ++i) {
@@ -235,218 +349,181 @@ __global__ __launch_bounds__(SS_THREADS, sizeof(InT) == 2 && P == 64 ? 2 : 1) vo
             }
         }
 
-        // products with S and R: rows n = (N / 4) wave + 16 m + .., columns token
+        // products with S and R: rows n0 .., columns token (tile rh + RS k)
         __builtin_amdgcn_sched_barrier(0);
-        float z = 0.f, u[TT], v[TT];
+        {
+            float z = 0.f;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) u[t] = v[t] = 0.f;
+            for (int ks = 0; ks < P / 32; ++ks)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int n0 = (N / 4) * wave + 16 * m;
-            f32x4 aC[TT], aB[TT];
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) aC[t] = aB[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int e = 0; e < 4; ++e) z = fmaf(fS[ks][k][e], fR[ks][k][e], z);
+            z = wave_sum_dpp(z);
+            if (lane == 0 && rh == 0) now.Z[rt] = z;
+        }
+        if constexpr (BF) {
+            if (rh == 0) {
+#pragma unroll
+                for (int ks = 0; ks < P / 32; ++ks) {
+                    u32x4 u;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        u[2 * k] = pack_bf2(fR[ks][k][0], fR[ks][k][1]);
+                        u[2 * k + 1] = pack_bf2(fR[ks][k][2], fR[ks][k][3]);
+                    }
+                    *reinterpret_cast<u32x4*>(tR + 8 * ss_unit<P / 8>(n0 + l15, 4 * ks + lg)) = u;
+                }
+            }
+        }
+        // first S with dy, then R with x: acc, its sum against C or B by token, and its share of dC or dB
+        auto with_state = [&](const f32x4 (&f)[P / 32][2], const __bf16* tok, const __bf16* own, const float* weight,
+                              float* sums, f32x4 (&grad)[RT]) {
+            f32x4 acc[RT];
+#pragma unroll
+            for (int k = 0; k < RT; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < P / 32; ++ks) {
-                float vS[8], vR[8];
+                float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    vS[e] = fS[m][ks][e / 4][e % 4];
-                    vR[e] = fR[m][ks][e / 4][e % 4];
-                    z = fmaf(vS[e], vR[e], z);
+                for (int e = 0; e < 8; ++e) v[e] = f[ks][e / 4][e % 4];
+                bf16x8 ps[SP];
+                parts8<SP>(v, ps);
+#pragma unroll
+                for (int k = 0; k < RT; ++k) {
+                    bf16x8 ft[XP];
+#pragma unroll
+                    for (int i = 0; i < XP; ++i) ft[i] = frag_row<P>(tok + i * L * P, 16 * (rh + RS * k), ks, rP);
+                    acc[k] = mma_parts<SP, XP>(ps, ft, acc[k]);
                 }
-                bf16x8 pS[SP], pR[SP];
-                parts8<SP>(vS, pS);
-                parts8<SP>(vR, pR);
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    bf16x8 fy[XP], fx[XP];
-#pragma unroll
-                    for (int i = 0; i < XP; ++i) {
-                        fy[i] = frag_row<P>(tY + i * L * P, 16 * t, ks, rP);
-                        fx[i] = frag_row<P>(tX + i * L * P, 16 * t, ks, rP);
-                    }
-                    aC[t] = mma_parts<SP, XP>(pS, fy, aC[t]);
-                    aB[t] = mma_parts<SP, XP>(pR, fx, aB[t]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                float c[4], b[4];
-                four(tC, L * N, 16 * t + l15, n0 + 4 * lg, c);
-                four(tB, L * N, 16 * t + l15, n0 + 4 * lg, b);
-                const float eg = dec.eg[16 * t + l15], w = dec.w[16 * t + l15];
+            for (int k = 0; k < RT; ++k) {
+                const int t = 16 * (rh + RS * k) + l15;
+                float o[4], u = 0.f;
+                four(own, L * N, t, n0 + 4 * lg, o);
+                const float w = weight[t];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    u[t] = fmaf(c[r], aC[t][r], u[t]);
-                    v[t] = fmaf(b[r], aB[t][r], v[t]);
-                    dC[m][t][r] = fmaf(eg, aC[t][r], dC[m][t][r]);
-                    dB[m][t][r] = fmaf(w, aB[t][r], dB[m][t][r]);
+                    u = fmaf(o[r], acc[k][r], u);
+                    grad[k][r] = fmaf(w, acc[k][r], grad[k][r]);
                 }
+                u = sum_lane_groups(u);
+                if (lg == 0) sums[t] = u;
             }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        z = wave_sum_dpp(z);
-        if (lane == 0) sZ[wave] = z;
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const float a = sum_lane_groups(u[t]), b = sum_lane_groups(v[t]);
-            if (lg == 0) {
-                sU[wave][16 * t + l15] = a;
-                sV[wave][16 * t + l15] = b;
-            }
-        }
+        };
+        with_state(fS, tY, tC, dec.eg, now.U[rt], dC);
+        __builtin_amdgcn_sched_barrier(0);
+        with_state(fR, tX, tB, dec.w, now.V[rt], dB);
+        __builtin_amdgcn_sched_barrier(0);
+        if (hk + 1 < hwn) fetch_states(hw + 1);   // in flight until the next head's products
         lds_barrier();   // the chunk matrices and the partial sums are whole
-        if (hw + 1 < hw0 + hwn) fetch(hw + 1);
+        if (hk + 1 < hwn) fetch(hw + 1);
 
         // products with the chunk matrices
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int n0 = (N / 4) * wave + 16 * m;
+        for (int ks = 0; ks < L / 32; ++ks) {
+            bf16x8 fb[XP], fc[XP];
 #pragma unroll
-            for (int ks = 0; ks < L / 32; ++ks) {
-                bf16x8 fb[XP], fc[XP];
+            for (int i = 0; i < XP; ++i) {
+                fb[i] = frag_col<N>(tB + i * L * N, n0, ks, cN);
+                fc[i] = frag_col<N>(tC + i * L * N, n0, ks, cN);
+            }
 #pragma unroll
-                for (int i = 0; i < XP; ++i) {
-                    fb[i] = frag_col<N>(tB + i * L * N, n0, ks, cN);
-                    fc[i] = frag_col<N>(tC + i * L * N, n0, ks, cN);
+            for (int k = 0; k < RT; ++k) {
+                const int t = rh + RS * k;
+                constexpr bool even = RS == 2;
+                const int last = even ? k : k / 2;   // = t / 2, the slab with the diagonal
+                if (ks <= last) {
+                    bf16x8 fk[KP];
+#pragma unroll
+                    for (int i = 0; i < KP; ++i) fk[i] = frag_row<L>(tK + i * L * L, 16 * t, ks, rL);
+                    dC[k] = mma_parts<XP, KP>(fb, fk, dC[k]);
                 }
+                if (ks >= last) {
+                    bf16x8 fk[KP];
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    if (ks <= t / 2) {
-                        bf16x8 fk[KP];
-#pragma unroll
-                        for (int i = 0; i < KP; ++i) fk[i] = frag_row<L>(tK + i * L * L, 16 * t, ks, rL);
-                        dC[m][t] = mma_parts<XP, KP>(fb, fk, dC[m][t]);
-                    }
-                    if (ks >= t / 2) {
-                        bf16x8 fk[KP];
-#pragma unroll
-                        for (int i = 0; i < KP; ++i) fk[i] = frag_col<L>(tK + i * L * L, 16 * t, ks, cL);
-                        dB[m][t] = mma_parts<XP, KP>(fc, fk, dB[m][t]);
-                    }
+                    for (int i = 0; i < KP; ++i) fk[i] = frag_col<L>(tK + i * L * L, 16 * t, ks, cL);
+                    dB[k] = mma_parts<XP, KP>(fc, fk, dB[k]);
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        {
+            f32x4 dX[CT];
 #pragma unroll
-        for (int c = 0; c < PT; ++c) {
-            const int p0 = (P / 4) * wave + 16 * c;
-            f32x4 dX[TT];
-#pragma unroll
-            for (int t = 0; t < TT; ++t) dX[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < CT; ++k) dX[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < N / 32; ++ks) {
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = R[(32 * ks + 8 * lg + e) * P + p0 + l15];
                 bf16x8 pR[RP];
-                parts8<RP>(f, pR);
+                if constexpr (BF) pR[0] = frag_col<P>(tR, p0, ks, cP);
+                else parts8<RP>(fRc[ks], pR);
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
+                for (int k = 0; k < CT; ++k) {
                     bf16x8 fb[XP];
 #pragma unroll
-                    for (int i = 0; i < XP; ++i) fb[i] = frag_row<N>(tB + i * L * N, 16 * t, ks, rN);
-                    dX[t] = mma_parts<RP, XP>(pR, fb, dX[t]);
+                    for (int i = 0; i < XP; ++i) fb[i] = frag_row<N>(tB + i * L * N, 16 * (ch + CS * k), ks, rN);
+                    dX[k] = mma_parts<RP, XP>(pR, fb, dX[k]);
                 }
             }
 #pragma unroll
-            for (int t = 0; t < TT; ++t) dX[t] *= dec.w[16 * t + l15];
+            for (int k = 0; k < CT; ++k) dX[k] *= dec.w[16 * (ch + CS * k) + l15];
 #pragma unroll
             for (int ks = 0; ks < L / 32; ++ks) {
                 bf16x8 fy[XP];
 #pragma unroll
                 for (int i = 0; i < XP; ++i) fy[i] = frag_col<P>(tY + i * L * P, p0, ks, cP);
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    if (ks < t / 2) continue;
+                for (int k = 0; k < CT; ++k) {
+                    if (ks < (CS == 2 ? k : k / 2)) continue;
                     bf16x8 fm[KP];
 #pragma unroll
-                    for (int i = 0; i < KP; ++i) fm[i] = frag_col<L>(tM + i * L * L, 16 * t, ks, cL);
-                    dX[t] = mma_parts<XP, KP>(fy, fm, dX[t]);
+                    for (int i = 0; i < KP; ++i) fm[i] = frag_col<L>(tM + i * L * L, 16 * (ch + CS * k), ks, cL);
+                    dX[k] = mma_parts<XP, KP>(fy, fm, dX[k]);
                 }
             }
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const int row = 16 * t + l15;
+            for (int k = 0; k < CT; ++k) {
+                const int row = 16 * (ch + CS * k) + l15;
                 if (row < valid) {
                     const int64_t at = (row0 + row) * q.gx_stride + (int64_t)h * P + p0 + 4 * lg;
                     if constexpr (BF)
                         *reinterpret_cast<u32x2*>((__bf16*)q.gx + at) =
-                            u32x2{pack_bf2(dX[t][0], dX[t][1]), pack_bf2(dX[t][2], dX[t][3])};
+                            u32x2{pack_bf2(dX[k][0], dX[k][1]), pack_bf2(dX[k][2], dX[k][3])};
                     else
-                        *reinterpret_cast<f32x4*>((float*)q.gx + at) = dX[t];
+                        *reinterpret_cast<f32x4*>((float*)q.gx + at) = dX[k];
                 }
             }
         }
 
-        // gradients of the decay and of dt: one token per lane of wave 0
-        if (wave == 0) {
-            const int t = lane < L ? lane : L - 1;
-            float R_ = 0.f, Q = 0.f;
-#pragma unroll
-            for (int k = 0; k < TT; ++k) {
-                if (k <= t / 16) R_ += sR[k][t];
-                if (k >= t / 16) Q += sQ[k][t];
-            }
-            const float dt = dec.dt[t];
-            const float er = expf((dec.gh[L - 1] - dec.gh[t]) + (dec.gl[L - 1] - dec.gl[t]));
-            const float U = dec.eg[t] * ((sU[0][t] + sU[1][t]) + (sU[2][t] + sU[3][t]));
-            const float V = er * ((sV[0][t] + sV[1][t]) + (sV[2][t] + sV[3][t]));   // without dt
-            const float Z = dec.eL * ((sZ[0] + sZ[1]) + (sZ[2] + sZ[3]));
-            double suf = lane < L ? (double)R_ - (double)(Q * dt) + (double)U : 0.0;
-            double pre = lane < L ? (double)(V * dt) : 0.0;
-            const double own = pre;
-#pragma unroll
-            for (int o = 1; o < L; o <<= 1) {
-                const double a = __shfl_down(suf, o), b = __shfl_up(pre, o);
-                if (lane + o < L) suf += a;
-                if (lane >= o) pre += b;
-            }
-            const float da = (float)(suf + (pre - own) + (double)Z);
-            float ddt = (Q + sW[t]) + V + A * da;
-            if (p.softplus) ddt *= 1.f / (1.f + expf(-raw));
-            const bool on = lane < valid;
-            if (on) q.gdt[(row0 + lane) * p.H + h] = ddt;
-            const float a = wave_sum_dpp(on ? dt * da : 0.f);
-            const float d = wave_sum_dpp(on ? sE[t] : 0.f);
-            const float b = wave_sum_dpp(on ? ddt : 0.f);
-            if (lane == 0) {
-                float* to = q.sums + (slot * heads + hw) * 3;
-                to[0] = a;
-                to[1] = d;
-                to[2] = b;
-            }
-        }
         lds_barrier();   // the tiles are consumed (rows and stores stay in flight)
     }
+
+    if (wave == SG_WAVES - 1) finish(hwn - 1);
 
     // dB and dC of these heads: the gradients themselves, or a partial sum
     const int l15 = lane & 15, lg = lane >> 4;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const int row = 16 * t + l15, n = (N / 4) * wave + 16 * m + 4 * lg;
-            if (row >= valid) continue;
-            if (q.blocks == 1) {
-                const int64_t b = (row0 + row) * q.gB_stride + grp * N + n, c = (row0 + row) * q.gC_stride + grp * N + n;
-                if constexpr (BF) {
-                    *reinterpret_cast<u32x2*>((__bf16*)q.gB + b) =
-                        u32x2{pack_bf2(dB[m][t][0], dB[m][t][1]), pack_bf2(dB[m][t][2], dB[m][t][3])};
-                    *reinterpret_cast<u32x2*>((__bf16*)q.gC + c) =
-                        u32x2{pack_bf2(dC[m][t][0], dC[m][t][1]), pack_bf2(dC[m][t][2], dC[m][t][3])};
-                } else {
-                    *reinterpret_cast<f32x4*>((float*)q.gB + b) = dB[m][t];
-                    *reinterpret_cast<f32x4*>((float*)q.gC + c) = dC[m][t];
-                }
+    for (int k = 0; k < RT; ++k) {
+        const int row = 16 * (rh + RS * k) + l15, n = n0 + 4 * lg;
+        if (row >= valid) continue;
+        if (q.blocks == 1) {
+            const int64_t b = (row0 + row) * q.gB_stride + grp * N + n, c = (row0 + row) * q.gC_stride + grp * N + n;
+            if constexpr (BF) {
+                *reinterpret_cast<u32x2*>((__bf16*)q.gB + b) =
+                    u32x2{pack_bf2(dB[k][0], dB[k][1]), pack_bf2(dB[k][2], dB[k][3])};
+                *reinterpret_cast<u32x2*>((__bf16*)q.gC + c) =
+                    u32x2{pack_bf2(dC[k][0], dC[k][1]), pack_bf2(dC[k][2], dC[k][3])};
             } else {
-                const int64_t at = (((int64_t)blk * p.gn + gw) * p.rows + row0 + row) * N + n;
-                *reinterpret_cast<f32x4*>(q.part + at) = dB[m][t];
-                *reinterpret_cast<f32x4*>(q.part + (int64_t)q.blocks * p.gn * p.rows * N + at) = dC[m][t];
+                *reinterpret_cast<f32x4*>((float*)q.gB + b) = dB[k];
+                *reinterpret_cast<f32x4*>((float*)q.gC + c) = dC[k];
             }
+        } else {
+            const int64_t at = (((int64_t)blk * p.gn + gw) * p.rows + row0 + row) * N + n;
+            *reinterpret_cast<f32x4*>(q.part + at) = dB[k];
+            *reinterpret_cast<f32x4*>(q.part + (int64_t)q.blocks * p.gn * p.rows * N + at) = dC[k];
         }
+    }
 }
 
 // Adds up the head blocks' partial sums of dB and dC, four channels per lane.
@@ -500,11 +577,11 @@ static hipError_t run_grad(const SsmGradParams& q, hipStream_t stream) {
     const SsmScanParams& p = q.f;
     const dim3 block(SS_THREADS);
     if (q.slots > 0) {
-        const dim3 grid((unsigned)(q.slots * p.gn * q.blocks));
-        if (p.N == 128 && p.P == 64) hipLaunchKernelGGL((ssm_grad_kernel<InT, 128, 64>), grid, block, 0, stream, q);
-        else if (p.N == 128) hipLaunchKernelGGL((ssm_grad_kernel<InT, 128, 128>), grid, block, 0, stream, q);
-        else if (p.P == 64) hipLaunchKernelGGL((ssm_grad_kernel<InT, 64, 64>), grid, block, 0, stream, q);
-        else hipLaunchKernelGGL((ssm_grad_kernel<InT, 64, 128>), grid, block, 0, stream, q);
+        const dim3 grid((unsigned)(q.slots * p.gn * q.blocks)), wide(SG_THREADS);
+        if (p.N == 128 && p.P == 64) hipLaunchKernelGGL((ssm_grad_kernel<InT, 128, 64>), grid, wide, 0, stream, q);
+        else if (p.N == 128) hipLaunchKernelGGL((ssm_grad_kernel<InT, 128, 128>), grid, wide, 0, stream, q);
+        else if (p.P == 64) hipLaunchKernelGGL((ssm_grad_kernel<InT, 64, 64>), grid, wide, 0, stream, q);
+        else hipLaunchKernelGGL((ssm_grad_kernel<InT, 64, 128>), grid, wide, 0, stream, q);
     }
     if (q.blocks > 1 && p.rows > 0) {
         const int64_t n = 2 * (int64_t)p.gn * p.rows * (p.N / 4);

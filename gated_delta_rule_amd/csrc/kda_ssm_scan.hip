@@ -186,7 +186,15 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p
         const int64_t next = REV ? (ch > 0 ? row0 - L : s.r1) : row0 + L;
         fetch(next, 4);
         const ChunkDecay<L>& d = dc[wh];
-        if constexpr (MODE == kWalk) save(p.states + ((chunk0 + ch) * heads + h - hfirst) * (N * P));
+        if constexpr (MODE == kWalk) {   // whole tiles, see walk_at
+            if (live) {
+                f32x4* to = reinterpret_cast<f32x4*>(p.states + ((chunk0 + ch) * heads + h - hfirst) * (N * P));
+#pragma unroll
+                for (int c = 0; c < SC_CT; ++c)
+#pragma unroll
+                    for (int m = 0; m < NT; ++m) __builtin_nontemporal_store(S[c][m], &to[walk_at<N>(pc / 16 + c, m, lane)]);
+            }
+        }
 
         f32x4 Y[SC_CT][TT];
         if constexpr (OUT) {
@@ -419,16 +427,24 @@ __global__ __launch_bounds__(SS_THREADS) void ssm_merge_kernel(SsmScanParams p) 
     if (segs == 0 && p.S_T) reinterpret_cast<f32x4*>(p.S_T)[seq_at] = run;
     f32x4* E = reinterpret_cast<f32x4*>(p.seg) + (base * heads + h) * np4 + e;
     const float* dec = p.seg_decay + base * heads + h;
-    for (int64_t k = 0; k < segs; ++k) {
-        const int64_t j = REV ? segs - 1 - k : k;
-        f32x4 loc = {0.f, 0.f, 0.f, 0.f};
-        float f = 0.f;
-        if (k + 1 < segs) {
-            loc = E[j * heads * np4];
-            f = dec[j * heads];
+    constexpr int AHEAD = 8;   // segments read together
+    for (int64_t k0 = 0; k0 < segs; k0 += AHEAD) {
+        f32x4 loc[AHEAD];
+        float f[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int64_t j = REV ? segs - 1 - (k0 + i) : k0 + i;
+            const bool there = k0 + i + 1 < segs;
+            loc[i] = there ? E[j * heads * np4] : f32x4{0.f, 0.f, 0.f, 0.f};
+            f[i] = there ? dec[j * heads] : 0.f;
         }
-        E[j * heads * np4] = run;
-        run = run * f + loc;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (k0 + i >= segs) break;
+            const int64_t j = REV ? segs - 1 - (k0 + i) : k0 + i;
+            E[j * heads * np4] = run;
+            run = run * f[i] + loc[i];
+        }
     }
 }
 

@@ -74,7 +74,15 @@ __device__ __forceinline__ SsmPiece ssm_piece(const int32_t* cu, int64_t rows, i
     return s;
 }
 
-typedef __attribute__((address_space(3))) uint16_t lds_u16;
+// Where the walks leave a state's four columns 16 ct + 4 (l >> 4) .. + 3 of row
+// 16 m + (l & 15), in 16-byte pieces: tiles of 16 x 16, each 1 KB as a wave
+// holds it, so that a store is contiguous (rows of the state in order would
+// be 64-byte pieces: 97 against 82 us for 0.27 GB).
+template <int N>
+__device__ __forceinline__ int walk_at(int ct, int m, int l) {
+    return (ct * (N / 16) + m) * 64 + l;
+}
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // Place of unit u (8 columns) of a row in a tile with U units per row.
@@ -248,6 +256,27 @@ __device__ __forceinline__ double wave_scan_f64(double x) {
     x = dpp_add_f64<0x143, 0xc>(x);   // row_bcast:31 into rows 2 and 3
     return x;
 }
+// The value of lane LANE (the last: 63), for all lanes.
+template <int LANE = 63>
+__device__ __forceinline__ double wave_last_f64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, LANE);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), LANE);
+    return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+// Sums over a lane and the later lanes of its 16, and over it and the earlier ones.
+__device__ __forceinline__ double row_suffix_f64(double x) {
+    x = dpp_add_f64<0x101, 0xf>(x);   // row_shl:1
+    x = dpp_add_f64<0x102, 0xf>(x);
+    x = dpp_add_f64<0x104, 0xf>(x);
+    return dpp_add_f64<0x108, 0xf>(x);
+}
+__device__ __forceinline__ double row_prefix_f64(double x) {
+    x = dpp_add_f64<0x111, 0xf>(x);   // row_shr:1
+    x = dpp_add_f64<0x112, 0xf>(x);
+    x = dpp_add_f64<0x114, 0xf>(x);
+    return dpp_add_f64<0x118, 0xf>(x);
+}
 // dt_raw: this lane's token, `valid` whether it exists.  Returns g_end.
 template <int L>
 __device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bool valid, float bias, int softplus,
@@ -259,10 +288,7 @@ __device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bo
         if (softplus) dt = ss_softplus(dt);
     }
     const double g = wave_scan_f64((double)(dt * A));
-    const uint64_t gu = __builtin_bit_cast(uint64_t, g);
-    const double end = __builtin_bit_cast(
-        double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)gu, L - 1) |
-                    ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(gu >> 32), L - 1) << 32));
+    const double end = wave_last_f64<L - 1>(g);
     if (lane < L) {
         const float h = (float)g;
         d.gh[lane] = h;

@@ -18,25 +18,31 @@ channels of one convolution's output:
 from __future__ import annotations
 
 import contextlib
-import ctypes
+import math
 
-from . import KDA_BF16, KDA_F32, KDAError, _check, _in_dtype, _ptr, _status, load_library
+from . import KDA_BF16, KDA_F32, KDAError, _check, _in_dtype, _status, load_library
 
 __all__ = ["ssm_conv_fwd", "ssm_conv_step", "ssm_conv_bwd", "ssm_chunk_fwd", "ssm_chunk_bwd",
            "ssm_recurrent_fwd", "ssm_chunk_fwd_workspace_bytes", "ssm_chunk_bwd_workspace_bytes",
            "verify_drafts"]
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(dev):
     """Makes `dev` the current device for the call's launches."""
     import torch
-    if dev.type != "cuda" or dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    return _NOTHING if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _stream(dev):
+    """The current stream of `dev` (torch.cuda.current_stream builds an object for it, 2 us)."""
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check_rows(t, name, lead, tail, dtype, dev):
@@ -45,6 +51,8 @@ def _check_rows(t, name, lead, tail, dtype, dev):
     import torch
     if not isinstance(t, torch.Tensor):
         raise KDAError(f"{name} must be a torch.Tensor")
+    if t.is_contiguous() and t.is_cuda and t.dtype == dtype and t.device == dev and t.shape == lead + tail:
+        return math.prod(tail)
     if not t.is_cuda:
         raise KDAError(f"{name} must be a device tensor")
     if t.device != dev:
