@@ -18,6 +18,7 @@ constexpr int64_t kScanFill = 512;        // chains that fill the 256 compute un
 constexpr int64_t kScanMinSeg = 256;      // shortest segment worth its state's traffic
 constexpr int64_t kScanMinCut = 3;        // segments from which two passes are shorter than one chain
 constexpr int64_t kScanAlign = 64;
+constexpr int64_t kVerifyFill = 2048;     // workgroups of the verification (512 to 2048: the same time)
 constexpr int64_t kGradFill = 512;        // workgroups of the gradient kernel that fill the GPU
 
 struct Span {
@@ -658,6 +659,7 @@ int kda_verify_drafts(const void* p_target, const void* p_draft, int in_dtype,
     v.B = B;
     v.K = K;
     v.n_parts = (int32_t)parts;
+    v.run = (int32_t)(B * parts / kVerifyFill > 1 ? ceil_div(B * parts, kVerifyFill) : 1);
     return kda::launch_verify(v, in_dtype == KDA_BF16, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 

@@ -85,10 +85,11 @@ struct VerifyParams {
     int32_t* tokens;         // [B, K + 1]
     double* partial;         // [B, n_parts, 2]
     int64_t V;
-    int32_t B, K, n_parts;
+    int32_t B, K, n_parts, run;   // run: parts per workgroup of the first launch
 };
-// Vocabulary entries per partial sum of a row.
+// Vocabulary entries per partial sum of a row, threads that read them.
 constexpr int64_t kVerifyPart = 4096;
+constexpr int kVerifyThreads = 256;
 hipError_t launch_verify(const VerifyParams& p, bool bf16_in, hipStream_t stream);
 
 // Scan over whole sequences.  Every sequence is cut into segments of seg_len
