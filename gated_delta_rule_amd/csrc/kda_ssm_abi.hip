@@ -101,11 +101,12 @@ struct ScanPlan {
     bool cut;
     int64_t seg_len, slots;
 };
-ScanPlan scan_plan(int32_t n_seqs, int64_t T, int64_t blocks, bool varlen) {
+// `dirs` directions (the backward pass: two) run side by side.
+ScanPlan scan_plan(int32_t n_seqs, int64_t T, int64_t blocks, bool varlen, int64_t dirs) {
     const int64_t rows = varlen ? T : n_seqs * T;
     const ScanPlan whole{false, T > 0 ? T : 1, n_seqs};
-    if (n_seqs * blocks >= kScanFill) return whole;
-    int64_t len = ceil_div(rows * blocks, kScanFill);
+    if (n_seqs * blocks * dirs >= kScanFill) return whole;
+    int64_t len = ceil_div(rows * blocks * dirs, kScanFill);
     if (len < kScanMinSeg) len = kScanMinSeg;
     const int64_t segs = ceil_div(T, len);
     if (segs < kScanMinCut) return whole;
@@ -119,14 +120,14 @@ struct BwdPlan {
     ScanPlan scan;
     int64_t slots;           // chunks
     int32_t heads_per_block, blocks;
-    int64_t states, dstates, seg, seg_decay, part, sums, total;
+    int64_t states, dstates, seg[2], seg_decay[2], part, sums, total;   // seg: of each direction
 };
 bool bwd_plan(int in_dtype, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, int32_t N,
               int32_t P, bool varlen, int32_t groups, BwdPlan* b) {
     const int64_t len = kda::ssm_chunk_tokens(in_dtype == KDA_BF16);
     const int64_t hpg = H / G, heads = groups * hpg;
     b->slots = varlen ? rows / len + n_seqs : n_seqs * ceil_div(T, len);
-    b->scan = scan_plan(n_seqs, T, scan_blocks((int32_t)heads, groups, P), varlen);
+    b->scan = scan_plan(n_seqs, T, scan_blocks((int32_t)heads, groups, P), varlen, 2);
     // as many heads of a group in one workgroup (fewer partial sums) as leave
     // enough workgroups to fill the GPU
     const int64_t want = ceil_div(kGradFill, b->slots * groups > 0 ? b->slots * groups : 1);
@@ -141,10 +142,12 @@ bool bwd_plan(int in_dtype, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, 
     const int64_t four = 3;   // every array starts on 16 bytes
     b->states = 0;
     b->dstates = b->states + st;
-    b->seg = b->dstates + st;
-    b->part = b->seg + seg;
-    b->seg_decay = b->part + part;
-    b->sums = (b->seg_decay + (b->scan.cut ? b->scan.slots * heads : 0) + four) & ~four;
+    b->seg[0] = b->dstates + st;
+    b->seg[1] = b->seg[0] + seg;
+    b->part = b->seg[1] + seg;
+    b->seg_decay[0] = b->part + part;
+    b->seg_decay[1] = b->seg_decay[0] + (b->scan.cut ? b->scan.slots * heads : 0);
+    b->sums = (b->seg_decay[1] + (b->scan.cut ? b->scan.slots * heads : 0) + four) & ~four;
     b->total = b->sums + ((b->slots * heads * 3 + 4 + four) & ~four);
     return b->total <= INT64_MAX / 8 && st <= INT64_MAX / 16 && seg <= INT64_MAX / 16 && part <= INT64_MAX / 16;
 }
@@ -321,7 +324,7 @@ size_t kda_ssm_chunk_fwd_workspace_bytes(int32_t n_seqs, int64_t T, int32_t H, i
     int64_t rows = T;
     if (!varlen && (!mul_ok((int64_t)n_seqs, T, &rows) || rows > ((int64_t)1 << 38))) return 0;
     if (rows > ((int64_t)1 << 38)) return 0;
-    const ScanPlan s = scan_plan(n_seqs, T, scan_blocks(H, G, P), varlen != 0);
+    const ScanPlan s = scan_plan(n_seqs, T, scan_blocks(H, G, P), varlen != 0, 1);
     return s.cut ? (size_t)s.slots * H * ((size_t)N * P + 1) * 4 : 0;
 }
 
@@ -359,7 +362,7 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* B, int64_t B_
     if (overlaps(ry, rs0) || overlaps(ry, rst)) return KDA_ERR_ALIASING;
     if (S0 != (const float*)S_T && overlaps(rs0, rst)) return KDA_ERR_ALIASING;
 
-    ScanPlan s = scan_plan(n_seqs, T, scan_blocks(H, G, P), cu_seqlens != nullptr);
+    ScanPlan s = scan_plan(n_seqs, T, scan_blocks(H, G, P), cu_seqlens != nullptr, 1);
     const size_t need = kda_ssm_chunk_fwd_workspace_bytes(n_seqs, T, H, G, N, P, cu_seqlens != nullptr);
     if (s.cut && (!workspace || workspace_bytes < need))
         s = ScanPlan{false, T, n_seqs};
@@ -514,13 +517,14 @@ int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_
         f.cut = b.scan.cut;
         f.seg_len = b.scan.seg_len;
         f.slots = b.scan.slots;
-        f.seg = b.scan.cut ? ws + b.seg : nullptr;
-        f.seg_decay = b.scan.cut ? ws + b.seg_decay : nullptr;
         if (n_seqs > 0) {
-            kda::SsmScanParams w = f;      // S at every chunk's start
-            w.states = ws + b.states;
-            if (rows > 0 && kda::launch_ssm_walk(w, bf16_in, false, stream) != hipSuccess) return KDA_ERR_HIP;
-            w = f;                         // the state gradient at every chunk's end
+            kda::SsmScanDirs walks{{f, f}};
+            for (int i = 0; b.scan.cut && i < 2; ++i) {
+                walks.dir[i].seg = ws + b.seg[i];
+                walks.dir[i].seg_decay = ws + b.seg_decay[i];
+            }
+            walks.dir[0].states = ws + b.states;   // S at every chunk's start
+            kda::SsmScanParams& w = walks.dir[1];  // the state gradient at every chunk's end
             w.x = grad_y;
             w.x_stride = xw;
             w.B = C;
@@ -528,7 +532,7 @@ int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_
             w.S0 = grad_S_T;
             w.S_T = grad_S0;
             w.states = ws + b.dstates;
-            if (kda::launch_ssm_walk(w, bf16_in, true, stream) != hipSuccess) return KDA_ERR_HIP;
+            if (kda::launch_ssm_walks(walks, bf16_in, stream) != hipSuccess) return KDA_ERR_HIP;
         }
         kda::SsmGradParams q{};
         q.f = f;

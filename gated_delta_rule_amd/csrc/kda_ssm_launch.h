@@ -124,12 +124,16 @@ struct SsmScanParams {
 };
 hipError_t launch_ssm_chunk_fwd(const SsmScanParams& p, bool bf16_in, hipStream_t stream);
 
-// The backward pass's walks: the state at every chunk's start, and (reverse)
-// the state gradient at every chunk's end, from C as B, grad_y as x,
-// grad_S_T as S0; reverse leaves the gradient of the initial states in S_T.
+// The backward pass's walks: dir[0], the state at every chunk's start; dir[1],
+// from the sequences' ends, the state gradient at every chunk's end, from C as
+// B, grad_y as x, grad_S_T as S0, leaving the gradient of the initial states
+// in S_T.  Same shapes, segments and slots in both.
 // Chunks of ssm_chunk_tokens(bf16) tokens; chunk c of sequence n has slot
 //   equal lengths: n * ceil(T / tokens) + c,  packed: cu[n] / tokens + n + c.
-hipError_t launch_ssm_walk(const SsmScanParams& p, bool bf16_in, bool reverse, hipStream_t stream);
+struct SsmScanDirs {
+    SsmScanParams dir[2];
+};
+hipError_t launch_ssm_walks(const SsmScanDirs& d, bool bf16_in, hipStream_t stream);
 constexpr int64_t ssm_chunk_tokens(bool bf16_in) { return bf16_in ? 64 : 32; }
 
 struct SsmGradParams {

@@ -7,12 +7,12 @@
 //   S'   = e^{g_end} S + sum_s B_s (e^{g_end - g_s} dt_s x_s)^T
 // Every exponent is <= 0, so nothing overflows however strong the decay.
 //
-// A workgroup runs one chain of chunks for 128 columns of x: two heads of 64
-// of one group, which share the B and C tiles and the products C . B, or one
-// head of 128.  A wave owns 32 columns and keeps its part of the state in
-// accumulator registers in an order in which it is, without any move, also
-// the operand of the next chunk's S^T C.  Per chunk: the next chunk's rows are
-// requested, the four waves share out the 16 x 16 tiles of C . B below the
+// A workgroup of eight waves runs one chain of chunks for 128 columns of x:
+// two heads of 64 of one group, which share the B and C tiles and the products
+// C . B, or one head of 128.  A wave owns 16 columns and keeps its part of the
+// state in accumulator registers in an order in which it is, without any move,
+// also the operand of the next chunk's S^T C.  Per chunk: the next chunk's rows
+// are requested, the waves share out the 16 x 16 tiles of C . B up to the
 // diagonal and put them, weighted and with D on the diagonal, into LDS while
 // each also computes its S^T C; after one barrier each adds M x, stores y and
 // updates its state.
@@ -45,13 +45,15 @@ enum ScanMode {
     kLocal = 1,    // each segment's final state from zero, and its decay
     kWalk = 2,     // the state before every chunk
 };
-// REV: from the sequence's end to its start, for the state gradient
+// Second direction (blockIdx.y = 1): from the sequence's end to its start, for
+// the state gradient
 //   dS' = e^{g_end} dS + sum_t C_t (e^{g_t} dy_t)^T
 // (C takes B's place, dy takes x's).
-template <typename InT, int N, int P, int MODE, bool REV>
-__global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p, int32_t hblocks) {
+template <typename InT, int N, int P, int MODE>
+__global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dirs, int32_t hblocks) {
     constexpr bool OUT = MODE == kOut;
-    static_assert(!(OUT && REV), "outputs run forward");
+    const bool rev = !OUT && blockIdx.y;
+    const SsmScanParams& p = dirs.dir[OUT ? 0 : blockIdx.y];
     using Cfg = ScanCfg<InT, N, P>;
     constexpr int L = Cfg::L, XP = Cfg::XP, MP = Cfg::MP, SP = Cfg::SP, WP = Cfg::WP, HPW = Cfg::HPW;
     constexpr int TT = L / 16, NT = N / 16;
@@ -86,7 +88,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p
         s = ssm_piece(p.cu, p.rows, p.T, p.n_seqs, p.seg_len, slot);
         if (s.piece < 0) return;
         // nothing follows the last segment (the full pass gives its final state)
-        if (MODE == kLocal && (REV ? s.r0 == s.start : s.r1 == s.end)) return;
+        if (MODE == kLocal && (rev ? s.r0 == s.start : s.r1 == s.end)) return;
     } else {
         const SsmRange r = ssm_range(p.cu, p.rows, p.T, slot);
         s = SsmPiece{slot, 0, r.start, r.end, r.start, r.end};
@@ -149,7 +151,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p
     const float Ah = dec_live ? p.A[h0 + dh] : 0.f;
     float gdt = 0.f;
     auto dt_there = [&](int64_t k, int64_t& row) {   // this lane's token of the k-th chunk of the walk
-        row = s.r0 + (REV ? chunks - 1 - k : k) * L + lane;
+        row = s.r0 + (rev ? chunks - 1 - k : k) * L + lane;
         return dec_live && k < chunks && lane < L && row < s.r1;
     };
     auto fetch_dt = [&](int64_t k) {
@@ -160,12 +162,12 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p
     double total = 0.0;
     // this chain's first chunk among the slots of the states array
     const int64_t chunk0 = (p.cu ? s.start / L + s.n : s.n * ((p.T + L - 1) / L)) + (s.r0 - s.start) / L;
-    const int64_t first = chunks == 0 ? s.r1 : REV ? s.r0 + (chunks - 1) * L : s.r0;   // (an empty sequence: no row)
+    const int64_t first = chunks == 0 ? s.r1 : rev ? s.r0 + (chunks - 1) * L : s.r0;   // (an empty sequence: no row)
     fetch(first, 7);
     fetch_dt(dk);
 
     for (int64_t i = 0; i < chunks; ++i) {
-        const int64_t ch = REV ? chunks - 1 - i : i;
+        const int64_t ch = rev ? chunks - 1 - i : i;
         const int64_t row0 = s.r0 + ch * L;
         const int valid = s.r1 - row0 < L ? (int)(s.r1 - row0) : L;
         hide(lane), hide(rN), hide(rL), hide(cB), hide(cX);
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p
         lds_barrier();
         // the next chunk's rows, a tile at a time between the products: a
         // wave would stand at a burst of requests
-        const int64_t next = REV ? (ch > 0 ? row0 - L : s.r1) : row0 + L;
+        const int64_t next = rev ? (ch > 0 ? row0 - L : s.r1) : row0 + L;
         fetch(next, 4);
         const ChunkDecay<L>& d = dc[wh];
         if constexpr (MODE == kWalk) {   // whole tiles, see walk_at
@@ -354,7 +356,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p
 #pragma unroll
             for (int c = 0; c < SC_CT; ++c) {
                 float v[8];
-                const f32x4* ws = reinterpret_cast<const f32x4*>(&(REV ? d.eg : d.w)[32 * ks + 8 * lg]);
+                const f32x4* ws = reinterpret_cast<const f32x4*>(&(rev ? d.eg : d.w)[32 * ks + 8 * lg]);
                 const f32x4 w0 = ws[0], w1 = ws[1];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -403,16 +405,17 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanParams p
             p.seg_decay[slot * heads + h0 - hfirst + tid] = expf((float)g);
         }
     } else {
-        if (p.S_T && (REV ? s.r0 == s.start : s.r1 == s.end)) save(p.S_T + seq_at);
+        if (p.S_T && (rev ? s.r0 == s.start : s.r1 == s.end)) save(p.S_T + seq_at);
     }
 }
 
 // Incoming state of every segment from the segments' final states from zero,
-// in place: S_0, then S_{j+1} = decay_j S_j + E_j (REV: from the last segment
-// to the first).  The E of the segment at the far end is not read.  Empty
+// in place: S_0, then S_{j+1} = decay_j S_j + E_j (second direction: from the
+// last segment to the first).  The E of the segment at the far end is not read.  Empty
 // sequences have no segment: their final state is their initial one.
-template <bool REV>
-__global__ __launch_bounds__(SS_THREADS) void ssm_merge_kernel(SsmScanParams p) {
+__global__ __launch_bounds__(SS_THREADS) void ssm_merge_kernel(SsmScanDirs dirs) {
+    const bool rev = blockIdx.y;
+    const SsmScanParams& p = dirs.dir[blockIdx.y];
     const int64_t np4 = (int64_t)p.N * p.P / 4, hpg = p.H / p.G, heads = p.gn * hpg;
     const int64_t i = (int64_t)blockIdx.x * SS_THREADS + threadIdx.x;
     if (i >= np4 * p.n_seqs * heads) return;
@@ -433,7 +436,7 @@ __global__ __launch_bounds__(SS_THREADS) void ssm_merge_kernel(SsmScanParams p) 
         float f[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int64_t j = REV ? segs - 1 - (k0 + i) : k0 + i;
+            const int64_t j = rev ? segs - 1 - (k0 + i) : k0 + i;
             const bool there = k0 + i + 1 < segs;
             loc[i] = there ? E[j * heads * np4] : f32x4{0.f, 0.f, 0.f, 0.f};
             f[i] = there ? dec[j * heads] : 0.f;
@@ -441,41 +444,45 @@ __global__ __launch_bounds__(SS_THREADS) void ssm_merge_kernel(SsmScanParams p) 
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             if (k0 + i >= segs) break;
-            const int64_t j = REV ? segs - 1 - (k0 + i) : k0 + i;
+            const int64_t j = rev ? segs - 1 - (k0 + i) : k0 + i;
             E[j * heads * np4] = run;
             run = run * f[i] + loc[i];
         }
     }
 }
 
-// MODE kOut or kWalk, with the passes before it where sequences are cut.
-template <typename InT, int N, int P, int MODE, bool REV>
-static hipError_t run_scan(const SsmScanParams& p, hipStream_t stream) {
+// MODE kOut (one direction) or kWalk (both), with the passes before it where
+// sequences are cut.  Both directions of the backward pass share their
+// launches: neither waits for the other.
+template <typename InT, int N, int P, int MODE>
+static hipError_t run_scan(const SsmScanDirs& d, hipStream_t stream) {
     constexpr int HPW = 128 / P;
+    const SsmScanParams& p = d.dir[0];
     const int hpg = p.H / p.G;
     const int32_t hblocks = p.gn * ((hpg + HPW - 1) / HPW);
-    const dim3 grid((unsigned)(p.slots * hblocks)), block(SC_THREADS);
+    const unsigned dirs = MODE == kOut ? 1 : 2;
+    const dim3 grid((unsigned)(p.slots * hblocks), dirs), block(SC_THREADS);
     if (p.cut) {
-        hipLaunchKernelGGL((ssm_scan_kernel<InT, N, P, kLocal, REV>), grid, block, 0, stream, p, hblocks);
+        hipLaunchKernelGGL((ssm_scan_kernel<InT, N, P, kLocal>), grid, block, 0, stream, d, hblocks);
         const int64_t n = (int64_t)p.n_seqs * p.gn * hpg * N * P / 4;
-        hipLaunchKernelGGL((ssm_merge_kernel<REV>), dim3((unsigned)((n + SS_THREADS - 1) / SS_THREADS)),
-                           dim3(SS_THREADS), 0, stream, p);
+        hipLaunchKernelGGL(ssm_merge_kernel, dim3((unsigned)((n + SS_THREADS - 1) / SS_THREADS), dirs),
+                           dim3(SS_THREADS), 0, stream, d);
     }
-    hipLaunchKernelGGL((ssm_scan_kernel<InT, N, P, MODE, REV>), grid, block, 0, stream, p, hblocks);
+    hipLaunchKernelGGL((ssm_scan_kernel<InT, N, P, MODE>), grid, block, 0, stream, d, hblocks);
     return hipGetLastError();
 }
-template <typename InT, int MODE, bool REV>
-static hipError_t run_scan(const SsmScanParams& p, hipStream_t stream) {
-    if (p.N == 128)
-        return p.P == 64 ? run_scan<InT, 128, 64, MODE, REV>(p, stream) : run_scan<InT, 128, 128, MODE, REV>(p, stream);
-    return p.P == 64 ? run_scan<InT, 64, 64, MODE, REV>(p, stream) : run_scan<InT, 64, 128, MODE, REV>(p, stream);
+template <typename InT, int MODE>
+static hipError_t run_scan(const SsmScanDirs& d, hipStream_t stream) {
+    if (d.dir[0].N == 128)
+        return d.dir[0].P == 64 ? run_scan<InT, 128, 64, MODE>(d, stream) : run_scan<InT, 128, 128, MODE>(d, stream);
+    return d.dir[0].P == 64 ? run_scan<InT, 64, 64, MODE>(d, stream) : run_scan<InT, 64, 128, MODE>(d, stream);
 }
 hipError_t launch_ssm_chunk_fwd(const SsmScanParams& p, bool bf16_in, hipStream_t stream) {
-    return bf16_in ? run_scan<__bf16, kOut, false>(p, stream) : run_scan<float, kOut, false>(p, stream);
+    const SsmScanDirs d{{p, SsmScanParams{}}};
+    return bf16_in ? run_scan<__bf16, kOut>(d, stream) : run_scan<float, kOut>(d, stream);
 }
-hipError_t launch_ssm_walk(const SsmScanParams& p, bool bf16_in, bool reverse, hipStream_t stream) {
-    if (reverse) return bf16_in ? run_scan<__bf16, kWalk, true>(p, stream) : run_scan<float, kWalk, true>(p, stream);
-    return bf16_in ? run_scan<__bf16, kWalk, false>(p, stream) : run_scan<float, kWalk, false>(p, stream);
+hipError_t launch_ssm_walks(const SsmScanDirs& d, bool bf16_in, hipStream_t stream) {
+    return bf16_in ? run_scan<__bf16, kWalk>(d, stream) : run_scan<float, kWalk>(d, stream);
 }
 
 }  // namespace kda
