@@ -26,6 +26,8 @@
 // wrote: 16 N P bytes per chunk and head against 6 L P of x, dy and dx.
 #include "kda_ssm_tile.h"
 
+#include <type_traits>
+
 namespace kda {
 
 __device__ __forceinline__ float sum_lane_groups(float v) {   // over lanes with equal l & 15
@@ -39,7 +41,6 @@ __device__ __forceinline__ float sum_lane_groups(float v) {   // over lanes with
 // second 16-token tile); towards dx one 16-column tile of x (with P = 64,
 // every second token tile).
 constexpr int SG_WAVES = 8, SG_THREADS = 64 * SG_WAVES;
-constexpr int SG_HEADS = 4;   // heads whose decay sums are computed together, one per wave
 
 template <typename InT, int N, int P>
 __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q) {
@@ -49,21 +50,24 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
     constexpr int KP = BF ? 1 : 3;      // ... of the chunk matrices (their products are rounded to the input type)
     constexpr int RP = BF ? 1 : 3;      // ... of R in dx
     constexpr int SP = 3;               // ... of S and R where U and V come from (float32 results)
-    constexpr int TT = L / 16, NTILE = TT * (TT + 1) / 2, EW = SG_WAVES - 1, TPW = (NTILE + EW - 1) / EW;   // (the last wave has no tile)
+    constexpr int TT = L / 16, OFFD = TT * (TT - 1) / 2;   // 16 x 16 tiles below the diagonal
+    constexpr int OW = SG_WAVES - TT, TPW = (OFFD + OW - 1) / OW;      // the waves that own them, tiles per wave
     constexpr int RW = N / 16, RS = SG_WAVES / RW, RT = TT / RS;   // row tiles; waves per row tile; its token tiles per wave
     constexpr int CW = P / 16, CS = SG_WAVES / CW, CT = TT / CS;   // column tiles of x, likewise
+    // Heads whose decay sums are computed together, one per wave, and whose
+    // decay gradients are, as many as LDS holds the sums of: a wave at a time
+    // would keep the others waiting (a wave per head: 227 against 220 us).
+    constexpr int HB = P == 64 ? SG_WAVES : SG_WAVES / 2;
     __shared__ __attribute__((aligned(16))) __bf16 tB[XP * L * N], tC[XP * L * N];
     __shared__ __attribute__((aligned(16))) __bf16 tX[XP * L * P], tY[XP * L * P];
     __shared__ __attribute__((aligned(16))) __bf16 tK[KP * L * L], tM[KP * L * L];
-    __shared__ ChunkDecay<L> decs[2 * SG_HEADS];
+    __shared__ ChunkDecay<L> decs[HB];
     // R in bf16, for its columns (float32: they come from memory, three planes being too large)
     __shared__ __attribute__((aligned(16))) __bf16 tR[BF ? N * P : 8];
-    // a head's sums, read while the next head's are written
     struct __attribute__((aligned(16))) Sums {
         float R[TT][L], Q[TT][L], U[RW][L], V[RW][L], W[L], E[L], Z[RW];
     };
-    __shared__ Sums sums[2];
-    __shared__ float sRaw[2 * SG_HEADS][L];
+    __shared__ Sums sums[HB];
 
     const SsmScanParams& p = q.f;
     const int tid = threadIdx.x;
@@ -116,30 +120,30 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
     }
     // this wave's rows of a head's S and R, one head ahead
     f32x4 fS[P / 32][2], fR[P / 32][2];
-    auto fetch_states = [&](int hw) {
-        const f32x4* S = reinterpret_cast<const f32x4*>(q.states + (slot * heads + hw) * (N * P));
-        const f32x4* R = reinterpret_cast<const f32x4*>(q.dstates + (slot * heads + hw) * (N * P));
+    auto fetch_state = [&](f32x4 (&f)[P / 32][2], const float* states, int hw) {
+        const f32x4* S = reinterpret_cast<const f32x4*>(states + (slot * heads + hw) * (N * P));
         const int l15 = lane & 15, lg = lane >> 4;
 #pragma unroll
         for (int ks = 0; ks < P / 32; ++ks)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {   // columns 32 ks + 8 lg + 4 k .. + 3 of row n0 + l15
-                const int at = walk_at<N>(2 * ks + (lg >> 1), rt, l15 + 16 * (2 * (lg & 1) + k));
-                fS[ks][k] = S[at];
-                fR[ks][k] = R[at];
-            }
+            for (int k = 0; k < 2; ++k)   // columns 32 ks + 8 lg + 4 k .. + 3 of row n0 + l15
+                f[ks][k] = S[walk_at<N>(2 * ks + (lg >> 1), rt, l15 + 16 * (2 * (lg & 1) + k))];
     };
     fetch(hw0);
-    fetch_states(hw0);
-    float raw_next = wave < SG_HEADS ? raw_dt(wave) : 0.f;
+    fetch_state(fS, q.states, hw0);
+    fetch_state(fR, q.dstates, hw0);
+    float raw = 0.f, raw_next = wave < HB ? raw_dt(wave) : 0.f;   // of the head that this wave ends
     __syncthreads();
 
     // tiles of G^T (rows s, columns t), kept for all heads
     f32x4 G[TPW];
+    // (the first TT waves own one on the diagonal each, the others the rest)
+    const bool on_diag = wave < TT;
     auto tile_of = [&](int k, int& tt, int& st) {
-        const int idx = wave + EW * k < NTILE ? wave + EW * k : NTILE - 1;
-        tt = (idx >= 1) + (idx >= 3) + (idx >= 6);
-        st = idx - tt * (tt + 1) / 2;
+        int idx = wave - TT + OW * k;
+        idx = idx < OFFD ? idx : OFFD - 1;
+        tt = on_diag ? wave : 1 + (idx >= 1) + (idx >= 3);
+        st = on_diag ? wave : idx - tt * (tt - 1) / 2;
     };
 #pragma unroll
     for (int k = 0; k < TPW; ++k) {
@@ -172,15 +176,16 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
         }
     };
 
-    // gradients of the decay and of dt of a head whose sums are whole: one
-    // token per lane of the last wave
-    auto finish = [&](int hk) {
-        const int hw = hw0 + hk, h = hfirst + hw, at = hk % (2 * SG_HEADS);
-        const Sums& o = sums[hk & 1];
-        const ChunkDecay<L>& dec = decs[at];
+    // gradients of the decay and of dt of head hk0 + wave, whose sums are
+    // whole: one token per lane
+    auto finish = [&](int hk0) {
+        if (wave >= HB || hk0 + wave >= hwn) return;
+        const int hw = hw0 + hk0 + wave, h = hfirst + hw;
+        const Sums& o = sums[wave];
+        const ChunkDecay<L>& dec = decs[wave];
         const int t = lane < L ? lane : L - 1;
         const bool on = lane < valid;
-        const float raw = sRaw[at][t], A = p.A[h];
+        const float A = p.A[h];
         // W across token t: tiles (u's tile a, s's tile b) around t's tile k.
         // Whole tiles and whole rows or columns of them only add up; just
         // within the tile on the diagonal do row and column sums cancel.
@@ -246,15 +251,18 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
         const float D = p.D ? p.D[h] : 0.f;
         gX.put(tX);
         gY.put(tY);
-        if (hk % SG_HEADS == 0 && wave < SG_HEADS) {   // (the last four heads' stay for the sums that are still open)
-            const int k = hk + wave, at = k % (2 * SG_HEADS);
-            const float a = k < hwn ? p.A[hfirst + hw0 + k] : 0.f;
-            chunk_decay<L>(decs[at], raw_next, k < hwn && lane < valid, 0.f, p.softplus, a);
-            if (lane < L) sRaw[at][lane] = raw_next;
-            raw_next = raw_dt(k + SG_HEADS);
+        if (hk % HB == 0) {
+            if (hk > 0) finish(hk - HB);
+            if (wave < HB) {
+                const int k = hk + wave;
+                const float a = k < hwn ? p.A[hfirst + hw0 + k] : 0.f;
+                raw = raw_next;
+                chunk_decay<L>(decs[wave], raw, k < hwn && lane < valid, 0.f, p.softplus, a);
+                raw_next = raw_dt(k + HB);
+            }
         }
-        const ChunkDecay<L>& dec = decs[hk % (2 * SG_HEADS)];
-        Sums& now = sums[hk & 1];
+        const ChunkDecay<L>& dec = decs[hk % HB];
+        Sums& now = sums[hk % HB];
         lds_barrier();
         // R by columns, for dx (float32): out of cache, its rows having come for fR
         float fRc[BF ? 1 : N / 32][8];
@@ -268,13 +276,8 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
-        // the last wave ends the previous head while the others start this one
-        if (wave == SG_WAVES - 1 && hk > 0) finish(hk - 1);
-
         // chunk matrices, a lane holding four neighbouring s of one t
-#pragma unroll
-        for (int k = 0; k < TPW; ++k) {
-            if (wave == EW || wave + EW * k >= NTILE) break;
+        auto scores = [&](int k) {
             int tt, st;
             tile_of(k, tt, st);
             f32x4 E = {0.f, 0.f, 0.f, 0.f};
@@ -288,24 +291,26 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
                 }
                 E = mma_parts<XP, XP>(fx, fy, E);
             }
+            return E;
+        };
+        auto weigh = [&](const f32x4& E, int k, auto diag) {
+            int tt, st;
+            tile_of(k, tt, st);
             const int t = 16 * tt + l15, s0 = 16 * st + 4 * lg;
             const float ht = dec.gh[t], lt = dec.gl[t];
             const f32x4 hs = *reinterpret_cast<const f32x4*>(&dec.gh[s0]);
             const f32x4 ls = *reinterpret_cast<const f32x4*>(&dec.gl[s0]);
             const f32x4 ds = *reinterpret_cast<const f32x4*>(&dec.dt[s0]);
             float K[4], M[4], row = 0.f, col[4];
-            if (tt != st) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (!diag) {
                     const float l = __expf((ht - hs[r]) + (lt - ls[r]));
                     K[r] = E[r] * l * ds[r];
                     M[r] = G[k][r] * l * ds[r];
                     col[r] = G[k][r] * l * E[r];
                     row = fmaf(col[r], ds[r], row);
-                }
-            } else {   // the diagonal tile: nothing above the diagonal, D on it, and W's diagonal apart
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
+                } else {   // nothing above the diagonal, D on it, and W's diagonal apart
                     const int sr = s0 + r;
                     const float l = sr <= t ? __expf((ht - hs[r]) + (lt - ls[r])) : 0.f;
                     K[r] = sr <= t ? E[r] * l * ds[r] : 0.f;
@@ -347,6 +352,15 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
                     }
                 }
             }
+        };
+        if (on_diag) {
+            weigh(scores(0), 0, std::true_type{});
+        } else if (TPW > 1 && wave - TT + OW < OFFD) {
+            const f32x4 E0 = scores(0), E1 = scores(TPW - 1);
+            weigh(E0, 0, std::false_type{});
+            weigh(E1, TPW - 1, std::false_type{});
+        } else if (wave - TT < OFFD) {
+            weigh(scores(0), 0, std::false_type{});
         }
 
         // products with S and R: rows n0 .., columns token (tile rh + RS k)
@@ -413,10 +427,13 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
             }
         };
         with_state(fS, tY, tC, dec.eg, now.U[rt], dC);
+        // (the next head's requests apart: a wave would stand at a burst)
+        __builtin_amdgcn_sched_barrier(0);
+        if (hk + 1 < hwn) fetch_state(fS, q.states, hw + 1);
         __builtin_amdgcn_sched_barrier(0);
         with_state(fR, tX, tB, dec.w, now.V[rt], dB);
         __builtin_amdgcn_sched_barrier(0);
-        if (hk + 1 < hwn) fetch_states(hw + 1);   // in flight until the next head's products
+        if (hk + 1 < hwn) fetch_state(fR, q.dstates, hw + 1);
         lds_barrier();   // the chunk matrices and the partial sums are whole
         if (hk + 1 < hwn) fetch(hw + 1);
 
@@ -499,7 +516,7 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
         lds_barrier();   // the tiles are consumed (rows and stores stay in flight)
     }
 
-    if (wave == SG_WAVES - 1) finish(hwn - 1);
+    finish((hwn - 1) / HB * HB);
 
     // dB and dC of these heads: the gradients themselves, or a partial sum
     const int l15 = lane & 15, lg = lane >> 4;
