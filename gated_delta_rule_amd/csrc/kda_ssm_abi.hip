@@ -12,7 +12,8 @@ namespace {
 
 // Workgroups of a launch: below 2^24, so that workgroups times 256 threads
 // stay below 2^32.
-constexpr int64_t kMaxWorkgroups = (1 << 24) - 1;
+constexpr int64_t kMaxWorkgroups = (1 << 24) - 1;   // of 256 threads: fewer than 2^32 threads per launch
+constexpr int64_t kMaxWide = kMaxWorkgroups / 2;    // of 512
 constexpr int32_t kMaxTokens = 64;        // tokens per request in the step forms
 constexpr int64_t kScanFill = 512;        // chains that fill the 256 compute units (two each)
 constexpr int64_t kScanMinSeg = 256;      // shortest segment worth its state's traffic
@@ -373,7 +374,7 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* B, int64_t B_
             if (overlaps(rw, r)) return KDA_ERR_ALIASING;
         if (overlaps(rw, ry) || overlaps(rw, rs0) || overlaps(rw, rst)) return KDA_ERR_ALIASING;
     }
-    if (s.slots * scan_blocks(H, G, P) > kMaxWorkgroups ||
+    if (s.slots * scan_blocks(H, G, P) > kMaxWide ||
         ceil_div((int64_t)n_seqs * H * N * P, 1024) > kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
     kda::SsmScanParams p{};
@@ -462,8 +463,9 @@ int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_
     }
     if (!workspace || groups < 1) return KDA_ERR_WORKSPACE;
     const int64_t per = scan_blocks(groups * (H / G), groups, P);
-    if (b.scan.slots * per > kMaxWorkgroups || b.slots * groups * b.blocks > kMaxWorkgroups ||
-        ceil_div((int64_t)n_seqs * H * N * P, 1024) > kMaxWorkgroups || ceil_div(rows * groups * N, 512) > kMaxWorkgroups)
+    if (b.scan.slots * per > kMaxWide || b.slots * groups * b.blocks > kMaxWide ||
+        ceil_div((int64_t)n_seqs * H * N * P, 1024) > kMaxWorkgroups ||
+        ceil_div(rows * groups * N, 512) + groups * (int64_t)(H / G) > kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
 
     // outputs overlap nothing, except that grad_x, grad_B and grad_C may

@@ -545,7 +545,7 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
 
 // Adds up the head blocks' partial sums of dB and dC, four channels per lane.
 template <typename InT>
-__global__ __launch_bounds__(SS_THREADS) void ssm_grad_bc_kernel(SsmGradParams q) {
+__device__ __forceinline__ void ssm_grad_bc(const SsmGradParams& q) {
     const SsmScanParams& p = q.f;
     const int64_t n4 = p.N / 4, per = (int64_t)p.gn * p.rows * n4;   // pieces of one block's array
     const int64_t i = (int64_t)blockIdx.x * SS_THREADS + threadIdx.x;
@@ -566,9 +566,9 @@ __global__ __launch_bounds__(SS_THREADS) void ssm_grad_bc_kernel(SsmGradParams q
 }
 
 // Per head: the chunks' sums for A, D and dt_bias, in slot order per lane.
-__global__ __launch_bounds__(SS_THREADS) void ssm_grad_sums_kernel(SsmGradParams q) {
+__device__ __forceinline__ void ssm_grad_sums(const SsmGradParams& q, int64_t hw) {
     const SsmScanParams& p = q.f;
-    const int64_t hw = blockIdx.x, heads = (int64_t)p.gn * (p.H / p.G);
+    const int64_t heads = (int64_t)p.gn * (p.H / p.G);
     double a[3] = {0.0, 0.0, 0.0};
     for (int64_t s = threadIdx.x; s < q.slots; s += SS_THREADS)
 #pragma unroll
@@ -589,10 +589,16 @@ __global__ __launch_bounds__(SS_THREADS) void ssm_grad_sums_kernel(SsmGradParams
     }
 }
 
+// Both in one launch: `bc` workgroups for dB and dC, then one per head.
+template <typename InT>
+__global__ __launch_bounds__(SS_THREADS) void ssm_grad_tail_kernel(SsmGradParams q, int64_t bc) {
+    if (blockIdx.x < bc) ssm_grad_bc<InT>(q);
+    else ssm_grad_sums(q, (int64_t)blockIdx.x - bc);
+}
+
 template <typename InT>
 static hipError_t run_grad(const SsmGradParams& q, hipStream_t stream) {
     const SsmScanParams& p = q.f;
-    const dim3 block(SS_THREADS);
     if (q.slots > 0) {
         const dim3 grid((unsigned)(q.slots * p.gn * q.blocks)), wide(SG_THREADS);
         if (p.N == 128 && p.P == 64) hipLaunchKernelGGL((ssm_grad_kernel<InT, 128, 64>), grid, wide, 0, stream, q);
@@ -600,11 +606,9 @@ static hipError_t run_grad(const SsmGradParams& q, hipStream_t stream) {
         else if (p.P == 64) hipLaunchKernelGGL((ssm_grad_kernel<InT, 64, 64>), grid, wide, 0, stream, q);
         else hipLaunchKernelGGL((ssm_grad_kernel<InT, 64, 128>), grid, wide, 0, stream, q);
     }
-    if (q.blocks > 1 && p.rows > 0) {
-        const int64_t n = 2 * (int64_t)p.gn * p.rows * (p.N / 4);
-        hipLaunchKernelGGL(ssm_grad_bc_kernel<InT>, dim3((unsigned)((n + SS_THREADS - 1) / SS_THREADS)), block, 0, stream, q);
-    }
-    hipLaunchKernelGGL(ssm_grad_sums_kernel, dim3((unsigned)(p.gn * (p.H / p.G))), block, 0, stream, q);
+    const int64_t n = q.blocks > 1 ? 2 * (int64_t)p.gn * p.rows * (p.N / 4) : 0, bc = (n + SS_THREADS - 1) / SS_THREADS;
+    hipLaunchKernelGGL(ssm_grad_tail_kernel<InT>, dim3((unsigned)(bc + p.gn * (p.H / p.G))), dim3(SS_THREADS), 0, stream,
+                       q, bc);
     return hipGetLastError();
 }
 hipError_t launch_ssm_grad(const SsmGradParams& q, bool bf16_in, hipStream_t stream) {

@@ -412,9 +412,11 @@ __global__ __launch_bounds__(CV_THREADS) void conv_bwd_kernel(ConvBwdParams q) {
     }
 }
 
+constexpr int CB_TAIL = 256;   // threads of the launch behind it
+
 // Sums the partial weight gradients: 64 columns by 4 strides per workgroup.
 template <int W>
-__global__ __launch_bounds__(256) void conv_bwd_reduce_kernel(ConvBwdParams q, int64_t n_part) {
+__device__ __forceinline__ void conv_bwd_reduce(const ConvBwdParams& q, int64_t n_part) {
     const int64_t cols = (int64_t)(W + 1) * q.f.channels;
     const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
     const int k = threadIdx.x >> 6;
@@ -442,11 +444,11 @@ __global__ __launch_bounds__(256) void conv_bwd_reduce_kernel(ConvBwdParams q, i
 // Gradient of the cache: its entry m (position m - W + 1) is read by the
 // positions t < W - 1 with t - (W - 1 - j) = m - W + 1, that is tap j = m - t.
 template <typename InT, int W>
-__global__ __launch_bounds__(64) void conv_bwd_cache_kernel(ConvBwdParams q) {
+__device__ __forceinline__ void conv_bwd_cache(const ConvBwdParams& q, int64_t block) {
     constexpr int N = 4;
     const ConvParams& p = q.f;
     const int64_t nv = p.channels / N;
-    const int64_t idx = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    const int64_t idx = block * CB_TAIL + threadIdx.x;
     if (idx >= nv * p.n_seqs) return;
     const int64_t n = idx / nv, c0 = (idx - n * nv) * N;
     const Seq s = seq_range(p, n);
@@ -489,6 +491,14 @@ __global__ __launch_bounds__(64) void conv_bwd_cache_kernel(ConvBwdParams q) {
         for (int c = 0; c < N; ++c) q.gcache[(n * (W - 1) + m) * p.channels + c0 + c] = gc[m][c];
 }
 
+// Both in one launch: the first `sums` workgroups add up, the others take the
+// cache.
+template <typename InT, int W>
+__global__ __launch_bounds__(CB_TAIL) void conv_bwd_tail_kernel(ConvBwdParams q, int64_t n_part, int64_t sums) {
+    if (blockIdx.x < sums) conv_bwd_reduce<W>(q, n_part);
+    else conv_bwd_cache<InT, W>(q, (int64_t)blockIdx.x - sums);
+}
+
 template <typename InT, int W>
 static hipError_t run_conv_fwd(const ConvParams& p, hipStream_t stream) {
     if (p.rows > 0) {
@@ -516,12 +526,10 @@ static hipError_t run_conv_bwd(const ConvBwdParams& q, hipStream_t stream) {
         const dim3 grid((unsigned)(cv_strips(p.channels) * parts));
         hipLaunchKernelGGL((conv_bwd_kernel<InT, W>), grid, dim3(CV_THREADS), 0, stream, q);
     }
-    const int64_t cols = (int64_t)(W + 1) * p.channels;
-    hipLaunchKernelGGL((conv_bwd_reduce_kernel<W>), dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream, q, parts);
-    if (q.gcache && p.n_seqs > 0) {
-        const int64_t n = (int64_t)p.n_seqs * (p.channels / 4);
-        hipLaunchKernelGGL((conv_bwd_cache_kernel<InT, W>), dim3((unsigned)((n + 63) / 64)), dim3(64), 0, stream, q);
-    }
+    const int64_t sums = ((int64_t)(W + 1) * p.channels + 63) / 64;
+    const int64_t lanes = q.gcache ? (int64_t)p.n_seqs * (p.channels / 4) : 0;
+    hipLaunchKernelGGL((conv_bwd_tail_kernel<InT, W>), dim3((unsigned)(sums + (lanes + CB_TAIL - 1) / CB_TAIL)),
+                       dim3(CB_TAIL), 0, stream, q, parts, sums);
     return hipGetLastError();
 }
 
