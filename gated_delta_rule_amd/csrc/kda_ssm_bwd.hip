@@ -224,7 +224,9 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
         // U of this token and the later ones, V of the earlier ones
         const double x = lane < L ? (double)U : 0.0, y = lane < L ? (double)(V * dt) : 0.0;
         const double sx = wave_scan_f64(x), sy = wave_scan_f64(y);
-        const float da = (float)(X + (wave_last_f64(sx) - sx + x) + (sy - y) + (double)Z);
+        const double across = X + (wave_last_f64(sx) - sx + x) + (sy - y) + (double)Z;   // (by all lanes)
+        // (rounding's remainder of the sums times a large dt is no gradient of A)
+        const float da = dt * A < kDecayEnds ? 0.f : (float)across;
         float ddt = (Q + o.W[t]) + V + A * da;
         if (p.softplus) ddt *= 1.f / (1.f + expf(-raw));
         if (on) q.gdt[(row0 + lane) * p.H + h] = ddt;

@@ -277,6 +277,11 @@ __device__ __forceinline__ double row_prefix_f64(double x) {
     x = dpp_add_f64<0x114, 0xf>(x);
     return dpp_add_f64<0x118, 0xf>(x);
 }
+// A token's decay below this ends all memory: e^a is zero in float32 (half the
+// least subnormal number is e^-103.97).  Decays are cut off at kDecayCut, which
+// changes no factor and keeps the sums where their differences are exact to
+// float32 rounding: beside a term of -2^40 or an overflow they are not.
+constexpr float kDecayEnds = -104.f, kDecayCut = -256.f;
 // dt_raw: this lane's token, `valid` whether it exists.  Returns g_end.
 template <int L>
 __device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bool valid, float bias, int softplus,
@@ -287,7 +292,8 @@ __device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bo
         dt = dt_raw + bias;
         if (softplus) dt = ss_softplus(dt);
     }
-    const double g = wave_scan_f64((double)(dt * A));
+    const float a = dt * A;   // (NaN stays)
+    const double g = wave_scan_f64((double)(a < kDecayCut ? kDecayCut : a));
     const double end = wave_last_f64<L - 1>(g);
     if (lane < L) {
         const float h = (float)g;

@@ -390,6 +390,51 @@ def test_scan_backward_long_and_by_groups():
     check_bwd(r2, a, use, torch.bfloat16)
 
 
+def reset_case(dtype, dt, A):
+    """Every 21st token and the chunks' borders end all memory: a = dt A with
+    e^a = 0 in float32, x there scaled so that its own term is of the others'
+    size (dt x ~ 1)."""
+    a = scan_case([200, 3, 64], 2, 1, 64, 64, dtype, seed=31, amin=0.5, amax=2.0)
+    T = a["x"].shape[0]
+    at = np.unique(np.concatenate([np.arange(5, T, 21), [0, 63, 64, 127, 199, 200, 202, 266]]))
+    a["A"] = np.float32(a["A"] * A).astype(np.float64)
+    a["dt"] = np.float32(np.abs(a["dt"]) * 0.1 / A).astype(np.float64)
+    a["dt"][at] = np.float32(dt)
+    a["x"][at] = q(a["x"][at] / dt, dtype) if dt < 1e30 else 0.0
+    return a, at
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dt,A", [(1e4, 1.0), (2.0 ** 40, 1.0), (1e37, 100.0)])
+def test_scan_resets(dt, A, dtype):
+    """However large dt |A|, up to a product beyond float32, the tokens after
+    a reset keep their own decays."""
+    a, _ = reset_case(dtype, dt, A)
+    y, S = kda.ssm_chunk_fwd(dev(a["x"], dtype), dev(a["dt"]), dev(a["A"]), dev(a["B"], dtype), dev(a["C"], dtype), None,
+                             dev(a["S0"]), dev(a["cu"], torch.int32), softplus=False)
+    torch.cuda.synchronize()
+    ry, my, rS, mS, _, _ = oracle_scan(a, ("S0",), soft=False)
+    check("y", host(y), np.concatenate(ry), np.concatenate(my), dtype)
+    check("S_T", host(S), np.stack(rS), np.stack(mS), torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dt", [1e4, 2.0 ** 40])
+def test_scan_backward_resets(dt, dtype):
+    """A token that ends all memory has da = 0: grad_A = sum dt da is of the
+    other tokens' size, however large dt there is."""
+    a, at = reset_case(dtype, dt, 1.0)
+    use = ("S0", "gS")
+    r = run_bwd(a, dtype, use, soft=False)
+    torch.cuda.synchronize()
+    check_bwd(r, a, use, dtype, soft=False)
+    _, _, _, _, g, _ = oracle_scan(a, use, back=True, soft=False)
+    rest = dict(a, dt=a["dt"].copy())
+    rest["dt"][at] = 1.0   # the tolerance of tokens with ordinary steps only
+    _, _, _, _, _, m = oracle_scan(rest, use, back=True, soft=False)
+    check("grad_A", host(r[2]), sum(d["A"] for d in g), sum(d["A"] for d in m), torch.float32)
+
+
 def test_scan_backward_against_differences():
     """The directional derivative of the float32 forward pass.  A step h of
     2^-9 leaves h^2 of the third derivative and 2 y's rounding over h: a
