@@ -10,17 +10,20 @@
 
 namespace {
 
-// Workgroups of a launch: below 2^24, so that workgroups times 256 threads
-// stay below 2^32.
-constexpr int64_t kMaxWorkgroups = (1 << 24) - 1;   // of 256 threads: fewer than 2^32 threads per launch
+// Workgroups of a launch: fewer than 2^32 threads.
+constexpr int64_t kMaxWorkgroups = (1 << 24) - 1;   // of 256 threads
 constexpr int64_t kMaxWide = kMaxWorkgroups / 2;    // of 512
 constexpr int32_t kMaxTokens = 64;        // tokens per request in the step forms
-constexpr int64_t kScanFill = 512;        // chains that fill the 256 compute units (two each)
-constexpr int64_t kScanMinSeg = 256;      // shortest segment worth its state's traffic
+constexpr int64_t kScanUnits = 256;       // compute units
+constexpr int64_t kScanFill = 2 * kScanUnits;   // chains that fill them
+constexpr int64_t kScanLongSeg = 512, kScanMinSeg = 128;   // see scan_plan
 constexpr int64_t kScanMinCut = 3;        // segments from which two passes are shorter than one chain
 constexpr int64_t kScanAlign = 64;
 constexpr int64_t kVerifyFill = 2048;     // workgroups of the verification (512 to 2048: the same time)
-constexpr int64_t kGradFill = 512;        // workgroups of the gradient kernel that fill the GPU
+// Workgroups of the gradient kernel that fill the GPU (its LDS leaves room for
+// one per compute unit): 256 against 512 is 90 / 103 us for a backward pass of
+// 1024 tokens of 64 heads, 432 / 445 for 2 x 4096.
+constexpr int64_t kGradFill = 256;
 
 struct Span {
     uintptr_t lo, hi;      // [lo, hi)
@@ -95,9 +98,15 @@ int scan_shape(int in_dtype, int32_t n_seqs, int64_t T, int32_t H, int32_t G, in
 // Workgroups per chain set: two heads of 64 of one group, or one of 128.
 int64_t scan_blocks(int32_t H, int32_t G, int32_t P) { return (int64_t)G * ceil_div(H / G, 128 / P); }
 
-// How sequences are cut into segments: enough chains to fill the GPU, but no
-// segment so short that its state's traffic (two reads and writes of N x P
-// floats per head) weighs against its tokens'.
+// How sequences are cut into segments.  A chain alone on a compute unit takes
+// 4.3 us per chunk, two take 6.3 us together, and a segment costs its state's
+// traffic (two reads and writes of N x P floats per head): long segments for
+// two chains per unit, shorter ones for one, none below 128 tokens.  Measured
+// (64 heads of 64, one group, N 128, bf16, one sequence, cut against one
+// chain): 512 tokens 31.5 against 37.0 us, 1024 35.4 / 69, 2048 48 / 137, 8192
+// 117 / 531; segments of 64 tokens at 256 tokens 25.7 / 20.8.  Other lengths:
+// segments of 128 at 2048 tokens 54 us, of 256 at 1024 tokens 42, of 1024 at
+// 8192 tokens 122.
 struct ScanPlan {
     bool cut;
     int64_t seg_len, slots;
@@ -107,8 +116,10 @@ ScanPlan scan_plan(int32_t n_seqs, int64_t T, int64_t blocks, bool varlen, int64
     const int64_t rows = varlen ? T : n_seqs * T;
     const ScanPlan whole{false, T > 0 ? T : 1, n_seqs};
     if (n_seqs * blocks * dirs >= kScanFill) return whole;
-    int64_t len = ceil_div(rows * blocks * dirs, kScanFill);
-    if (len < kScanMinSeg) len = kScanMinSeg;
+    const int64_t work = rows * blocks * dirs;
+    int64_t len = ceil_div(work, kScanUnits);
+    len = len < kScanMinSeg ? kScanMinSeg : len > kScanLongSeg ? kScanLongSeg : len;
+    if (len < ceil_div(work, kScanFill)) len = ceil_div(work, kScanFill);
     const int64_t segs = ceil_div(T, len);
     if (segs < kScanMinCut) return whole;
     if (!varlen) len = ceil_div(T, segs);

@@ -32,7 +32,7 @@
  *     later ones of that head's sequence (not other sequences).
  *   - Token rows: tensors with a `_stride` argument may be parts of wider
  *     rows; the argument is the number of elements from one token row to the
- *     next (a multiple of 16 bytes, below 2^23 elements), so x, B and C can
+ *     next (a multiple of 16 bytes, at most KDA_SSM_MAX_STRIDE elements), so x, B and C can
  *     be the channels that one convolution put out.  Row b * T + t holds
  *     token t of sequence b; the row itself is contiguous.  Tensors without
  *     one are contiguous.
