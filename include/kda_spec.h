@@ -1,10 +1,10 @@
 /*
  * kda_spec.h -- verification of drafted tokens against the target's
  * probabilities (MI355X, gfx950): the step of speculative decoding between
- * the model's outputs for the drafts and the next call's replay.  Its
- * n_accepted is the n_replay of the next kda_recurrent_fwd,
- * kda_ssm_recurrent_fwd and kda_ssm_conv_step.  Same library and conventions
- * as kda.h.
+ * the model's outputs for the drafts and the next call's replay.  The next
+ * kda_recurrent_fwd, kda_ssm_recurrent_fwd and kda_ssm_conv_step replay the
+ * token before the drafts, if it ran with them, and the accepted drafts:
+ * n_replay is n_accepted + 1.  Same library and conventions as kda.h.
  */
 #ifndef KDA_SPEC_H_
 #define KDA_SPEC_H_

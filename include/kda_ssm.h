@@ -32,10 +32,10 @@
  *     later ones of that head's sequence (not other sequences).
  *   - Token rows: tensors with a `_stride` argument may be parts of wider
  *     rows; the argument is the number of elements from one token row to the
- *     next (a multiple of 16 bytes, at most KDA_SSM_MAX_STRIDE elements), so x, B and C can
- *     be the channels that one convolution put out.  Row b * T + t holds
- *     token t of sequence b; the row itself is contiguous.  Tensors without
- *     one are contiguous.
+ *     next (a multiple of 16 bytes, at most KDA_SSM_MAX_STRIDE elements), so
+ *     x, B and C can be the channels that one convolution put out.  Row
+ *     b * T + t holds token t of sequence b; the row itself is contiguous.
+ *     Tensors without one are contiguous.
  *   - Packed batches: cu_seqlens int32 [n_seqs + 1] on the device, as in
  *     kda.h, with T the number of token rows.  Rows before cu_seqlens[0] and
  *     from cu_seqlens[n_seqs] on belong to no sequence: they affect nothing,
@@ -106,7 +106,7 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
                      size_t workspace_bytes, hipStream_t stream);
 
 /*
- * Scan over whole sequences, in chunks of 64 tokens.
+ * Scan over whole sequences, in chunks of 64 tokens (32 with KDA_F32).
  *   x [rows, H, P] (x_stride), B, C [rows, G, N] (B_stride, C_stride),
  *   dt [rows, H], dt_bias [H] or NULL, A [H], D [H] or NULL,
  *   S0 [n_seqs, H, N, P] or NULL (zeros), y [rows, H, P] contiguous,
@@ -119,10 +119,12 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
  * (or NULL) every sequence runs as one chain, with the same result up to
  * rounding.
  * Numerics: decay sums in float64 within a chunk, everything else
- * accumulated in float32.  The products run on bf16 matrix cores; float32
- * operands (and, with KDA_F32, the inputs) enter as sums of two or three
- * bf16 parts, so that S_T is accurate to float32 rounding and y to its own
- * type.
+ * accumulated in float32.  The products run on bf16 matrix cores.  The state
+ * update takes its float32 operands (and, with KDA_F32, the inputs) as sums
+ * of three bf16 parts, so S_T is accurate to float32 rounding; so is y with
+ * KDA_F32.  With KDA_BF16, S in S^T C and the weighted products C . B are
+ * rounded to bf16 once each, a half step of the output's type.
+ * A token with dt A < -104 (a reset) ends all memory.
  */
 size_t kda_ssm_chunk_fwd_workspace_bytes(int32_t n_seqs, int64_t T, int32_t H, int32_t G,
                                          int32_t N, int32_t P, int varlen);

@@ -697,6 +697,116 @@ def test_speculative_decoding_loop():
         check("S", host(S[i]), ref, mag, torch.float32)
 
 
+def test_captured_decode_step():
+    """Convolution, scan and verification captured as one graph: each replay
+    reads the accepted counts that the replay before it left on the device
+    and updates cache and state in place, as the eager calls do, bitwise."""
+    H, G, N, P, K, V, n = 4, 2, 64, 64, 3, 1001, 3
+    c, T = H * P + 2 * G * N, K + 1
+    gen = torch.Generator(device="cuda").manual_seed(50)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)   # noqa: E731
+    w, bias, A = rnd(c, 4) / 2, rnd(c), -torch.rand(H, device="cuda") - 0.1
+    raw, dt = rnd(2, n, T, c).bfloat16(), rnd(2, n, T, H)
+    p, un = torch.softmax(rnd(n, T, V), -1), torch.rand(n, device="cuda")
+    u = torch.tensor([[0.0, 0, 0], [0, 1, 0], [1, 0, 0]], device="cuda")   # 0: the draft stands, 1: it does not
+    drafts = torch.zeros(n, K, dtype=torch.int32, device="cuda")
+
+    def split(t):
+        return (t[..., :H * P].unflatten(-1, (H, P)), t[..., H * P:H * P + G * N].unflatten(-1, (G, N)),
+                t[..., H * P + G * N:].unflatten(-1, (G, N)))
+
+    def step(st):
+        xbc = kda.ssm_conv_step(raw[0], w, bias, st["cache"], replay=raw[1], n_replay=st["acc"], commit=False)
+        x, B, C = split(xbc)
+        ox, oB, _ = split(st["old"])
+        y = kda.ssm_recurrent_fwd(x, dt[0], A, B, C, st["S"], replay=(ox, dt[1], oB), n_replay=st["acc"], commit=False)
+        acc, tok = kda.verify_drafts(p, drafts, u, un)
+        st["acc"].copy_(acc)
+        st["old"].copy_(xbc)
+        return y, tok
+
+    def fresh():
+        return dict(cache=torch.ones(n, 3, c, device="cuda"), S=torch.ones(n, H, N, P, device="cuda"),
+                    acc=torch.ones(n, dtype=torch.int32, device="cuda"),
+                    old=torch.zeros(n, T, c, device="cuda", dtype=torch.bfloat16))
+
+    warm = fresh()
+    step(warm)
+    torch.cuda.synchronize()
+    a, b = fresh(), fresh()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(a)
+    counts = set()
+    for i in range(4):
+        for t in (raw, dt, p):
+            t.copy_(t.roll(1, -1))
+        u.copy_(u.roll(1, 0))
+        drafts.copy_(p[:, :K].argsort(-1, descending=True)[..., i].int())
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        want = step(b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+        assert all(torch.equal(a[k], b[k]) for k in a)
+        counts |= set(a["acc"].tolist())
+    assert counts == {0, 1, 3}
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^32 bytes (and elements past 2^31): what stands
+    at their end is what the same call gives for it alone."""
+    gen = torch.Generator(device="cuda").manual_seed(51)
+    rnd = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)   # noqa: E731
+    # convolution, packed: one long sequence and a last one of 70 tokens
+    T, c, t = 270000, 8192, 70
+    x, gy, w = rnd(T, c), rnd(T, c), torch.randn(c, 4, device="cuda", generator=gen)
+    cu = torch.tensor([0, T - t, T], dtype=torch.int32, device="cuda")
+    one = torch.tensor([0, t], dtype=torch.int32, device="cuda")
+    tail = lambda v: v[T - t:].clone()   # noqa: E731
+    assert torch.equal(kda.ssm_conv_fwd(x, w, cu_seqlens=cu)[T - t:], kda.ssm_conv_fwd(tail(x), w, cu_seqlens=one))
+    gx = kda.ssm_conv_bwd(x, w, None, gy, cu_seqlens=cu)[0]
+    assert torch.equal(gx[T - t:], kda.ssm_conv_bwd(tail(x), w, None, tail(gy), cu_seqlens=one)[0])
+    del gx, gy
+    # scan, the same rows as 128 heads of 64: chunks of one sequence are the
+    # same products whatever stands before it
+    H = 128
+    x = x.view(T, H, 64)
+    B, C = rnd(T, 1, 64), rnd(T, 1, 64)
+    dt, A = torch.rand(T, H, device="cuda", generator=gen), -torch.rand(H, device="cuda", generator=gen) - 0.05
+    y, S = kda.ssm_chunk_fwd(x, dt, A, B, C, cu_seqlens=cu, sequence_parallel=False)
+    y1, S1 = kda.ssm_chunk_fwd(tail(x), tail(dt), A, tail(B), tail(C), cu_seqlens=one, sequence_parallel=False)
+    assert torch.equal(y[T - t:], y1) and torch.equal(S[1], S1[0])
+    r = kda.ssm_chunk_bwd(x, dt, A, B, C, None, None, y, cu_seqlens=cu)
+    r1 = kda.ssm_chunk_bwd(tail(x), tail(dt), A, tail(B), tail(C), None, None, y1, cu_seqlens=one)
+    assert torch.equal(r[0][T - t:], r1[0])
+    torch.testing.assert_close(r[1][T - t:], r1[1], rtol=1e-5, atol=1e-5 * float(r1[1].abs().max()))
+    for k in (3, 4):   # (the heads' partial sums meet in another order: two roundings to bf16)
+        torch.testing.assert_close(r[k][T - t:].float(), r1[k].float(), rtol=2 ** -7, atol=1e-5 * float(r1[k].abs().max()))
+    del x, y, r
+    # states of 4.6 GB
+    n, H = 1100, 128
+    S = torch.empty(n, H, 128, 64, device="cuda").normal_(generator=gen)
+    x, dt = rnd(n, 2, H, 64), torch.rand(n, 2, H, device="cuda", generator=gen)
+    B, C = rnd(n, 2, 1, 128), rnd(n, 2, 1, 128)
+    last = S[n - 1:].clone()
+    y = kda.ssm_recurrent_fwd(x, dt, A, B, C, S)
+    y1 = kda.ssm_recurrent_fwd(x[n - 1:], dt[n - 1:], A, B[n - 1:], C[n - 1:], last)
+    assert torch.equal(y[n - 1:], y1) and torch.equal(S[n - 1:], last)
+    del S
+    # 160 requests of 17 rows of 10^6 probabilities
+    n, K, V = 160, 16, 10 ** 6
+    p = torch.empty(n, K + 1, V, dtype=torch.bfloat16, device="cuda").uniform_(generator=gen)
+    d = torch.randint(0, V, (n, K), dtype=torch.int32, device="cuda", generator=gen)
+    u, un = torch.rand(n, K, device="cuda", generator=gen) * 0.02, torch.rand(n, device="cuda", generator=gen)
+    u[n - 1] = 0
+    na, tok = kda.verify_drafts(p, d, u, un)
+    na1, tok1 = kda.verify_drafts(p[n - 1:].clone(), d[n - 1:].clone(), u[n - 1:].clone(), un[n - 1:].clone())
+    torch.cuda.synchronize()
+    assert torch.equal(na[n - 1:], na1) and torch.equal(tok[n - 1:], tok1) and int(na1) == K
+
+
 def test_python_refusals():
     x = torch.zeros(2, 8, 4, 64, device="cuda")
     dt, A, B = torch.zeros(2, 8, 4, device="cuda"), torch.zeros(4, device="cuda"), torch.zeros(2, 8, 1, 64, device="cuda")
