@@ -73,10 +73,12 @@ int check_stride(int64_t stride, int64_t width, int64_t es) {
 }
 
 // Token rows of a batch, bounded so that no product of sizes below can wrap.
-int count_rows(const int32_t* cu, int32_t n_seqs, int64_t T, int64_t* rows) {
-    if (cu) *rows = T;
+constexpr int64_t kMaxRows = (int64_t)1 << 36, kMaxState = (int64_t)1 << 56;
+int count_rows(bool varlen, int32_t n_seqs, int64_t T, int64_t* rows) {
+    if (T > kMaxRows) return KDA_ERR_TOO_LARGE;
+    if (varlen) *rows = T;
     else if (!mul_ok((int64_t)n_seqs, T, rows)) return KDA_ERR_TOO_LARGE;
-    return *rows <= ((int64_t)1 << 38) ? KDA_OK : KDA_ERR_TOO_LARGE;
+    return *rows <= kMaxRows ? KDA_OK : KDA_ERR_TOO_LARGE;
 }
 
 int conv_shape(int in_dtype, int32_t n_seqs, int64_t T, int32_t channels, int32_t width) {
@@ -92,7 +94,7 @@ int scan_shape(int in_dtype, int32_t n_seqs, int64_t T, int32_t H, int32_t G, in
         (P != 64 && P != 128))
         return KDA_ERR_BAD_SHAPE;
     if (H > KDA_MAX_HEADS || (int64_t)H * P > KDA_SSM_MAX_STRIDE) return KDA_ERR_TOO_LARGE;
-    return KDA_OK;
+    return (int64_t)n_seqs * H <= kMaxState / ((int64_t)N * P) ? KDA_OK : KDA_ERR_TOO_LARGE;
 }
 
 // Workgroups per chain set: two heads of 64 of one group, or one of 128.
@@ -149,6 +151,7 @@ bool bwd_plan(int in_dtype, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, 
     if (!mul_ok(b->slots * heads, (int64_t)N * P, &st) || !mul_ok(b->scan.slots * heads, (int64_t)N * P, &seg) ||
         !mul_ok(2 * (int64_t)b->blocks * groups * N, rows, &part))
         return false;
+    if (st > INT64_MAX / 64 || seg > INT64_MAX / 64 || part > INT64_MAX / 64) return false;
     if (!b->scan.cut) seg = 0;
     if (b->blocks == 1) part = 0;
     const int64_t four = 3;   // every array starts on 16 bytes
@@ -161,7 +164,7 @@ bool bwd_plan(int in_dtype, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, 
     b->seg_decay[1] = b->seg_decay[0] + (b->scan.cut ? b->scan.slots * heads : 0);
     b->sums = (b->seg_decay[1] + (b->scan.cut ? b->scan.slots * heads : 0) + four) & ~four;
     b->total = b->sums + ((b->slots * heads * 3 + 4 + four) & ~four);
-    return b->total <= INT64_MAX / 8 && st <= INT64_MAX / 16 && seg <= INT64_MAX / 16 && part <= INT64_MAX / 16;
+    return b->total <= INT64_MAX / 8;
 }
 
 }  // namespace
@@ -175,7 +178,7 @@ int kda_ssm_conv_fwd(const void* x, int64_t x_stride, int in_dtype, const float*
     int rc = conv_shape(in_dtype, n_seqs, T, channels, width);
     if (rc) return rc;
     int64_t rows = 0;
-    if ((rc = count_rows(cu_seqlens, n_seqs, T, &rows))) return rc;
+    if ((rc = count_rows(cu_seqlens != nullptr, n_seqs, T, &rows))) return rc;
     if (n_seqs == 0) return KDA_OK;
     if (ceil_div(rows, 32) * ceil_div(channels, 256) > kMaxWorkgroups ||
         ceil_div((int64_t)n_seqs * channels, 256) > kMaxWorkgroups)
@@ -260,7 +263,7 @@ int kda_ssm_conv_step(const void* x, int64_t x_stride, int in_dtype, const float
 }
 
 size_t kda_ssm_conv_bwd_workspace_bytes(int64_t rows, int32_t channels, int32_t width) {
-    if (rows < 0 || rows > ((int64_t)1 << 38) || conv_shape(KDA_BF16, 0, 0, channels, width)) return 0;
+    if (rows < 0 || rows > kMaxRows || conv_shape(KDA_BF16, 0, 0, channels, width)) return 0;
     const int64_t parts = kda::conv_bwd_parts(rows, channels);
     int64_t n = 0;
     if (!mul_ok(parts, (int64_t)(width + 1) * channels * 4, &n)) return 0;
@@ -276,7 +279,7 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
     int rc = conv_shape(in_dtype, n_seqs, T, channels, width);
     if (rc) return rc;
     int64_t rows = 0;
-    if ((rc = count_rows(cu_seqlens, n_seqs, T, &rows))) return rc;
+    if ((rc = count_rows(cu_seqlens != nullptr, n_seqs, T, &rows))) return rc;
     if (n_seqs == 0) rows = 0;
     if (ceil_div(rows, 32) * ceil_div(channels, 256) > kMaxWorkgroups ||
         ceil_div((int64_t)n_seqs * channels, 256) > kMaxWorkgroups)
@@ -333,9 +336,8 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
 size_t kda_ssm_chunk_fwd_workspace_bytes(int32_t n_seqs, int64_t T, int32_t H, int32_t G,
                                          int32_t N, int32_t P, int varlen) {
     if (scan_shape(KDA_BF16, n_seqs, T, H, G, N, P)) return 0;
-    int64_t rows = T;
-    if (!varlen && (!mul_ok((int64_t)n_seqs, T, &rows) || rows > ((int64_t)1 << 38))) return 0;
-    if (rows > ((int64_t)1 << 38)) return 0;
+    int64_t rows = 0;
+    if (count_rows(varlen != 0, n_seqs, T, &rows)) return 0;
     const ScanPlan s = scan_plan(n_seqs, T, scan_blocks(H, G, P), varlen != 0, 1);
     return s.cut ? (size_t)s.slots * H * ((size_t)N * P + 1) * 4 : 0;
 }
@@ -349,7 +351,7 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* B, int64_t B_
     int rc = scan_shape(in_dtype, n_seqs, T, H, G, N, P);
     if (rc) return rc;
     int64_t rows = 0;
-    if ((rc = count_rows(cu_seqlens, n_seqs, T, &rows))) return rc;
+    if ((rc = count_rows(cu_seqlens != nullptr, n_seqs, T, &rows))) return rc;
     if (n_seqs == 0) return KDA_OK;
     if ((int64_t)n_seqs * H > INT32_MAX) return KDA_ERR_TOO_LARGE;
     if (!A || (rows > 0 && (!x || !B || !C || !dt || !y))) return KDA_ERR_NULL_POINTER;
@@ -425,9 +427,8 @@ size_t kda_ssm_chunk_bwd_workspace_bytes(int in_dtype, int32_t n_seqs, int64_t T
                                          int32_t G, int32_t N, int32_t P, int varlen,
                                          int32_t groups) {
     if (scan_shape(in_dtype, n_seqs, T, H, G, N, P) || groups < 1) return 0;
-    int64_t rows = T;
-    if (!varlen && !mul_ok((int64_t)n_seqs, T, &rows)) return 0;
-    if (rows > ((int64_t)1 << 38)) return 0;
+    int64_t rows = 0;
+    if (count_rows(varlen != 0, n_seqs, T, &rows)) return 0;
     BwdPlan b;
     if (!bwd_plan(in_dtype, n_seqs, T, rows, H, G, N, P, varlen != 0, groups < G ? groups : G, &b)) return 0;
     return (size_t)b.total * 4;
@@ -445,7 +446,7 @@ int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_
     int rc = scan_shape(in_dtype, n_seqs, T, H, G, N, P);
     if (rc) return rc;
     int64_t rows = 0;
-    if ((rc = count_rows(cu_seqlens, n_seqs, T, &rows))) return rc;
+    if ((rc = count_rows(cu_seqlens != nullptr, n_seqs, T, &rows))) return rc;
     if (n_seqs == 0) rows = 0;
     if ((int64_t)n_seqs * H > INT32_MAX) return KDA_ERR_TOO_LARGE;
     if (!A || !grad_A || (rows > 0 && (!x || !B || !C || !dt || !grad_y || !grad_x || !grad_B || !grad_C || !grad_dt)))
