@@ -90,8 +90,9 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
         // nothing follows the last segment (the full pass gives its final state)
         if (MODE == kLocal && (rev ? s.r0 == s.start : s.r1 == s.end)) return;
     } else {
-        const SsmRange r = ssm_range(p.cu, p.rows, p.T, slot);
-        s = SsmPiece{slot, 0, r.start, r.end, r.start, r.end};
+        const int64_t n = p.cu && p.n_seqs <= 64 ? ssm_longest(p.cu, p.rows, p.n_seqs, (int)slot) : slot;
+        const SsmRange r = ssm_range(p.cu, p.rows, p.T, n);
+        s = SsmPiece{n, 0, r.start, r.end, r.start, r.end};
     }
 
     // State in accumulator registers.  With outputs: element (tile m = 2 j + o,

@@ -295,6 +295,24 @@ def test_scan_ragged_segments():
     check("S_T", host(S), np.stack(rS), np.stack(mS), torch.float32)
 
 
+@pytest.mark.parametrize("n", [64, 65, 200])
+def test_scan_many_short_sequences(n):
+    """Around the number of sequences up to which chains start with the
+    longest, forward and backward."""
+    lens = [int(v) for v in np.random.default_rng(n).integers(0, 70, n) // np.random.default_rng(n + 1).integers(1, 12, n)]
+    lens[3] = lens[5] = 70
+    a = scan_case(lens, 2, 1, 64, 64, torch.bfloat16, seed=33)
+    use = ("S0", "gS")
+    y, S = kda.ssm_chunk_fwd(dev(a["x"], torch.bfloat16), dev(a["dt"]), dev(a["A"]), dev(a["B"], torch.bfloat16),
+                             dev(a["C"], torch.bfloat16), None, dev(a["S0"]), dev(a["cu"], torch.int32))
+    r = run_bwd(a, torch.bfloat16, use)
+    torch.cuda.synchronize()
+    ry, my, rS, mS, _, _ = oracle_scan(a, ("S0",))
+    check("y", host(y), np.concatenate(ry), np.concatenate(my), torch.bfloat16)
+    check("S_T", host(S), np.stack(rS), np.stack(mS), torch.float32)
+    check_bwd(r, a, use, torch.bfloat16)
+
+
 @pytest.mark.parametrize("case", ["strong", "none", "mixed"])
 def test_scan_extreme_decay(case):
     """Decays that wipe the state out within a token, none at all, and a huge
