@@ -200,19 +200,18 @@ struct Stager {
     static constexpr int PPR = COLS / EV;                 // pieces per row
     static constexpr int PER = L * PPR / THREADS;
     static constexpr int PARTS = sizeof(InT) == 2 ? 1 : 3;
-    static_assert(L * PPR % THREADS == 0, "whole pieces per thread");
+    static constexpr int ROWS = THREADS / PPR;            // rows per piece of all threads
+    static_assert(L * PPR % THREADS == 0 && THREADS % PPR == 0, "whole pieces per thread, whole rows");
     u32x4 r[PER];
 
     // base: first row's first column; cols: columns that exist (the others read as zero)
     __device__ __forceinline__ void load(const InT* base, int64_t stride, int valid, int cols) {
-        const int bytes = valid > 0 ? (int)((valid - 1) * stride + cols) * (int)sizeof(InT) : 0;
-        const auto rs = make_rsrc(base, bytes);
+        const int row = (int)threadIdx.x / PPR, c = ((int)threadIdx.x - row * PPR) * EV;
+        const uint32_t off = c < cols ? (uint32_t)(row * (int)stride + c) * (uint32_t)sizeof(InT) : 0x80000000u;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int idx = (int)threadIdx.x + THREADS * j;
-            const int row = idx / PPR, c = (idx - row * PPR) * EV;
-            const uint32_t off = row < valid && c < cols ? (uint32_t)(row * (int)stride + c) * (uint32_t)sizeof(InT)
-                                                         : 0x80000000u;
+        for (int j = 0; j < PER; ++j) {   // (a buffer of the rows that exist: further ones read as zero)
+            const int left = valid - j * ROWS;
+            const auto rs = make_rsrc(base + j * ROWS * stride, left > 0 ? ((left - 1) * (int)stride + cols) * (int)sizeof(InT) : 0);
             r[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
         }
     }

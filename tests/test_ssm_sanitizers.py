@@ -7,7 +7,8 @@ import shutil
 
 import pytest
 
-from test_sanitizers import ROOT, SAN, _build_and_run
+_san = pytest.importorskip("test_sanitizers")   # (absent where only GPU tests are)
+ROOT, SAN, _build_and_run = _san.ROOT, _san.SAN, _san._build_and_run
 
 
 @pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
