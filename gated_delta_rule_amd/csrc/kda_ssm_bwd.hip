@@ -21,9 +21,14 @@
 // A workgroup runs one chunk for several heads of a group in turn: B, C and
 // the tiles of G stay on chip, and dB and dC are summed over the heads in
 // registers, so that only one partial sum per workgroup goes through memory.
-// S and R come straight from memory into operand
-// registers, each row once.  Bound by the traffic of S and R, which the walks
-// wrote: 16 N P bytes per chunk and head against 6 L P of x, dy and dx.
+// S and R come straight from memory into operand registers, each row once and
+// one head ahead; R's bf16 rounding for dx goes through LDS.
+//
+// Measured (MI355X, 2 x 4096 tokens, 64 heads of 64, N 128, bf16): 210 us for
+// 0.74 GB, 0.54 GB of them S and R.  Bound by vector instructions: 14 000
+// cycles per chunk and head, a third of them in the two products with S and R
+// (their float32 operands are split into three bf16 parts), 1 100 in requests,
+// matrix cores 0.16 busy.
 #include "kda_ssm_tile.h"
 
 #include <type_traits>

@@ -11,7 +11,9 @@
 // the same for all lanes, so sequence boundaries cost scalar instructions
 // only.  Eight channels per lane and all rows requested at once, the first
 // form, needs 180 to 400 registers: 42 us forward and 121 us backward at 8192
-// rows of 4352 channels.
+// rows of 4352 channels, against 32 (4.4 TB/s) and 62 us.  Backward, about 30
+// vector instructions per element, two of them transcendental, take 40 us by
+// themselves.
 #include "kda_device.h"
 #include "kda_ssm_launch.h"
 
