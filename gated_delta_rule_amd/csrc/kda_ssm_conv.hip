@@ -11,11 +11,13 @@
 // the same for all lanes, so sequence boundaries cost scalar instructions
 // only.  Eight channels per lane and all rows requested at once, the first
 // form, needs 180 to 400 registers: 42 us forward and 121 us backward at 8192
-// rows of 4352 channels, against 32 (4.4 TB/s) and 62 us.  Backward, about 30
-// vector instructions per element, two of them transcendental, take 40 us by
-// themselves.
+// rows of 4352 channels, against 32 (4.4 TB/s) and 57 us (62 with a branch per
+// channel).  Backward, about 30 vector instructions per element, two of them
+// transcendental, take 40 us by themselves.
 #include "kda_device.h"
 #include "kda_ssm_launch.h"
+
+#include <type_traits>
 
 namespace kda {
 
@@ -310,16 +312,14 @@ __global__ __launch_bounds__(CV_THREADS) void conv_bwd_kernel(ConvBwdParams q) {
     if (live && r0 < p.rows) {
         const int64_t r1 = r0 + q.rows_per_wave < p.rows ? r0 + q.rows_per_wave : p.rows;
         const int64_t r2 = r1 + W - 1;
-        typename Vec<InT>::raw xa[CB_AHEAD], ga[CB_AHEAD], xn[CB_AHEAD], gn[CB_AHEAD];
-        auto request = [&](int64_t r) {
-#pragma unroll
-            for (int i = 0; i < CB_AHEAD; ++i) {
-                const int64_t k = r + i < p.rows ? r + i : p.rows - 1;
-                xa[i] = Vec<InT>::fetch(p.x, k * p.x_stride + c0);
-                ga[i] = Vec<InT>::fetch(q.gy, k * q.gy_stride + c0);
-            }
+        typename Vec<InT>::raw xa[CB_AHEAD], ga[CB_AHEAD];   // the next rows, in order
+        auto request = [&](int i, int64_t row) {
+            const int64_t k = row < p.rows ? row : p.rows - 1;
+            xa[i] = Vec<InT>::fetch(p.x, k * p.x_stride + c0);
+            ga[i] = Vec<InT>::fetch(q.gy, k * q.gy_stride + c0);
         };
-        request(r0);
+#pragma unroll
+        for (int i = 0; i < CB_AHEAD; ++i) request(i, r0 + i);
         float w[W][4], b[4];
         load_w<W, 4>(p.w, c0, w);
 #pragma unroll
@@ -333,59 +333,71 @@ __global__ __launch_bounds__(CV_THREADS) void conv_bwd_kernel(ConvBwdParams q) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) dx[d][c] = 0.f;
         uint32_t mine = 0;   // bit d: the row d before the current one is of a sequence and this wave's
-        for (int64_t r = r0; r < r2; r += CB_AHEAD) {
+        // One row.  INSIDE: it, the W - 1 rows before it and this wave's rows
+        // are of one sequence and the activation is on, which nearly all rows
+        // are: no branch per channel then.
+        auto step = [&](auto inside, int i, int64_t row) {
+            constexpr bool INSIDE = decltype(inside)::value;
+            const bool in = INSIDE || (row < p.rows && k.at(p, row));
+            if (!INSIDE && in && row == k.s.start) {
 #pragma unroll
-            for (int i = 0; i < CB_AHEAD; ++i) {
-                xn[i] = xa[i];
-                gn[i] = ga[i];
+                for (int j = 0; j < W - 1; ++j) input_at<InT, W>(p, k.s, j - (W - 1), c0, win[j]);
             }
-            if (r + CB_AHEAD < r2) request(r + CB_AHEAD);
+            const bool act = INSIDE || p.activation;
+            mine = mine << 1 | (INSIDE || (in && row < r1) ? 1u : 0u);
+            // rows before this one that this row's z reaches (none outside its sequence)
+            const int reach = INSIDE ? W - 1 : in ? (row - k.s.start < W - 1 ? (int)(row - k.s.start) : W - 1) : -1;
+            float x[4], g[4];
+            Vec<InT>::open(xa[i], x);
+            Vec<InT>::open(ga[i], g);
+            request(i, row + CB_AHEAD < r2 ? row + CB_AHEAD : r2);
 #pragma unroll
-            for (int i = 0; i < CB_AHEAD; ++i) {
-                const int64_t row = r + i;
-                if (row >= r2) break;
-                const bool in = row < p.rows && k.at(p, row);
-                if (in && row == k.s.start) {
+            for (int c = 0; c < 4; ++c) {
+                float dz = g[c];
+                if (act) {
+                    float z = b[c];
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) input_at<InT, W>(p, k.s, j - (W - 1), c0, win[j]);
+                    for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
+                    z = fmaf(w[W - 1][c], x[c], z);
+                    const float sg = cv_sigm(z);
+                    dz = g[c] * sg * fmaf(z, 1.f - sg, 1.f);
                 }
-                mine = mine << 1 | (in && row < r1 ? 1u : 0u);
-                // rows before this one that this row's z reaches (none outside its sequence)
-                const int reach = in ? (row - k.s.start < W - 1 ? (int)(row - k.s.start) : W - 1) : -1;
-                float x[4], g[4];
-                Vec<InT>::open(xn[i], x);
-                Vec<InT>::open(gn[i], g);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float dz = g[c];
-                    if (p.activation) {
-                        float z = b[c];
+                for (int d = W - 1; d >= 1; --d)
+                    dx[d][c] = INSIDE || d <= reach ? fmaf(w[W - 1 - d][c], dz, dx[d - 1][c]) : dx[d - 1][c];
+                dx[0][c] = w[W - 1][c] * dz;
+                if (INSIDE || (mine & 1)) {
 #pragma unroll
-                        for (int j = 0; j < W - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
-                        z = fmaf(w[W - 1][c], x[c], z);
-                        const float sg = cv_sigm(z);
-                        dz = g[c] * sg * fmaf(z, 1.f - sg, 1.f);
-                    }
-                    if (reach == W - 1) {
-#pragma unroll
-                        for (int d = W - 1; d >= 1; --d) dx[d][c] = fmaf(w[W - 1 - d][c], dz, dx[d - 1][c]);
-                    } else {
-#pragma unroll
-                        for (int d = W - 1; d >= 1; --d)
-                            dx[d][c] = d <= reach ? fmaf(w[W - 1 - d][c], dz, dx[d - 1][c]) : dx[d - 1][c];
-                    }
-                    dx[0][c] = w[W - 1][c] * dz;
-                    if (mine & 1) {
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) gw[j][c] = fmaf(dz, win[j][c], gw[j][c]);
-                        gw[W - 1][c] = fmaf(dz, x[c], gw[W - 1][c]);
-                        gw[W][c] += dz;
-                    }
-#pragma unroll
-                    for (int j = 0; j + 1 < W - 1; ++j) win[j][c] = win[j + 1][c];
-                    win[W - 2][c] = x[c];
+                    for (int j = 0; j < W - 1; ++j) gw[j][c] = fmaf(dz, win[j][c], gw[j][c]);
+                    gw[W - 1][c] = fmaf(dz, x[c], gw[W - 1][c]);
+                    gw[W][c] += dz;
                 }
-                if (mine >> (W - 1) & 1) Vec<InT>::store(q.gx, (row - (W - 1)) * p.channels + c0, dx[W - 1]);
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) win[j][c] = win[j + 1][c];
+                win[W - 2][c] = x[c];
+            }
+            if (mine >> (W - 1) & 1) Vec<InT>::store(q.gx, (row - (W - 1)) * p.channels + c0, dx[W - 1]);
+        };
+        for (int64_t r = r0; r < r2;) {
+            if (p.activation && r >= k.s.start + W - 1 && r + CB_AHEAD <= k.s.end && r + CB_AHEAD <= r1) {
+#pragma unroll
+                for (int i = 0; i < CB_AHEAD; ++i) {
+                    step(std::true_type{}, i, r + i);
+                    __builtin_amdgcn_sched_barrier(0);   // (four rows at once: 184 registers)
+                }
+                r += CB_AHEAD;
+            } else {
+                step(std::false_type{}, 0, r);
+                const auto x0 = xa[0];
+                const auto g0 = ga[0];
+#pragma unroll
+                for (int i = 0; i + 1 < CB_AHEAD; ++i) {
+                    xa[i] = xa[i + 1];
+                    ga[i] = ga[i + 1];
+                }
+                xa[CB_AHEAD - 1] = x0;
+                ga[CB_AHEAD - 1] = g0;
+                ++r;
             }
         }
     }
