@@ -51,8 +51,13 @@ def _check_rows(t, name, lead, tail, dtype, dev):
     import torch
     if not isinstance(t, torch.Tensor):
         raise KDAError(f"{name} must be a torch.Tensor")
-    if t.is_contiguous() and t.is_cuda and t.dtype == dtype and t.device == dev and t.shape == lead + tail:
-        return math.prod(tail)
+    if t.get_device() == dev.index and t.dtype is dtype and t.shape == lead + tail:   # the usual rows
+        if t.is_contiguous():
+            return math.prod(tail)
+        st, nl = t.stride(), len(lead)
+        if lead[-1] > 1 and st[-1] == 1 and (len(tail) == 1 or tail[0] == 1 or st[-2] == tail[1]) and \
+                (nl == 1 or lead[0] == 1 or st[0] == lead[1] * st[1]) and t.numel():
+            return st[nl - 1]
     if not t.is_cuda:
         raise KDAError(f"{name} must be a device tensor")
     if t.device != dev:
@@ -104,7 +109,11 @@ def _lead(x, tail_dims, cu_seqlens, name, dev):
 
 def _check_shape(t, name, shape, dev, dtype=None):
     import torch
-    _check(t, name, dtype or torch.float32, dev)
+    dtype = dtype or torch.float32
+    if t.__class__ is torch.Tensor and t.get_device() == dev.index and t.dtype is dtype and t.shape == shape and \
+            t.is_contiguous():
+        return
+    _check(t, name, dtype, dev)
     if tuple(t.shape) != tuple(shape):
         raise KDAError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
@@ -115,6 +124,12 @@ def _workspace(workspace, need, dev):
         return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _check(workspace, "workspace", None, dev)
     return workspace
+
+
+def _like(t):
+    """An uninitialised contiguous tensor like t (half the time of torch.empty)."""
+    import torch
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _nbytes(t):
@@ -150,7 +165,7 @@ def ssm_conv_fwd(x, w, bias=None, cache=None, cu_seqlens=None, *, activation=Tru
     if cache is not None:
         _check_shape(cache, "cache", (n_seqs, width - 1, channels), dev)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = _like(x)
     else:
         _check_shape(y, "y", x.shape, dev, x.dtype)
     with _on(dev):
@@ -184,7 +199,7 @@ def ssm_conv_step(x, w, bias, cache, *, replay=None, n_replay=None, commit=True,
     if n_replay is not None:
         _check_shape(n_replay, "n_replay", (B,), dev, torch.int32)
     if y is None:
-        y = torch.empty((B, T, channels), dtype=x.dtype, device=dev)
+        y = _like(x)
     else:
         _check_shape(y, "y", (B, T, channels), dev, x.dtype)
     with _on(dev):
@@ -209,10 +224,9 @@ def ssm_conv_bwd(x, w, bias, grad_y, cache=None, cu_seqlens=None, *, activation=
     gs = _check_rows(grad_y, "grad_y", lead, (channels,), x.dtype, dev)
     if cache is not None:
         _check_shape(cache, "cache", (n_seqs, width - 1, channels), dev)
-    gx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    gw = torch.empty((channels, width), dtype=torch.float32, device=dev)
-    gb = None if bias is None else torch.empty(channels, dtype=torch.float32, device=dev)
-    gc = None if cache is None else torch.empty_like(cache)
+    gx, gw = _like(x), _like(w)
+    gb = None if bias is None else _like(bias)
+    gc = None if cache is None else _like(cache)
     rows = T if cu_seqlens is not None else n_seqs * T
     ws = _workspace(workspace, int(lib.kda_ssm_conv_bwd_workspace_bytes(rows, channels, width)), dev)
     with _on(dev):
@@ -268,13 +282,13 @@ def ssm_chunk_fwd(x, dt, A, B, C, D=None, S0=None, cu_seqlens=None, *, dt_bias=N
     lib = load_library()
     a = _Scan(x, dt, A, B, C, D, S0, cu_seqlens, dt_bias)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=a.dev)
+        y = _like(x)
     else:
         _check_shape(y, "y", x.shape, a.dev, x.dtype)
     if S_T is not None:
         _check_shape(S_T, "S_T", a.state, a.dev)
     elif output_final_state:
-        S_T = torch.empty(a.state, dtype=torch.float32, device=a.dev)
+        S_T = torch.empty(a.state, dtype=torch.float32, device=a.dev) if S0 is None else _like(S0)
     ws = None
     if sequence_parallel:
         ws = _workspace(workspace, ssm_chunk_fwd_workspace_bytes(a.n_seqs, a.T, a.H, a.G, a.N, a.P,
@@ -314,18 +328,19 @@ def ssm_chunk_bwd(x, dt, A, B, C, D, S0, grad_y, grad_S_T=None, cu_seqlens=None,
     _check_shape(grad_y, "grad_y", x.shape, a.dev, x.dtype)
     if grad_S_T is not None:
         _check_shape(grad_S_T, "grad_S_T", a.state, a.dev)
-    f32 = dict(dtype=torch.float32, device=a.dev)
     outs = []
     for name, t, like, tail in (("grad_x", grad_x, x, (a.H, a.P)), ("grad_B", grad_B, B, (a.G, a.N)),
                                 ("grad_C", grad_C, C, (a.G, a.N))):
         if t is None:
-            t = torch.empty(like.shape, dtype=x.dtype, device=a.dev)
+            t = _like(like)
         outs.append((t, _check_rows(t, name, a.lead, tail, x.dtype, a.dev)))
     (gx, gxs), (gB, gBs), (gC, gCs) = outs
-    gdt, gA = torch.empty(dt.shape, **f32), torch.empty(a.H, **f32)
-    gD = None if D is None else torch.empty(a.H, **f32)
-    gbias = None if dt_bias is None else torch.empty(a.H, **f32)
-    gS0 = torch.empty(a.state, **f32) if want_grad_S0 else None
+    gdt, gA = _like(dt), _like(A)
+    gD = None if D is None else _like(D)
+    gbias = None if dt_bias is None else _like(dt_bias)
+    like = S0 if S0 is not None else grad_S_T
+    gS0 = None if not want_grad_S0 else _like(like) if like is not None else \
+        torch.empty(a.state, dtype=torch.float32, device=a.dev)
     ws = _workspace(workspace, ssm_chunk_bwd_workspace_bytes(x.dtype, a.n_seqs, a.T, a.H, a.G, a.N, a.P,
                                                              cu_seqlens is not None), a.dev)
     with _on(a.dev):
@@ -367,7 +382,7 @@ def ssm_recurrent_fwd(x, dt, A, B, C, S, D=None, *, dt_bias=None, softplus=True,
     if S is None:
         raise KDAError("S must be a torch.Tensor")
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=a.dev)
+        y = _like(x)
     else:
         _check_shape(y, "y", x.shape, a.dev, x.dtype)
     with _on(a.dev):
@@ -408,7 +423,7 @@ def verify_drafts(p_target, drafts, u, u_next, p_draft=None, n_draft=None, *, wo
         _check_shape(p_draft, "p_draft", (B, K, V), dev, p_target.dtype)
     if n_draft is not None:
         _check_shape(n_draft, "n_draft", (B,), dev, torch.int32)
-    n_acc = torch.empty(B, dtype=torch.int32, device=dev)
+    n_acc = torch.empty((B,), dtype=torch.int32, device=dev)
     tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
     ws = _workspace(workspace, int(lib.kda_verify_drafts_workspace_bytes(B, K, V)), dev)
     with _on(dev):
