@@ -136,13 +136,11 @@ __host__ __device__ __forceinline__ int64_t cv_strips(int64_t channels) { return
 // The rows of a walk, one after the other, all wave-uniform.
 struct Walk {
     Seq s;
-    int64_t r;
-    __device__ __forceinline__ Walk(const ConvParams& p, int64_t row) : s(seq_of_row(p, row)), r(row) {}
-    // moves to row r; whether it belongs to a sequence (then s is that one)
+    __device__ __forceinline__ Walk(const ConvParams& p, int64_t row) : s(seq_of_row(p, row)) {}
+    // moves to a row; whether it belongs to a sequence (then s is that one)
     __device__ __forceinline__ bool at(const ConvParams& p, int64_t row) {
-        r = row;
-        while (r >= s.end && s.n + 1 < p.n_seqs) s = seq_range(p, s.n + 1);
-        return r >= s.start && r < s.end;
+        while (row >= s.end && s.n + 1 < p.n_seqs) s = seq_range(p, s.n + 1);
+        return row >= s.start && row < s.end;
     }
 };
 

@@ -136,7 +136,7 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _conv_args(x, w, bias, cu_seqlens, n_lead=None):
+def _conv_args(x, w, bias):
     import torch
     dev = x.device
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
@@ -159,7 +159,7 @@ def ssm_conv_fwd(x, w, bias=None, cache=None, cu_seqlens=None, *, activation=Tru
     """
     import torch
     lib = load_library()
-    dev, dt, channels, width = _conv_args(x, w, bias, cu_seqlens)
+    dev, dt, channels, width = _conv_args(x, w, bias)
     lead, n_seqs, T = _lead(x, 1, cu_seqlens, "x", dev)
     xs = _check_rows(x, "x", lead, (channels,), x.dtype, dev)
     if cache is not None:
@@ -186,7 +186,7 @@ def ssm_conv_step(x, w, bias, cache, *, replay=None, n_replay=None, commit=True,
     """
     import torch
     lib = load_library()
-    dev, dt, channels, width = _conv_args(x, w, bias, None)
+    dev, dt, channels, width = _conv_args(x, w, bias)
     lead, B, T = _lead(x, 1, None, "x", dev)
     xs = _check_rows(x, "x", lead, (channels,), x.dtype, dev)
     _check_shape(cache, "cache", (B, width - 1, channels), dev)
@@ -218,7 +218,7 @@ def ssm_conv_bwd(x, w, bias, grad_y, cache=None, cu_seqlens=None, *, activation=
     """
     import torch
     lib = load_library()
-    dev, dt, channels, width = _conv_args(x, w, bias, cu_seqlens)
+    dev, dt, channels, width = _conv_args(x, w, bias)
     lead, n_seqs, T = _lead(x, 1, cu_seqlens, "x", dev)
     xs = _check_rows(x, "x", lead, (channels,), x.dtype, dev)
     gs = _check_rows(grad_y, "grad_y", lead, (channels,), x.dtype, dev)
