@@ -41,6 +41,24 @@ __device__ __forceinline__ float sum_lane_groups(float v) {   // over lanes with
     return v + swap_halves(v);
 }
 
+// The same for RT values (two or four) at once: a lane gets the sum of value
+// (l >> 4) % RT, so that each exchange halves the values along with the groups.
+template <int RT>
+__device__ __forceinline__ float sum_lane_groups(const float (&v)[RT]) {
+    static_assert(RT == 2 || RT == 4, "");
+    auto swap32 = [](float a, float b) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    };
+    auto swap16 = [](float a, float b) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    };
+    if constexpr (RT == 4) return swap16(swap32(v[0], v[2]), swap32(v[1], v[3]));
+    const float a = swap16(v[0], v[1]);   // rows 0, 2: the first value, rows 1, 3: the second
+    return a + swap_halves(a);
+}
+
 // Eight waves.  For the products with S, R and the chunk matrices towards dB
 // and dC a wave owns one 16-row tile of the state (and, with N = 64, every
 // second 16-token tile); towards dx one 16-column tile of x (with P = 64,
@@ -418,19 +436,26 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
                     acc[k] = mma_parts<SP, XP>(ps, ft, acc[k]);
                 }
             }
+            float u[RT];
 #pragma unroll
             for (int k = 0; k < RT; ++k) {
                 const int t = 16 * (rh + RS * k) + l15;
-                float o[4], u = 0.f;
+                float o[4];
                 four(own, L * N, t, n0 + 4 * lg, o);
                 const float w = weight[t];
+                u[k] = 0.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    u = fmaf(o[r], acc[k][r], u);
+                    u[k] = fmaf(o[r], acc[k][r], u[k]);
                     grad[k][r] = fmaf(w, acc[k][r], grad[k][r]);
                 }
-                u = sum_lane_groups(u);
-                if (lg == 0) sums[t] = u;
+            }
+            if constexpr (RT == 1) {
+                const float v = sum_lane_groups(u[0]);
+                if (lg == 0) sums[16 * rh + l15] = v;
+            } else {
+                const float v = sum_lane_groups<RT>(u);
+                if (lg < RT) sums[16 * (rh + RS * lg) + l15] = v;
             }
         };
         with_state(fS, tY, tC, dec.eg, now.U[rt], dC);
