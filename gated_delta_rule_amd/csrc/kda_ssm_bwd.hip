@@ -199,6 +199,19 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
         }
     };
 
+    // this wave's rows of C and B by token, for the sums against them: the
+    // same for all heads (with P = 128 there are no registers left for them)
+    constexpr bool KEEP = P == 64;
+    float ownC[RT][4], ownB[RT][4];
+    auto own_rows = [&](const __bf16* tile, float (&o)[RT][4]) {
+#pragma unroll
+        for (int k = 0; k < RT; ++k) four(tile, L * N, 16 * (rh + RS * k) + (lane & 15), n0 + 4 * (lane >> 4), o[k]);
+    };
+    if constexpr (KEEP) {
+        own_rows(tC, ownC);
+        own_rows(tB, ownB);
+    }
+
     // gradients of the decay and of dt of head hk0 + wave, whose sums are
     // whole: one token per lane
     auto finish = [&](int hk0) {
@@ -416,7 +429,7 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
             }
         }
         // first S with dy, then R with x: acc, its sum against C or B by token, and its share of dC or dB
-        auto with_state = [&](const f32x4 (&f)[P / 32][2], const __bf16* tok, const __bf16* own, const float* weight,
+        auto with_state = [&](const f32x4 (&f)[P / 32][2], const __bf16* tok, const float (&own)[RT][4], const float* weight,
                               float* sums, f32x4 (&grad)[RT]) {
             f32x4 acc[RT];
 #pragma unroll
@@ -440,13 +453,11 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
 #pragma unroll
             for (int k = 0; k < RT; ++k) {
                 const int t = 16 * (rh + RS * k) + l15;
-                float o[4];
-                four(own, L * N, t, n0 + 4 * lg, o);
                 const float w = weight[t];
                 u[k] = 0.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    u[k] = fmaf(o[r], acc[k][r], u[k]);
+                    u[k] = fmaf(own[k][r], acc[k][r], u[k]);
                     grad[k][r] = fmaf(w, acc[k][r], grad[k][r]);
                 }
             }
@@ -458,12 +469,14 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
                 if (lg < RT) sums[16 * (rh + RS * lg) + l15] = v;
             }
         };
-        with_state(fS, tY, tC, dec.eg, now.U[rt], dC);
+        if constexpr (!KEEP) own_rows(tC, ownC);
+        with_state(fS, tY, ownC, dec.eg, now.U[rt], dC);
         // (the next head's requests apart: a wave would stand at a burst)
         __builtin_amdgcn_sched_barrier(0);
         if (hk + 1 < hwn) fetch_state(fS, q.states, hw + 1);
         __builtin_amdgcn_sched_barrier(0);
-        with_state(fR, tX, tB, dec.w, now.V[rt], dB);
+        if constexpr (!KEEP) own_rows(tB, ownB);
+        with_state(fR, tX, ownB, dec.w, now.V[rt], dB);
         __builtin_amdgcn_sched_barrier(0);
         if (hk + 1 < hwn) fetch_state(fR, q.dstates, hw + 1);
         lds_barrier();   // the chunk matrices and the partial sums are whole
