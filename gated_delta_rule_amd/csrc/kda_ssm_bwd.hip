@@ -207,9 +207,19 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
 #pragma unroll
         for (int k = 0; k < RT; ++k) four(tile, L * N, 16 * (rh + RS * k) + (lane & 15), n0 + 4 * (lane >> 4), o[k]);
     };
+    bf16x8 colB[L / 32][XP], colC[L / 32][XP];   // and its columns of them by 32 tokens
+    auto own_cols = [&](int ks) {
+#pragma unroll
+        for (int i = 0; i < XP; ++i) {
+            colB[ks][i] = frag_col<N>(tB + i * L * N, n0, ks, cN);
+            colC[ks][i] = frag_col<N>(tC + i * L * N, n0, ks, cN);
+        }
+    };
     if constexpr (KEEP) {
         own_rows(tC, ownC);
         own_rows(tB, ownB);
+#pragma unroll
+        for (int ks = 0; ks < L / 32; ++ks) own_cols(ks);
     }
 
     // gradients of the decay and of dt of head hk0 + wave, whose sums are
@@ -485,12 +495,8 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
         // products with the chunk matrices
 #pragma unroll
         for (int ks = 0; ks < L / 32; ++ks) {
-            bf16x8 fb[XP], fc[XP];
-#pragma unroll
-            for (int i = 0; i < XP; ++i) {
-                fb[i] = frag_col<N>(tB + i * L * N, n0, ks, cN);
-                fc[i] = frag_col<N>(tC + i * L * N, n0, ks, cN);
-            }
+            if constexpr (!KEEP) own_cols(ks);
+            const auto &fb = colB[ks], &fc = colC[ks];
 #pragma unroll
             for (int k = 0; k < RT; ++k) {
                 const int t = rh + RS * k;
