@@ -73,6 +73,7 @@ int check_stride(int64_t stride, int64_t width, int64_t es) {
 }
 
 // Token rows of a batch, bounded so that no product of sizes below can wrap.
+constexpr int64_t kMaxChain = (int64_t)1 << 30;   // tokens of a scan's sequence, counted in 32 bits with room for whole chunks
 constexpr int64_t kMaxRows = (int64_t)1 << 36, kMaxState = (int64_t)1 << 56;
 int count_rows(bool varlen, int32_t n_seqs, int64_t T, int64_t* rows) {
     if (T > kMaxRows) return KDA_ERR_TOO_LARGE;
@@ -93,7 +94,7 @@ int scan_shape(int in_dtype, int32_t n_seqs, int64_t T, int32_t H, int32_t G, in
     if (n_seqs < 0 || T < 0 || H < 1 || G < 1 || H % G != 0 || (N != 64 && N != 128) ||
         (P != 64 && P != 128))
         return KDA_ERR_BAD_SHAPE;
-    if (H > KDA_MAX_HEADS || (int64_t)H * P > KDA_SSM_MAX_STRIDE) return KDA_ERR_TOO_LARGE;
+    if (H > KDA_MAX_HEADS || (int64_t)H * P > KDA_SSM_MAX_STRIDE || T > kMaxChain) return KDA_ERR_TOO_LARGE;
     return (int64_t)n_seqs * H <= kMaxState / ((int64_t)N * P) ? KDA_OK : KDA_ERR_TOO_LARGE;
 }
 

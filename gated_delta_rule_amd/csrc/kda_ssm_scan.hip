@@ -141,51 +141,59 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
             reinterpret_cast<u32x4*>(tM)[i] = u32x4{0, 0, 0, 0};
     }
 
-    const int64_t chunks = (s.r1 - s.r0 + L - 1) / L;
+    // From here on all counts are of this chain's tokens, in 32 bits, and the
+    // pointers run along the chain: scalar registers that spill cost vector
+    // instructions (24 of them: 121 against 118 us).
+    const int len = (int)(s.r1 - s.r0), chunks = (len + L - 1) / L;
+    const int way = rev ? -L : L;
+    const int at0 = rev && chunks > 0 ? (chunks - 1) * L : 0;   // token of the first chunk
     // requests for a chunk's rows, one chunk ahead
     Stager<InT, L, N, SC_THREADS> gB, gC;
     Stager<InT, L, 128, SC_THREADS> gX;
-    auto fetch = [&](int64_t row0, int what) {
-        const int valid = s.r1 - row0 < L ? (s.r1 > row0 ? (int)(s.r1 - row0) : 0) : L;
-        const int64_t r = valid > 0 ? row0 : s.r0;
-        if (what & 1) gB.load((const InT*)p.B + r * p.B_stride + grp * N, p.B_stride, valid, N);
-        if constexpr (OUT)
-            if (what & 2) gC.load((const InT*)p.C + r * p.C_stride + grp * N, p.C_stride, valid, N);
-        if (what & 4) gX.load((const InT*)p.x + r * p.x_stride + (int64_t)h0 * P, p.x_stride, valid, nh * P);
-    };
+    const int xs = (int)p.x_stride, bs = (int)p.B_stride, cs = (int)p.C_stride;
+    const InT* nx = (const InT*)p.x + (s.r0 + at0) * p.x_stride + (int64_t)h0 * P;
+    const InT* nb = (const InT*)p.B + (s.r0 + at0) * p.B_stride + grp * N;
+    const InT* nc = OUT ? (const InT*)p.C + (s.r0 + at0) * p.C_stride + grp * N : nullptr;
+    auto rows_at = [&](int at) { return at < 0 || at >= len ? 0 : len - at < L ? len - at : L; };
     const int dh = wave % HPW, dk = wave / HPW;   // the head and, within a block, the chunk
     const bool dec_live = dh < nh;
     const float bias = p.dt_bias && dec_live ? p.dt_bias[h0 + dh] : 0.f;
     const float Ah = dec_live ? p.A[h0 + dh] : 0.f;
     float gdt = 0.f;
-    auto dt_there = [&](int64_t k, int64_t& row) {   // this lane's token of the k-th chunk of the walk
-        row = s.r0 + (rev ? chunks - 1 - k : k) * L + lane;
-        return dec_live && k < chunks && lane < L && row < s.r1;
+    const float* dts = p.dt + s.r0 * p.H + h0 + dh;
+    const int H = p.H;
+    auto dt_there = [&](int k, int& at) {   // this lane's token of the k-th chunk of the walk
+        at = at0 + k * way + lane;
+        return dec_live && k < chunks && lane < L && at < len;
     };
-    auto fetch_dt = [&](int64_t k) {
-        int64_t row;
-        gdt = dt_there(k, row) ? p.dt[row * p.H + h0 + dh] : 0.f;
+    auto fetch_dt = [&](int k) {
+        int at;
+        gdt = dt_there(k, at) ? dts[(int64_t)at * H] : 0.f;
     };
     const float D0 = OUT && p.D ? p.D[h0] : 0.f, D1 = OUT && p.D && nh > 1 ? p.D[h0 + 1] : 0.f;
     double total = 0.0;
     // this chain's first chunk among the slots of the states array
     const int64_t chunk0 = (p.cu ? s.start / L + s.n : s.n * ((p.T + L - 1) / L)) + (s.r0 - s.start) / L;
-    const int64_t first = chunks == 0 ? s.r1 : rev ? s.r0 + (chunks - 1) * L : s.r0;   // (an empty sequence: no row)
-    fetch(first, 7);
+    float* walk = MODE == kWalk ? p.states + ((chunk0 + at0 / L) * heads + h - hfirst) * (N * P) : nullptr;
+    char* yrow = OUT ? (char*)p.y + (((s.r0 + at0) * p.H + h) * P + pc) * (int64_t)sizeof(InT) : nullptr;
+    {
+        const int valid = rows_at(at0);   // (an empty sequence: no row)
+        gX.load(nx, xs, valid, nh * P);
+        gB.load(nb, bs, valid, N);
+        if constexpr (OUT) gC.load(nc, cs, valid, N);
+    }
     fetch_dt(dk);
 
-    for (int64_t i = 0; i < chunks; ++i) {
-        const int64_t ch = rev ? chunks - 1 - i : i;
-        const int64_t row0 = s.r0 + ch * L;
-        const int valid = s.r1 - row0 < L ? (int)(s.r1 - row0) : L;
+    for (int i = 0, at = at0; i < chunks; ++i, at += way) {
+        const int valid = rows_at(at), next = rows_at(at + way);
         hide(lane), hide(rN), hide(rL), hide(cB), hide(cX);
         const int l15 = lane & 15, lg = lane >> 4;
         gB.put(tB);
         if constexpr (OUT) gC.put(tC);
         gX.put(tX);
         if (i % DB == 0) {
-            int64_t row;
-            const bool there = dt_there(i + dk, row);
+            int token;
+            const bool there = dt_there(i + dk, token);
             total += chunk_decay<L>(dec[dk][dh], gdt, there, bias, p.softplus, Ah);
             fetch_dt(i + DB + dk);
         }
@@ -193,12 +201,12 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
         lds_barrier();
         // the next chunk's rows, a tile at a time between the products: a
         // wave would stand at a burst of requests
-        const int64_t next = rev ? (ch > 0 ? row0 - L : s.r1) : row0 + L;
-        fetch(next, 4);
+        nx += (int64_t)way * xs;
+        gX.load(nx, xs, next, nh * P);
         const ChunkDecay<L>& d = dc[wh];
         if constexpr (MODE == kWalk) {   // whole tiles, see walk_at
             if (live) {
-                f32x4* to = reinterpret_cast<f32x4*>(p.states + ((chunk0 + ch) * heads + h - hfirst) * (N * P));
+                f32x4* to = reinterpret_cast<f32x4*>(walk);
 #pragma unroll
                 for (int c = 0; c < SC_CT; ++c)
 #pragma unroll
@@ -271,7 +279,8 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
                     weigh(raw_tile(tt, st), tt, st, wave % HPW);
                 }
             }
-            fetch(next, 1);
+            nb += (int64_t)way * bs;
+            gB.load(nb, bs, next, N);
             // Y^T = S^T C^T, rows p, columns t
 #pragma unroll
             for (int c = 0; c < SC_CT; ++c)
@@ -308,7 +317,13 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
             lds_barrier();   // M is whole
         }
 
-        fetch(next, OUT ? 2 : 1);
+        if constexpr (OUT) {
+            nc += (int64_t)way * cs;
+            gC.load(nc, cs, next, N);
+        } else {
+            nb += (int64_t)way * bs;
+            gB.load(nb, bs, next, N);
+        }
         // x columns as operands: k runs over the tokens
         bf16x8 fx[SC_CT][L / 32][XP];
 #pragma unroll
@@ -336,14 +351,14 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
             for (int tt = 0; tt < TT; ++tt) {
                 const int t = 16 * tt + l15;
                 if (live && t < valid) {
-                    const int64_t at = ((row0 + t) * p.H + h) * P + pc + 4 * lg;
+                    char* to = yrow + (uint32_t)(t * H * P + 4 * lg) * (uint32_t)sizeof(InT);
 #pragma unroll
                     for (int c = 0; c < SC_CT; ++c) {
                         if constexpr (Cfg::BF) {
-                            *reinterpret_cast<u32x2*>((__bf16*)p.y + at + 16 * c) =
+                            reinterpret_cast<u32x2*>(to)[4 * c] =
                                 u32x2{pack_bf2(Y[c][tt][0], Y[c][tt][1]), pack_bf2(Y[c][tt][2], Y[c][tt][3])};
                         } else {
-                            *reinterpret_cast<f32x4*>((float*)p.y + at + 16 * c) = Y[c][tt];
+                            reinterpret_cast<f32x4*>(to)[4 * c] = Y[c][tt];
                         }
                     }
                 }
@@ -399,6 +414,8 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
                         }
             }
         }
+        if constexpr (MODE == kWalk) walk += (rev ? -1 : 1) * heads * (N * P);
+        if constexpr (OUT) yrow += (int64_t)L * H * P * (int64_t)sizeof(InT);
         lds_barrier();   // the tiles are consumed (rows and stores stay in flight)
     }
 
