@@ -24,8 +24,8 @@
 // head), and the full pass runs all segments side by side.
 //
 // Measured (MI355X, bf16, N 128): 8192 tokens of 64 heads of 64 in 16 segments
-// 119 us (local 42, merge 13, outputs 72); 16 packed sequences of 8192 tokens,
-// 96 heads of 128, one pass, 206 us.  Neither HBM (28 and 124 us) nor the
+// 110 to 118 us (local 42, merge 13, outputs 70); 16 packed sequences of 8192
+// tokens, 96 heads of 128, one pass, 200 to 205 us.  Neither HBM (28 and 124 us) nor the
 // matrix cores (0.28 busy): per chunk the compute unit's two workgroups take
 // 13 000 cycles, with vector instructions in 0.56 and LDS in 0.38 of them, and
 // three barriers between dependent products.
