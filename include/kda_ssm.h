@@ -52,7 +52,8 @@
 extern "C" {
 #endif
 
-/* Largest row stride (elements) of a token row. */
+/* Largest row stride (elements) of a token row.  Sequences of the scan have at
+ * most 2^30 tokens (KDA_ERR_TOO_LARGE). */
 #define KDA_SSM_MAX_STRIDE (1 << 23)
 
 /*
@@ -124,7 +125,9 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
  * of three bf16 parts, so S_T is accurate to float32 rounding; so is y with
  * KDA_F32.  With KDA_BF16, S in S^T C and the weighted products C . B are
  * rounded to bf16 once each, a half step of the output's type.
- * A token with dt A < -104 (a reset) ends all memory.
+ * A token with dt A < -104 (a reset) ends all memory.  One with dt = 0 (the
+ * softplus of a large negative number) leaves the state as it is, so a batch
+ * may be padded at its end with finite tokens of such dt.
  */
 size_t kda_ssm_chunk_fwd_workspace_bytes(int32_t n_seqs, int64_t T, int32_t H, int32_t G,
                                          int32_t N, int32_t P, int varlen);

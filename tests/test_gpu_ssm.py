@@ -538,6 +538,97 @@ def test_captured_graph_replays(op):
         assert all(torch.equal(i, j) for i, j in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_padded_batch(dtype):
+    """Sequences padded with tokens of dt = 0 give the packed batch's outputs,
+    states and gradients."""
+    lens, T, H, G, N, P = [150, 64, 3], 160, 4, 2, 64, 64
+    a = scan_case(lens, H, G, N, P, dtype, seed=42)
+    t = {k: dev(a[k], torch.float32 if k == "dt" else dtype) for k in ("x", "dt", "B", "C", "gy")}
+    A, D, S0, gS, cu = dev(a["A"]), dev(a["D"]), dev(a["S0"]), dev(a["gS"]), dev(a["cu"], torch.int32)
+    pad = {}
+    for k, v in t.items():
+        pad[k] = torch.full((len(lens), T) + v.shape[1:], {"dt": -1e4, "gy": 0.0}.get(k, 3.0), dtype=v.dtype, device="cuda")
+        for i, (s, e) in enumerate(zip(a["cu"], a["cu"][1:])):
+            pad[k][i, :e - s] = v[s:e]
+    real = lambda v: torch.cat([v[i, :n] for i, n in enumerate(lens)])   # noqa: E731
+    y, S = kda.ssm_chunk_fwd(t["x"], t["dt"], A, t["B"], t["C"], D, S0, cu)
+    yp, Sp = kda.ssm_chunk_fwd(pad["x"], pad["dt"], A, pad["B"], pad["C"], D, S0)
+    r = kda.ssm_chunk_bwd(t["x"], t["dt"], A, t["B"], t["C"], D, S0, t["gy"], gS, cu)
+    rp = kda.ssm_chunk_bwd(pad["x"], pad["dt"], A, pad["B"], pad["C"], D, S0, pad["gy"], gS)
+    torch.cuda.synchronize()
+    assert torch.equal(real(yp), y) and torch.equal(Sp, S)
+    assert torch.equal(real(rp[0]), r[0]) and torch.equal(rp[7], r[7])
+    # sums whose chunks or blocks of heads differ: float32 rounding, and one of the input type
+    for i in (1, 3, 4):
+        got, want = real(rp[i]).float(), r[i].float()
+        torch.testing.assert_close(got, want, rtol=2 ** -7 if dtype == torch.bfloat16 and i > 1 else 1e-5,
+                                   atol=1e-5 * float(want.abs().max()))
+    for i in (2, 5):
+        torch.testing.assert_close(rp[i], r[i], rtol=1e-5, atol=1e-5 * float(r[1].abs().max()))
+
+
+def test_sequences_without_tokens():
+    """T = 0: states and caches stay, gradients of the parameters are zero and
+    the state's passes through; no sequences at all: nothing."""
+    H, N, P, c, n = 3, 64, 64, 24, 2
+    f = lambda *s: torch.randn(*s, device="cuda")   # noqa: E731
+    A, D, S0, gS = -torch.rand(H, device="cuda"), f(H), f(n, H, N, P), f(n, H, N, P)
+    x, dt, B = f(n, 0, H, P), f(n, 0, H), f(n, 0, 1, N)
+    cu = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    for a, packed in (((x, dt, A, B, B), None), ((x[0], dt[0], A, B[0], B[0]), cu)):
+        y, S = kda.ssm_chunk_fwd(*a, D, S0, packed)
+        assert y.shape == a[0].shape and torch.equal(S, S0)
+        r = kda.ssm_chunk_bwd(*a, D, S0, a[0], gS, packed, dt_bias=D)
+        assert torch.equal(r[7], gS) and all(not t.any() for t in (r[2], r[5], r[6]))
+    w, bias, cache = f(c, 4), f(c), f(n, 3, c)
+    old = cache.clone()
+    for v, packed in ((f(n, 0, c), None), (f(0, c), cu)):
+        assert kda.ssm_conv_fwd(v, w, bias, cache, packed).shape == v.shape and torch.equal(cache, old)
+        g = kda.ssm_conv_bwd(v, w, bias, v, cache, packed)
+        assert all(not t.any() for t in g[1:])
+    assert kda.ssm_conv_step(f(n, 0, c), w, bias, cache).numel() == 0 and torch.equal(cache, old)
+    none = kda.ssm_chunk_bwd(x[:0], dt[:0], A, B[:0], B[:0], D, S0[:0], x[:0])
+    assert not none[2].any() and not none[5].any()
+    na, tok = kda.verify_drafts(f(0, 3, 9), torch.zeros(0, 2, dtype=torch.int32, device="cuda"), f(0, 2), f(0))
+    torch.cuda.synchronize()
+    assert na.shape == (0,) and tok.shape == (0, 3)
+
+
+@pytest.mark.parametrize("lens", [[130, 0, 65], [700]])
+def test_given_outputs_and_state_gradient_in_place(lens):
+    """Outputs and workspaces of the caller, too long a workspace among them,
+    and grad_S0 written over grad_S_T through the C ABI (with and without
+    segments)."""
+    a = scan_case(lens, 2, 1, 64, 64, torch.bfloat16, seed=41)
+    b = torch.bfloat16
+    t = {k: dev(a[k], b) for k in ("x", "B", "C", "gy")}
+    f = {k: dev(a[k]) for k in ("dt", "A", "D", "S0", "gS")}
+    cu, n, T = dev(a["cu"], torch.int32), len(lens), sum(lens)
+    args = (t["x"], f["dt"], f["A"], t["B"], t["C"], f["D"], f["S0"])
+    y, S = kda.ssm_chunk_fwd(*args, cu)
+    ws = torch.empty(kda.ssm_chunk_fwd_workspace_bytes(n, T, 2, 1, 64, 64, True) + 4096, dtype=torch.uint8, device="cuda")
+    y2, S2 = torch.empty_like(y), torch.empty_like(S)
+    out = kda.ssm_chunk_fwd(*args, cu, y=y2, S_T=S2, workspace=ws)
+    torch.cuda.synchronize()
+    assert out[0] is y2 and out[1] is S2 and torch.equal(y, y2) and torch.equal(S, S2)
+    want = kda.ssm_chunk_bwd(*args, t["gy"], f["gS"], cu)
+    lib = kda.load_library()
+    need = kda.ssm_chunk_bwd_workspace_bytes(b, n, T, 2, 1, 64, 64, True)
+    ws = torch.empty(need + 4096, dtype=torch.uint8, device="cuda")
+    g = [torch.empty_like(v) for v in (t["x"], t["B"], t["C"], f["dt"], f["A"], f["D"])]
+    state = f["gS"].clone()
+    p = lambda v: v.data_ptr()   # noqa: E731
+    rc = lib.kda_ssm_chunk_bwd(p(t["x"]), 128, p(t["B"]), 64, p(t["C"]), 64, kda.KDA_BF16, p(f["dt"]), None, 1, p(f["A"]),
+                               p(f["D"]), p(f["S0"]), p(cu), n, T, 2, 1, 64, 64, p(t["gy"]), p(state), p(g[0]), 128, p(g[1]),
+                               64, p(g[2]), 64, p(g[3]), p(g[4]), p(g[5]), None, p(state), p(ws), ws.numel(),
+                               torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0
+    for got, ref in zip(g + [state], (want[0], want[3], want[4], want[1], want[2], want[5], want[7])):
+        assert torch.equal(got, ref)
+
+
 def test_two_streams_at_once():
     """Two calls in flight on two streams give the bits of each alone."""
     runs = []
