@@ -102,6 +102,16 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
         s = SsmPiece{n, 0, r.start, r.end, r.start, r.end};
     }
 
+    // The state changes its sign with every chunk (minus before odd ones): the
+    // matrix cores round their sums a little towards minus infinity (a
+    // hundredth of a unit in the last place), which in a state of one sign adds
+    // up, all elements alike, and in dA, a sum over all tokens, comes to 2e-6 of
+    // it (0.7e-6 with the signs, the same time).  The factors of chunk_decay
+    // carry them, loads and stores of the state put them on and take them off.
+    const int len = (int)(s.r1 - s.r0), chunks = (len + L - 1) / L;
+    auto sign_of = [](int chunk) { return chunk & 1 ? -1.f : 1.f; };
+    const float sign0 = sign_of(rev ? chunks - 1 : 0), sign1 = sign_of(rev ? -1 : chunks);
+
     // State in accumulator registers.  With outputs: element (tile m = 2 j + o,
     // register r) is row 32 j + 8 lg + 4 o + r, column pc + 16 c + l15, the
     // order in which it is an operand of S^T C.  Without: row 16 m + l15,
@@ -120,7 +130,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
 #pragma unroll
         for (int m = 0; m < NT; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[c][m][r] = init ? init[state_at(c, m, r)] : 0.f;
+            for (int r = 0; r < 4; ++r) S[c][m][r] = init ? sign0 * init[state_at(c, m, r)] : 0.f;
     auto save = [&](float* to) {
         if (!live) return;
 #pragma unroll
@@ -129,9 +139,9 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
             for (int m = 0; m < NT; ++m) {
                 if constexpr (OUT) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) to[state_at(c, m, r)] = S[c][m][r];
+                    for (int r = 0; r < 4; ++r) to[state_at(c, m, r)] = sign1 * S[c][m][r];
                 } else {
-                    *reinterpret_cast<f32x4*>(to + state_at(c, m, 0)) = S[c][m];
+                    *reinterpret_cast<f32x4*>(to + state_at(c, m, 0)) = sign1 * S[c][m];
                 }
             }
     };
@@ -144,7 +154,6 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
     // From here on all counts are of this chain's tokens, in 32 bits, and the
     // pointers run along the chain: scalar registers that spill cost vector
     // instructions (24 of them: 121 against 118 us).
-    const int len = (int)(s.r1 - s.r0), chunks = (len + L - 1) / L;
     const int way = rev ? -L : L;
     const int at0 = rev && chunks > 0 ? (chunks - 1) * L : 0;   // token of the first chunk
     // requests for a chunk's rows, one chunk ahead
@@ -194,7 +203,8 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
         if (i % DB == 0) {
             int token;
             const bool there = dt_there(i + dk, token);
-            total += chunk_decay<L>(dec[dk][dh], gdt, there, bias, p.softplus, Ah);
+            const float sign = sign_of(at0 / L + (rev ? -(i + dk) : i + dk));   // of the state before that chunk
+            total += chunk_decay<L>(dec[dk][dh], gdt, there, bias, p.softplus, Ah, rev ? -sign : sign, -sign, -1.f);
             fetch_dt(i + DB + dk);
         }
         const ChunkDecay<L>* dc = dec[i % DB];
@@ -207,10 +217,11 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
         if constexpr (MODE == kWalk) {   // whole tiles, see walk_at
             if (live) {
                 f32x4* to = reinterpret_cast<f32x4*>(walk);
+                const float sign = sign_of(at / L);
 #pragma unroll
                 for (int c = 0; c < SC_CT; ++c)
 #pragma unroll
-                    for (int m = 0; m < NT; ++m) __builtin_nontemporal_store(S[c][m], &to[walk_at<N>(pc / 16 + c, m, lane)]);
+                    for (int m = 0; m < NT; ++m) __builtin_nontemporal_store(S[c][m] * sign, &to[walk_at<N>(pc / 16 + c, m, lane)]);
             }
         }
 

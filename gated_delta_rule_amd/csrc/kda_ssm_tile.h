@@ -309,10 +309,11 @@ __device__ __forceinline__ double row_prefix_f64(double x) {
 // changes no factor and keeps the sums where their differences are exact to
 // float32 rounding: beside a term of -2^40 or an overflow they are not.
 constexpr float kDecayEnds = -104.f, kDecayCut = -256.f;
-// dt_raw: this lane's token, `valid` whether it exists.  Returns g_end.
+// dt_raw: this lane's token, `valid` whether it exists.  Returns g_end.  The
+// factors are stored with the signs se (eg), sw (w) and sL (eL).
 template <int L>
 __device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bool valid, float bias, int softplus,
-                                              float A) {
+                                              float A, float se = 1.f, float sw = 1.f, float sL = 1.f) {
     const int lane = threadIdx.x & 63;
     float dt = 0.f;
     if (valid) {
@@ -327,9 +328,9 @@ __device__ __forceinline__ double chunk_decay(ChunkDecay<L>& d, float dt_raw, bo
         d.gh[lane] = h;
         d.gl[lane] = (float)(g - (double)h);
         d.dt[lane] = dt;
-        d.eg[lane] = expf(h);
-        d.w[lane] = expf((float)(end - g)) * dt;
-        if (lane == 0) d.eL = expf((float)end);
+        d.eg[lane] = se * expf(h);
+        d.w[lane] = sw * (expf((float)(end - g)) * dt);
+        if (lane == 0) d.eL = sL * expf((float)end);
     }
     return end;
 }
