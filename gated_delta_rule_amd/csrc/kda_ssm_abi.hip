@@ -16,7 +16,7 @@ constexpr int64_t kMaxWide = kMaxWorkgroups / 2;    // of 512
 constexpr int32_t kMaxTokens = 64;        // tokens per request in the step forms
 constexpr int64_t kScanUnits = 256;       // compute units
 constexpr int64_t kScanFill = 2 * kScanUnits;   // chains that fill them
-constexpr int64_t kScanLongSeg = 512, kScanMinSeg = 128;   // see scan_plan
+constexpr int64_t kScanLongSeg = 512, kScanMinSeg = 128, kScanMinSegF32 = 64;   // see scan_plan
 constexpr int64_t kScanMinCut = 3;        // segments from which two passes are shorter than one chain
 constexpr int64_t kScanAlign = 64;
 constexpr int64_t kVerifyFill = 2048;     // workgroups of the verification (512 to 2048: the same time)
@@ -109,25 +109,34 @@ int64_t scan_blocks(int32_t H, int32_t G, int32_t P) { return (int64_t)G * ceil_
 // chain): 512 tokens 31.5 against 37.0 us, 1024 35.4 / 69, 2048 48 / 137, 8192
 // 117 / 531; segments of 64 tokens at 256 tokens 25.7 / 20.8.  Other lengths:
 // segments of 128 at 2048 tokens 54 us, of 256 at 1024 tokens 42, of 1024 at
-// 8192 tokens 122.
+// 8192 tokens 122.  Float32 chains take four times as long per token, so their
+// segments go down to 64 (16 heads of 64, N 128: 256 tokens 26 against 37 us
+// with 128, 1024 tokens 32 against 40; 16 of 128, N 64: 20.5 against 24 and 29
+// against 31, but 4 x 256 tokens 27 against 25).
 struct ScanPlan {
     bool cut;
     int64_t seg_len, slots;
 };
 // `dirs` directions (the backward pass: two) run side by side.
-ScanPlan scan_plan(int32_t n_seqs, int64_t T, int64_t blocks, bool varlen, int64_t dirs) {
+ScanPlan scan_plan(bool bf16_in, int32_t n_seqs, int64_t T, int64_t blocks, bool varlen, int64_t dirs) {
     const int64_t rows = varlen ? T : n_seqs * T;
     const ScanPlan whole{false, T > 0 ? T : 1, n_seqs};
     if (n_seqs * blocks * dirs >= kScanFill) return whole;
     const int64_t work = rows * blocks * dirs;
+    const int64_t least = bf16_in ? kScanMinSeg : kScanMinSegF32;
     int64_t len = ceil_div(work, kScanUnits);
-    len = len < kScanMinSeg ? kScanMinSeg : len > kScanLongSeg ? kScanLongSeg : len;
+    len = len < least ? least : len > kScanLongSeg ? kScanLongSeg : len;
     if (len < ceil_div(work, kScanFill)) len = ceil_div(work, kScanFill);
     const int64_t segs = ceil_div(T, len);
     if (segs < kScanMinCut) return whole;
     if (!varlen) len = ceil_div(T, segs);
     len = ceil_div(len, kScanAlign) * kScanAlign;
     return ScanPlan{true, len, varlen ? T / len + n_seqs : n_seqs * ceil_div(T, len)};
+}
+
+// Segments' states and decays.
+size_t scan_bytes(const ScanPlan& s, int32_t H, int32_t N, int32_t P) {
+    return s.cut ? (size_t)s.slots * H * ((size_t)N * P + 1) * 4 : 0;
 }
 
 // Backward: arrays (offsets in floats) for `groups` groups of heads at a time.
@@ -142,7 +151,7 @@ bool bwd_plan(int in_dtype, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, 
     const int64_t len = kda::ssm_chunk_tokens(in_dtype == KDA_BF16);
     const int64_t hpg = H / G, heads = groups * hpg;
     b->slots = varlen ? rows / len + n_seqs : n_seqs * ceil_div(T, len);
-    b->scan = scan_plan(n_seqs, T, scan_blocks((int32_t)heads, groups, P), varlen, 2);
+    b->scan = scan_plan(in_dtype == KDA_BF16, n_seqs, T, scan_blocks((int32_t)heads, groups, P), varlen, 2);
     // as many heads of a group in one workgroup (fewer partial sums) as leave
     // enough workgroups to fill the GPU
     const int64_t want = ceil_div(kGradFill, b->slots * groups > 0 ? b->slots * groups : 1);
@@ -339,8 +348,12 @@ size_t kda_ssm_chunk_fwd_workspace_bytes(int32_t n_seqs, int64_t T, int32_t H, i
     if (scan_shape(KDA_BF16, n_seqs, T, H, G, N, P)) return 0;
     int64_t rows = 0;
     if (count_rows(varlen != 0, n_seqs, T, &rows)) return 0;
-    const ScanPlan s = scan_plan(n_seqs, T, scan_blocks(H, G, P), varlen != 0, 1);
-    return s.cut ? (size_t)s.slots * H * ((size_t)N * P + 1) * 4 : 0;
+    size_t need = 0;   // of either type
+    for (int bf16_in = 0; bf16_in < 2; ++bf16_in) {
+        const size_t n = scan_bytes(scan_plan(bf16_in != 0, n_seqs, T, scan_blocks(H, G, P), varlen != 0, 1), H, N, P);
+        if (n > need) need = n;
+    }
+    return need;
 }
 
 int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* B, int64_t B_stride,
@@ -377,8 +390,8 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* B, int64_t B_
     if (overlaps(ry, rs0) || overlaps(ry, rst)) return KDA_ERR_ALIASING;
     if (S0 != (const float*)S_T && overlaps(rs0, rst)) return KDA_ERR_ALIASING;
 
-    ScanPlan s = scan_plan(n_seqs, T, scan_blocks(H, G, P), cu_seqlens != nullptr, 1);
-    const size_t need = kda_ssm_chunk_fwd_workspace_bytes(n_seqs, T, H, G, N, P, cu_seqlens != nullptr);
+    ScanPlan s = scan_plan(in_dtype == KDA_BF16, n_seqs, T, scan_blocks(H, G, P), cu_seqlens != nullptr, 1);
+    const size_t need = scan_bytes(s, H, N, P);
     if (s.cut && (!workspace || workspace_bytes < need))
         s = ScanPlan{false, T, n_seqs};
     if (s.cut) {

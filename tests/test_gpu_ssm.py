@@ -552,17 +552,19 @@ def test_padded_batch(dtype):
         for i, (s, e) in enumerate(zip(a["cu"], a["cu"][1:])):
             pad[k][i, :e - s] = v[s:e]
     real = lambda v: torch.cat([v[i, :n] for i, n in enumerate(lens)])   # noqa: E731
-    y, S = kda.ssm_chunk_fwd(t["x"], t["dt"], A, t["B"], t["C"], D, S0, cu)
-    yp, Sp = kda.ssm_chunk_fwd(pad["x"], pad["dt"], A, pad["B"], pad["C"], D, S0)
+    y, S = kda.ssm_chunk_fwd(t["x"], t["dt"], A, t["B"], t["C"], D, S0, cu, sequence_parallel=False)
+    yp, Sp = kda.ssm_chunk_fwd(pad["x"], pad["dt"], A, pad["B"], pad["C"], D, S0, sequence_parallel=False)
     r = kda.ssm_chunk_bwd(t["x"], t["dt"], A, t["B"], t["C"], D, S0, t["gy"], gS, cu)
     rp = kda.ssm_chunk_bwd(pad["x"], pad["dt"], A, pad["B"], pad["C"], D, S0, pad["gy"], gS)
     torch.cuda.synchronize()
     assert torch.equal(real(yp), y) and torch.equal(Sp, S)
-    assert torch.equal(real(rp[0]), r[0]) and torch.equal(rp[7], r[7])
-    # sums whose chunks or blocks of heads differ: float32 rounding, and one of the input type
-    for i in (1, 3, 4):
+    # The packed rows and the padded ones are cut into other segments, up to
+    # four, whose states pass through two more roundings each: 8 half steps,
+    # 5e-7 of the largest state; and the input type's own rounding, once.
+    torch.testing.assert_close(rp[7], r[7], rtol=0, atol=1e-5 * float(r[7].abs().max()))
+    for i in (0, 1, 3, 4):
         got, want = real(rp[i]).float(), r[i].float()
-        torch.testing.assert_close(got, want, rtol=2 ** -7 if dtype == torch.bfloat16 and i > 1 else 1e-5,
+        torch.testing.assert_close(got, want, rtol=2 ** -7 if dtype == torch.bfloat16 and i != 1 else 1e-5,
                                    atol=1e-5 * float(want.abs().max()))
     for i in (2, 5):
         torch.testing.assert_close(rp[i], r[i], rtol=1e-5, atol=1e-5 * float(r[1].abs().max()))
