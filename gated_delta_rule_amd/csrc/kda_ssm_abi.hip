@@ -537,14 +537,17 @@ int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_
     f.N = N;
     f.P = P;
     f.softplus = softplus != 0;
+    // One plan for all passes.  A last pass of fewer groups keeps the segments
+    // and head blocks of the others, so that each of its arrays is a smaller
+    // one in the same place: a plan of its own could need more than they do
+    // (segments where `groups` groups fill the GPU without, more head blocks).
+    f.cut = b.scan.cut;
+    f.seg_len = b.scan.seg_len;
+    f.slots = b.scan.slots;
     for (int32_t g0 = 0; g0 < G; g0 += groups) {
         const int32_t gn = G - g0 < groups ? G - g0 : groups;
-        if (gn != groups && !bwd_plan(in_dtype, n_seqs, T, rows, H, G, N, P, varlen, gn, &b)) return KDA_ERR_TOO_LARGE;
         f.g0 = g0;
         f.gn = gn;
-        f.cut = b.scan.cut;
-        f.seg_len = b.scan.seg_len;
-        f.slots = b.scan.slots;
         if (n_seqs > 0) {
             kda::SsmScanDirs walks{{f, f}};
             for (int i = 0; b.scan.cut && i < 2; ++i) {
