@@ -13,9 +13,9 @@
 // state in accumulator registers in an order in which it is, without any move,
 // also the operand of the next chunk's S^T C.  Per chunk: the next chunk's rows
 // are requested, the waves share out the 16 x 16 tiles of C . B up to the
-// diagonal and put them, weighted and with D on the diagonal, into LDS while
-// each also computes its S^T C; after one barrier each adds M x, stores y and
-// updates its state.
+// diagonal and put them, weighted, into LDS while each also computes its
+// S^T C; after one barrier each adds M x and D x (in float32: D is no operand
+// of the matrix cores), stores y and updates its state.
 //
 // Chains: one per (sequence, head pair) where those fill the GPU; otherwise
 // each sequence is cut into segments.  A first pass computes each segment's
@@ -78,6 +78,8 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
     int lane = tid & 63;
     int rN = lane_row<N>(lane), rL = lane_row<L>(lane);
     int2 cB = lane_col<N, OUT ? 8 : 4>(lane), cX = lane_col<128, 4>(lane);
+    // this lane's four columns of x in row l & 15 (as it holds y)
+    int oX = 16 * ss_unit<16>(lane & 15, wave * (SC_COLS / 8) + (lane >> 5)) + 8 * (lane >> 4 & 1);
     const int64_t slot = blockIdx.x / (uint32_t)hblocks;
     const int hb = (int)(blockIdx.x - (uint32_t)slot * hblocks);
     const int hpg = p.H / p.G, bpg = (hpg + HPW - 1) / HPW;
@@ -179,7 +181,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
         int at;
         gdt = dt_there(k, at) ? dts[(int64_t)at * H] : 0.f;
     };
-    const float D0 = OUT && p.D ? p.D[h0] : 0.f, D1 = OUT && p.D && nh > 1 ? p.D[h0 + 1] : 0.f;
+    const float D = OUT && p.D ? p.D[h] : 0.f;
     double total = 0.0;
     // this chain's first chunk among the slots of the states array
     const int64_t chunk0 = (p.cu ? s.start / L + s.n : s.n * ((p.T + L - 1) / L)) + (s.r0 - s.start) / L;
@@ -195,7 +197,7 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
 
     for (int i = 0, at = at0; i < chunks; ++i, at += way) {
         const int valid = rows_at(at), next = rows_at(at + way);
-        hide(lane), hide(rN), hide(rL), hide(cB), hide(cX);
+        hide(lane), hide(rN), hide(rL), hide(cB), hide(cX), hide(oX);
         const int l15 = lane & 15, lg = lane >> 4;
         gB.put(tB);
         if constexpr (OUT) gC.put(tC);
@@ -257,10 +259,9 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
                 float m[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) m[r] = acc[r] * (__expf((ht - hs[r]) + (lt - ls[r])) * ds[r]);
-                if (tt == st) {   // the diagonal tile: nothing above the diagonal, D on it
-                    const float Dh = hh == 0 ? D0 : D1;
+                if (tt == st) {   // the diagonal tile: nothing above the diagonal
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) m[r] = s0 + r < t ? m[r] : s0 + r == t ? m[r] + Dh : 0.f;
+                    for (int r = 0; r < 4; ++r) m[r] = s0 + r <= t ? m[r] : 0.f;
                 }
                 __bf16* at = tM + hh * MP * L * L + 8 * ss_unit<L / 8>(t, s0 >> 3) + (s0 & 7);
 #pragma unroll
@@ -357,10 +358,23 @@ __global__ __launch_bounds__(SC_THREADS, 4) void ssm_scan_kernel(SsmScanDirs dir
 #pragma unroll
                     for (int c = 0; c < SC_CT; ++c) Y[c][tt] = mma_parts<XP, MP>(fx[c][ks], fm, Y[c][tt]);
                 }
-            // a lane stores four neighbouring columns of token 16 tt + l15
+            // D x, and a lane stores four neighbouring columns of token 16 tt + l15
+            static_assert(SC_CT == 1, "one column tile per wave");
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt) {
                 const int t = 16 * tt + l15;
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = XP - 1; i >= 0; --i) {
+                    const u32x2 u = *reinterpret_cast<const u32x2*>(reinterpret_cast<const char*>(tX + (i * L + 16 * tt) * 128) + oX);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        x[2 * k] += bf2_first(u[k]);
+                        x[2 * k + 1] += bf2_second(u[k]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) Y[0][tt][k] = fmaf(D, x[k], Y[0][tt][k]);
                 if (live && t < valid) {
                     char* to = yrow + (uint32_t)(t * H * P + 4 * lg) * (uint32_t)sizeof(InT);
 #pragma unroll

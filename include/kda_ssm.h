@@ -124,7 +124,8 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
  * update takes its float32 operands (and, with KDA_F32, the inputs) as sums
  * of three bf16 parts, so S_T is accurate to float32 rounding; so is y with
  * KDA_F32.  With KDA_BF16, S in S^T C and the weighted products C . B are
- * rounded to bf16 once each, a half step of the output's type.
+ * rounded to bf16 once each, a half step of the output's type; D x is added
+ * to them in float32.
  * A token with dt A < -104 (a reset) ends all memory.  One with dt = 0 (the
  * softplus of a large negative number) leaves the state as it is, so a batch
  * may be padded at its end with finite tokens of such dt.

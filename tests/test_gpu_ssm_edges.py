@@ -10,7 +10,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU-only container
     pytest.skip("no GPU", allow_module_level=True)
 
 import gated_delta_rule_amd as kda  # noqa: E402
-from test_gpu_ssm import check_bwd, run_bwd, scan_case  # noqa: E402
+from test_gpu_ssm import F32, HALF, check_bwd, dev, host, oracle_scan, run_bwd, scan_case  # noqa: E402
 
 USE = ("D", "S0", "gS", "dt_bias")
 
@@ -58,3 +58,35 @@ def test_backward_by_groups_bitwise(dtype):
         got = by_groups(a, dtype, len(lens), H, G, N, P, groups)
         for i, (g, w) in enumerate(zip(got, want)):
             assert torch.equal(g, w), i
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("P", [64, 128])
+def test_skip_term_is_float32(P, dtype):
+    """Where dt is zero and so is the state, y is D x, rounded once to its
+    type, also where D itself is not of that type; a prompt and single tokens
+    agree.  And beside other terms D's share of y keeps that accuracy."""
+    H, N, T = 3, 64, 70
+    gen = torch.Generator(device="cuda").manual_seed(63)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)   # noqa: E731
+    x, B, C = rnd(1, T, H, P).to(dtype), rnd(1, T, 1, N).to(dtype), rnd(1, T, 1, N).to(dtype)
+    D = torch.tensor([1 + 2 ** -8 + 2 ** -12, -0.37, 1e-3], device="cuda")
+    A, dt = -torch.ones(H, device="cuda"), torch.full((1, T, H), -1e4, device="cuda")
+    y, _ = kda.ssm_chunk_fwd(x, dt, A, B, C, D)
+    S = torch.zeros(1, H, N, P, device="cuda")
+    step = torch.cat([kda.ssm_recurrent_fwd(x[:, i:i + 64], dt[:, i:i + 64], A, B[:, i:i + 64], C[:, i:i + 64], S, D)
+                      for i in (0, 64)], 1)
+    torch.cuda.synchronize()
+    want = (D[:, None] * x.float()).to(dtype)
+    assert torch.equal(y, want) and torch.equal(step, want)
+    a = scan_case([T], H, 1, N, P, dtype, seed=64)
+    a["D"] = host(D)
+    y, _ = kda.ssm_chunk_fwd(dev(a["x"], dtype), dev(a["dt"]), dev(a["A"]), dev(a["B"], dtype), dev(a["C"], dtype), D,
+                             None, dev(a["cu"], torch.int32))
+    torch.cuda.synchronize()
+    ry, my, _, _, _, _ = oracle_scan(a, ("D",))
+    _, rest, _, _, _, _ = oracle_scan(a, ())
+    tol = F32 * my[0]
+    if dtype == torch.bfloat16:
+        tol = tol + 1.01 * HALF * (np.abs(ry[0]) + rest[0])
+    assert (np.abs(host(y) - ry[0]) <= tol).all()
