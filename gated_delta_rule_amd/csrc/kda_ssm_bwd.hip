@@ -99,6 +99,8 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
     int lane = tid & 63;
     int rN = lane_row<N>(lane), rP = lane_row<P>(lane), rL = lane_row<L>(lane);
     int2 cN = lane_col<N, 4>(lane), cP = lane_col<P, 4>(lane), cL = lane_col<L, 4>(lane);
+    // this lane's four columns of dy in row l & 15 (as it holds dx)
+    int oY = 16 * ss_unit<P / 8>(lane & 15, wave % (P / 16) * 2 + (lane >> 5)) + 8 * (lane >> 4 & 1);
     const int rt = wave % RW, rh = wave / RW;      // this wave's row tile and its share of the token tiles
     const int ct = wave % CW, ch = wave / CW;      // ... column tile ...
     const int n0 = 16 * rt, p0 = 16 * ct;
@@ -294,7 +296,7 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
 
     for (int hk = 0; hk < hwn; ++hk) {
         const int hw = hw0 + hk, h = hfirst + hw;
-        hide(lane), hide(rN), hide(rP), hide(rL), hide(cN), hide(cP), hide(cL);
+        hide(lane), hide(rN), hide(rP), hide(rL), hide(cN), hide(cP), hide(cL), hide(oY);
         const int l15 = lane & 15, lg = lane >> 4;
         const float* R = q.dstates + (slot * heads + hw) * (N * P);
         const float D = p.D ? p.D[h] : 0.f;
@@ -359,7 +361,7 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
                     M[r] = G[k][r] * l * ds[r];
                     col[r] = G[k][r] * l * E[r];
                     row = fmaf(col[r], ds[r], row);
-                } else {   // nothing above the diagonal, D on it, and W's diagonal apart
+                } else {   // nothing above the diagonal, and W's diagonal apart
                     const int sr = s0 + r;
                     const float l = sr <= t ? __expf((ht - hs[r]) + (lt - ls[r])) : 0.f;
                     K[r] = sr <= t ? E[r] * l * ds[r] : 0.f;
@@ -368,7 +370,6 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
                     col[r] = sr < t ? w : 0.f;
                     row = fmaf(col[r], ds[r], row);
                     if (sr == t) {
-                        M[r] += D;
                         now.W[t] = w;
                         now.E[t] = E[r];
                     }
@@ -554,6 +555,19 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
 #pragma unroll
             for (int k = 0; k < CT; ++k) {
                 const int row = 16 * (ch + CS * k) + l15;
+                float y[4] = {0.f, 0.f, 0.f, 0.f};   // D dy, in float32
+#pragma unroll
+                for (int i = XP - 1; i >= 0; --i) {
+                    const u32x2 u = *reinterpret_cast<const u32x2*>(
+                        reinterpret_cast<const char*>(tY + (i * L + 16 * (ch + CS * k)) * P) + oY);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        y[2 * e] += bf2_first(u[e]);
+                        y[2 * e + 1] += bf2_second(u[e]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dX[k][e] = fmaf(D, y[e], dX[k][e]);
                 if (row < valid) {
                     const int64_t at = (row0 + row) * q.gx_stride + (int64_t)h * P + p0 + 4 * lg;
                     if constexpr (BF)

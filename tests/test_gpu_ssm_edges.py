@@ -90,3 +90,29 @@ def test_skip_term_is_float32(P, dtype):
     if dtype == torch.bfloat16:
         tol = tol + 1.01 * HALF * (np.abs(ry[0]) + rest[0])
     assert (np.abs(host(y) - ry[0]) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("P", [64, 128])
+def test_skip_gradient_is_float32(P, dtype):
+    """Where dt is zero and the state has no gradient, dx is D dy, rounded
+    once; beside other terms D's share of dx keeps that accuracy."""
+    H, N, T = 3, 64, 70
+    gen = torch.Generator(device="cuda").manual_seed(65)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)   # noqa: E731
+    x, B, C, gy = (rnd(1, T, *s).to(dtype) for s in ((H, P), (1, N), (1, N), (H, P)))
+    D = torch.tensor([1 + 2 ** -8 + 2 ** -12, -0.37, 1e-3], device="cuda")
+    A, dt = -torch.ones(H, device="cuda"), torch.full((1, T, H), -1e4, device="cuda")
+    gx = kda.ssm_chunk_bwd(x, dt, A, B, C, D, None, gy)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(gx, (D[:, None] * gy.float()).to(dtype))
+    a = scan_case([T], H, 1, N, P, dtype, seed=66)
+    a["D"] = host(D)
+    gx = run_bwd(a, dtype, ("D",))[0]
+    torch.cuda.synchronize()
+    _, _, _, _, g, m = oracle_scan(a, ("D",), back=True)
+    _, _, _, _, _, rest = oracle_scan(a, (), back=True)
+    tol = F32 * m[0]["x"]
+    if dtype == torch.bfloat16:
+        tol = tol + 1.01 * HALF * (np.abs(g[0]["x"]) + rest[0]["x"])
+    assert (np.abs(host(gx) - g[0]["x"]) <= tol).all()
