@@ -123,9 +123,9 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
  * accumulated in float32.  The products run on bf16 matrix cores.  The state
  * update takes its float32 operands (and, with KDA_F32, the inputs) as sums
  * of three bf16 parts, so S_T is accurate to float32 rounding; so is y with
- * KDA_F32.  With KDA_BF16, S in S^T C and the weighted products C . B are
- * rounded to bf16 once each, a half step of the output's type; D x is added
- * to them in float32.
+ * KDA_F32.  With KDA_BF16, the weighted products C . B within a chunk are
+ * rounded to bf16, a half step of the output's type; S enters S^T C as the sum
+ * of two bf16 parts (2^-16 of it is lost), and D x is added in float32.
  * A token with dt A < -104 (a reset) ends all memory.  One with dt = 0 (the
  * softplus of a large negative number) leaves the state as it is, so a batch
  * may be padded at its end with finite tokens of such dt.

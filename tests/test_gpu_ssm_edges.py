@@ -116,3 +116,19 @@ def test_skip_gradient_is_float32(P, dtype):
     if dtype == torch.bfloat16:
         tol = tol + 1.01 * HALF * (np.abs(g[0]["x"]) + rest[0]["x"])
     assert (np.abs(host(gx) - g[0]["x"]) <= tol).all()
+
+
+@pytest.mark.parametrize("N,P", [(64, 64), (128, 64), (128, 128)])
+def test_state_enters_outputs_beyond_bf16(N, P):
+    """Tokens of dt = 0 read the initial state: y = S0^T C, rounded once.  The
+    state's two bf16 parts leave 2^-16 of it, so a sum whose terms cancel keeps
+    that accuracy (float32 sums as elsewhere)."""
+    H, T = 3, 70
+    a = scan_case([T], H, 1, N, P, torch.bfloat16, seed=67)
+    a["dt"][:] = -1e4
+    y, S = kda.ssm_chunk_fwd(dev(a["x"], torch.bfloat16), dev(a["dt"]), dev(a["A"]), dev(a["B"], torch.bfloat16),
+                             dev(a["C"], torch.bfloat16), None, dev(a["S0"]), dev(a["cu"], torch.int32))
+    torch.cuda.synchronize()
+    ry, my, _, _, _, _ = oracle_scan(a, ("S0",))
+    assert (np.abs(host(y) - ry[0]) <= 1.01 * HALF * np.abs(ry[0]) + (2.0 ** -16 + F32) * my[0]).all()
+    assert torch.equal(S, dev(a["S0"]))
