@@ -132,3 +132,21 @@ def test_state_enters_outputs_beyond_bf16(N, P):
     ry, my, _, _, _, _ = oracle_scan(a, ("S0",))
     assert (np.abs(host(y) - ry[0]) <= 1.01 * HALF * np.abs(ry[0]) + (2.0 ** -16 + F32) * my[0]).all()
     assert torch.equal(S, dev(a["S0"]))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_conv_steps_continue_the_prompt_bitwise(W, dtype):
+    """The convolution of 300 tokens at once, in steps of 64 and one by one:
+    the same bits in outputs and cache."""
+    n, T, c = 2, 300, 520
+    gen = torch.Generator(device="cuda").manual_seed(68)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)   # noqa: E731
+    x, w, bias, cache = (4 * rnd(n, T, c)).to(dtype), rnd(c, W), rnd(c), rnd(n, W - 1, c)
+    whole = cache.clone()
+    y = kda.ssm_conv_fwd(x, w, bias, whole)
+    for step in (64, 1):
+        c1 = cache.clone()
+        parts = [kda.ssm_conv_step(x[:, i:i + step].contiguous(), w, bias, c1) for i in range(0, T, step)]
+        torch.cuda.synchronize()
+        assert torch.equal(torch.cat(parts, 1), y) and torch.equal(c1, whole)
