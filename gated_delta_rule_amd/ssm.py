@@ -45,6 +45,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _of(x):
+    """Device and element type of a call's x."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise KDAError("x must be a torch.Tensor")
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+        raise KDAError(f"x must be bfloat16 or float32, got {x.dtype}")
+    return x.device, _in_dtype(x)
+
+
 def _check_rows(t, name, lead, tail, dtype, dev):
     """A tensor [*lead, *tail] whose rows (the tail) are contiguous and evenly
     spaced over the leading axes; returns the row stride in elements."""
@@ -138,14 +148,14 @@ def _nbytes(t):
 
 def _conv_args(x, w, bias):
     import torch
-    dev = x.device
+    dev, dt = _of(x)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise KDAError("w must be [channels, width]")
     _check(w, "w", torch.float32, dev)
     channels, width = w.shape
     if bias is not None:
         _check_shape(bias, "bias", (channels,), dev)
-    return dev, _in_dtype(x), channels, width
+    return dev, dt, channels, width
 
 
 def ssm_conv_fwd(x, w, bias=None, cache=None, cu_seqlens=None, *, activation=True, y=None):
@@ -242,8 +252,8 @@ class _Scan:
 
     def __init__(self, x, dt, A, B, C, D, S0, cu_seqlens, dt_bias):
         import torch
-        self.dev = dev = x.device
-        self.dtype = _in_dtype(x)
+        dev, self.dtype = _of(x)
+        self.dev = dev
         self.lead, self.n_seqs, self.T = _lead(x, 2, cu_seqlens, "x", dev)
         self.H, self.P = x.shape[-2:]
         if not isinstance(B, torch.Tensor) or B.dim() < 2:
@@ -370,6 +380,8 @@ def ssm_recurrent_fwd(x, dt, A, B, C, S, D=None, *, dt_bias=None, softplus=True,
     a = _Scan(x, dt, A, B, C, D, S, None, dt_bias)
     Tr, rx, rdt, rB, rxs, rbs = 0, None, None, None, a.H * a.P, a.G * a.N
     if replay is not None:
+        if not isinstance(replay, (tuple, list)) or len(replay) != 3:
+            raise KDAError("replay must be (x, dt, B)")
         rx, rdt, rB = replay
         rlead, Br, Tr = _lead(rx, 2, None, "replay x", a.dev)
         if Br != a.n_seqs:

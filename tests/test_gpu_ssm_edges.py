@@ -150,3 +150,10 @@ def test_conv_steps_continue_the_prompt_bitwise(W, dtype):
         parts = [kda.ssm_conv_step(x[:, i:i + step].contiguous(), w, bias, c1) for i in range(0, T, step)]
         torch.cuda.synchronize()
         assert torch.equal(torch.cat(parts, 1), y) and torch.equal(c1, whole)
+
+
+@pytest.mark.parametrize("replay", [3, torch.zeros(1), (None, None, None), (None, None)])
+def test_replay_is_no_triple_of_tensors(replay):
+    x, dt, A, B = (torch.zeros(s, device="cuda") for s in ((1, 2, 2, 64), (1, 2, 2), (2,), (1, 2, 1, 64)))
+    with pytest.raises(kda.KDAError):
+        kda.ssm_recurrent_fwd(x, dt, A, B, B, torch.zeros(1, 2, 64, 64, device="cuda"), replay=replay)
