@@ -101,6 +101,9 @@ def load_library():
             "kda_verify_drafts": [vp, vp, ci, ip, ip, fp, fp, i32, i32, i64, ip, ip, vp, sz, vp]}.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ci
+    for name in ("kda_ssm_conv_bwd", "kda_ssm_chunk_bwd"):   # (csrc/kda_ssm_launch.h)
+        getattr(lib, name + "_fresh").argtypes = getattr(lib, name).argtypes + [ci]
+        getattr(lib, name + "_fresh").restype = ci
     for name, args in {
             "kda_ssm_conv_bwd_workspace_bytes": [i64, i32, i32],
             "kda_ssm_chunk_fwd_workspace_bytes": [i32, i64, i32, i32, i32, i32, ci],

@@ -280,12 +280,12 @@ size_t kda_ssm_conv_bwd_workspace_bytes(int64_t rows, int32_t channels, int32_t 
     return (size_t)(n < 16 ? 16 : n);
 }
 
-int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float* w,
-                     const float* bias, const float* cache, const int32_t* cu_seqlens,
-                     int32_t n_seqs, int64_t T, int32_t channels, int32_t width, int activation,
-                     const void* grad_y, int64_t grad_y_stride, void* grad_x, float* grad_w,
-                     float* grad_bias, float* grad_cache, void* workspace, size_t workspace_bytes,
-                     hipStream_t stream) {
+int kda_ssm_conv_bwd_fresh(const void* x, int64_t x_stride, int in_dtype, const float* w,
+                           const float* bias, const float* cache, const int32_t* cu_seqlens,
+                           int32_t n_seqs, int64_t T, int32_t channels, int32_t width, int activation,
+                           const void* grad_y, int64_t grad_y_stride, void* grad_x, float* grad_w,
+                           float* grad_bias, float* grad_cache, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream, int fresh) {
     int rc = conv_shape(in_dtype, n_seqs, T, channels, width);
     if (rc) return rc;
     int64_t rows = 0;
@@ -340,7 +340,18 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
     q.partial = (float*)workspace;
     q.gy_stride = grad_y_stride;
     q.rows_per_wave = (int32_t)kda::conv_rows_per_wave(rows, channels);
+    q.zero_rest = cu_seqlens && (fresh & KDA_FRESH_X);
     return kda::launch_conv_bwd(q, in_dtype == KDA_BF16, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float* w,
+                     const float* bias, const float* cache, const int32_t* cu_seqlens,
+                     int32_t n_seqs, int64_t T, int32_t channels, int32_t width, int activation,
+                     const void* grad_y, int64_t grad_y_stride, void* grad_x, float* grad_w,
+                     float* grad_bias, float* grad_cache, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream) {
+    return kda_ssm_conv_bwd_fresh(x, x_stride, in_dtype, w, bias, cache, cu_seqlens, n_seqs, T, channels, width,
+                                  activation, grad_y, grad_y_stride, grad_x, grad_w, grad_bias, grad_cache,
+                                  workspace, workspace_bytes, stream, 0);
 }
 
 size_t kda_ssm_chunk_fwd_workspace_bytes(int32_t n_seqs, int64_t T, int32_t H, int32_t G,
@@ -448,15 +459,15 @@ size_t kda_ssm_chunk_bwd_workspace_bytes(int in_dtype, int32_t n_seqs, int64_t T
     return (size_t)b.total * 4;
 }
 
-int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_stride,
-                      const void* C, int64_t C_stride, int in_dtype, const float* dt,
-                      const float* dt_bias, int softplus, const float* A, const float* D,
-                      const float* S0, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
-                      int32_t H, int32_t G, int32_t N, int32_t P, const void* grad_y,
-                      const float* grad_S_T, void* grad_x, int64_t grad_x_stride, void* grad_B,
-                      int64_t grad_B_stride, void* grad_C, int64_t grad_C_stride, float* grad_dt,
-                      float* grad_A, float* grad_D, float* grad_dt_bias, float* grad_S0,
-                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+int kda_ssm_chunk_bwd_fresh(const void* x, int64_t x_stride, const void* B, int64_t B_stride,
+                            const void* C, int64_t C_stride, int in_dtype, const float* dt,
+                            const float* dt_bias, int softplus, const float* A, const float* D,
+                            const float* S0, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
+                            int32_t H, int32_t G, int32_t N, int32_t P, const void* grad_y,
+                            const float* grad_S_T, void* grad_x, int64_t grad_x_stride, void* grad_B,
+                            int64_t grad_B_stride, void* grad_C, int64_t grad_C_stride, float* grad_dt,
+                            float* grad_A, float* grad_D, float* grad_dt_bias, float* grad_S0,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream, int fresh) {
     int rc = scan_shape(in_dtype, n_seqs, T, H, G, N, P);
     if (rc) return rc;
     int64_t rows = 0;
@@ -491,7 +502,7 @@ int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_
     const int64_t per = scan_blocks(groups * (H / G), groups, P);
     if (b.scan.slots * per > kMaxWide || b.slots * groups * b.blocks > kMaxWide ||
         ceil_div((int64_t)n_seqs * H * N * P, 1024) > kMaxWorkgroups ||
-        ceil_div(rows * groups * N, 512) + groups * (int64_t)(H / G) > kMaxWorkgroups)
+        ceil_div(rows * groups * N, 512) + groups * (int64_t)(H / G) + kda::kGradRest > kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
 
     // outputs overlap nothing, except that grad_x, grad_B and grad_C may
@@ -585,9 +596,24 @@ int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_
         q.slots = n_seqs > 0 ? b.slots : 0;
         q.heads_per_block = b.heads_per_block;
         q.blocks = b.blocks;
+        q.zero_rest = varlen && g0 == 0 ? fresh : 0;
         if (kda::launch_ssm_grad(q, bf16_in, stream) != hipSuccess) return KDA_ERR_HIP;
     }
     return KDA_OK;
+}
+int kda_ssm_chunk_bwd(const void* x, int64_t x_stride, const void* B, int64_t B_stride,
+                      const void* C, int64_t C_stride, int in_dtype, const float* dt,
+                      const float* dt_bias, int softplus, const float* A, const float* D,
+                      const float* S0, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
+                      int32_t H, int32_t G, int32_t N, int32_t P, const void* grad_y,
+                      const float* grad_S_T, void* grad_x, int64_t grad_x_stride, void* grad_B,
+                      int64_t grad_B_stride, void* grad_C, int64_t grad_C_stride, float* grad_dt,
+                      float* grad_A, float* grad_D, float* grad_dt_bias, float* grad_S0,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    return kda_ssm_chunk_bwd_fresh(x, x_stride, B, B_stride, C, C_stride, in_dtype, dt, dt_bias, softplus, A, D, S0,
+                                   cu_seqlens, n_seqs, T, H, G, N, P, grad_y, grad_S_T, grad_x, grad_x_stride,
+                                   grad_B, grad_B_stride, grad_C, grad_C_stride, grad_dt, grad_A, grad_D,
+                                   grad_dt_bias, grad_S0, workspace, workspace_bytes, stream, 0);
 }
 
 int kda_ssm_recurrent_fwd(const void* x, int64_t x_stride, const void* Bm, int64_t B_stride,

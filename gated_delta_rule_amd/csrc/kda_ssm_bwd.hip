@@ -655,11 +655,35 @@ __device__ __forceinline__ void ssm_grad_sums(const SsmGradParams& q, int64_t hw
     }
 }
 
-// Both in one launch: `bc` workgroups for dB and dC, then one per head.
+// Zeros in the rows of no sequence (packed batches), a row per workgroup at a
+// time; all columns, of every group of heads.
+template <typename InT>
+__device__ __forceinline__ void ssm_grad_rest(const SsmGradParams& q, int64_t first, int64_t step) {
+    const SsmScanParams& p = q.f;
+    const int64_t begin = ssm_range(p.cu, p.rows, p.T, 0).start;
+    const int64_t end = ssm_range(p.cu, p.rows, p.T, p.n_seqs - 1).end;
+    auto clear = [&](void* to, int64_t at, int64_t n) {   // n elements from `at`, whole 16-byte pieces
+        u32x4* t = reinterpret_cast<u32x4*>((InT*)to + at);
+        for (int64_t i = threadIdx.x; i < n * (int64_t)sizeof(InT) / 16; i += SS_THREADS) t[i] = u32x4{0, 0, 0, 0};
+    };
+    for (int64_t i = first; i < begin + (p.rows - end); i += step) {
+        const int64_t row = i < begin ? i : end + (i - begin);
+        if (q.zero_rest & KDA_FRESH_X) clear(q.gx, row * q.gx_stride, (int64_t)p.H * p.P);
+        if (q.zero_rest & KDA_FRESH_B) clear(q.gB, row * q.gB_stride, (int64_t)p.G * p.N);
+        if (q.zero_rest & KDA_FRESH_C) clear(q.gC, row * q.gC_stride, (int64_t)p.G * p.N);
+        if (q.zero_rest & KDA_FRESH_DT)
+            for (int h = threadIdx.x; h < p.H; h += SS_THREADS) q.gdt[row * p.H + h] = 0.f;
+    }
+}
+
+// All in one launch: `bc` workgroups for dB and dC, then one per head, then
+// those for the rows of no sequence.
 template <typename InT>
 __global__ __launch_bounds__(SS_THREADS) void ssm_grad_tail_kernel(SsmGradParams q, int64_t bc) {
-    if (blockIdx.x < bc) ssm_grad_bc<InT>(q);
-    else ssm_grad_sums(q, (int64_t)blockIdx.x - bc);
+    const int64_t heads = (int64_t)q.f.gn * (q.f.H / q.f.G), i = (int64_t)blockIdx.x - bc;
+    if (i < 0) ssm_grad_bc<InT>(q);
+    else if (i < heads) ssm_grad_sums(q, i);
+    else ssm_grad_rest<InT>(q, i - heads, (int64_t)gridDim.x - bc - heads);
 }
 
 template <typename InT>
@@ -673,8 +697,9 @@ static hipError_t run_grad(const SsmGradParams& q, hipStream_t stream) {
         else hipLaunchKernelGGL((ssm_grad_kernel<InT, 64, 128>), grid, wide, 0, stream, q);
     }
     const int64_t n = q.blocks > 1 ? 2 * (int64_t)p.gn * p.rows * (p.N / 4) : 0, bc = (n + SS_THREADS - 1) / SS_THREADS;
-    hipLaunchKernelGGL(ssm_grad_tail_kernel<InT>, dim3((unsigned)(bc + p.gn * (p.H / p.G))), dim3(SS_THREADS), 0, stream,
-                       q, bc);
+    const int64_t rest = q.zero_rest && p.n_seqs > 0 ? (p.rows < kGradRest ? p.rows : kGradRest) : 0;
+    hipLaunchKernelGGL(ssm_grad_tail_kernel<InT>, dim3((unsigned)(bc + p.gn * (p.H / p.G) + rest)), dim3(SS_THREADS), 0,
+                       stream, q, bc);
     return hipGetLastError();
 }
 hipError_t launch_ssm_grad(const SsmGradParams& q, bool bf16_in, hipStream_t stream) {

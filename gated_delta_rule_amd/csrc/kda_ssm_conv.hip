@@ -348,6 +348,10 @@ __global__ __launch_bounds__(CV_THREADS) void conv_bwd_kernel(ConvBwdParams q) {
             }
             const bool act = INSIDE || p.activation;
             mine = mine << 1 | (INSIDE || (in && row < r1) ? 1u : 0u);
+            if (!INSIDE && q.zero_rest && !in && row < r1) {
+                const float none[4] = {0.f, 0.f, 0.f, 0.f};
+                Vec<InT>::store(q.gx, row * p.channels + c0, none);
+            }
             // rows before this one that this row's z reaches (none outside its sequence)
             const int reach = INSIDE ? W - 1 : in ? (row - k.s.start < W - 1 ? (int)(row - k.s.start) : W - 1) : -1;
             float x[4], g[4];

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime_api.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace kda {
@@ -50,6 +51,7 @@ struct ConvBwdParams {
     float* partial;
     int64_t gy_stride;
     int32_t rows_per_wave;
+    int32_t zero_rest;       // rows of gx that belong to no sequence become zero
 };
 hipError_t launch_conv_bwd(const ConvBwdParams& p, bool bf16_in, hipStream_t stream);
 
@@ -153,7 +155,35 @@ struct SsmGradParams {
     int64_t gx_stride, gB_stride, gC_stride;
     int64_t slots;           // chunk slots
     int32_t heads_per_block, blocks;   // heads of a group per workgroup; workgroups per group
+    int32_t zero_rest;       // KDA_FRESH_*: these outputs' rows of no sequence become zero
 };
+constexpr int64_t kGradRest = 256;   // workgroups that see to them, at most
 hipError_t launch_ssm_grad(const SsmGradParams& p, bool bf16_in, hipStream_t stream);
 
 }  // namespace kda
+
+// The backward passes for outputs of the binding's own making: as their
+// namesakes in include/kda_ssm.h, but rows of no sequence become zero (the
+// gradient of rows that affect nothing) in the outputs that `fresh` names,
+// where the others keep what their owner has put there.
+#define KDA_FRESH_X 1
+#define KDA_FRESH_B 2
+#define KDA_FRESH_C 4
+#define KDA_FRESH_DT 8
+extern "C" {
+int kda_ssm_conv_bwd_fresh(const void* x, int64_t x_stride, int in_dtype, const float* w,
+                           const float* bias, const float* cache, const int32_t* cu_seqlens,
+                           int32_t n_seqs, int64_t T, int32_t channels, int32_t width, int activation,
+                           const void* grad_y, int64_t grad_y_stride, void* grad_x, float* grad_w,
+                           float* grad_bias, float* grad_cache, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream, int fresh);
+int kda_ssm_chunk_bwd_fresh(const void* x, int64_t x_stride, const void* B, int64_t B_stride,
+                            const void* C, int64_t C_stride, int in_dtype, const float* dt,
+                            const float* dt_bias, int softplus, const float* A, const float* D,
+                            const float* S0, const int32_t* cu_seqlens, int32_t n_seqs, int64_t T,
+                            int32_t H, int32_t G, int32_t N, int32_t P, const void* grad_y,
+                            const float* grad_S_T, void* grad_x, int64_t grad_x_stride, void* grad_B,
+                            int64_t grad_B_stride, void* grad_C, int64_t grad_C_stride, float* grad_dt,
+                            float* grad_A, float* grad_D, float* grad_dt_bias, float* grad_S0,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream, int fresh);
+}

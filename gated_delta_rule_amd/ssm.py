@@ -142,6 +142,17 @@ def _like(t):
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
+# Outputs that a backward call makes itself, by their bits in csrc/kda_ssm_launch.h.
+_FRESH_X, _FRESH_B, _FRESH_C, _FRESH_DT = 1, 2, 4, 8
+
+
+def _grad_like(t, n_seqs):
+    """Like _like, for the gradient of token rows: the kernels write every row
+    of a batch that has a sequence at all."""
+    import torch
+    return _like(t) if n_seqs else torch.zeros_like(t, memory_format=torch.contiguous_format)
+
+
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -165,7 +176,9 @@ def ssm_conv_fwd(x, w, bias=None, cache=None, cu_seqlens=None, *, activation=Tru
     x [B, T, channels] (or packed [T, channels] with cu_seqlens), bfloat16 or
     float32; w [channels, width] float32; bias [channels] or None; cache
     [n_seqs, width - 1, channels] float32, updated in place, or None.
-    activation=False leaves out the SiLU.  Returns y like x, contiguous.
+    activation=False leaves out the SiLU.  Returns y like x, contiguous.  Rows
+    of no sequence are not written: in a packed batch that has some, a y that
+    is not given is undefined there.
     """
     import torch
     lib = load_library()
@@ -224,7 +237,8 @@ def ssm_conv_bwd(x, w, bias, grad_y, cache=None, cu_seqlens=None, *, activation=
     """Backward pass of ssm_conv_fwd (see kda_ssm_conv_bwd in
     include/kda_ssm.h).  `cache` is the one from before the forward call.
     Returns (grad_x in x's dtype, grad_w, grad_bias, grad_cache); grad_bias
-    and grad_cache are None where bias and cache are.
+    and grad_cache are None where bias and cache are.  In packed batches
+    grad_x is zero in rows of no sequence.
     """
     import torch
     lib = load_library()
@@ -234,15 +248,16 @@ def ssm_conv_bwd(x, w, bias, grad_y, cache=None, cu_seqlens=None, *, activation=
     gs = _check_rows(grad_y, "grad_y", lead, (channels,), x.dtype, dev)
     if cache is not None:
         _check_shape(cache, "cache", (n_seqs, width - 1, channels), dev)
-    gx, gw = _like(x), _like(w)
+    gx, gw = _grad_like(x, n_seqs), _like(w)
     gb = None if bias is None else _like(bias)
     gc = None if cache is None else _like(cache)
     rows = T if cu_seqlens is not None else n_seqs * T
     ws = _workspace(workspace, int(lib.kda_ssm_conv_bwd_workspace_bytes(rows, channels, width)), dev)
     with _on(dev):
-        rc = lib.kda_ssm_conv_bwd(_ptr(x), xs, dt, _ptr(w), _ptr(bias), _ptr(cache), _ptr(cu_seqlens),
-                                  n_seqs, T, channels, width, int(bool(activation)), _ptr(grad_y), gs,
-                                  _ptr(gx), _ptr(gw), _ptr(gb), _ptr(gc), _ptr(ws), _nbytes(ws), _stream(dev))
+        rc = lib.kda_ssm_conv_bwd_fresh(_ptr(x), xs, dt, _ptr(w), _ptr(bias), _ptr(cache), _ptr(cu_seqlens),
+                                        n_seqs, T, channels, width, int(bool(activation)), _ptr(grad_y), gs,
+                                        _ptr(gx), _ptr(gw), _ptr(gb), _ptr(gc), _ptr(ws), _nbytes(ws),
+                                        _stream(dev), _FRESH_X)
     _status(rc, "kda_ssm_conv_bwd")
     return gx, gw, gb, gc
 
@@ -286,7 +301,9 @@ def ssm_chunk_fwd(x, dt, A, B, C, D=None, S0=None, cu_seqlens=None, *, dt_bias=N
     softplus of dt + dt_bias (softplus=False: dt + dt_bias as given); A, D,
     dt_bias [H] float32; S0 [n_seqs, H, N, P] float32 or None.  Returns
     (y like x, contiguous; S_T [n_seqs, H, N, P] float32 or None).
-    sequence_parallel=False keeps every sequence on one chain.
+    sequence_parallel=False keeps every sequence on one chain.  Rows of no
+    sequence are not written: in a packed batch that has some, a y that is not
+    given is undefined there.
     """
     import torch
     lib = load_library()
@@ -330,7 +347,9 @@ def ssm_chunk_bwd(x, dt, A, B, C, D, S0, grad_y, grad_S_T=None, cu_seqlens=None,
     float32 or None.  grad_x, grad_B, grad_C may be given as views of wider
     rows, like x, B and C.  Returns (grad_x, grad_dt, grad_A, grad_B, grad_C,
     grad_D, grad_dt_bias, grad_S0); grad_D and grad_dt_bias are None where D
-    and dt_bias are, grad_S0 with want_grad_S0=False.
+    and dt_bias are, grad_S0 with want_grad_S0=False.  In packed batches, rows
+    of no sequence keep what they held in tensors that are given and are zero
+    in the others.
     """
     import torch
     lib = load_library()
@@ -338,14 +357,16 @@ def ssm_chunk_bwd(x, dt, A, B, C, D, S0, grad_y, grad_S_T=None, cu_seqlens=None,
     _check_shape(grad_y, "grad_y", x.shape, a.dev, x.dtype)
     if grad_S_T is not None:
         _check_shape(grad_S_T, "grad_S_T", a.state, a.dev)
-    outs = []
-    for name, t, like, tail in (("grad_x", grad_x, x, (a.H, a.P)), ("grad_B", grad_B, B, (a.G, a.N)),
-                                ("grad_C", grad_C, C, (a.G, a.N))):
+    outs, fresh = [], _FRESH_DT
+    for name, t, like, tail, bit in (("grad_x", grad_x, x, (a.H, a.P), _FRESH_X),
+                                     ("grad_B", grad_B, B, (a.G, a.N), _FRESH_B),
+                                     ("grad_C", grad_C, C, (a.G, a.N), _FRESH_C)):
         if t is None:
-            t = _like(like)
+            t = _grad_like(like, a.n_seqs)
+            fresh |= bit
         outs.append((t, _check_rows(t, name, a.lead, tail, x.dtype, a.dev)))
     (gx, gxs), (gB, gBs), (gC, gCs) = outs
-    gdt, gA = _like(dt), _like(A)
+    gdt, gA = _grad_like(dt, a.n_seqs), _like(A)
     gD = None if D is None else _like(D)
     gbias = None if dt_bias is None else _like(dt_bias)
     like = S0 if S0 is not None else grad_S_T
@@ -354,12 +375,12 @@ def ssm_chunk_bwd(x, dt, A, B, C, D, S0, grad_y, grad_S_T=None, cu_seqlens=None,
     ws = _workspace(workspace, ssm_chunk_bwd_workspace_bytes(x.dtype, a.n_seqs, a.T, a.H, a.G, a.N, a.P,
                                                              cu_seqlens is not None), a.dev)
     with _on(a.dev):
-        rc = lib.kda_ssm_chunk_bwd(_ptr(x), a.xs, _ptr(B), a.bs, _ptr(C), a.cs, a.dtype, _ptr(dt),
-                                   _ptr(dt_bias), int(bool(softplus)), _ptr(A), _ptr(D), _ptr(S0),
-                                   _ptr(cu_seqlens), a.n_seqs, a.T, a.H, a.G, a.N, a.P, _ptr(grad_y),
-                                   _ptr(grad_S_T), _ptr(gx), gxs, _ptr(gB), gBs, _ptr(gC), gCs, _ptr(gdt),
-                                   _ptr(gA), _ptr(gD), _ptr(gbias), _ptr(gS0), _ptr(ws), _nbytes(ws),
-                                   _stream(a.dev))
+        rc = lib.kda_ssm_chunk_bwd_fresh(_ptr(x), a.xs, _ptr(B), a.bs, _ptr(C), a.cs, a.dtype, _ptr(dt),
+                                         _ptr(dt_bias), int(bool(softplus)), _ptr(A), _ptr(D), _ptr(S0),
+                                         _ptr(cu_seqlens), a.n_seqs, a.T, a.H, a.G, a.N, a.P, _ptr(grad_y),
+                                         _ptr(grad_S_T), _ptr(gx), gxs, _ptr(gB), gBs, _ptr(gC), gCs, _ptr(gdt),
+                                         _ptr(gA), _ptr(gD), _ptr(gbias), _ptr(gS0), _ptr(ws), _nbytes(ws),
+                                         _stream(a.dev), fresh)
     _status(rc, "kda_ssm_chunk_bwd")
     return gx, gdt, gA, gB, gC, gD, gbias, gS0
 

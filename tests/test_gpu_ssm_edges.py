@@ -157,3 +157,56 @@ def test_replay_is_no_triple_of_tensors(replay):
     x, dt, A, B = (torch.zeros(s, device="cuda") for s in ((1, 2, 2, 64), (1, 2, 2), (2,), (1, 2, 1, 64)))
     with pytest.raises(kda.KDAError):
         kda.ssm_recurrent_fwd(x, dt, A, B, B, torch.zeros(1, 2, 64, 64, device="cuda"), replay=replay)
+
+
+def dirty(*likes):
+    """Leaves NaN in the memory that the next tensors of these sizes get."""
+    old = [torch.full_like(t, float("nan")) for t in likes for _ in range(3)]
+    torch.cuda.synchronize()
+    del old
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("before,lens,behind", [(5, [70, 9], 16), (0, [33, 0, 1], 300), (64, [40], 0), (3, [0], 4), (2, [], 30)])
+def test_gradients_of_rows_of_no_sequence_are_zero(before, lens, behind, dtype):
+    """What the call allocates is zero there, what is given stays, and the
+    gradients of the sequences' rows are those of a batch without such rows."""
+    H, G, N, P, c = 4, 2, 64, 64, 72
+    n, real, T = len(lens), sum(lens), before + sum(lens) + behind
+    gen = torch.Generator(device="cuda").manual_seed(69)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=gen)   # noqa: E731
+    at = slice(before, before + real)
+    cu = torch.tensor([before + sum(lens[:i]) for i in range(n + 1)], dtype=torch.int32, device="cuda")
+    x, B, C, gy = (rnd(T, *s).to(dtype) for s in ((H, P), (G, N), (G, N), (H, P)))
+    dt, A, D, S0 = rnd(T, H), -torch.rand(H, device="cuda", generator=gen), rnd(H), rnd(n, H, N, P)
+    cx, cg, w, bias, cache = rnd(T, c).to(dtype), rnd(T, c).to(dtype), rnd(c, 4), rnd(c), rnd(n, 3, c)
+    rest = [i for i in range(T) if not before <= i < before + real]
+    for t in (x, B, C, gy, dt, cx, cg):
+        t[rest] = float("nan")
+    own = cu - before
+    args = (x, dt, A, B, C, D, S0)
+    part = tuple(t[at].contiguous() for t in (x, dt)) + (A,) + tuple(t[at].contiguous() for t in (B, C)) + (D, S0)
+    dirty(x, B, C, dt, cx)
+    for activation in (True, False):
+        g = kda.ssm_conv_bwd(cx, w, bias, cg, cache, cu, activation=activation)
+        ref = kda.ssm_conv_bwd(cx[at].contiguous(), w, bias, cg[at].contiguous(), cache, own, activation=activation)
+        torch.cuda.synchronize()
+        assert not g[0][rest].any() and torch.equal(g[0][at], ref[0]) and torch.equal(g[3], ref[3])
+        assert torch.isfinite(g[1]).all() and torch.isfinite(g[2]).all()
+    dirty(x, B, C, dt)
+    r = kda.ssm_chunk_bwd(*args, gy, None, cu, dt_bias=D)
+    given = [torch.full_like(t, 3.0) for t in (x, B, C)]
+    r2 = kda.ssm_chunk_bwd(*args, gy, None, cu, dt_bias=D, grad_x=given[0], grad_B=given[1], grad_C=given[2])
+    ref = kda.ssm_chunk_bwd(*part, gy[at].contiguous(), None, own, dt_bias=D)
+    torch.cuda.synchronize()
+    for i in (0, 1, 3, 4):
+        assert not r[i][rest].any()
+        if i != 1:
+            assert (r2[i][rest] == 3).all()
+        else:
+            assert not r2[i][rest].any()
+        assert torch.equal(r2[i][at], r[i][at])
+        got, want = r[i][at].float(), ref[i].float()   # (segments may start elsewhere: rounding)
+        torch.testing.assert_close(got, want, rtol=2 ** -7 if dtype == torch.bfloat16 and i != 1 else 1e-5,
+                                   atol=1e-5 * float(want.abs().max()) if want.numel() else 0)
+    assert all(torch.isfinite(t).all() for t in r)
