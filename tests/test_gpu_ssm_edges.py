@@ -212,3 +212,29 @@ def test_gradients_of_rows_of_no_sequence_are_zero(before, lens, behind, dtype):
         torch.testing.assert_close(got, want, rtol=2 ** -7 if dtype == torch.bfloat16 and i != 1 else 1e-5,
                                    atol=1e-5 * float(want.abs().max()) if want.numel() else 0)
     assert all(torch.isfinite(t).all() for t in r)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_padded_batch_gradients(dtype):
+    """Sequences padded with tokens of dt = 0, too short to be cut: the packed
+    batch's gradients, bitwise where the padding only adds zeros to the same
+    sums, and each sum over all tokens within its own tolerance."""
+    lens, T, H, G, N, P = [150, 64, 3], 160, 4, 2, 64, 64
+    a = scan_case(lens, H, G, N, P, dtype, seed=70)
+    t = {k: dev(a[k], torch.float32 if k == "dt" else dtype) for k in ("x", "dt", "B", "C", "gy")}
+    pad = {}
+    for k, v in t.items():
+        pad[k] = torch.full((len(lens), T) + v.shape[1:], {"dt": -1e4, "gy": 0.0}.get(k, 3.0), dtype=v.dtype, device="cuda")
+        for i, (s, e) in enumerate(zip(a["cu"], a["cu"][1:])):
+            pad[k][i, :e - s] = v[s:e]
+    rest = [dev(a[k]) for k in ("D", "S0")]
+    call = lambda v, cu: kda.ssm_chunk_bwd(v["x"], v["dt"], dev(a["A"]), v["B"], v["C"], *rest, v["gy"], dev(a["gS"]), cu,   # noqa: E731
+                                           dt_bias=dev(a["dt_bias"]))
+    r, rp = call(t, dev(a["cu"], torch.int32)), list(call(pad, None))
+    torch.cuda.synchronize()
+    for i in (0, 1, 3, 4):
+        rp[i] = torch.cat([rp[i][j, :n] for j, n in enumerate(lens)])
+        assert torch.equal(rp[i], r[i]), i
+    assert torch.equal(rp[7], r[7])
+    check_bwd(r, a, USE, dtype)
+    check_bwd(rp, a, USE, dtype)
