@@ -17,7 +17,7 @@ constexpr int32_t kMaxTokens = 64;        // tokens per request in the step form
 constexpr int64_t kScanUnits = 256;       // compute units
 constexpr int64_t kScanFill = 2 * kScanUnits;   // chains that fill them
 constexpr int64_t kScanLongSeg = 512, kScanMinSeg = 128, kScanMinSegF32 = 64;   // see scan_plan
-constexpr int64_t kScanMinCut = 3, kScanMinCutBwd = 5;   // segments from which two passes are shorter than one chain
+constexpr int64_t kScanMinCut = 3;        // segments from which two passes are shorter than one chain
 constexpr int64_t kScanAlign = 64;
 constexpr int64_t kVerifyFill = 2048;     // workgroups of the verification (512 to 2048: the same time)
 // Workgroups of the gradient kernel that fill the GPU (its LDS leaves room for
@@ -112,11 +112,17 @@ int64_t scan_blocks(int32_t H, int32_t G, int32_t P) { return (int64_t)G * ceil_
 // 8192 tokens 122.  Float32 chains take four times as long per token, so their
 // segments go down to 64 (16 heads of 64, N 128: 256 tokens 26 against 37 us
 // with 128, 1024 tokens 32 against 40; 16 of 128, N 64: 20.5 against 24 and 29
-// against 31, but 4 x 256 tokens 27 against 25).  The backward pass, whose two
-// directions fill twice as much, cuts from five segments (bf16, heads of 64,
-// cut / one chain: 300 tokens of 16 heads 50 / 44 us, 512 of 64 heads 70 / 62,
-// 640 of 16 heads 53 / 58; float32: 256 of 64 heads 70 / 62, 300 of 16 heads
-// 54 / 56, 440 of 16 heads 54 / 67).
+// against 31, but 4 x 256 tokens 27 against 25).
+//
+// The backward pass's two directions fill the GPU twice as far, so it cuts
+// from four segments of twice the least length, or five.  Cut / whole, us: three
+// segments, bf16, 3 x 512 tokens of 32 heads of 64 99 / 76, 3 x 4096 of 64 heads
+// 644 / 624, float32 3 x 1024 of 32 heads 252 / 220; four short ones, bf16 512
+// tokens of 64 heads 71 / 64, float32 256 tokens 70 / 62; four longer ones, bf16
+// 1024 tokens 88 / 89, 1536 134 / 142, 2 x 4096 409 / 420 (but 2 x 2048 228 /
+// 216), float32 512 tokens 90 / 91, 1024 131 / 148; five and more, bf16 640
+// tokens of 16 heads 53 / 58, 4096 of 64 heads 229 / 283, float32 300 tokens of
+// 16 heads 54 / 56, 2048 of 32 heads 132 / 224.
 struct ScanPlan {
     bool cut;
     int64_t seg_len, slots;
@@ -132,7 +138,7 @@ ScanPlan scan_plan(bool bf16_in, int32_t n_seqs, int64_t T, int64_t blocks, bool
     len = len < least ? least : len > kScanLongSeg ? kScanLongSeg : len;
     if (len < ceil_div(work, kScanFill)) len = ceil_div(work, kScanFill);
     const int64_t segs = ceil_div(T, len);
-    if (segs < (dirs == 2 ? kScanMinCutBwd : kScanMinCut)) return whole;
+    if (segs < (dirs == 1 ? kScanMinCut : len >= 2 * least ? kScanMinCut + 1 : kScanMinCut + 2)) return whole;
     if (!varlen) len = ceil_div(T, segs);
     len = ceil_div(len, kScanAlign) * kScanAlign;
     return ScanPlan{true, len, varlen ? T / len + n_seqs : n_seqs * ceil_div(T, len)};
