@@ -17,7 +17,7 @@ constexpr int32_t kMaxTokens = 64;        // tokens per request in the step form
 constexpr int64_t kScanUnits = 256;       // compute units
 constexpr int64_t kScanFill = 2 * kScanUnits;   // chains that fill them
 constexpr int64_t kScanLongSeg = 512, kScanMinSeg = 128, kScanMinSegF32 = 64;   // see scan_plan
-constexpr int64_t kScanMinCut = 3;        // segments from which two passes are shorter than one chain
+constexpr int64_t kScanMinCut = 4;        // segments from which two passes are shorter than one chain
 constexpr int64_t kScanAlign = 64;
 constexpr int64_t kVerifyFill = 2048;     // workgroups of the verification (512 to 2048: the same time)
 // Workgroups of the gradient kernel that fill the GPU (its LDS leaves room for
@@ -114,6 +114,11 @@ int64_t scan_blocks(int32_t H, int32_t G, int32_t P) { return (int64_t)G * ceil_
 // with 128, 1024 tokens 32 against 40; 16 of 128, N 64: 20.5 against 24 and 29
 // against 31, but 4 x 256 tokens 27 against 25).
 //
+// Three segments leave the two passes as long as one chain.  Cut / whole, us:
+// bf16 300 tokens of 64 heads 29 / 26, 6 x 400 of 32 heads 54 / 36, 6 x 4096 of
+// 64 heads 325 / 280, float32 6 x 2048 of 64 heads 373 / 281; four, bf16 400 tokens of 64 heads 31 / 34, 4 x 2048 122 / 140,
+// float32 2 x 512 48 / 74 (but 4 x 400 of 16 heads of 128 27 / 23).
+//
 // The backward pass's two directions fill the GPU twice as far, so it cuts
 // from four segments of twice the least length, or five.  Cut / whole, us: three
 // segments, bf16, 3 x 512 tokens of 32 heads of 64 99 / 76, 3 x 4096 of 64 heads
@@ -138,7 +143,7 @@ ScanPlan scan_plan(bool bf16_in, int32_t n_seqs, int64_t T, int64_t blocks, bool
     len = len < least ? least : len > kScanLongSeg ? kScanLongSeg : len;
     if (len < ceil_div(work, kScanFill)) len = ceil_div(work, kScanFill);
     const int64_t segs = ceil_div(T, len);
-    if (segs < (dirs == 1 ? kScanMinCut : len >= 2 * least ? kScanMinCut + 1 : kScanMinCut + 2)) return whole;
+    if (segs < (dirs == 1 || len >= 2 * least ? kScanMinCut : kScanMinCut + 1)) return whole;
     if (!varlen) len = ceil_div(T, segs);
     len = ceil_div(len, kScanAlign) * kScanAlign;
     return ScanPlan{true, len, varlen ? T / len + n_seqs : n_seqs * ceil_div(T, len)};
