@@ -208,9 +208,9 @@ int kda_ssm_conv_fwd(const void* x, int64_t x_stride, int in_dtype, const float*
     if (ceil_div(rows, 32) * ceil_div(channels, 256) > kMaxWorkgroups ||
         ceil_div((int64_t)n_seqs * channels, 256) > kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
-    if ((rows > 0 && (!x || !w || !y))) return KDA_ERR_NULL_POINTER;
+    if (rows > 0 && (!x || !w || !y)) return KDA_ERR_NULL_POINTER;
     const int64_t es = elem_size(in_dtype);
-    if ((rc = check_stride(x_stride, channels, es))) return rc;
+    if (rows > 0 && (rc = check_stride(x_stride, channels, es))) return rc;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(cache, 16) ||
         !aligned(bias, 4) || !aligned(cu_seqlens, 4))
         return KDA_ERR_MISALIGNED;

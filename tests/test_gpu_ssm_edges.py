@@ -238,3 +238,27 @@ def test_padded_batch_gradients(dtype):
     assert torch.equal(rp[7], r[7])
     check_bwd(r, a, USE, dtype)
     check_bwd(rp, a, USE, dtype)
+
+
+def test_calls_without_rows_need_no_stride():
+    """No token rows: no pointer or row stride of theirs is looked at, by any
+    of the calls, and states and caches stay."""
+    lib, s = kda.load_library(), torch.cuda.current_stream().cuda_stream
+    H, N, P, c, n = 2, 64, 64, 16, 3
+    f = lambda *sh: torch.randn(*sh, device="cuda")   # noqa: E731
+    cache, S, A, w, gA, gw = f(n, 3, c), f(n, H, N, P), -torch.rand(H, device="cuda"), f(c, 4), f(H), f(c, 4)
+    old, S_old = cache.clone(), S.clone()
+    p = lambda t: t.data_ptr()   # noqa: E731
+    assert lib.kda_ssm_conv_fwd(None, 0, 0, p(w), None, p(cache), None, n, 0, c, 4, 1, None, s) == 0
+    assert lib.kda_ssm_conv_step(None, 0, 0, p(w), None, p(cache), None, 0, None, n, 0, 0, c, 4, 1, 1, None, s) == 0
+    assert lib.kda_ssm_conv_bwd(None, 0, 0, p(w), None, None, None, n, 0, c, 4, 1, None, 0, None, p(gw), None, None, None,
+                                0, s) == 0
+    assert lib.kda_ssm_chunk_fwd(None, 0, None, 0, None, 0, 0, None, None, 1, p(A), None, p(S), None, n, 0, H, 1, N, P, None,
+                                 p(S), None, 0, s) == 0
+    ws = torch.empty(kda.ssm_chunk_bwd_workspace_bytes(torch.bfloat16, n, 0, H, 1, N, P, False), dtype=torch.uint8, device="cuda")
+    assert lib.kda_ssm_chunk_bwd(None, 0, None, 0, None, 0, 0, None, None, 1, p(A), None, None, None, n, 0, H, 1, N, P, None,
+                                 p(S), None, 0, None, 0, None, 0, None, p(gA), None, None, p(S), p(ws), ws.numel(), s) == 0
+    assert lib.kda_ssm_recurrent_fwd(None, 0, None, 0, None, 0, 0, None, None, 1, p(A), None, None, 0, None, 0, None, None,
+                                     p(S), n, 0, 0, H, 1, N, P, 1, None, s) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(cache, old) and torch.equal(S, S_old) and not gA.any() and not gw.any()
