@@ -106,10 +106,13 @@ int64_t scan_blocks(int32_t H, int32_t G, int32_t P) { return (int64_t)G * ceil_
 // traffic (two reads and writes of N x P floats per head): long segments for
 // two chains per unit, shorter ones for one, none below 128 tokens.  Measured
 // (64 heads of 64, one group, N 128, bf16, one sequence, cut against one
-// chain): 512 tokens 31.5 against 37.0 us, 1024 35.4 / 69, 2048 48 / 137, 8192
-// 117 / 531; segments of 64 tokens at 256 tokens 25.7 / 20.8.  Other lengths:
-// segments of 128 at 2048 tokens 54 us, of 256 at 1024 tokens 42, of 1024 at
-// 8192 tokens 122.  Float32 chains take four times as long per token, so their
+// chain): 512 tokens 32.4 against 38.4 us, 1024 36 / 71, 2048 49 / 138, 4096
+// 71 / 270; segments of 64 tokens at 256 tokens 25.7 / 20.8.  Other lengths
+// (against 48, 35 and 117 us at that time): segments of 128 at 2048 tokens 54
+// us, of 256 at 1024 tokens 42, of 1024 at 8192 tokens 122.  A packed batch is
+// planned by the number of its sequences, whatever their lengths: one long
+// one beside so many short ones that there are 512 chains runs as one chain.
+// Float32 chains take four times as long per token, so their
 // segments go down to 64 (16 heads of 64, N 128: 256 tokens 26 against 37 us
 // with 128, 1024 tokens 32 against 40; 16 of 128, N 64: 20.5 against 24 and 29
 // against 31, but 4 x 256 tokens 27 against 25).

@@ -24,8 +24,8 @@
 // S and R come straight from memory into operand registers, each row once and
 // one head ahead; R's bf16 rounding for dx goes through LDS.
 //
-// Measured (MI355X, 2 x 4096 tokens, 64 heads of 64, N 128, bf16): 191 us for
-// 0.74 GB, 0.54 GB of them S and R.  Bound by issue: 12 500 cycles per chunk
+// Measured (MI355X, 2 x 4096 tokens, 64 heads of 64, N 128, bf16): 195 us for
+// 0.74 GB, 0.54 GB of them S and R.  Bound by issue: 12 700 cycles per chunk
 // and head, half of them vector instructions, a third in the two products with
 // S and R (their float32 operands are split into three bf16 parts), 1 100 in
 // requests; matrix cores 0.18 busy.  What is the same for all heads stays in
@@ -71,8 +71,10 @@ __global__ __launch_bounds__(SG_THREADS, 2) void ssm_grad_kernel(SsmGradParams q
     constexpr bool BF = sizeof(InT) == 2;
     constexpr int L = BF ? 64 : 32;
     constexpr int XP = BF ? 1 : 3;      // bf16 parts of an input
-    constexpr int KP = BF ? 1 : 3;      // ... of the chunk matrices (their products are rounded to the input type)
-    constexpr int RP = BF ? 1 : 3;      // ... of R in dx
+    // ... of the chunk matrices, and of R in dx.  With one for bf16, dx, dB and
+    // dC are 1.94e-3 off 64 bits where rounding them alone is 1.66e-3 (the
+    // case above); a second plane of R does not fit in LDS.
+    constexpr int KP = BF ? 1 : 3, RP = BF ? 1 : 3;
     constexpr int SP = 3;               // ... of S and R where U and V come from (float32 results)
     constexpr int TT = L / 16, OFFD = TT * (TT - 1) / 2;   // 16 x 16 tiles below the diagonal
     constexpr int OW = SG_WAVES - TT, TPW = (OFFD + OW - 1) / OW;      // the waves that own them, tiles per wave

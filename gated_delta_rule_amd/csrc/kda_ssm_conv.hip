@@ -208,8 +208,8 @@ __global__ __launch_bounds__(CV_THREADS) void conv_fwd_kernel(ConvParams p, int3
     }
 }
 
-// The cache after the call, as a launch of its own: no lane of the
-// convolution reads an entry that another has replaced.
+// The cache after the call, as a launch of its own: a sequence's first W - 1
+// rows can belong to several waves, which all read the old entries.
 template <typename InT, int W>
 __global__ __launch_bounds__(64) void conv_cache_update_kernel(ConvParams p) {
     const int64_t nv = p.channels / 4;

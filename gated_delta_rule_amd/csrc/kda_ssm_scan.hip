@@ -24,10 +24,10 @@
 // head), and the full pass runs all segments side by side.
 //
 // Measured (MI355X, bf16, N 128): 8192 tokens of 64 heads of 64 in 16 segments
-// 110 to 118 us (local 42, merge 13, outputs 70); 16 packed sequences of 8192
-// tokens, 96 heads of 128, one pass, 200 to 205 us.  Neither HBM (28 and 124 us) nor the
-// matrix cores (0.28 busy): per chunk the compute unit's two workgroups take
-// 13 000 cycles, with vector instructions in 0.56 and LDS in 0.38 of them, and
+// 123 to 131 us (local 42, merge 13, outputs 81); 16 packed sequences of 8192
+// tokens, 96 heads of 128, one pass, 222 to 229 us.  Neither HBM (28 and 124 us) nor the
+// matrix cores (0.33 busy): per chunk the compute unit's two workgroups take
+// 14 000 cycles, with vector instructions in 0.63 and LDS in 0.38 of them, and
 // three barriers between dependent products.
 #include "kda_ssm_tile.h"
 

@@ -116,9 +116,9 @@ int kda_ssm_conv_bwd(const void* x, int64_t x_stride, int in_dtype, const float*
  * With few (sequence, head) pairs and long sequences each sequence is cut
  * into segments that run side by side: their local final states come first,
  * a merge gives each segment's incoming state, then all outputs run.  That
- * needs kda_ssm_chunk_fwd_workspace_bytes(...) (0: no cut pays); with less
- * (or NULL) every sequence runs as one chain, with the same result up to
- * rounding.
+ * needs at most kda_ssm_chunk_fwd_workspace_bytes(...), the larger need of the
+ * two types (0: neither is cut); with less than its own type's need (or NULL)
+ * every sequence runs as one chain, with the same result up to rounding.
  * Numerics: decay sums in float64 within a chunk, everything else
  * accumulated in float32.  The products run on bf16 matrix cores.  The state
  * update takes its float32 operands (and, with KDA_F32, the inputs) as sums
@@ -148,6 +148,11 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* B, int64_t B_
  *   be grad_S_T itself).
  * grad_B and grad_C are summed over a group's heads in float32 and rounded
  * once.  grad_dt is the gradient of the raw dt.
+ * Numerics: as for the forward call, the float32 gradients to float32
+ * rounding.  With KDA_BF16, the weighted products C . B (for grad_x) and
+ * grad_y . x (for grad_B and grad_C, per head) within a chunk and the state
+ * gradient in grad_x are rounded to bf16 once each; D grad_y is added in
+ * float32.
  * workspace: at least kda_ssm_chunk_bwd_workspace_bytes(..., 1) and at most
  * useful kda_ssm_chunk_bwd_workspace_bytes(..., G) bytes, 16-byte aligned,
  * clobbered: it holds the state at every chunk's start (64 tokens; 32
