@@ -16,6 +16,8 @@ calls raise; there is no fallback.
 The state space scan, its short convolution and the draft verification
 (include/kda_ssm.h, include/kda_spec.h) are in the same library; their calls
 (ssm_*, verify_drafts) are in gated_delta_rule_amd.ssm and re-exported here.
+Softmax attention, its paged cache and the pages' upkeep (include/kda_attn.h,
+include/kda_pages.h; attn_*, kv_*) are in gated_delta_rule_amd.attn.
 """
 from __future__ import annotations
 
@@ -27,7 +29,9 @@ __all__ = ["chunk_fwd", "decode_step", "recurrent_fwd", "prologue", "epilogue",
            "library_path", "load_library", "KDAError", "KDA_BF16", "KDA_F32", "HEAD_DIM",
            "ssm_conv_fwd", "ssm_conv_step", "ssm_conv_bwd", "ssm_chunk_fwd", "ssm_chunk_bwd",
            "ssm_recurrent_fwd", "ssm_chunk_fwd_workspace_bytes", "ssm_chunk_bwd_workspace_bytes",
-           "verify_drafts"]
+           "verify_drafts",
+           "attn_fwd", "attn_bwd", "attn_paged_fwd", "kv_append", "kv_resize", "kv_fork", "kv_compact",
+           "attn_bwd_workspace_bytes", "attn_paged_workspace_bytes"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -98,17 +102,31 @@ def load_library():
                                   sz, vp],
             "kda_ssm_recurrent_fwd": [vp, i64, vp, i64, vp, i64, ci, fp, fp, ci, fp, fp, vp, i64, vp, i64, fp,
                                       ip, fp, i32, i32, i32, i32, i32, i32, i32, ci, vp, vp],
-            "kda_verify_drafts": [vp, vp, ci, ip, ip, fp, fp, i32, i32, i64, ip, ip, vp, sz, vp]}.items():
+            "kda_verify_drafts": [vp, vp, ci, ip, ip, fp, fp, i32, i32, i64, ip, ip, vp, sz, vp],
+            "kda_attn_fwd": [vp, i64, vp, i64, vp, i64, ci, ip, i32, i64, i32, i32, i32, ctypes.c_float, ci, vp,
+                             fp, vp],
+            "kda_attn_bwd": [vp, i64, vp, i64, vp, i64, ci, ip, i32, i64, i32, i32, i32, ctypes.c_float, ci, vp,
+                             fp, vp, vp, i64, vp, i64, vp, i64, vp, sz, vp],
+            "kda_attn_paged_fwd": [vp, i64, ci, vp, vp, i64, i32, i32, ip, i32, ip, ip, i32, i64, i32, i32, i32,
+                                   ctypes.c_float, vp, fp, vp, sz, vp],
+            "kda_kv_append": [vp, i64, vp, i64, ci, vp, vp, i64, i32, i32, ip, i32, ip, ip, i32, i64, i32, i32, vp],
+            "kda_kv_resize": [ip, ip, ip, ip, ip, i32, i32, i32, i32, vp],
+            "kda_kv_fork": [ip, ip, ip, ip, ip, ip, i32, i32, i32, i32, i32, vp, vp, vp, i32, vp, sz, vp],
+            "kda_kv_compact": [ip, ip, ip, ip, ip, ip, i32, i32, i32, i32, vp, vp, vp, i32, vp, sz, vp]}.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ci
-    for name in ("kda_ssm_conv_bwd", "kda_ssm_chunk_bwd"):   # (csrc/kda_ssm_launch.h)
+    for name in ("kda_ssm_conv_bwd", "kda_ssm_chunk_bwd", "kda_attn_bwd"):   # (csrc/kda_*_launch.h)
         getattr(lib, name + "_fresh").argtypes = getattr(lib, name).argtypes + [ci]
         getattr(lib, name + "_fresh").restype = ci
     for name, args in {
             "kda_ssm_conv_bwd_workspace_bytes": [i64, i32, i32],
             "kda_ssm_chunk_fwd_workspace_bytes": [i32, i64, i32, i32, i32, i32, ci],
             "kda_ssm_chunk_bwd_workspace_bytes": [ci, i32, i64, i32, i32, i32, i32, ci, i32],
-            "kda_verify_drafts_workspace_bytes": [i32, i32, i64]}.items():
+            "kda_verify_drafts_workspace_bytes": [i32, i32, i64],
+            "kda_attn_bwd_workspace_bytes": [ci, i32, i64, i32, i32, i32, ci],
+            "kda_attn_paged_workspace_bytes": [ci, i32, i64, i32, i32, i32, i32, i32, ci],
+            "kda_kv_fork_workspace_bytes": [i32, i32, i32],
+            "kda_kv_compact_workspace_bytes": [i32]}.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = sz
     _lib = lib
@@ -454,3 +472,5 @@ def epilogue(o, g, w, *, out=None):
 from .ssm import (ssm_chunk_bwd, ssm_chunk_bwd_workspace_bytes, ssm_chunk_fwd,  # noqa: E402
                   ssm_chunk_fwd_workspace_bytes, ssm_conv_bwd, ssm_conv_fwd, ssm_conv_step,
                   ssm_recurrent_fwd, verify_drafts)
+from .attn import (attn_bwd, attn_bwd_workspace_bytes, attn_fwd, attn_paged_fwd,  # noqa: E402
+                   attn_paged_workspace_bytes, kv_append, kv_compact, kv_fork, kv_resize)

@@ -1,0 +1,218 @@
+// Softmax attention in float32, of whole sequences and of new tokens over a
+// paged cache (gfx950).  Semantics: include/kda_attn.h.
+//
+// One pass over the keys with the running maximum m and sum l of each row:
+//   m' = max(m, s), o' = e^{m - m'} o + e^{s - m'} v, l' = e^{m - m'} l + e^{s - m'}.
+// A workgroup has 64 rows (4 waves of 16) of one (sequence, group); keys and
+// values come 32 at a time through LDS.  S^T = K Q^T leaves lane l with row
+// l & 15 and keys 4 (l >> 4) + i: the place that P^T takes as an operand of
+// O^T = V^T P^T, so weights go from product to product in registers, and a
+// row's maximum and sum are one lane's values and two exchanges.  The next
+// tile's rows are requested before the products of this one.
+#include "kda_attn_tile.h"
+
+namespace kda {
+
+constexpr int AF_THREADS = 256, AF_KEYS = 32, AF_BLOCK = kAttnBlockF32;
+
+// Rows of a tile of AF_KEYS keys, as float32: eight threads to a row.
+template <typename InT, int D, bool PAGED>
+struct KeyStage {
+    static constexpr int PER = D / 8;     // values per thread
+    float k[PER], v[PER];
+    bool ok;
+    // key: this thread's; len: keys that exist
+    __device__ __forceinline__ void load(const AttnKeys<InT, PAGED>& a, int32_t key, int32_t len) {
+        int64_t ko = 0, vo = 0;
+        ok = key < len && a.at(key, ko, vo);
+        const int c = (threadIdx.x & 7) * 4;
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) {
+            float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+            if (ok) {
+                load4(a.k + ko + c + 32 * i, x);
+                load4(a.v + vo + c + 32 * i, y);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                k[4 * i + e] = x[e];
+                v[4 * i + e] = y[e];
+            }
+        }
+    }
+    __device__ __forceinline__ void put(float* ks, float* vs, int pitch) const {
+        const int row = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) {
+            *reinterpret_cast<f32x4*>(ks + row * pitch + c + 32 * i) = f32x4{k[4 * i], k[4 * i + 1], k[4 * i + 2], k[4 * i + 3]};
+            *reinterpret_cast<f32x4*>(vs + row * pitch + c + 32 * i) = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        }
+    }
+};
+
+template <typename InT, int D, bool PAGED>
+__global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) {
+    constexpr int PITCH = D + 4, S = D / 16;
+    __shared__ __attribute__((aligned(16))) float ks[AF_KEYS * PITCH], vs[AF_KEYS * PITCH];
+    __shared__ uint8_t there[AF_KEYS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
+    const AttnPlace pl = attn_place(blockIdx.x, p.slots * p.splits, p.G);
+    const int64_t slot = p.slots - 1 - pl.item / p.splits;   // (later blocks see more keys)
+    const int split = (int)(pl.item % p.splits);
+    const AttnBlock b = attn_block(p, slot, p.hpg, AF_BLOCK);
+    if (b.j < 0) return;
+    const int32_t len = PAGED ? attn_length(p, b.n) : b.tokens;
+    const int32_t first = len - b.tokens;                    // position of the first query token
+    const int row = b.r0 + wave * 16 + col;
+    const bool valid = row < b.r1;
+    const int32_t t = valid ? row / p.hpg : 0;
+    const int head = pl.g * p.hpg + (valid ? row - t * p.hpg : 0);
+    const int32_t sees = !valid ? 0 : p.causal ? first + t + 1 : len;   // keys [0, sees)
+    const int32_t most = p.causal ? first + (b.r1 - 1) / p.hpg + 1 : len;
+    const int32_t tiles = most > 0 ? (most + AF_KEYS - 1) / AF_KEYS : 0;
+    const int32_t t0 = (int32_t)((int64_t)tiles * split / p.splits), t1 = (int32_t)((int64_t)tiles * (split + 1) / p.splits);
+
+    float q[S][4];
+    const InT* qrow = (const InT*)p.q + (b.start + t) * p.q_stride + (int64_t)head * D;
+#pragma unroll
+    for (int s = 0; s < S; ++s) load4(qrow + 16 * s + 4 * grp, q[s]);
+
+    const AttnKeys<InT, PAGED> keys(p, b.n, b.start, pl.g);
+    f32x4 o[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) o[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+    const float c = p.scale * kLog2e;
+    KeyStage<InT, D, PAGED> st;
+    if (t0 < t1) st.load(keys, t0 * AF_KEYS + (tid >> 3), most);
+    for (int32_t tile = t0; tile < t1; ++tile) {
+        __syncthreads();
+        st.put(ks, vs, PITCH);
+        if ((tid & 7) == 0) there[tid >> 3] = st.ok;
+        __syncthreads();
+        if (tile + 1 < t1) st.load(keys, (tile + 1) * AF_KEYS + (tid >> 3), most);
+        float x[2][4], top = m;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float a[4];
+                load4(ks + (16 * kt + col) * PITCH + 16 * s + 4 * grp, a);
+                mma_k16<true, PLAIN>(acc, a, q[s]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = 16 * kt + 4 * grp + i;
+                x[kt][i] = tile * AF_KEYS + key < sees && (!PAGED || there[key]) ? acc[i] * c : -INFINITY;
+                top = fmaxf(top, x[kt][i]);
+            }
+        }
+        top = groups_max(top);
+        const float base = top == -INFINITY ? 0.f : top, fade = attn_exp2(m - base);
+        m = top;
+        l *= fade;
+#pragma unroll
+        for (int s = 0; s < S; ++s) o[s] *= fade;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[kt][i] = attn_exp2(x[kt][i] - base);
+                l += x[kt][i];
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float a[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] = vs[(16 * kt + 4 * grp + e) * PITCH + 16 * s + col];
+                mma_k16<true, PLAIN>(o[s], a, x[kt]);
+            }
+        }
+    }
+    l = groups_sum(l);
+    if (!valid) return;
+    if (p.splits > 1) {
+        float* to = p.part + (((slot * p.G + pl.g) * p.splits + split) * AF_BLOCK + (row - b.r0)) * (D + 2);
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[16 * s + 4 * grp + i] = o[s][i];
+        if (grp == 0) {
+            to[D] = l;
+            to[D + 1] = m;
+        }
+        return;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    InT* orow = (InT*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const float y[4] = {o[s][0] * inv, o[s][1] * inv, o[s][2] * inv, o[s][3] * inv};
+        store4(orow + 16 * s + 4 * grp, y);
+    }
+    if (p.lse && grp == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// The parts of a split block: o = sum_s e^{m_s - m} o_s / sum_s e^{m_s - m} l_s,
+// in the order of the parts.  A wave has a row.
+template <typename InT, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, int block) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t per = (uint32_t)block / 4;                 // workgroups of a block
+    const uint32_t unit = blockIdx.x / per;
+    const int64_t slot = unit / (uint32_t)p.G;
+    const int g = (int)(unit % (uint32_t)p.G);
+    const AttnBlock b = attn_block(p, slot, p.hpg, block);
+    const int r = (int)(blockIdx.x % per) * 4 + wave;
+    if (b.j < 0 || b.r0 + r >= b.r1) return;
+    const float* from = p.part + ((slot * p.G + g) * p.splits * block + r) * (int64_t)(D + 2);
+    const int64_t step = (int64_t)block * (D + 2);
+    float m = -INFINITY;
+    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, from[s * step + D + 1]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o0 = 0.f, o1 = 0.f;
+    for (int s = 0; s < p.splits; ++s) {
+        const float* at = from + s * step;
+        const float w = attn_exp2(at[D + 1] - base);
+        l += w * at[D];
+        o0 += w * at[lane];
+        if constexpr (D == 128) o1 += w * at[64 + lane];
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int row = b.r0 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
+    InT* orow = (InT*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
+    orow[lane] = (InT)(o0 * inv);
+    if constexpr (D == 128) orow[64 + lane] = (InT)(o1 * inv);
+    if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <typename InT, int D>
+static void run_fwd(const AttnParams& p, hipStream_t stream) {
+    const dim3 grid((uint32_t)(p.slots * p.G * p.splits));
+    if (p.lengths) attn_fwd_f32_kernel<InT, D, true><<<grid, AF_THREADS, 0, stream>>>(p);
+    else attn_fwd_f32_kernel<InT, D, false><<<grid, AF_THREADS, 0, stream>>>(p);
+}
+
+hipError_t launch_attn_fwd_f32(const AttnParams& p, bool bf16_in, hipStream_t stream) {
+    if (p.slots == 0) return hipSuccess;
+    if (bf16_in) p.D == 64 ? run_fwd<__bf16, 64>(p, stream) : run_fwd<__bf16, 128>(p, stream);
+    else p.D == 64 ? run_fwd<float, 64>(p, stream) : run_fwd<float, 128>(p, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    return launch_attn_join(p, bf16_in, AF_BLOCK, stream);
+}
+
+hipError_t launch_attn_join(const AttnParams& p, bool bf16_in, int block, hipStream_t stream) {
+    const dim3 grid((uint32_t)(p.slots * p.G * (block / 4)));
+    if (bf16_in) {
+        if (p.D == 64) attn_join_kernel<__bf16, 64><<<grid, 256, 0, stream>>>(p, block);
+        else attn_join_kernel<__bf16, 128><<<grid, 256, 0, stream>>>(p, block);
+    } else {
+        if (p.D == 64) attn_join_kernel<float, 64><<<grid, 256, 0, stream>>>(p, block);
+        else attn_join_kernel<float, 128><<<grid, 256, 0, stream>>>(p, block);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -1,0 +1,159 @@
+// Device-side pieces shared by the attention kernels (gfx950 only): which rows
+// a workgroup has, and where its keys and values lie.
+#pragma once
+
+#include "kda_attn_launch.h"
+#include "kda_device.h"
+
+namespace kda {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+__device__ __forceinline__ float attn_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Token rows [start, end) of sequence n, clamped into [0, rows].
+struct AttnRange {
+    int64_t start, end;
+};
+__device__ __forceinline__ AttnRange attn_range(const int32_t* cu, int64_t rows, int64_t T, int64_t n) {
+    if (!cu) return AttnRange{n * T, n * T + T};
+    int64_t a = cu[n], b = cu[n + 1];
+    a = a < 0 ? 0 : (a > rows ? rows : a);
+    b = b < a ? a : (b > rows ? rows : b);
+    return AttnRange{a, b};
+}
+
+// The block of `block` rows (`per` rows to a token) that a slot stands for
+// (see AttnParams); j -1: an unused slot.
+struct AttnBlock {
+    int64_t start;     // first token row of the sequence
+    int32_t n, j;      // sequence, block of it
+    int32_t tokens;    // of the sequence
+    int32_t r0, r1;    // rows [r0, r1) of the sequence's tokens * per
+};
+__device__ __forceinline__ AttnBlock attn_block(const AttnParams& p, int64_t slot, int per, int block) {
+    AttnBlock b;
+    int64_t j;
+    if (!p.cu) {
+        const int64_t each = (p.T * per + block - 1) / block;
+        b.n = (int32_t)(slot / each);
+        j = slot - (int64_t)b.n * each;
+    } else {
+        int lo = 0, hi = p.n_seqs;   // largest n whose first slot is not past this one
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (attn_range(p.cu, p.rows, p.T, mid).start * per / block + mid <= slot) lo = mid;
+            else hi = mid;
+        }
+        b.n = lo;
+        j = slot - (attn_range(p.cu, p.rows, p.T, lo).start * per / block + lo);
+    }
+    const AttnRange r = attn_range(p.cu, p.rows, p.T, b.n);
+    b.start = r.start;
+    b.tokens = (int32_t)(r.end - r.start);
+    const int64_t n_rows = (int64_t)b.tokens * per, r0 = j * block;
+    b.j = j < 0 || r0 >= n_rows ? -1 : (int32_t)j;
+    b.r0 = b.j < 0 ? 0 : (int32_t)r0;
+    b.r1 = b.j < 0 ? 0 : (int32_t)(r0 + block < n_rows ? r0 + block : n_rows);
+    return b;
+}
+
+// Tokens that request n holds, in [0, max_pages * page].
+__device__ __forceinline__ int32_t attn_length(const AttnParams& p, int n) {
+    const int64_t most = (int64_t)p.max_pages << p.page_shift;
+    const int32_t len = p.lengths[n];
+    return len < 0 ? 0 : (int32_t)(len < most ? len : most);
+}
+
+// Keys and values of one (sequence, group).
+template <typename InT, bool PAGED>
+struct AttnKeys {
+    const InT *k, *v;          // first token's row, or page 0, of this group
+    int64_t k_stride, v_stride;
+    const int32_t* pages;      // of this request
+    int32_t n_pages, shift, D;
+    __device__ __forceinline__ AttnKeys(const AttnParams& p, int n, int64_t start, int g) {
+        D = p.D;
+        if constexpr (PAGED) {
+            shift = p.page_shift;
+            k = (const InT*)p.k + ((int64_t)g << shift) * D;
+            v = (const InT*)p.v + ((int64_t)g << shift) * D;
+            k_stride = v_stride = p.page_stride;
+            pages = p.table + (int64_t)n * p.max_pages;
+            n_pages = p.n_pages;
+        } else {
+            k = (const InT*)p.k + start * p.k_stride + (int64_t)g * D;
+            v = (const InT*)p.v + start * p.v_stride + (int64_t)g * D;
+            k_stride = p.k_stride;
+            v_stride = p.v_stride;
+        }
+    }
+    // Offsets of token x's rows (0 <= x < the sequence's length); false: its page is none.
+    __device__ __forceinline__ bool at(int32_t x, int64_t& ko, int64_t& vo) const {
+        if constexpr (PAGED) {
+            const int32_t page = pages[x >> shift];
+            ko = vo = (int64_t)page * k_stride + (int64_t)(x & ((1 << shift) - 1)) * D;
+            return page >= 0 && page < n_pages;
+        } else {
+            ko = (int64_t)x * k_stride;
+            vo = (int64_t)x * v_stride;
+            return true;
+        }
+    }
+};
+
+// Four values as float32.
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+    const f32x4 r = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = r[i];
+}
+__device__ __forceinline__ void load4(const __bf16* p, float (&x)[4]) {
+    const u32x2 r = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[2 * i] = bf2_first(r[i]);
+        x[2 * i + 1] = bf2_second(r[i]);
+    }
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+    f32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = x[i];
+    *reinterpret_cast<f32x4*>(p) = r;
+}
+__device__ __forceinline__ void store4(__bf16* p, const float (&x)[4]) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3])};
+}
+
+// Over the four 16-lane groups of a wave (lanes with equal l & 15).
+__device__ __forceinline__ float groups_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float groups_sum(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// Workgroups of one (sequence, group) on one XCD (workgroup w starts on XCD w
+// mod 8), so that its keys and values stay in that L2: workgroup w works on
+// item `at` of group `g`.  Groups are dealt to the XCDs in turn; where they do
+// not divide by 8, the items are dealt in their own order.
+struct AttnPlace {
+    int64_t item;
+    int32_t g;
+};
+__device__ __forceinline__ AttnPlace attn_place(uint32_t w, int64_t items, int32_t G) {
+    AttnPlace a;
+    if (G % 8 == 0) {
+        const uint32_t x = w & 7, i = w >> 3;
+        a.g = (int32_t)(x + 8 * (i / (uint32_t)items));
+        a.item = i % (uint32_t)items;
+    } else {
+        a.g = (int32_t)(w % (uint32_t)G);
+        a.item = w / (uint32_t)G;
+    }
+    return a;
+}
+
+}  // namespace kda

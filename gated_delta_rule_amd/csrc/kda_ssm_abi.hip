@@ -6,12 +6,13 @@
 
 #include "../../include/kda_spec.h"
 #include "../../include/kda_ssm.h"
+#include "kda_host.h"
 #include "kda_ssm_launch.h"
 
 namespace {
 
-// Workgroups of a launch: fewer than 2^32 threads.
-constexpr int64_t kMaxWorkgroups = (1 << 24) - 1;   // of 256 threads
+using namespace kda::host;
+
 constexpr int64_t kMaxWide = kMaxWorkgroups / 2;    // of 512
 constexpr int32_t kMaxTokens = 64;        // tokens per request in the step forms
 constexpr int64_t kScanUnits = 256;       // compute units
@@ -24,45 +25,6 @@ constexpr int64_t kVerifyFill = 2048;     // workgroups of the verification (512
 // one per compute unit): 256 against 512 is 90 / 103 us for a backward pass of
 // 1024 tokens of 64 heads, 432 / 445 for 2 x 4096.
 constexpr int64_t kGradFill = 256;
-
-struct Span {
-    uintptr_t lo, hi;      // [lo, hi)
-    uintptr_t stride, width;   // bytes from row to row, bytes of a row (0: contiguous)
-};
-Span span(const void* p, int64_t bytes) {
-    const uintptr_t a = (uintptr_t)p;
-    return Span{a, a + (uintptr_t)(p && bytes > 0 ? bytes : 0), 0, 0};
-}
-// rows of `width` elements, `stride` apart
-Span rows_span(const void* p, int64_t rows, int64_t stride, int64_t width, int64_t es) {
-    Span s = span(p, rows > 0 ? ((rows - 1) * stride + width) * es : 0);
-    s.stride = (uintptr_t)(stride * es);
-    s.width = (uintptr_t)(width * es);
-    return s;
-}
-bool overlaps(const Span& a, const Span& b) {
-    if (a.lo == a.hi || b.lo == b.hi) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
-// Like overlaps, but two sets of rows with one stride may lie side by side
-// within the same wider rows.
-bool overlaps_rows(const Span& a, const Span& b) {
-    if (!overlaps(a, b)) return false;
-    if (a.stride == 0 || a.stride != b.stride) return true;
-    const Span &f = a.lo <= b.lo ? a : b, &g = a.lo <= b.lo ? b : a;
-    const uintptr_t d = (g.lo - f.lo) % f.stride;
-    return !(d >= f.width && d + g.width <= f.stride);
-}
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > INT64_MAX / a) return false;
-    *out = a * b;
-    return true;
-}
-bool dtype_ok(int t) { return t == KDA_BF16 || t == KDA_F32; }
-int64_t elem_size(int t) { return t == KDA_BF16 ? 2 : 4; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // A row stride: at least the row, whole 16-byte pieces, small enough for
 // 32-bit offsets within a chunk.
