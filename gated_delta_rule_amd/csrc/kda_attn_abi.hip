@@ -80,10 +80,11 @@ struct PagedPlan {
     int64_t slots, splits, bytes;
     int block;
 };
-PagedPlan paged_plan(int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, int32_t D, int64_t max_tokens,
-                     bool varlen) {
+int block_rows(bool bf16) { return bf16 ? kda::kAttnBlockBf16 : kda::kAttnBlockF32; }
+PagedPlan paged_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, int32_t D,
+                     int64_t max_tokens, bool varlen) {
     PagedPlan a{};
-    a.block = kda::kAttnBlockF32;
+    a.block = block_rows(bf16);
     a.slots = block_slots(rows, n_seqs, T, H / G, a.block, varlen);
     const int64_t units = a.slots * G;
     const int64_t want = units > 0 ? kFill / units : 1, most = max_tokens / kMinSplitKeys;
@@ -135,9 +136,9 @@ int kda_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_strid
     kda::AttnParams p = attn_params(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, n_seqs, T, rows, H, G, D,
                                     scale, causal, o, lse);
     const bool bf16 = in_dtype == KDA_BF16;
-    p.slots = block_slots(rows, n_seqs, T, p.hpg, kda::kAttnBlockF32, cu_seqlens != nullptr);
+    p.slots = block_slots(rows, n_seqs, T, p.hpg, block_rows(bf16), cu_seqlens != nullptr);
     if (p.slots > kMaxWideGroups / G) return KDA_ERR_TOO_LARGE;
-    return status(kda::launch_attn_fwd_f32(p, bf16, stream));
+    return status(bf16 ? kda::launch_attn_fwd_bf16(p, stream) : kda::launch_attn_fwd_f32(p, false, stream));
 }
 
 size_t kda_attn_bwd_workspace_bytes(int in_dtype, int32_t n_seqs, int64_t T, int32_t H, int32_t G, int32_t D,
@@ -278,7 +279,7 @@ size_t kda_attn_paged_workspace_bytes(int in_dtype, int32_t n_seqs, int64_t T, i
     if (attn_shape(in_dtype, n_seqs, T, H, G, D, varlen != 0, &rows) || page_shift(page_size) < 0 || max_pages < 0 ||
         rows == 0)
         return 0;
-    return (size_t)paged_plan(n_seqs, T, rows, H, G, D, (int64_t)max_pages * page_size, varlen != 0).bytes;
+    return (size_t)paged_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, D, (int64_t)max_pages * page_size, varlen != 0).bytes;
 }
 
 int kda_attn_paged_fwd(const void* q, int64_t q_stride, int in_dtype, const void* k_pages, const void* v_pages,
@@ -298,7 +299,7 @@ int kda_attn_paged_fwd(const void* q, int64_t q_stride, int in_dtype, const void
     if (!q || !o) return KDA_ERR_NULL_POINTER;
     if ((rc = check_stride(q_stride, HD, es))) return rc;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16)) return KDA_ERR_MISALIGNED;
-    const PagedPlan plan = paged_plan(n_seqs, T, rows, H, G, D, (int64_t)max_pages * page_size, varlen);
+    const PagedPlan plan = paged_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, D, (int64_t)max_pages * page_size, varlen);
     if (plan.slots > kMaxWideGroups / G / plan.splits / 32) return KDA_ERR_TOO_LARGE;
     if (plan.bytes > 0 && (!workspace || workspace_bytes < (size_t)plan.bytes)) return KDA_ERR_WORKSPACE;
     const Span outs[] = {span(o, rows * HD * es), span(lse, rows * H * 4), span(workspace, plan.bytes)};
@@ -323,7 +324,7 @@ int kda_attn_paged_fwd(const void* q, int64_t q_stride, int in_dtype, const void
     p.slots = plan.slots;
     p.splits = (int32_t)plan.splits;
     p.part = (float*)workspace;
-    return status(kda::launch_attn_fwd_f32(p, in_dtype == KDA_BF16, stream));
+    return status(in_dtype == KDA_BF16 ? kda::launch_attn_fwd_bf16(p, stream) : kda::launch_attn_fwd_f32(p, false, stream));
 }
 
 // ------------------------------------------------------------------ pages

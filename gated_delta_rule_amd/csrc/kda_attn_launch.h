@@ -41,6 +41,7 @@ struct AttnParams {
 constexpr int kAttnBlockF32 = 64;    // rows of a block
 constexpr int kAttnBlockBf16 = 128;
 hipError_t launch_attn_fwd_f32(const AttnParams& p, bool bf16_in, hipStream_t stream);
+hipError_t launch_attn_fwd_bf16(const AttnParams& p, hipStream_t stream);
 hipError_t launch_attn_join(const AttnParams& p, bool bf16_in, int block, hipStream_t stream);
 
 struct AttnBwdParams {
