@@ -97,10 +97,10 @@ PagedPlan paged_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t
 struct BwdPlan {
     int64_t slots, key_slots, bytes;
 };
-BwdPlan bwd_plan(int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, bool varlen) {
+BwdPlan bwd_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, bool varlen) {
     BwdPlan b{};
-    b.slots = block_slots(rows, n_seqs, T, H / G, 64, varlen);
-    b.key_slots = block_slots(rows, n_seqs, T, 1, 64, varlen);
+    b.slots = block_slots(rows, n_seqs, T, H / G, block_rows(bf16), varlen);
+    b.key_slots = block_slots(rows, n_seqs, T, 1, block_rows(bf16), varlen);
     b.bytes = (rows * H * 4 + 15) / 16 * 16;
     return b;
 }
@@ -138,14 +138,14 @@ int kda_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_strid
     const bool bf16 = in_dtype == KDA_BF16;
     p.slots = block_slots(rows, n_seqs, T, p.hpg, block_rows(bf16), cu_seqlens != nullptr);
     if (p.slots > kMaxWideGroups / G) return KDA_ERR_TOO_LARGE;
-    return status(bf16 ? kda::launch_attn_fwd_bf16(p, stream) : kda::launch_attn_fwd_f32(p, false, stream));
+    return status(bf16 ? kda::launch_attn_fwd_bf16(p, stream) : kda::launch_attn_fwd_f32(p, stream));
 }
 
 size_t kda_attn_bwd_workspace_bytes(int in_dtype, int32_t n_seqs, int64_t T, int32_t H, int32_t G, int32_t D,
                                     int varlen) {
     int64_t rows = 0;
     if (attn_shape(in_dtype, n_seqs, T, H, G, D, varlen != 0, &rows) || rows == 0) return 0;
-    return (size_t)bwd_plan(n_seqs, T, rows, H, G, varlen != 0).bytes;
+    return (size_t)bwd_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, varlen != 0).bytes;
 }
 
 int kda_attn_bwd_fresh(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -168,7 +168,7 @@ int kda_attn_bwd_fresh(const void* q, int64_t q_stride, const void* k, int64_t k
     for (const void* a : wide)
         if (!aligned(a, 16)) return KDA_ERR_MISALIGNED;
     if (!aligned(lse, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_MISALIGNED;
-    const BwdPlan plan = bwd_plan(n_seqs, T, rows, H, G, varlen);
+    const BwdPlan plan = bwd_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, varlen);
     if (plan.slots > kMaxWideGroups / G || plan.key_slots > kMaxWideGroups / G || rows * H / 8 >= kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
     if (!workspace || workspace_bytes < (size_t)plan.bytes) return KDA_ERR_WORKSPACE;
@@ -197,7 +197,7 @@ int kda_attn_bwd_fresh(const void* q, int64_t q_stride, const void* k, int64_t k
     a.gv_stride = grad_v_stride;
     a.delta = (float*)workspace;
     a.zero_rest = fresh;
-    return status(kda::launch_attn_bwd_f32(a, in_dtype == KDA_BF16, stream));
+    return status(in_dtype == KDA_BF16 ? kda::launch_attn_bwd_bf16(a, stream) : kda::launch_attn_bwd_f32(a, stream));
 }
 
 int kda_attn_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -324,7 +324,7 @@ int kda_attn_paged_fwd(const void* q, int64_t q_stride, int in_dtype, const void
     p.slots = plan.slots;
     p.splits = (int32_t)plan.splits;
     p.part = (float*)workspace;
-    return status(in_dtype == KDA_BF16 ? kda::launch_attn_fwd_bf16(p, stream) : kda::launch_attn_fwd_f32(p, false, stream));
+    return status(in_dtype == KDA_BF16 ? kda::launch_attn_fwd_bf16(p, stream) : kda::launch_attn_fwd_f32(p, stream));
 }
 
 // ------------------------------------------------------------------ pages

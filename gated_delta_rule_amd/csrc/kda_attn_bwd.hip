@@ -1,0 +1,273 @@
+// Gradients of softmax attention with bf16 inputs (gfx950).  Semantics:
+// include/kda_attn.h.
+//
+// As in the float32 form, P and dP are formed twice, by the blocks of keys and
+// by the blocks of rows, so that every sum stays in one wave's registers (no
+// atomics).  Both kernels take 64 rows of the other side at a time, which
+// come from memory straight into the other half of LDS while the half before
+// is computed with:
+//   keys: wave w has 32 keys and walks the rows (all heads of the group):
+//     S = Q K^T, dP = dO V^T, then dV^T += dO^T P, dK^T += Q^T dS;
+//   rows: wave w has 32 rows and walks the keys:
+//     S^T = K Q^T, dP^T = V dO^T, then dQ^T += K^T dS^T.
+// P and dS go from product to product in registers, rounded to bf16 once.
+#include "kda_attn_mma.h"
+
+namespace kda {
+
+constexpr int BW_THREADS = 256, BW_BLOCK = kAttnBlockBf16, BW_STEP = 64;
+
+// grad_k and grad_v of 128 keys of one (sequence, group).
+template <int D>
+__global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParams a) {
+    const AttnParams& p = a.f;
+    constexpr int ROWB = 2 * D, UNITS = D / 8, TILE = BW_STEP * ROWB, LOADS = D / 32, RPL = 1024 / ROWB;
+    constexpr int S = D / 16, O = D / 32;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // q, q, grad_o, grad_o
+    __shared__ __attribute__((aligned(16))) float stat[2][2][BW_STEP];   // of each row: lse in base 2, delta
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const AttnPlace pl = attn_place(blockIdx.x, a.key_slots, p.G);
+    const AttnBlock b = attn_block(p, pl.item, 1, BW_BLOCK);
+    if (b.j < 0) return;
+    const int32_t key = b.r0 + wave * 32 + col;
+    const bool valid = key < b.r1;
+    const int32_t n_rows = b.tokens * p.hpg;
+
+    bf16x8 k[S], v[S];
+    {
+        const int64_t row = b.start + (valid ? key : b.r0);
+        const __bf16* kr = (const __bf16*)p.k + row * p.k_stride + (int64_t)pl.g * D + 8 * half;
+        const __bf16* vr = (const __bf16*)p.v + row * p.v_stride + (int64_t)pl.g * D + 8 * half;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            k[s] = *reinterpret_cast<const bf16x8*>(kr + 16 * s);
+            v[s] = *reinterpret_cast<const bf16x8*>(vr + 16 * s);
+        }
+    }
+    f32x16 gk[O], gv[O];
+#pragma unroll
+    for (int i = 0; i < O; ++i) gk[i] = gv[i] = zero16();
+
+    const float c = p.scale * kLog2e;
+    const int32_t r_first = p.causal ? (int32_t)((int64_t)b.r0 * p.hpg / BW_STEP * BW_STEP) : 0;
+    const int32_t from = p.causal ? key * p.hpg : 0;                          // rows from here on see this lane's key
+    const int32_t from_most = __builtin_amdgcn_readlane(from, 31), from_least = __builtin_amdgcn_readfirstlane(from);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+    const int64_t gstride = (int64_t)p.H * D;
+    const uint32_t inv = p.hpg > 1 ? 0xffffffffu / (uint32_t)p.hpg + 1 : 0;   // i / hpg = i * inv >> 32 for the i below
+    float mine = 0.f;
+    auto request = [&](int32_t r0, int buf) {
+        const int32_t t0 = r0 / p.hpg, h0 = r0 - t0 * p.hpg;                  // first row of the tile
+        const auto qrs = make_rsrc((const __bf16*)p.q + (b.start + t0) * p.q_stride + (int64_t)pl.g * p.hpg * D, 0x40000000);
+        const auto grs = make_rsrc((const __bf16*)a.go + (b.start + t0) * gstride + (int64_t)pl.g * p.hpg * D, 0x40000000);
+        const uint32_t to = lds0 + buf * TILE + wave * 16 * ROWB;
+        uint32_t qoff[LOADS], goff[LOADS];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int r = wave * 16 + i * RPL + lane / UNITS, u = (lane % UNITS) ^ tile_swap<D>(r);
+            const uint32_t x = (uint32_t)(h0 + r), t = p.hpg > 1 ? __umulhi(x, inv) : x, hh = x - t * (uint32_t)p.hpg;
+            const uint32_t at = hh * (2 * D) + u * 16;
+            const bool in = r0 + r < n_rows;                                  // rows behind the last one read as zero
+            qoff[i] = in ? t * (uint32_t)(p.q_stride * 2) + at : 0x80000000u;
+            goff[i] = in ? t * (uint32_t)(gstride * 2) + at : 0x80000000u;
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load_to_lds(qrs, qoff[i], to + i * 1024);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load_to_lds(grs, goff[i], to + 2 * TILE + i * 1024);
+        if (tid < 2 * BW_STEP) {
+            const int r = tid & (BW_STEP - 1);
+            const uint32_t x = (uint32_t)(h0 + r), t = p.hpg > 1 ? __umulhi(x, inv) : x, hh = x - t * (uint32_t)p.hpg;
+            const int64_t at = (b.start + t0 + t) * p.H + pl.g * p.hpg + hh;
+            // (a row that is not there has weight e^{-inf})
+            mine = r0 + r < n_rows ? (tid < BW_STEP ? p.lse[at] * kLog2e : a.delta[at]) : (tid < BW_STEP ? INFINITY : 0.f);
+        }
+    };
+    const int rat = lane_rows<D>(lane);
+    const int2 cat = lane_cols<D>(lane);
+    request(r_first, 0);
+    for (int32_t r0 = r_first; r0 < n_rows; r0 += BW_STEP) {
+        const int buf = ((r0 - r_first) / BW_STEP) & 1;
+        if (tid < 2 * BW_STEP) stat[buf][tid / BW_STEP][tid & (BW_STEP - 1)] = mine;
+        tiles_barrier();
+        if (r0 + BW_STEP < n_rows) request(r0 + BW_STEP, buf ^ 1);
+        if (r0 + BW_STEP <= from_least) continue;
+        const char* qs = lds + buf * TILE;
+        const char* gs = lds + 2 * TILE + buf * TILE;
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+            f32x16 x = zero16(), y = zero16();
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                x = mfma32x32(read_rows(qs + rt * 32 * ROWB, rat ^ (32 * s)), k[s], x);
+                y = mfma32x32(read_rows(gs + rt * 32 * ROWB, rat ^ (32 * s)), v[s], y);
+            }
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) {
+                const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&stat[buf][0][32 * rt + 8 * e4 + 4 * half]);
+                const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[buf][1][32 * rt + 8 * e4 + 4 * half]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = attn_exp2(fmaf(x[4 * e4 + i], c, -lse2[i]));
+                    x[4 * e4 + i] = w;
+                    y[4 * e4 + i] = y[4 * e4 + i] - delta[i];
+                }
+            }
+            if (r0 + 32 * rt < from_most) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[e] = r0 + 32 * rt + 8 * (e >> 2) + 4 * half + (e & 3) >= from ? x[e] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] *= x[e];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const bf16x8 pw = as_operand(x, s), ds = as_operand(y, s);
+                const int at = (2 * rt + s) * 16 * ROWB;
+#pragma unroll
+                for (int i = 0; i < O; ++i) {
+                    gv[i] = mfma32x32(read_cols(gs + at, cat, i), pw, gv[i]);
+                    gk[i] = mfma32x32(read_cols(qs + at, cat, i), ds, gk[i]);
+                }
+            }
+        }
+    }
+    if (!valid) return;
+    __bf16* tk = (__bf16*)a.gk + (b.start + key) * a.gk_stride + (int64_t)pl.g * D + 4 * half;
+    __bf16* tv = (__bf16*)a.gv + (b.start + key) * a.gv_stride + (int64_t)pl.g * D + 4 * half;
+#pragma unroll
+    for (int i = 0; i < O; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float y[4], z[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                y[n] = gk[i][4 * e + n] * p.scale;
+                z[n] = gv[i][4 * e + n];
+            }
+            store4(tk + 32 * i + 8 * e, y);
+            store4(tv + 32 * i + 8 * e, z);
+        }
+}
+
+// grad_q of 128 rows of one (sequence, group).
+template <int D>
+__global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams a) {
+    const AttnParams& p = a.f;
+    constexpr int ROWB = 2 * D, UNITS = D / 8, TILE = BW_STEP * ROWB, LOADS = D / 32, RPL = 1024 / ROWB;
+    constexpr int S = D / 16, O = D / 32;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // keys, keys, values, values
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const AttnPlace pl = attn_place(blockIdx.x, p.slots, p.G);
+    const AttnBlock b = attn_block(p, p.slots - 1 - pl.item, p.hpg, BW_BLOCK);   // (later blocks see more keys)
+    if (b.j < 0) return;
+    const int row = b.r0 + wave * 32 + col;
+    const bool valid = row < b.r1;
+    const int32_t t = (valid ? row : b.r1 - 1) / p.hpg;
+    const int head = pl.g * p.hpg + (valid ? row - t * p.hpg : 0);
+    const int64_t at = (b.start + t) * p.H + head;
+    const int32_t sees = p.causal ? t + 1 : b.tokens, most = p.causal ? (b.r1 - 1) / p.hpg + 1 : b.tokens;
+    const int32_t sees_least = __builtin_amdgcn_readfirstlane(sees), sees_most = __builtin_amdgcn_readlane(sees, 31);
+
+    bf16x8 q[S], go[S];
+    {
+        const __bf16* qr = (const __bf16*)p.q + (b.start + t) * p.q_stride + (int64_t)head * D + 8 * half;
+        const __bf16* gr = (const __bf16*)a.go + at * D + 8 * half;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            q[s] = *reinterpret_cast<const bf16x8*>(qr + 16 * s);
+            go[s] = *reinterpret_cast<const bf16x8*>(gr + 16 * s);
+        }
+    }
+    const float lse2 = p.lse[at] * kLog2e, delta = a.delta[at], c = p.scale * kLog2e;
+    f32x16 gq[O];
+#pragma unroll
+    for (int i = 0; i < O; ++i) gq[i] = zero16();
+
+    const AttnKeys<__bf16, false> keys(p, b.n, b.start, pl.g);
+    uint32_t koff[LOADS], voff[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int r = i * RPL + lane / UNITS, u = (lane % UNITS) ^ tile_swap<D>(r);
+        koff[i] = (uint32_t)(r * (int)keys.k_stride * 2 + u * 16);
+        voff[i] = (uint32_t)(r * (int)keys.v_stride * 2 + u * 16);
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+    auto request = [&](int32_t tile, int buf) {
+        const int32_t key = tile * BW_STEP + 16 * wave;
+        const int32_t left = most - key < 16 ? most - key : 16;
+        const int64_t first = left > 0 ? key : 0;
+        const auto krs = make_rsrc(keys.k + first * keys.k_stride, left > 0 ? ((left - 1) * (int)keys.k_stride + D) * 2 : 0);
+        const auto vrs = make_rsrc(keys.v + first * keys.v_stride, left > 0 ? ((left - 1) * (int)keys.v_stride + D) * 2 : 0);
+        const uint32_t to = lds0 + buf * TILE + wave * 16 * ROWB;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load_to_lds(krs, koff[i], to + i * 1024);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load_to_lds(vrs, voff[i], to + 2 * TILE + i * 1024);
+    };
+    const int rat = lane_rows<D>(lane);
+    const int2 cat = lane_cols<D>(lane);
+    const int32_t tiles = (most + BW_STEP - 1) / BW_STEP;
+    request(0, 0);
+    for (int32_t tile = 0; tile < tiles; ++tile) {
+        const int buf = tile & 1;
+        tiles_barrier();
+        if (tile + 1 < tiles) request(tile + 1, buf ^ 1);
+        const int32_t key0 = tile * BW_STEP;
+        if (key0 >= sees_most) continue;
+        const char* ks = lds + buf * TILE;
+        const char* vs = lds + 2 * TILE + buf * TILE;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            f32x16 x = zero16(), y = zero16();
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                x = mfma32x32(read_rows(ks + kt * 32 * ROWB, rat ^ (32 * s)), q[s], x);
+                y = mfma32x32(read_rows(vs + kt * 32 * ROWB, rat ^ (32 * s)), go[s], y);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = attn_exp2(fmaf(x[e], c, -lse2)) * (y[e] - delta);
+            if (key0 + 32 * kt + 32 > sees_least) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[e] = key0 + 32 * kt + 8 * (e >> 2) + 4 * half + (e & 3) < sees ? x[e] : 0.f;
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const bf16x8 ds = as_operand(x, s);
+#pragma unroll
+                for (int i = 0; i < O; ++i) gq[i] = mfma32x32(read_cols(ks + (2 * kt + s) * 16 * ROWB, cat, i), ds, gq[i]);
+            }
+        }
+    }
+    if (!valid) return;
+    __bf16* to = (__bf16*)a.gq + (b.start + t) * a.gq_stride + (int64_t)head * D + 4 * half;
+#pragma unroll
+    for (int i = 0; i < O; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float y[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) y[n] = gq[i][4 * e + n] * p.scale;
+            store4(to + 32 * i + 8 * e, y);
+        }
+}
+
+template <int D>
+static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
+    attn_bwd_kv_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G)), BW_THREADS, 0, stream>>>(a);
+    attn_bwd_q_kernel<D><<<dim3((uint32_t)(a.f.slots * a.f.G)), BW_THREADS, 0, stream>>>(a);
+}
+
+hipError_t launch_attn_bwd_bf16(const AttnBwdParams& a, hipStream_t stream) {
+    if (a.f.rows == 0) return hipSuccess;
+    const hipError_t e = launch_attn_delta(a, true, stream);
+    if (e != hipSuccess) return e;
+    if (a.f.D == 64) run_bwd<64>(a, stream);
+    else run_bwd<128>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace kda

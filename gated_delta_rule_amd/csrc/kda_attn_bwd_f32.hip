@@ -229,17 +229,27 @@ __global__ __launch_bounds__(AB_THREADS) void attn_bwd_q_f32_kernel(AttnBwdParam
 }
 
 template <typename InT, int D>
-static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
+static void run_delta(const AttnBwdParams& a, hipStream_t stream) {
     constexpr int LANES = D / (16 / (int)sizeof(InT));
     attn_delta_kernel<InT, D><<<dim3((uint32_t)((a.f.rows * a.f.H * LANES + 255) / 256)), 256, 0, stream>>>(a);
+}
+hipError_t launch_attn_delta(const AttnBwdParams& a, bool bf16_in, hipStream_t stream) {
+    if (bf16_in) a.f.D == 64 ? run_delta<__bf16, 64>(a, stream) : run_delta<__bf16, 128>(a, stream);
+    else a.f.D == 64 ? run_delta<float, 64>(a, stream) : run_delta<float, 128>(a, stream);
+    return hipGetLastError();
+}
+
+template <typename InT, int D>
+static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
     attn_bwd_kv_f32_kernel<InT, D><<<dim3((uint32_t)(a.key_slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
     attn_bwd_q_f32_kernel<InT, D><<<dim3((uint32_t)(a.f.slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
 }
 
-hipError_t launch_attn_bwd_f32(const AttnBwdParams& a, bool bf16_in, hipStream_t stream) {
+hipError_t launch_attn_bwd_f32(const AttnBwdParams& a, hipStream_t stream) {
     if (a.f.rows == 0) return hipSuccess;
-    if (bf16_in) a.f.D == 64 ? run_bwd<__bf16, 64>(a, stream) : run_bwd<__bf16, 128>(a, stream);
-    else a.f.D == 64 ? run_bwd<float, 64>(a, stream) : run_bwd<float, 128>(a, stream);
+    const hipError_t e = launch_attn_delta(a, false, stream);
+    if (e != hipSuccess) return e;
+    a.f.D == 64 ? run_bwd<float, 64>(a, stream) : run_bwd<float, 128>(a, stream);
     return hipGetLastError();
 }
 

@@ -194,13 +194,12 @@ static void run_fwd(const AttnParams& p, hipStream_t stream) {
     else attn_fwd_f32_kernel<InT, D, false><<<grid, AF_THREADS, 0, stream>>>(p);
 }
 
-hipError_t launch_attn_fwd_f32(const AttnParams& p, bool bf16_in, hipStream_t stream) {
+hipError_t launch_attn_fwd_f32(const AttnParams& p, hipStream_t stream) {
     if (p.slots == 0) return hipSuccess;
-    if (bf16_in) p.D == 64 ? run_fwd<__bf16, 64>(p, stream) : run_fwd<__bf16, 128>(p, stream);
-    else p.D == 64 ? run_fwd<float, 64>(p, stream) : run_fwd<float, 128>(p, stream);
+    p.D == 64 ? run_fwd<float, 64>(p, stream) : run_fwd<float, 128>(p, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    return launch_attn_join(p, bf16_in, AF_BLOCK, stream);
+    return launch_attn_join(p, false, AF_BLOCK, stream);
 }
 
 hipError_t launch_attn_join(const AttnParams& p, bool bf16_in, int block, hipStream_t stream) {

@@ -14,50 +14,12 @@
 // weights are then up to 2^8 instead of 1, which costs no precision (l and o
 // are float32, a bf16 weight has the same relative error), and the products
 // with e^{m - m'} are left out of nearly all tiles.
-#include "kda_attn_tile.h"
+#include "kda_attn_mma.h"
 
 namespace kda {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ f32x16 mfma32x32(bf16x8 a, bf16x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-
 constexpr int FW_THREADS = 256, FW_BLOCK = kAttnBlockBf16, FW_KEYS = 64;
 constexpr float FW_LOWEST = -3.0e38f;   // below every score
-
-// Place of 16-byte unit u of a row in LDS is u ^ fw_swap(row): the 16 rows of
-// one unit (operand rows, 16 lanes at a time) fall into 16 places of the banks'
-// 256 bytes, and so do four neighbouring units of four rows (transposed reads,
-// 32 lanes at a time).
-template <int D>
-__device__ __forceinline__ int fw_swap(int row) {
-    return D == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
-}
-
-#pragma clang diagnostic ignored "-Winline-asm"   // (m0 as a clobber)
-
-// 16 bytes per lane from a buffer to LDS at `to` + 16 lane.  Written out
-// because the compiler would wait for these before every LDS read.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(to), "v"(off), "s"(rs) : "memory", "m0");
-}
-// All of this wave's loads to LDS have arrived and its LDS reads are done; then the workgroup's barrier.
-__device__ __forceinline__ void tiles_barrier() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-__device__ __forceinline__ bf16x8 read_cols(const char* lo, const char* hi) {
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lo);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)hi);
-    bf16x8 f;
-    __builtin_memcpy(&f, &a, 8);
-    __builtin_memcpy(reinterpret_cast<char*>(&f) + 8, &b, 8);
-    return f;
-}
 
 template <int D, bool PAGED>
 __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams p) {
@@ -106,7 +68,7 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
     uint32_t koff[LOADS], voff[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-        const int r = i * RPL + lane / UNITS, u = (lane % UNITS) ^ fw_swap<D>(r);
+        const int r = i * RPL + lane / UNITS, u = (lane % UNITS) ^ tile_swap<D>(r);
         koff[i] = (uint32_t)(r * (int)kstep * 2 + u * 16);
         voff[i] = (uint32_t)(r * (int)vstep * 2 + u * 16);
     }
@@ -145,17 +107,12 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
     };
 
     // where this lane reads its operands
-    const int kat = col * ROWB + ((half ^ fw_swap<D>(col)) * 16);                        // ^ 32 s, + 32 rows
-    const int ti = lane & 15, tq = (lane >> 4) & 1, tr = 4 * half + (ti >> 2);
-    const int tu = 2 * tq + ((ti & 3) >> 1);
-    const int vat0 = tr * ROWB + ((tu ^ fw_swap<D>(tr)) * 16) + 8 * (ti & 1);             // ^ 64 dt, + 16 rows s
-    const int vat1 = (tr + 8) * ROWB + ((tu ^ fw_swap<D>(tr + 8)) * 16) + 8 * (ti & 1);
+    const int kat = lane_rows<D>(lane);
+    const int2 vat = lane_cols<D>(lane);
 
     f32x16 o[O];
 #pragma unroll
-    for (int i = 0; i < O; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+    for (int i = 0; i < O; ++i) o[i] = zero16();
     float m = FW_LOWEST, l = 0.f;
 
     if (t0 < t1) request(t0, 0);
@@ -170,13 +127,9 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
         f32x16 x[2];
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
+            x[kt] = zero16();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[kt][e] = 0.f;
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const bf16x8 a = *reinterpret_cast<const bf16x8*>(ks + kt * 32 * ROWB + (kat ^ (32 * s)));
-                x[kt] = mfma32x32(a, q[s], x[kt]);
-            }
+            for (int s = 0; s < S; ++s) x[kt] = mfma32x32(read_rows(ks + kt * 32 * ROWB, kat ^ (32 * s)), q[s], x[kt]);
         }
         bool whole = key0 + FW_KEYS <= sees_least;
         if constexpr (PAGED) whole = whole && (there[buf][0] & there[buf][1] & there[buf][2] & there[buf][3]);
@@ -217,14 +170,11 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                float w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = x[kt][8 * s + e];
-                const bf16x8 pw = round8(w);
+                const bf16x8 pw = as_operand(x[kt], s);
                 const int at = (2 * kt + s) * 16 * ROWB;
 #pragma unroll
                 for (int i = 0; i < O; ++i)
-                    o[i] = mfma32x32(read_cols(vs + at + (vat0 ^ (64 * i)), vs + at + (vat1 ^ (64 * i))), pw, o[i]);
+                    o[i] = mfma32x32(read_cols(vs + at, vat, i), pw, o[i]);
             }
         }
     }

@@ -40,7 +40,7 @@ struct AttnParams {
 // 2), at part + (((slot * G + g) * splits + s) * block + row) * (D + 2).
 constexpr int kAttnBlockF32 = 64;    // rows of a block
 constexpr int kAttnBlockBf16 = 128;
-hipError_t launch_attn_fwd_f32(const AttnParams& p, bool bf16_in, hipStream_t stream);
+hipError_t launch_attn_fwd_f32(const AttnParams& p, hipStream_t stream);
 hipError_t launch_attn_fwd_bf16(const AttnParams& p, hipStream_t stream);
 hipError_t launch_attn_join(const AttnParams& p, bool bf16_in, int block, hipStream_t stream);
 
@@ -55,7 +55,9 @@ struct AttnBwdParams {
     int64_t key_slots;       // blocks of keys per group
     int32_t zero_rest;       // KDA_FRESH_*: these outputs' rows of no sequence become zero
 };
-hipError_t launch_attn_bwd_f32(const AttnBwdParams& p, bool bf16_in, hipStream_t stream);
+hipError_t launch_attn_delta(const AttnBwdParams& p, bool bf16_in, hipStream_t stream);
+hipError_t launch_attn_bwd_f32(const AttnBwdParams& p, hipStream_t stream);
+hipError_t launch_attn_bwd_bf16(const AttnBwdParams& p, hipStream_t stream);
 
 struct AppendParams {
     const void* k;

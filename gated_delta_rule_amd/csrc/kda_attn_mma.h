@@ -1,0 +1,84 @@
+// Tiles of bf16 rows in LDS and the 32x32x16 matrix instruction, for the
+// attention kernels with bf16 inputs (gfx950 only).
+//
+// Operands of the instruction: lane l supplies row (A) or column (B) l & 31
+// and k = 8 (l >> 5) .. + 7; it receives column l & 31, rows 8 b + 4 (l >> 5) + i
+// of the product in register 4 b + i.  Two operands may agree on any order of
+// k, so registers 8 s .. 8 s + 7 of a product, as bf16, are the operand whose
+// k are its rows 16 s .. 16 s + 15: lane half h has k = 4 h .. + 3 and 8 + 4 h .. + 3
+// of the 16, and the transposing reads below give the other operand in that
+// order.
+#pragma once
+
+#include "kda_attn_tile.h"
+
+namespace kda {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x16 mfma32x32(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Place of 16-byte unit u of a row in LDS is u ^ tile_swap(row): the 16 rows of
+// one unit (operand rows, 16 lanes at a time) fall into 16 places of the banks'
+// 256 bytes, and so do four neighbouring units of four rows (transposed reads,
+// 32 lanes at a time).
+template <int D>
+__device__ __forceinline__ int tile_swap(int row) {
+    return D == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+}
+
+#pragma clang diagnostic ignored "-Winline-asm"   // (m0 as a clobber)
+
+// 16 bytes per lane from a buffer to LDS at `to` + 16 lane.  Written out
+// because the compiler would wait for these before every LDS read.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(to), "v"(off), "s"(rs) : "memory", "m0");
+}
+// All of this wave's loads to LDS have arrived and its LDS reads are done; then the workgroup's barrier.
+__device__ __forceinline__ void tiles_barrier() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Where a lane reads its operands in a tile of rows of D values (byte offsets).
+// k along the row: row l & 31 (+ 32 kt rows), values 16 s + 8 (l >> 5) .. + 7: at ^ 32 s.
+template <int D>
+__device__ __forceinline__ int lane_rows(int lane) {
+    const int r = lane & 31;
+    return r * 2 * D + (((lane >> 5) ^ tile_swap<D>(r)) * 16);
+}
+// k along the rows: column 32 c + (l & 31), rows 16 s + 4 (l >> 5) .. + 3 (x)
+// and 8 more (y): at ^ 64 c, + 16 s rows.
+template <int D>
+__device__ __forceinline__ int2 lane_cols(int lane) {
+    const int i = lane & 15, r = 4 * (lane >> 5) + (i >> 2), u = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+    return make_int2(r * 2 * D + ((u ^ tile_swap<D>(r)) * 16) + 8 * (i & 1),
+                     (r + 8) * 2 * D + ((u ^ tile_swap<D>(r + 8)) * 16) + 8 * (i & 1));
+}
+__device__ __forceinline__ bf16x8 read_rows(const char* tile, int at) { return *reinterpret_cast<const bf16x8*>(tile + at); }
+__device__ __forceinline__ bf16x8 read_cols(const char* tile, int2 at, int c) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(tile + (at.x ^ (64 * c))));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(tile + (at.y ^ (64 * c))));
+    bf16x8 f;
+    __builtin_memcpy(&f, &a, 8);
+    __builtin_memcpy(reinterpret_cast<char*>(&f) + 8, &b, 8);
+    return f;
+}
+// Registers 8 s .. of a product as an operand.
+__device__ __forceinline__ bf16x8 as_operand(const f32x16& x, int s) {
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = x[8 * s + e];
+    return round8(w);
+}
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = 0.f;
+    return z;
+}
+
+}  // namespace kda
