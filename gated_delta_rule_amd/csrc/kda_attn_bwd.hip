@@ -26,23 +26,32 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
     __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // q, q, grad_o, grad_o
     __shared__ __attribute__((aligned(16))) float stat[2][2][BW_STEP];   // of each row: lse in base 2, delta
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 31, half = lane >> 5;
-    const AttnPlace pl = attn_place(blockIdx.x, a.key_slots, p.G);
-    const AttnBlock b = attn_block(p, pl.item, 1, BW_BLOCK);
+    const AttnPlace pl = attn_place(attn_zigzag(blockIdx.x, gridDim.x, p.G), a.key_slots, p.G);
+    int64_t slot = pl.item;
+    if (!p.cu && p.causal) {   // the first blocks of all sequences, then the second ones: they have the most rows
+        const int64_t each = a.key_slots / p.n_seqs;
+        slot = (slot % p.n_seqs) * each + slot / p.n_seqs;
+    }
+    const AttnBlock b = attn_block(p, slot, 1, BW_BLOCK);
     if (b.j < 0) return;
-    const int32_t key = b.r0 + wave * 32 + col;
-    const bool valid = key < b.r1;
+    const int32_t key0 = b.r0 + wave * 32;   // this wave's first key
     const int32_t n_rows = b.tokens * p.hpg;
 
     bf16x8 k[S], v[S];
     {
-        const int64_t row = b.start + (valid ? key : b.r0);
-        const __bf16* kr = (const __bf16*)p.k + row * p.k_stride + (int64_t)pl.g * D + 8 * half;
-        const __bf16* vr = (const __bf16*)p.v + row * p.v_stride + (int64_t)pl.g * D + 8 * half;
+        const int key = key0 + (lane & 31);
+        const int64_t row = b.start + (key < b.r1 ? key : b.r0);
+        const __bf16* kr = (const __bf16*)p.k + row * p.k_stride + (int64_t)pl.g * D + 8 * (lane >> 5);
+        const __bf16* vr = (const __bf16*)p.v + row * p.v_stride + (int64_t)pl.g * D + 8 * (lane >> 5);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             k[s] = *reinterpret_cast<const bf16x8*>(kr + 16 * s);
             v[s] = *reinterpret_cast<const bf16x8*>(vr + 16 * s);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            arrive(k[s]);
+            arrive(v[s]);
         }
     }
     f32x16 gk[O], gv[O];
@@ -51,8 +60,8 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
 
     const float c = p.scale * kLog2e;
     const int32_t r_first = p.causal ? (int32_t)((int64_t)b.r0 * p.hpg / BW_STEP * BW_STEP) : 0;
-    const int32_t from = p.causal ? key * p.hpg : 0;                          // rows from here on see this lane's key
-    const int32_t from_most = __builtin_amdgcn_readlane(from, 31), from_least = __builtin_amdgcn_readfirstlane(from);
+    // key x is seen by the rows from x * hpg on
+    const int32_t from_least = p.causal ? key0 * p.hpg : 0, from_most = p.causal ? (key0 + 31) * p.hpg : 0;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
     const int64_t gstride = (int64_t)p.H * D;
     const uint32_t inv = p.hpg > 1 ? 0xffffffffu / (uint32_t)p.hpg + 1 : 0;   // i / hpg = i * inv >> 32 for the i below
@@ -62,34 +71,30 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
         const auto qrs = make_rsrc((const __bf16*)p.q + (b.start + t0) * p.q_stride + (int64_t)pl.g * p.hpg * D, 0x40000000);
         const auto grs = make_rsrc((const __bf16*)a.go + (b.start + t0) * gstride + (int64_t)pl.g * p.hpg * D, 0x40000000);
         const uint32_t to = lds0 + buf * TILE + wave * 16 * ROWB;
-        uint32_t qoff[LOADS], goff[LOADS];
+        int ln = lane;
+        hide(ln);   // (offsets are formed anew: there are no registers to keep them)
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int r = wave * 16 + i * RPL + lane / UNITS, u = (lane % UNITS) ^ tile_swap<D>(r);
+            const int r = wave * 16 + i * RPL + ln / UNITS, u = (ln % UNITS) ^ tile_swap<D>(r);
             const uint32_t x = (uint32_t)(h0 + r), t = p.hpg > 1 ? __umulhi(x, inv) : x, hh = x - t * (uint32_t)p.hpg;
             const uint32_t at = hh * (2 * D) + u * 16;
             const bool in = r0 + r < n_rows;                                  // rows behind the last one read as zero
-            qoff[i] = in ? t * (uint32_t)(p.q_stride * 2) + at : 0x80000000u;
-            goff[i] = in ? t * (uint32_t)(gstride * 2) + at : 0x80000000u;
+            load_to_lds(qrs, in ? t * (uint32_t)(p.q_stride * 2) + at : 0x80000000u, to + i * 1024);
+            load_to_lds(grs, in ? t * (uint32_t)(gstride * 2) + at : 0x80000000u, to + 2 * TILE + i * 1024);
         }
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(qrs, qoff[i], to + i * 1024);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(grs, goff[i], to + 2 * TILE + i * 1024);
         if (tid < 2 * BW_STEP) {
             const int r = tid & (BW_STEP - 1);
             const uint32_t x = (uint32_t)(h0 + r), t = p.hpg > 1 ? __umulhi(x, inv) : x, hh = x - t * (uint32_t)p.hpg;
-            const int64_t at = (b.start + t0 + t) * p.H + pl.g * p.hpg + hh;
-            // (a row that is not there has weight e^{-inf})
-            mine = r0 + r < n_rows ? (tid < BW_STEP ? p.lse[at] * kLog2e : a.delta[at]) : (tid < BW_STEP ? INFINITY : 0.f);
+            if (r0 + r < n_rows) mine = (tid < BW_STEP ? p.lse : a.delta)[(b.start + t0 + t) * p.H + pl.g * p.hpg + hh];
         }
     };
-    const int rat = lane_rows<D>(lane);
-    const int2 cat = lane_cols<D>(lane);
     request(r_first, 0);
     for (int32_t r0 = r_first; r0 < n_rows; r0 += BW_STEP) {
         const int buf = ((r0 - r_first) / BW_STEP) & 1;
-        if (tid < 2 * BW_STEP) stat[buf][tid / BW_STEP][tid & (BW_STEP - 1)] = mine;
+        if (tid < 2 * BW_STEP) {   // (a row that is not there has weight e^{-inf})
+            const int r = tid & (BW_STEP - 1);
+            stat[buf][tid / BW_STEP][r] = tid < BW_STEP ? (r0 + r < n_rows ? mine * kLog2e : INFINITY) : mine;
+        }
         tiles_barrier();
         if (r0 + BW_STEP < n_rows) request(r0 + BW_STEP, buf ^ 1);
         if (r0 + BW_STEP <= from_least) continue;
@@ -97,43 +102,58 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
         const char* gs = lds + 2 * TILE + buf * TILE;
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
-            f32x16 x = zero16(), y = zero16();
+            const char *qt = qs + rt * 32 * ROWB, *gt = gs + rt * 32 * ROWB;
+            int ln = lane;
+            hide(ln);   // (nor any for these)
+            const int half = ln >> 5, rat = lane_rows<D>(ln);
+            const int2 cat = lane_cols<D>(ln);
+            f32x16 x = zero16();
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                x = mfma32x32(read_rows(qs + rt * 32 * ROWB, rat ^ (32 * s)), k[s], x);
-                y = mfma32x32(read_rows(gs + rt * 32 * ROWB, rat ^ (32 * s)), v[s], y);
-            }
+            for (int s = 0; s < S; ++s) x = mfma32x32(read_rows(qt, rat ^ (32 * s)), k[s], x);
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
                 const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&stat[buf][0][32 * rt + 8 * e4 + 4 * half]);
-                const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[buf][1][32 * rt + 8 * e4 + 4 * half]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float w = attn_exp2(fmaf(x[4 * e4 + i], c, -lse2[i]));
-                    x[4 * e4 + i] = w;
-                    y[4 * e4 + i] = y[4 * e4 + i] - delta[i];
-                }
+                for (int i = 0; i < 4; ++i) x[4 * e4 + i] = attn_exp2(fmaf(x[4 * e4 + i], c, -lse2[i]));
             }
             if (r0 + 32 * rt < from_most) {
+                const int32_t from = (key0 + (ln & 31)) * p.hpg;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     x[e] = r0 + 32 * rt + 8 * (e >> 2) + 4 * half + (e & 3) >= from ? x[e] : 0.f;
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] *= x[e];
+            __builtin_amdgcn_sched_barrier(0);   // (registers: 192 of 256 are sums, keys and values)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const bf16x8 pw = as_operand(x, s), ds = as_operand(y, s);
-                const int at = (2 * rt + s) * 16 * ROWB;
+                const bf16x8 pw = as_operand(x, s);
 #pragma unroll
-                for (int i = 0; i < O; ++i) {
-                    gv[i] = mfma32x32(read_cols(gs + at, cat, i), pw, gv[i]);
-                    gk[i] = mfma32x32(read_cols(qs + at, cat, i), ds, gk[i]);
-                }
+                for (int i = 0; i < O; ++i) gv[i] = mfma32x32(read_cols(gt + s * 16 * ROWB, cat, i), pw, gv[i]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            f32x16 y = zero16();
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                y = mfma32x32(read_rows(gt, rat ^ (32 * s)), v[s], y);
+                if (s % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) {
+                const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[buf][1][32 * rt + 8 * e4 + 4 * half]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4 * e4 + i] *= y[4 * e4 + i] - delta[i];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const bf16x8 ds = as_operand(x, s);
+#pragma unroll
+                for (int i = 0; i < O; ++i) gk[i] = mfma32x32(read_cols(qt + s * 16 * ROWB, cat, i), ds, gk[i]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
-    if (!valid) return;
+    const int key = key0 + (lane & 31), half = lane >> 5;
+    if (key >= b.r1) return;
     __bf16* tk = (__bf16*)a.gk + (b.start + key) * a.gk_stride + (int64_t)pl.g * D + 4 * half;
     __bf16* tv = (__bf16*)a.gv + (b.start + key) * a.gv_stride + (int64_t)pl.g * D + 4 * half;
 #pragma unroll
@@ -180,8 +200,15 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
             q[s] = *reinterpret_cast<const bf16x8*>(qr + 16 * s);
             go[s] = *reinterpret_cast<const bf16x8*>(gr + 16 * s);
         }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            arrive(q[s]);
+            arrive(go[s]);
+        }
     }
-    const float lse2 = p.lse[at] * kLog2e, delta = a.delta[at], c = p.scale * kLog2e;
+    float lse2 = p.lse[at] * kLog2e, delta = a.delta[at];
+    asm volatile("" : "+v"(lse2), "+v"(delta));   // (arrive, too)
+    const float c = p.scale * kLog2e;
     f32x16 gq[O];
 #pragma unroll
     for (int i = 0; i < O; ++i) gq[i] = zero16();

@@ -60,6 +60,8 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
         for (int i = 0; i < 4; ++i) w[i] = (w[i] & keep) ^ flip;
         q[s] = __builtin_bit_cast(bf16x8, w);
     }
+#pragma unroll
+    for (int s = 0; s < S; ++s) arrive(q[s]);
     const float c = scale * kLog2e;
 
     // this wave's 16 rows of each tile

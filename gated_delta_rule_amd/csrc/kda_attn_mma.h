@@ -43,6 +43,14 @@ __device__ __forceinline__ void tiles_barrier() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// Keeps the compiler from holding what is formed from x in registers across a loop.
+__device__ __forceinline__ void hide(int& x) { asm volatile("" : "+v"(x)); }
+
+// Has x arrive here.  A register that a loop only reads is otherwise waited for
+// in the loop, as if its load could still be under way, and with it for the
+// loads to LDS that were requested since.
+__device__ __forceinline__ void arrive(bf16x8& x) { asm volatile("" : "+v"(x)); }
+
 // Where a lane reads its operands in a tile of rows of D values (byte offsets).
 // k along the row: row l & 31 (+ 32 kt rows), values 16 s + 8 (l >> 5) .. + 7: at ^ 32 s.
 template <int D>

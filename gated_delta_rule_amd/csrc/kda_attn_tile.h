@@ -135,6 +135,16 @@ __device__ __forceinline__ float groups_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
+// Workgroup numbers for work that shrinks from the first workgroup to the last:
+// every second round of one workgroup per compute unit (32 of each XCD) is
+// turned round, so that the units' shares are alike.
+__device__ __forceinline__ uint32_t attn_zigzag(uint32_t w, uint32_t n, int32_t G) {
+    const uint32_t x = G % 8 == 0 ? w & 7 : 0, step = G % 8 == 0 ? 8 : 1, wide = 256 / step;
+    const uint32_t i = w / step, round = i / wide;
+    if (!(round & 1) || (round + 1) * wide > n / step) return w;
+    return (2 * round * wide + wide - 1 - i) * step + x;
+}
+
 // Workgroups of one (sequence, group) on one XCD (workgroup w starts on XCD w
 // mod 8), so that its keys and values stay in that L2: workgroup w works on
 // item `at` of group `g`.  Groups are dealt to the XCDs in turn; where they do
