@@ -20,8 +20,9 @@ pool[:, layer, 1] of [n_pages, layers, 2, G, page_size, D].
 from __future__ import annotations
 
 import ctypes
+import functools
 
-from . import KDAError, _check, _in_dtype, _status, load_library
+from . import KDA_BF16, KDA_F32, KDAError, _check, _in_dtype, _status, load_library
 from .ssm import _check_rows, _check_shape, _grad_like, _lead, _like, _nbytes, _on, _ptr, _stream, _workspace
 
 __all__ = ["attn_fwd", "attn_bwd", "attn_paged_fwd", "kv_append", "kv_resize", "kv_fork", "kv_compact",
@@ -33,6 +34,11 @@ _FRESH_Q, _FRESH_K, _FRESH_V = 1, 2, 4
 
 def _of(q, name="q"):
     import torch
+    if q.__class__ is torch.Tensor and q.dim() > 2:   # the usual tensors
+        if q.dtype is torch.bfloat16:
+            return q.device, KDA_BF16
+        if q.dtype is torch.float32:
+            return q.device, KDA_F32
     if not isinstance(q, torch.Tensor):
         raise KDAError(f"{name} must be a torch.Tensor")
     if q.dtype is not torch.bfloat16 and q.dtype is not torch.float32:
@@ -142,8 +148,22 @@ def attn_bwd(q, k, v, o, lse, grad_o, cu_seqlens=None, *, scale=None, causal=Tru
 class _Cache:
     """Checked pages and table of a paged cache."""
 
+    __slots__ = ("n_pages", "G", "page_size", "D", "stride", "n_seqs", "max_pages")
+
     def __init__(self, k_pages, v_pages, table, lengths, dtype, dev):
         import torch
+        tensor, index = torch.Tensor, dev.index
+        if k_pages.__class__ is tensor and v_pages.__class__ is tensor and table.__class__ is tensor:   # the usual cache
+            shape, st = k_pages.shape, k_pages.stride()
+            if len(shape) == 4 and k_pages.dtype is dtype and v_pages.dtype is dtype and v_pages.shape == shape and \
+                    v_pages.stride() == st and st[3] == 1 and st[2] == shape[3] and st[1] == shape[2] * st[2] and \
+                    k_pages.get_device() == index and v_pages.get_device() == index and table.dtype is torch.int32 and \
+                    table.get_device() == index and table.dim() == 2 and table.is_contiguous():
+                self.n_pages, self.G, self.page_size, self.D = shape
+                self.stride = st[0]
+                self.n_seqs, self.max_pages = table.shape
+                _check_shape(lengths, "lengths", (self.n_seqs,), dev, torch.int32)
+                return
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
             if not isinstance(t, torch.Tensor) or t.dim() != 4:
                 raise KDAError(f"{name} must be [n_pages, G, page_size, D]")
@@ -196,11 +216,15 @@ def kv_append(k, v, k_pages, v_pages, table, lengths, cu_seqlens=None):
     _status(rc, "kda_kv_append")
 
 
+@functools.lru_cache(maxsize=256)
+def _paged_bytes(*sizes) -> int:
+    return int(load_library().kda_attn_paged_workspace_bytes(*sizes))
+
+
 def attn_paged_workspace_bytes(dtype, n_seqs, T, H, G, D, page_size, max_pages, varlen) -> int:
     """Workspace of attn_paged_fwd for q of this dtype."""
     import torch
-    return int(load_library().kda_attn_paged_workspace_bytes(int(dtype == torch.float32), n_seqs, T, H, G, D, page_size,
-                                                             max_pages, int(bool(varlen))))
+    return _paged_bytes(int(dtype == torch.float32), n_seqs, T, H, G, D, page_size, max_pages, int(bool(varlen)))
 
 
 def attn_paged_fwd(q, k_pages, v_pages, table, lengths, cu_seqlens=None, *, scale=None, o=None, lse=None,
@@ -224,8 +248,8 @@ def attn_paged_fwd(q, k_pages, v_pages, table, lengths, cu_seqlens=None, *, scal
         raise KDAError(f"q must have head dimension {c.D}, got {D}")
     qs = _check_rows(q, "q", lead, (H, D), q.dtype, dev)
     o, lse = _outputs(q, lead, H, dev, o, lse)
-    ws = _workspace(workspace, int(lib.kda_attn_paged_workspace_bytes(dt, n_seqs, T, H, c.G, D, c.page_size, c.max_pages,
-                                                                      int(cu_seqlens is not None))), dev)
+    ws = _workspace(workspace, _paged_bytes(dt, n_seqs, T, H, c.G, D, c.page_size, c.max_pages,
+                                            int(cu_seqlens is not None)), dev)
     with _on(dev):
         rc = lib.kda_attn_paged_fwd(_ptr(q), qs, dt, _ptr(k_pages), _ptr(v_pages), c.stride, c.n_pages, c.page_size,
                                     _ptr(table), c.max_pages, _ptr(lengths), _ptr(cu_seqlens), n_seqs, T, H, c.G, D,

@@ -15,7 +15,7 @@ LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_abi.hip", "kda_noalloc.hip", "kda_prefill.hip", "kda_prefill_pipe.hip", "kda_segment.hip", "kda_recurrent.hip",
            "kda_layer.hip", "kda_backward.hip", "kda_ssm_abi.hip", "kda_ssm_conv.hip", "kda_ssm_scan.hip",
            "kda_ssm_bwd.hip", "kda_ssm_recurrent.hip", "kda_spec.hip",
-           "kda_attn_abi.hip", "kda_attn_f32.hip", "kda_attn_fwd.hip", "kda_attn_bwd_f32.hip", "kda_attn_bwd.hip", "kda_pages.hip"]
+           "kda_attn_abi.hip", "kda_attn_f32.hip", "kda_attn_fwd.hip", "kda_attn_step.hip", "kda_attn_bwd_f32.hip", "kda_attn_bwd.hip", "kda_pages.hip"]
 HEADERS = ["kda_device.h", "kda_launch.h", "kda_chunk.h", "kda_ssm_launch.h", "kda_ssm_tile.h",
            "kda_host.h", "kda_attn_launch.h", "kda_attn_tile.h", "kda_attn_mma.h"]
 ARCH = "gfx950"

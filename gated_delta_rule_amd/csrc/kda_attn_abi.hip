@@ -16,6 +16,7 @@ using namespace kda::host;
 constexpr int64_t kMaxWideGroups = kMaxWorkgroups / 4;   // workgroups of up to 1024 threads
 constexpr int64_t kMaxRows = (int64_t)1 << 36;
 constexpr int64_t kMaxSeqRows = (int64_t)1 << 30;        // tokens * heads of a group, counted in 32 bits
+constexpr int64_t kUnits = 256;                          // compute units
 constexpr int64_t kFill = 512;                           // workgroups that fill the GPU (two per compute unit)
 constexpr int64_t kMinSplitKeys = 256;                   // keys of a part, at least
 
@@ -77,13 +78,24 @@ kda::AttnParams attn_params(const void* q, int64_t q_stride, const void* k, int6
 // Parts of a request's keys (block kernels): so many that the GPU is full,
 // with kMinSplitKeys keys each where a request holds all it can.
 struct PagedPlan {
-    int64_t slots, splits, bytes;
+    bool step;
+    int64_t slots, splits, workgroups, max_rows, bytes;
     int block;
 };
 int block_rows(bool bf16) { return bf16 ? kda::kAttnBlockBf16 : kda::kAttnBlockF32; }
 PagedPlan paged_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, int32_t D,
                      int64_t max_tokens, bool varlen) {
     PagedPlan a{};
+    a.max_rows = T * (H / G);   // of a request (packed: T is all of them)
+    a.step = a.max_rows <= kda::kAttnStepRows;
+    if (a.step) {
+        // two workgroups per compute unit, or one where its LDS (128 KB with float32 and D 128) leaves no room
+        a.workgroups = bf16 || D == 64 ? 2 * kUnits : kUnits;
+        const int64_t units = (int64_t)n_seqs * G;
+        a.bytes = ((2 * units + 3) / 4 * 4 + (a.workgroups + units) * kda::step_row_tiles(a.max_rows) * 16 * (D + 4)) * 4;
+        a.splits = 1;
+        return a;
+    }
     a.block = block_rows(bf16);
     a.slots = block_slots(rows, n_seqs, T, H / G, a.block, varlen);
     const int64_t units = a.slots * G;
@@ -300,7 +312,9 @@ int kda_attn_paged_fwd(const void* q, int64_t q_stride, int in_dtype, const void
     if ((rc = check_stride(q_stride, HD, es))) return rc;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16)) return KDA_ERR_MISALIGNED;
     const PagedPlan plan = paged_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, D, (int64_t)max_pages * page_size, varlen);
-    if (plan.slots > kMaxWideGroups / G / plan.splits / 32) return KDA_ERR_TOO_LARGE;
+    if (plan.step ? (int64_t)n_seqs * G > kMaxWorkgroups / plan.max_rows
+                  : plan.slots > kMaxWideGroups / G / plan.splits / 32)
+        return KDA_ERR_TOO_LARGE;
     if (plan.bytes > 0 && (!workspace || workspace_bytes < (size_t)plan.bytes)) return KDA_ERR_WORKSPACE;
     const Span outs[] = {span(o, rows * HD * es), span(lse, rows * H * 4), span(workspace, plan.bytes)};
     const Span ins[] = {rows_span(q, rows, q_stride, HD, es), rows_span(k_pages, n_pages, page_stride, GD * page_size, es),
@@ -323,7 +337,9 @@ int kda_attn_paged_fwd(const void* q, int64_t q_stride, int in_dtype, const void
     p.page_shift = page_shift(page_size);
     p.slots = plan.slots;
     p.splits = (int32_t)plan.splits;
+    p.workgroups = (int32_t)plan.workgroups;
     p.part = (float*)workspace;
+    if (plan.step) return status(kda::launch_attn_step(p, in_dtype == KDA_BF16, (int32_t)plan.max_rows, stream));
     return status(in_dtype == KDA_BF16 ? kda::launch_attn_fwd_bf16(p, stream) : kda::launch_attn_fwd_f32(p, stream));
 }
 

@@ -19,7 +19,6 @@
 namespace kda {
 
 constexpr int FW_THREADS = 256, FW_BLOCK = kAttnBlockBf16, FW_KEYS = 64;
-constexpr float FW_LOWEST = -3.0e38f;   // below every score
 
 template <int D, bool PAGED>
 __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams p) {
@@ -115,7 +114,7 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
     f32x16 o[O];
 #pragma unroll
     for (int i = 0; i < O; ++i) o[i] = zero16();
-    float m = FW_LOWEST, l = 0.f;
+    float m = kAttnLowest, l = 0.f;
 
     if (t0 < t1) request(t0, 0);
     for (int32_t tile = t0; tile < t1; ++tile) {
@@ -151,7 +150,7 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, x[1][e]);
         top = fmaxf(top, swap_halves(top));
-        top = fmaxf(top * c, FW_LOWEST);
+        top = fmaxf(top * c, kAttnLowest);
         if (__any(top > m + 8.f)) {
             const float to = fmaxf(m, top), fade = attn_exp2(m - to);
             m = to;

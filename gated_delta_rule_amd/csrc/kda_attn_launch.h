@@ -44,6 +44,15 @@ hipError_t launch_attn_fwd_f32(const AttnParams& p, hipStream_t stream);
 hipError_t launch_attn_fwd_bf16(const AttnParams& p, hipStream_t stream);
 hipError_t launch_attn_join(const AttnParams& p, bool bf16_in, int block, hipStream_t stream);
 
+// Step kernel, for (request, group) pairs of at most kAttnStepRows rows, with
+// step_row_tiles tiles of 16 rows.  At `part`: two numbers for each pair u = b *
+// G + g, then (from the next 16 bytes on) the parts; workgroup w's part of pair
+// u has slot w + u, with D sums, the sum of weights, m and two unused floats
+// for each row of the tiles.
+constexpr int kAttnStepRows = 64;
+constexpr int step_row_tiles(int64_t rows) { return (int)((rows + 15) / 16); }
+hipError_t launch_attn_step(const AttnParams& p, bool bf16_in, int32_t max_rows, hipStream_t stream);
+
 struct AttnBwdParams {
     AttnParams f;            // inputs; o and lse as the forward call gave them
     const void* go;          // [rows, H, D]

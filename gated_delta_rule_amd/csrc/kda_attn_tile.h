@@ -8,6 +8,7 @@
 namespace kda {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kAttnLowest = -3.0e38f;   // below every score
 __device__ __forceinline__ float attn_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Token rows [start, end) of sequence n, clamped into [0, rows].

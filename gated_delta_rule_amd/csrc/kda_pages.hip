@@ -84,12 +84,11 @@ __device__ __forceinline__ int32_t block_before(int32_t x, int32_t* s, int32_t& 
     }
     return base + up - x;
 }
+// What this workgroup's atomics and writes have left in L2, where they are done
+// once a barrier has been passed (past the compute unit's own cache, which
+// atomics do not go through).
 __device__ __forceinline__ int32_t fresh_load(const int32_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void block_fence() {   // the workgroup's writes and atomics are done and seen
-    __threadfence();
-    __syncthreads();
 }
 // Which of this thread's PG_EACH pages from `at` on are free, as bits.
 __device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int64_t at, int32_t n_pages) {
@@ -176,7 +175,7 @@ __global__ __launch_bounds__(PG_THREADS) void kv_resize_kernel(PagesParams p) {
             row[col] = -1;
         }
     }
-    block_fence();
+    __syncthreads();
     const int64_t n_free = need_all > 0 ? count_free(refs, p.n_pages, need_all, s) : 0;
     int64_t upto = 0;
     for (int s0 = 0; s0 < p.n_slots; s0 += PG_THREADS) {
@@ -203,7 +202,7 @@ __global__ __launch_bounds__(PG_THREADS) void kv_resize_kernel(PagesParams p) {
                 const int i = owner_of(off, PG_THREADS, rank);
                 p.table_out[(int64_t)(s0 + i) * p.max_pages + held[i] + rank - off[i]] = page;
             });
-            block_fence();
+            __syncthreads();
         }
         if (slot < p.n_slots) {
             p.lengths_out[slot] = ok ? want : len;
@@ -238,12 +237,12 @@ __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p)
     int32_t *refs = p.refs_out, *owner = p.ws;
     ForkPlan* plan = fork_plans(p);
     for (int i = tid; i < p.n_slots; i += PG_THREADS) owner[i] = INT32_MAX;
-    block_fence();
+    __syncthreads();
     for (int i = tid; i < p.n; i += PG_THREADS) {
         const int32_t d = p.dst[i];
         if (d >= 0 && d < p.n_slots) atomicMin(owner + d, i);
     }
-    block_fence();
+    __syncthreads();
     int64_t need_all = 0;
     for (int i0 = 0; i0 < p.n; i0 += PG_THREADS) {
         const int i = i0 + tid;
@@ -284,12 +283,12 @@ __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p)
             plan[i] = f;
             if (p.ok) p.ok[i] = ok;
         }
-        block_fence();
+        __syncthreads();
         if (served > 0) {
             give_out(refs, p.n_pages, served, s, [&](int32_t rank, int32_t page) {
                 plan[i0 + owner_of(off, PG_THREADS, rank)].to = page;
             });
-            block_fence();
+            __syncthreads();
         }
         __syncthreads();
     }
