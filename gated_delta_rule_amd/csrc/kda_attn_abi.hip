@@ -111,8 +111,9 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, bool varlen) {
     BwdPlan b{};
-    b.slots = block_slots(rows, n_seqs, T, H / G, block_rows(bf16), varlen);
-    b.key_slots = block_slots(rows, n_seqs, T, 1, block_rows(bf16), varlen);
+    const int block = bf16 ? kda::kAttnBlockBf16 : kda::kAttnBwdBlockF32;
+    b.slots = block_slots(rows, n_seqs, T, H / G, block, varlen);
+    b.key_slots = block_slots(rows, n_seqs, T, 1, block, varlen);
     b.bytes = (rows * H * 4 + 15) / 16 * 16;
     return b;
 }

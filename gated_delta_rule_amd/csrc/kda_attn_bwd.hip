@@ -64,7 +64,7 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
     const int32_t from_least = p.causal ? key0 * p.hpg : 0, from_most = p.causal ? (key0 + 31) * p.hpg : 0;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
     const int64_t gstride = (int64_t)p.H * D;
-    const uint32_t inv = p.hpg > 1 ? 0xffffffffu / (uint32_t)p.hpg + 1 : 0;   // i / hpg = i * inv >> 32 for the i below
+    const RowOf rows(p.hpg);
     float mine = 0.f;
     auto request = [&](int32_t r0, int buf) {
         const int32_t t0 = r0 / p.hpg, h0 = r0 - t0 * p.hpg;                  // first row of the tile
@@ -76,7 +76,8 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int r = wave * 16 + i * RPL + ln / UNITS, u = (ln % UNITS) ^ tile_swap<D>(r);
-            const uint32_t x = (uint32_t)(h0 + r), t = p.hpg > 1 ? __umulhi(x, inv) : x, hh = x - t * (uint32_t)p.hpg;
+            uint32_t t, hh;
+            rows.of((uint32_t)(h0 + r), t, hh);
             const uint32_t at = hh * (2 * D) + u * 16;
             const bool in = r0 + r < n_rows;                                  // rows behind the last one read as zero
             load_to_lds(qrs, in ? t * (uint32_t)(p.q_stride * 2) + at : 0x80000000u, to + i * 1024);
@@ -84,7 +85,8 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
         }
         if (tid < 2 * BW_STEP) {
             const int r = tid & (BW_STEP - 1);
-            const uint32_t x = (uint32_t)(h0 + r), t = p.hpg > 1 ? __umulhi(x, inv) : x, hh = x - t * (uint32_t)p.hpg;
+            uint32_t t, hh;
+            rows.of((uint32_t)(h0 + r), t, hh);
             if (r0 + r < n_rows) mine = (tid < BW_STEP ? p.lse : a.delta)[(b.start + t0 + t) * p.H + pl.g * p.hpg + hh];
         }
     };

@@ -8,11 +8,11 @@
 // the rows take S = Q K^T, whose place in registers (key l & 15, rows
 // 4 (l >> 4) + i) is that of P^T as an operand of P^T dO; the one that sums
 // over the keys takes S^T = K Q^T.
-#include "kda_attn_tile.h"
+#include "kda_attn_mma.h"
 
 namespace kda {
 
-constexpr int AB_THREADS = 256, AB_ROWS = 32, AB_BLOCK = 64;
+constexpr int AB_THREADS = 256, AB_BLOCK = kAttnBwdBlockF32;
 
 // delta of every row; rows of no sequence become zero in new gradients.
 template <typename InT, int D>
@@ -51,180 +51,267 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnBwdParams a) {
     if (threadIdx.x % LANES == 0) a.delta[i] = s;
 }
 
-// grad_k and grad_v of 64 keys (16 per wave) of one (sequence, group), over
-// 32 rows at a time.
-template <typename InT, int D>
-__global__ __launch_bounds__(AB_THREADS) void attn_bwd_kv_f32_kernel(AttnBwdParams a) {
-    const AttnParams& p = a.f;
-    constexpr int PITCH = D + 4, S = D / 16, PER = D / 8;
-    __shared__ __attribute__((aligned(16))) float qs[AB_ROWS * PITCH], gs[AB_ROWS * PITCH];
-    __shared__ float lse2[AB_ROWS], delta[AB_ROWS];
-    __shared__ int32_t from[AB_ROWS];   // a row sees keys up to this one
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
-    const AttnPlace pl = attn_place(blockIdx.x, a.key_slots, p.G);
-    const AttnBlock b = attn_block(p, pl.item, 1, AB_BLOCK);
-    if (b.j < 0) return;
-    const int key = b.r0 + wave * 16 + col;
-    const bool valid = key < b.r1;
-    const int32_t n_rows = b.tokens * p.hpg;
-    const int64_t krow = b.start + (valid ? key : b.r0);
-    float k[S][4], v[S][4];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        load4((const InT*)p.k + krow * p.k_stride + (int64_t)pl.g * D + 16 * s + 4 * grp, k[s]);
-        load4((const InT*)p.v + krow * p.v_stride + (int64_t)pl.g * D + 16 * s + 4 * grp, v[s]);
+// Tiles of 16 float32 rows in LDS, 16-byte unit u of row r in place u ^ (r & 15).
+template <int D>
+struct F32Tile {
+    static constexpr int ROWB = 4 * D, UNITS = D / 4, BYTES = 16 * ROWB, LOADS = BYTES / 1024, RPL = 1024 / ROWB;
+    // row l & 15, values 16 s + 4 (l >> 4) .. + 3
+    static __device__ __forceinline__ void rows(const char* tile, int col, int grp, int s, float (&x)[4]) {
+        load4(reinterpret_cast<const float*>(tile + col * ROWB + ((4 * s + grp) ^ col) * 16), x);
     }
-    f32x4 gk[S], gv[S];
+    // rows 4 (l >> 4) .. + 3, value 16 s + (l & 15)
+    static __device__ __forceinline__ void cols(const char* tile, int col, int grp, int s, float (&x)[4]) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) gk[s] = gv[s] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const float c = p.scale * kLog2e;
-    const int32_t r_first = p.causal ? b.r0 * p.hpg / AB_ROWS * AB_ROWS : 0;
-    for (int32_t r0 = r_first; r0 < n_rows; r0 += AB_ROWS) {
-        __syncthreads();
-        {
-            const int row = r0 + (tid >> 3), cc = (tid & 7) * 4;
-            const bool in = row < n_rows;
-            const int32_t t = in ? row / p.hpg : 0;
-            const int64_t at = (b.start + t) * p.H + pl.g * p.hpg + (in ? row - t * p.hpg : 0);
-            const InT* qr = (const InT*)p.q + (b.start + t) * p.q_stride + (int64_t)(at - (b.start + t) * p.H) * D;
-#pragma unroll
-            for (int i = 0; i < PER / 4; ++i) {
-                float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-                if (in) {
-                    load4(qr + cc + 32 * i, x);
-                    load4((const InT*)a.go + at * D + cc + 32 * i, y);
-                }
-                *reinterpret_cast<f32x4*>(qs + (tid >> 3) * PITCH + cc + 32 * i) = f32x4{x[0], x[1], x[2], x[3]};
-                *reinterpret_cast<f32x4*>(gs + (tid >> 3) * PITCH + cc + 32 * i) = f32x4{y[0], y[1], y[2], y[3]};
-            }
-            if ((tid & 7) == 0) {
-                lse2[tid >> 3] = in ? p.lse[at] * kLog2e : 0.f;
-                delta[tid >> 3] = in ? a.delta[at] : 0.f;
-                from[tid >> 3] = !in ? -1 : p.causal ? t : b.tokens;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-            f32x4 sc = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float x[4];
-                load4(qs + (16 * rt + col) * PITCH + 16 * s + 4 * grp, x);
-                mma_k16<true, PLAIN>(sc, x, k[s]);
-                load4(gs + (16 * rt + col) * PITCH + 16 * s + 4 * grp, x);
-                mma_k16<true, PLAIN>(dp, x, v[s]);
-            }
-            float w[4], ds[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 16 * rt + 4 * grp + i;
-                w[i] = valid && key <= from[r] ? attn_exp2(sc[i] * c - lse2[r]) : 0.f;
-                ds[i] = w[i] * (dp[i] - delta[r]);
-            }
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float x[4], y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = gs[(16 * rt + 4 * grp + e) * PITCH + 16 * s + col];
-                    y[e] = qs[(16 * rt + 4 * grp + e) * PITCH + 16 * s + col];
-                }
-                mma_k16<true, PLAIN>(gv[s], w, x);
-                mma_k16<true, PLAIN>(gk[s], ds, y);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const int r = 4 * grp + e;
+            x[e] = *reinterpret_cast<const float*>(tile + r * ROWB + ((4 * s + (col >> 2)) ^ r) * 16 + 4 * (col & 3));
         }
     }
+};
+// Sums of the four waves, [16][D] each, N of them, in `joint`; x: column l & 15, rows 16 s + 4 (l >> 4) .. + 3.
+template <int D, int N>
+__device__ __forceinline__ float* join_waves(char* lds, const f32x4 (&x)[N][D / 16]) {
+    constexpr int PITCH = D + 4;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float* joint = reinterpret_cast<float*>(lds);
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int mine = b.r0 + wave * 16 + 4 * grp + i;
-        if (mine < b.r1) {
-            InT* tk = (InT*)a.gk + (b.start + mine) * a.gk_stride + (int64_t)pl.g * D;
-            InT* tv = (InT*)a.gv + (b.start + mine) * a.gv_stride + (int64_t)pl.g * D;
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                tk[16 * s + col] = (InT)(gk[s][i] * p.scale);
-                tv[16 * s + col] = (InT)gv[s][i];
-            }
-        }
+        for (int s = 0; s < D / 16; ++s)
+            *reinterpret_cast<f32x4*>(joint + ((wave * N + n) * 16 + (lane & 15)) * PITCH + 16 * s + 4 * (lane >> 4)) = x[n][s];
+    __syncthreads();
+    return joint;
+}
+template <int D, int N>
+__device__ __forceinline__ void joint_sum(const float* joint, int n, int row, int d, float (&y)[4]) {
+    constexpr int PITCH = D + 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const f32x4 z = *reinterpret_cast<const f32x4*>(joint + ((w * N + n) * 16 + row) * PITCH + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += z[e];
     }
 }
 
-// grad_q of 64 rows (16 per wave), over 32 keys at a time.
-template <typename InT, int D>
-__global__ __launch_bounds__(AB_THREADS) void attn_bwd_q_f32_kernel(AttnBwdParams a) {
+// grad_k and grad_v of 16 keys of one (sequence, group): the four waves take 16
+// rows each in turn, in LDS of their own, two deep, and join their sums at the
+// end (as one workgroup of 64 keys whose waves share the rows, 517 tokens of 6
+// heads took 72 us, with a quarter of the waves).
+template <int D>
+__global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_kernel(AttnBwdParams a) {
     const AttnParams& p = a.f;
-    constexpr int PITCH = D + 4, S = D / 16, PER = D / 8;
-    __shared__ __attribute__((aligned(16))) float ks[AB_ROWS * PITCH], vs[AB_ROWS * PITCH];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
+    typedef F32Tile<D> Tile;
+    constexpr int S = D / 16, LOADS = Tile::LOADS, HALF = 2 * Tile::BYTES + 512;   // q, grad_o, lse and delta of 16 rows
+    __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * HALF];
+    static_assert(4 * 2 * 16 * (D + 4) * 4 <= (int)sizeof(lds), "");
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, grp = lane >> 4;
+    const AttnPlace pl = attn_place(blockIdx.x, a.key_slots, p.G);
+    const AttnBlock b = attn_block(p, pl.item, 1, AB_BLOCK);
+    if (b.j < 0) return;
+    const int key = b.r0 + col;
+    const int32_t n_rows = b.tokens * p.hpg;
+    const int64_t krow = b.start + (key < b.r1 ? key : b.r0);
+    float k[S][4], v[S][4];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        load4((const float*)p.k + krow * p.k_stride + (int64_t)pl.g * D + 16 * s + 4 * grp, k[s]);
+        load4((const float*)p.v + krow * p.v_stride + (int64_t)pl.g * D + 16 * s + 4 * grp, v[s]);
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(k[s][e]), "+v"(v[s][e]));   // (arrive)
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 2 * HALF;
+    const char* own = lds + wave * 2 * HALF;
+    const int64_t gstride = (int64_t)p.H * D;
+    const RowOf rows(p.hpg);
+    auto request = [&](int32_t r0, int buf) {
+        const int32_t t0 = r0 / p.hpg, h0 = r0 - t0 * p.hpg;
+        const int64_t head = (int64_t)pl.g * p.hpg;
+        const auto qrs = make_rsrc((const float*)p.q + (b.start + t0) * p.q_stride + head * D, 0x40000000);
+        const auto grs = make_rsrc((const float*)a.go + (b.start + t0) * gstride + head * D, 0x40000000);
+        const auto lrs = make_rsrc(p.lse + (b.start + t0) * p.H + head, 0x40000000);
+        const auto drs = make_rsrc(a.delta + (b.start + t0) * p.H + head, 0x40000000);
+        const uint32_t to = lds0 + buf * HALF;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int r = i * Tile::RPL + lane / Tile::UNITS, u = (lane % Tile::UNITS) ^ r;
+            uint32_t t, hh;
+            rows.of((uint32_t)(h0 + r), t, hh);
+            const uint32_t at = hh * (4 * D) + u * 16;
+            const bool in = r0 + r < n_rows;                  // rows behind the last one read as zero
+            load_to_lds(qrs, in ? t * (uint32_t)(p.q_stride * 4) + at : 0x80000000u, to + i * 1024);
+            load_to_lds(grs, in ? t * (uint32_t)(gstride * 4) + at : 0x80000000u, to + Tile::BYTES + i * 1024);
+        }
+        uint32_t t, hh;
+        rows.of((uint32_t)(h0 + col), t, hh);
+        const uint32_t at = r0 + col < n_rows ? (t * (uint32_t)p.H + hh) * 4 : 0x80000000u;
+        load4_to_lds(lrs, at, to + 2 * Tile::BYTES);
+        load4_to_lds(drs, at, to + 2 * Tile::BYTES + 256);
+    };
+    f32x4 g[2][S];   // grad_k, grad_v
+#pragma unroll
+    for (int s = 0; s < S; ++s) g[0][s] = g[1][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const float c = p.scale * kLog2e;
+    const int32_t from = p.causal ? key * p.hpg : 0, from_most = p.causal ? (b.r0 + 15) * p.hpg : 0;
+    const int32_t first = (p.causal ? (int32_t)((int64_t)b.r0 * p.hpg / 16 * 16) : 0) + 16 * wave;
+    if (first < n_rows) request(first, 0);
+    for (int32_t r0 = first; r0 < n_rows; r0 += 64) {
+        const int buf = ((r0 - first) >> 6) & 1;
+        if (r0 + 64 < n_rows) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (the other half has been read)
+            request(r0 + 64, buf ^ 1);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * LOADS + 2) : "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        const char *qs = own + buf * HALF, *gs = qs + Tile::BYTES;
+        const float* stat = reinterpret_cast<const float*>(gs + Tile::BYTES);
+        f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float z[4];
+            Tile::rows(qs, col, grp, s, z);
+            mma_k16<true, PLAIN>(x, z, k[s]);
+            Tile::rows(gs, col, grp, s, z);
+            mma_k16<true, PLAIN>(y, z, v[s]);
+        }
+        float lse[4], delta[4], w[4], ds[4];
+        load4(stat + 4 * grp, lse);
+        load4(stat + 64 + 4 * grp, delta);
+        const bool some = r0 < from_most || r0 + 16 > n_rows;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 4 * grp + i;
+            w[i] = attn_exp2(fmaf(x[i], c, -lse[i] * kLog2e));
+            if (some) w[i] = r >= from && r < n_rows ? w[i] : 0.f;
+            ds[i] = w[i] * (y[i] - delta[i]);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float z[4];
+            Tile::cols(qs, col, grp, s, z);
+            mma_k16<true, PLAIN>(g[0][s], z, ds);
+            Tile::cols(gs, col, grp, s, z);
+            mma_k16<true, PLAIN>(g[1][s], z, w);
+        }
+    }
+    const float* joint = join_waves<D, 2>(lds, g);
+    const int mine = tid >> 4, d0 = (tid & 15) * 4;
+    if (b.r0 + mine >= b.r1) return;
+    float* tk = (float*)a.gk + (b.start + b.r0 + mine) * a.gk_stride + (int64_t)pl.g * D;
+    float* tv = (float*)a.gv + (b.start + b.r0 + mine) * a.gv_stride + (int64_t)pl.g * D;
+#pragma unroll
+    for (int n = 0; n < D / 64; ++n) {
+        float z[4];
+        joint_sum<D, 2>(joint, 0, mine, 64 * n + d0, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] *= p.scale;
+        store4(tk + 64 * n + d0, z);
+        joint_sum<D, 2>(joint, 1, mine, 64 * n + d0, z);
+        store4(tv + 64 * n + d0, z);
+    }
+}
+
+// grad_q of 16 rows, the waves taking 16 keys each in turn.
+template <int D>
+__global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_kernel(AttnBwdParams a) {
+    const AttnParams& p = a.f;
+    typedef F32Tile<D> Tile;
+    constexpr int S = D / 16, LOADS = Tile::LOADS, HALF = 2 * Tile::BYTES;   // keys, values
+    __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * HALF];
+    static_assert(4 * 16 * (D + 4) * 4 <= (int)sizeof(lds), "");
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, grp = lane >> 4;
     const AttnPlace pl = attn_place(blockIdx.x, p.slots, p.G);
     const AttnBlock b = attn_block(p, p.slots - 1 - pl.item, p.hpg, AB_BLOCK);
     if (b.j < 0) return;
-    const int row = b.r0 + wave * 16 + col;
+    const int row = b.r0 + col;
     const bool valid = row < b.r1;
-    const int32_t t = valid ? row / p.hpg : 0;
+    const int32_t t = (valid ? row : b.r1 - 1) / p.hpg;
     const int head = pl.g * p.hpg + (valid ? row - t * p.hpg : 0);
     const int64_t at = (b.start + t) * p.H + head;
-    const int32_t sees = !valid ? 0 : p.causal ? t + 1 : b.tokens;
-    const int32_t most = p.causal ? (b.r1 - 1) / p.hpg + 1 : b.tokens;
+    const int32_t sees = p.causal ? t + 1 : b.tokens, most = p.causal ? (b.r1 - 1) / p.hpg + 1 : b.tokens;
+    const int32_t sees_least = __builtin_amdgcn_readfirstlane(sees);
     float q[S][4], go[S][4];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        load4((const InT*)p.q + (b.start + t) * p.q_stride + (int64_t)head * D + 16 * s + 4 * grp, q[s]);
-        load4((const InT*)a.go + at * D + 16 * s + 4 * grp, go[s]);
+        load4((const float*)p.q + (b.start + t) * p.q_stride + (int64_t)head * D + 16 * s + 4 * grp, q[s]);
+        load4((const float*)a.go + at * D + 16 * s + 4 * grp, go[s]);
     }
-    const float lse2 = p.lse[at] * kLog2e, delta = a.delta[at], c = p.scale * kLog2e;
-    f32x4 gq[S];
+    float lse2 = p.lse[at] * kLog2e, delta = a.delta[at];
 #pragma unroll
-    for (int s = 0; s < S; ++s) gq[s] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int32_t k0 = 0; k0 < most; k0 += AB_ROWS) {
-        __syncthreads();
-        {
-            const int key = k0 + (tid >> 3), cc = (tid & 7) * 4;
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int i = 0; i < PER / 4; ++i) {
-                float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-                if (key < most) {
-                    load4((const InT*)p.k + (b.start + key) * p.k_stride + (int64_t)pl.g * D + cc + 32 * i, x);
-                    load4((const InT*)p.v + (b.start + key) * p.v_stride + (int64_t)pl.g * D + cc + 32 * i, y);
-                }
-                *reinterpret_cast<f32x4*>(ks + (tid >> 3) * PITCH + cc + 32 * i) = f32x4{x[0], x[1], x[2], x[3]};
-                *reinterpret_cast<f32x4*>(vs + (tid >> 3) * PITCH + cc + 32 * i) = f32x4{y[0], y[1], y[2], y[3]};
-            }
+        for (int e = 0; e < 4; ++e) asm volatile("" : "+v"(q[s][e]), "+v"(go[s][e]));   // (arrive)
+    asm volatile("" : "+v"(lse2), "+v"(delta));
+    const float c = p.scale * kLog2e;
+    const AttnKeys<float, false> keys(p, b.n, b.start, pl.g);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 2 * HALF;
+    const char* own = lds + wave * 2 * HALF;
+    auto request = [&](int32_t key, int buf) {
+        const int32_t left = most - key < 16 ? most - key : 16;
+        const auto krs = make_rsrc(keys.k + key * keys.k_stride, ((left - 1) * (int)keys.k_stride + D) * 4);
+        const auto vrs = make_rsrc(keys.v + key * keys.v_stride, ((left - 1) * (int)keys.v_stride + D) * 4);
+        const uint32_t to = lds0 + buf * HALF;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int r = i * Tile::RPL + lane / Tile::UNITS, u = (lane % Tile::UNITS) ^ r;
+            load_to_lds(krs, (uint32_t)(r * (int)keys.k_stride * 4 + u * 16), to + i * 1024);
+            load_to_lds(vrs, (uint32_t)(r * (int)keys.v_stride * 4 + u * 16), to + Tile::BYTES + i * 1024);
         }
-        __syncthreads();
+    };
+    f32x4 g[1][S];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            f32x4 sc = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < S; ++s) g[0][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int32_t first = 16 * wave;
+    if (first < most) request(first, 0);
+    for (int32_t k0 = first; k0 < most; k0 += 64) {
+        const int buf = (k0 >> 6) & 1;
+        if (k0 + 64 < most) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (the other half has been read)
+            request(k0 + 64, buf ^ 1);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * LOADS) : "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        const char *ks = own + buf * HALF, *vs = ks + Tile::BYTES;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float x[4];
-                load4(ks + (16 * kt + col) * PITCH + 16 * s + 4 * grp, x);
-                mma_k16<true, PLAIN>(sc, x, q[s]);
-                load4(vs + (16 * kt + col) * PITCH + 16 * s + 4 * grp, x);
-                mma_k16<true, PLAIN>(dp, x, go[s]);
-            }
-            float ds[4];
+        for (int s = 0; s < S; ++s) {
+            float z[4];
+            Tile::rows(ks, col, grp, s, z);
+            mma_k16<true, PLAIN>(x, z, q[s]);
+            Tile::rows(vs, col, grp, s, z);
+            mma_k16<true, PLAIN>(y, z, go[s]);
+        }
+        float ds[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool seen = k0 + 16 * kt + 4 * grp + i < sees;
-                ds[i] = seen ? attn_exp2(sc[i] * c - lse2) * (dp[i] - delta) : 0.f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            ds[i] = attn_exp2(fmaf(x[i], c, -lse2)) * (y[i] - delta);
+            if (k0 + 16 > sees_least) ds[i] = k0 + 4 * grp + i < sees ? ds[i] : 0.f;
+        }
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = ks[(16 * kt + 4 * grp + e) * PITCH + 16 * s + col];
-                mma_k16<true, PLAIN>(gq[s], x, ds);
-            }
+        for (int s = 0; s < S; ++s) {
+            float z[4];
+            Tile::cols(ks, col, grp, s, z);
+            mma_k16<true, PLAIN>(g[0][s], z, ds);
         }
     }
-    if (!valid) return;
-    InT* to = (InT*)a.gq + (b.start + t) * a.gq_stride + (int64_t)head * D;
+    const float* joint = join_waves<D, 1>(lds, g);
+    const int mine = b.r0 + (tid >> 4), d0 = (tid & 15) * 4;
+    if (mine >= b.r1) return;
+    const int32_t tm = mine / p.hpg;
+    float* to = (float*)a.gq + (b.start + tm) * a.gq_stride + (int64_t)(pl.g * p.hpg + mine - tm * p.hpg) * D;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const float y[4] = {gq[s][0] * p.scale, gq[s][1] * p.scale, gq[s][2] * p.scale, gq[s][3] * p.scale};
-        store4(to + 16 * s + 4 * grp, y);
+    for (int n = 0; n < D / 64; ++n) {
+        float z[4];
+        joint_sum<D, 1>(joint, 0, tid >> 4, 64 * n + d0, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] *= p.scale;
+        store4(to + 64 * n + d0, z);
     }
 }
 
@@ -239,17 +326,17 @@ hipError_t launch_attn_delta(const AttnBwdParams& a, bool bf16_in, hipStream_t s
     return hipGetLastError();
 }
 
-template <typename InT, int D>
+template <int D>
 static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
-    attn_bwd_kv_f32_kernel<InT, D><<<dim3((uint32_t)(a.key_slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
-    attn_bwd_q_f32_kernel<InT, D><<<dim3((uint32_t)(a.f.slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
+    attn_bwd_kv_f32_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
+    attn_bwd_q_f32_kernel<D><<<dim3((uint32_t)(a.f.slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
 }
 
 hipError_t launch_attn_bwd_f32(const AttnBwdParams& a, hipStream_t stream) {
     if (a.f.rows == 0) return hipSuccess;
     const hipError_t e = launch_attn_delta(a, false, stream);
     if (e != hipSuccess) return e;
-    a.f.D == 64 ? run_bwd<float, 64>(a, stream) : run_bwd<float, 128>(a, stream);
+    a.f.D == 64 ? run_bwd<64>(a, stream) : run_bwd<128>(a, stream);
     return hipGetLastError();
 }
 

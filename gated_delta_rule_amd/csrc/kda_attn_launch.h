@@ -40,6 +40,7 @@ struct AttnParams {
 // 2), at part + (((slot * G + g) * splits + s) * block + row) * (D + 2).
 constexpr int kAttnBlockF32 = 64;    // rows of a block
 constexpr int kAttnBlockBf16 = 128;
+constexpr int kAttnBwdBlockF32 = 16;
 hipError_t launch_attn_fwd_f32(const AttnParams& p, hipStream_t stream);
 hipError_t launch_attn_fwd_bf16(const AttnParams& p, hipStream_t stream);
 hipError_t launch_attn_join(const AttnParams& p, bool bf16_in, int block, hipStream_t stream);

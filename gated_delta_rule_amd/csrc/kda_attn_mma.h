@@ -38,6 +38,10 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t 
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :: "s"(to), "v"(off), "s"(rs) : "memory", "m0");
 }
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t to) {   // 4 bytes per lane
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :: "s"(to), "v"(off), "s"(rs) : "memory", "m0");
+}
 // All of this wave's loads to LDS have arrived and its LDS reads are done; then the workgroup's barrier.
 __device__ __forceinline__ void tiles_barrier() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -88,5 +92,16 @@ __device__ __forceinline__ f32x16 zero16() {
     for (int e = 0; e < 16; ++e) z[e] = 0.f;
     return z;
 }
+
+// Token and head of the group that row x of `per` rows to a token is, x <
+// 2^16: x / per = x * ceil(2^32 / per) >> 32.
+struct RowOf {
+    uint32_t per, inv;
+    __device__ __forceinline__ explicit RowOf(int32_t hpg) : per((uint32_t)hpg), inv(hpg > 1 ? 0xffffffffu / (uint32_t)hpg + 1 : 0) {}
+    __device__ __forceinline__ void of(uint32_t x, uint32_t& t, uint32_t& hh) const {
+        t = per > 1 ? __umulhi(x, inv) : x;
+        hh = x - t * per;
+    }
+};
 
 }  // namespace kda
