@@ -18,6 +18,7 @@ constexpr int64_t kMaxRows = (int64_t)1 << 36;
 constexpr int64_t kMaxSeqRows = (int64_t)1 << 30;        // tokens * heads of a group, counted in 32 bits
 constexpr int64_t kUnits = 256;                          // compute units
 constexpr int64_t kFill = 512;                           // workgroups that fill the GPU (two per compute unit)
+constexpr int64_t kMinPartRows = 256;                    // rows of a part of the backward pass
 constexpr int64_t kMinSplitKeys = 256;                   // keys of a part, at least
 
 int attn_shape(int in_dtype, int32_t n_seqs, int64_t T, int32_t H, int32_t G, int32_t D, bool varlen, int64_t* rows) {
@@ -75,8 +76,11 @@ kda::AttnParams attn_params(const void* q, int64_t q_stride, const void* k, int6
     return p;
 }
 
-// Parts of a request's keys (block kernels): so many that the GPU is full,
-// with kMinSplitKeys keys each where a request holds all it can.
+// Paged attention: a few rows per (request, group) go to the step kernel, whose
+// workgroups share all requests' keys equally; more of them to the block
+// kernels, where blocks that do not fill the GPU share their keys, too (bf16:
+// equal pieces of all blocks; float32: so many parts per block that the GPU is
+// full, with kMinSplitKeys keys each where a request holds all it can).
 struct PagedPlan {
     bool step;
     int64_t slots, splits, workgroups, max_rows, bytes;
@@ -98,7 +102,14 @@ PagedPlan paged_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t
     }
     a.block = block_rows(bf16);
     a.slots = block_slots(rows, n_seqs, T, H / G, a.block, varlen);
+    a.splits = 1;
     const int64_t units = a.slots * G;
+    if (bf16) {
+        // (from four blocks per workgroup on, the order of the blocks evens them out)
+        a.workgroups = units > 0 && units < 4 * kFill ? kFill : 0;
+        a.bytes = a.workgroups > 0 ? ((2 * units + 3) / 4 * 4 + 2 * a.workgroups * a.block * (D + 4)) * 4 : 0;
+        return a;
+    }
     const int64_t want = units > 0 ? kFill / units : 1, most = max_tokens / kMinSplitKeys;
     a.splits = want < most ? want : most;
     if (a.splits < 1) a.splits = 1;
@@ -106,15 +117,30 @@ PagedPlan paged_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t
     return a;
 }
 
+// The backward pass cuts the rows that a block of keys walks into parts, so
+// that there are about 1024 workgroups (twice as many as run at once: the
+// first keys' blocks walk the most rows) of at least 256 rows each; the parts'
+// sums are added by another launch.  32 heads of 128 on 8, with 1 / 2 / 4 / 8 / 16
+// parts, us: 512 tokens 112 / 77 / 60 / 51 / 51, 2048 tokens 407 / 256 / 189 / 186 / 246,
+// 4096 tokens 878 / 611 / 542 / 585 / 681, 2 x 4096 1150 / 1013 / 1034 / 1138 / 1352.
 struct BwdPlan {
-    int64_t slots, key_slots, bytes;
+    int64_t slots, key_slots, parts, delta, bytes;   // delta: bytes before the parts' sums
 };
-BwdPlan bwd_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, bool varlen) {
+BwdPlan bwd_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, int32_t G, int32_t D, bool varlen) {
     BwdPlan b{};
     const int block = bf16 ? kda::kAttnBlockBf16 : kda::kAttnBwdBlockF32;
     b.slots = block_slots(rows, n_seqs, T, H / G, block, varlen);
     b.key_slots = block_slots(rows, n_seqs, T, 1, block, varlen);
-    b.bytes = (rows * H * 4 + 15) / 16 * 16;
+    b.delta = (rows * H * 4 + 15) / 16 * 16;
+    b.parts = 1;
+    if (bf16) {
+        // (the same for a packed batch of equal lengths)
+        const int64_t most = rows * (H / G) / kMinPartRows, blocks = block_slots(rows, n_seqs, T, 1, block, true) * G;
+        b.parts = blocks > 0 ? (2 * kFill + blocks / 2) / blocks : 1;
+        if (b.parts > most) b.parts = most;
+        if (b.parts < 1) b.parts = 1;
+    }
+    b.bytes = b.delta + (b.parts > 1 ? b.parts * rows * G * 2 * D * 4 : 0);
     return b;
 }
 
@@ -158,7 +184,7 @@ size_t kda_attn_bwd_workspace_bytes(int in_dtype, int32_t n_seqs, int64_t T, int
                                     int varlen) {
     int64_t rows = 0;
     if (attn_shape(in_dtype, n_seqs, T, H, G, D, varlen != 0, &rows) || rows == 0) return 0;
-    return (size_t)bwd_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, varlen != 0).bytes;
+    return (size_t)bwd_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, D, varlen != 0).bytes;
 }
 
 int kda_attn_bwd_fresh(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -181,8 +207,9 @@ int kda_attn_bwd_fresh(const void* q, int64_t q_stride, const void* k, int64_t k
     for (const void* a : wide)
         if (!aligned(a, 16)) return KDA_ERR_MISALIGNED;
     if (!aligned(lse, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_MISALIGNED;
-    const BwdPlan plan = bwd_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, varlen);
-    if (plan.slots > kMaxWideGroups / G || plan.key_slots > kMaxWideGroups / G || rows * H / 8 >= kMaxWorkgroups)
+    const BwdPlan plan = bwd_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, D, varlen);
+    if (plan.slots > kMaxWideGroups / G || plan.key_slots * plan.parts > kMaxWideGroups / G ||
+        rows * H / 8 >= kMaxWorkgroups || rows * G / 4 >= kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
     if (!workspace || workspace_bytes < (size_t)plan.bytes) return KDA_ERR_WORKSPACE;
     const Span outs[] = {rows_span(grad_q, rows, grad_q_stride, HD, es), rows_span(grad_k, rows, grad_k_stride, GD, es),
@@ -209,6 +236,8 @@ int kda_attn_bwd_fresh(const void* q, int64_t q_stride, const void* k, int64_t k
     a.gk_stride = grad_k_stride;
     a.gv_stride = grad_v_stride;
     a.delta = (float*)workspace;
+    a.part = (float*)((char*)workspace + plan.delta);
+    a.parts = (int32_t)plan.parts;
     a.zero_rest = fresh;
     return status(in_dtype == KDA_BF16 ? kda::launch_attn_bwd_bf16(a, stream) : kda::launch_attn_bwd_f32(a, stream));
 }

@@ -26,8 +26,9 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
     __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // q, q, grad_o, grad_o
     __shared__ __attribute__((aligned(16))) float stat[2][2][BW_STEP];   // of each row: lse in base 2, delta
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const AttnPlace pl = attn_place(attn_zigzag(blockIdx.x, gridDim.x, p.G), a.key_slots, p.G);
-    int64_t slot = pl.item;
+    const AttnPlace pl = attn_place(attn_zigzag(blockIdx.x, gridDim.x, p.G), a.key_slots * a.parts, p.G);
+    int64_t slot = pl.item / a.parts;
+    const int part = (int)(pl.item % a.parts);
     if (!p.cu && p.causal) {   // the first blocks of all sequences, then the second ones: they have the most rows
         const int64_t each = a.key_slots / p.n_seqs;
         slot = (slot % p.n_seqs) * each + slot / p.n_seqs;
@@ -35,7 +36,6 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
     const AttnBlock b = attn_block(p, slot, 1, BW_BLOCK);
     if (b.j < 0) return;
     const int32_t key0 = b.r0 + wave * 32;   // this wave's first key
-    const int32_t n_rows = b.tokens * p.hpg;
 
     bf16x8 k[S], v[S];
     {
@@ -59,7 +59,11 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
     for (int i = 0; i < O; ++i) gk[i] = gv[i] = zero16();
 
     const float c = p.scale * kLog2e;
-    const int32_t r_first = p.causal ? (int32_t)((int64_t)b.r0 * p.hpg / BW_STEP * BW_STEP) : 0;
+    // rows [r_first, n_rows), of which this part takes whole steps
+    const int32_t all_rows = b.tokens * p.hpg, r_all = p.causal ? (int32_t)((int64_t)b.r0 * p.hpg / BW_STEP * BW_STEP) : 0;
+    const int64_t steps = ((int64_t)all_rows - r_all + BW_STEP - 1) / BW_STEP;
+    const int32_t r_first = r_all + (int32_t)(steps * part / a.parts) * BW_STEP;
+    const int32_t r_end = r_all + (int32_t)(steps * (part + 1) / a.parts) * BW_STEP, n_rows = r_end < all_rows ? r_end : all_rows;
     // key x is seen by the rows from x * hpg on
     const int32_t from_least = p.causal ? key0 * p.hpg : 0, from_most = p.causal ? (key0 + 31) * p.hpg : 0;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
@@ -90,7 +94,7 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
             if (r0 + r < n_rows) mine = (tid < BW_STEP ? p.lse : a.delta)[(b.start + t0 + t) * p.H + pl.g * p.hpg + hh];
         }
     };
-    request(r_first, 0);
+    if (r_first < n_rows) request(r_first, 0);
     for (int32_t r0 = r_first; r0 < n_rows; r0 += BW_STEP) {
         const int buf = ((r0 - r_first) / BW_STEP) & 1;
         if (tid < 2 * BW_STEP) {   // (a row that is not there has weight e^{-inf})
@@ -156,6 +160,19 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
     }
     const int key = key0 + (lane & 31), half = lane >> 5;
     if (key >= b.r1) return;
+    if (a.parts > 1) {
+        float* to = a.part + (((part * p.rows + b.start + key) * p.G + pl.g) * 2) * D + 4 * half;
+#pragma unroll
+        for (int i = 0; i < O; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y[4] = {gk[i][4 * e], gk[i][4 * e + 1], gk[i][4 * e + 2], gk[i][4 * e + 3]};
+                const float z[4] = {gv[i][4 * e], gv[i][4 * e + 1], gv[i][4 * e + 2], gv[i][4 * e + 3]};
+                store4(to + 32 * i + 8 * e, y);
+                store4(to + D + 32 * i + 8 * e, z);
+            }
+        return;
+    }
     __bf16* tk = (__bf16*)a.gk + (b.start + key) * a.gk_stride + (int64_t)pl.g * D + 4 * half;
     __bf16* tv = (__bf16*)a.gv + (b.start + key) * a.gv_stride + (int64_t)pl.g * D + 4 * half;
 #pragma unroll
@@ -171,6 +188,31 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
             store4(tk + 32 * i + 8 * e, y);
             store4(tv + 32 * i + 8 * e, z);
         }
+}
+
+// grad_k and grad_v from their parts, in order.
+template <int D>
+__global__ __launch_bounds__(256) void attn_bwd_join_kernel(AttnBwdParams a) {
+    const AttnParams& p = a.f;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, item = i / (D / 2);   // (row, group); four values per thread
+    if (item >= p.rows * p.G) return;
+    const int64_t row = item / p.G;
+    const int g = (int)(item - row * p.G), d = (int)(i % (D / 2)) * 4;
+    if (p.cu && (row < attn_range(p.cu, p.rows, p.T, 0).start || row >= attn_range(p.cu, p.rows, p.T, p.n_seqs - 1).end)) return;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int part = 0; part < a.parts; ++part) {
+        float x[4];
+        load4(a.part + ((part * p.rows * p.G + item) * 2) * D + d, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += x[e];
+    }
+    if (d < D) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] *= p.scale;
+        store4((__bf16*)a.gk + row * a.gk_stride + (int64_t)g * D + d, s);
+    } else {
+        store4((__bf16*)a.gv + row * a.gv_stride + (int64_t)g * D + d - D, s);
+    }
 }
 
 // grad_q of 128 rows of one (sequence, group).
@@ -286,7 +328,9 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
 
 template <int D>
 static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
-    attn_bwd_kv_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G)), BW_THREADS, 0, stream>>>(a);
+    attn_bwd_kv_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G * a.parts)), BW_THREADS, 0, stream>>>(a);
+    if (a.parts > 1)
+        attn_bwd_join_kernel<D><<<dim3((uint32_t)((a.f.rows * a.f.G * (D / 2) + 255) / 256)), 256, 0, stream>>>(a);
     attn_bwd_q_kernel<D><<<dim3((uint32_t)(a.f.slots * a.f.G)), BW_THREADS, 0, stream>>>(a);
 }
 

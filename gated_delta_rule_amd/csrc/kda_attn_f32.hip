@@ -16,13 +16,13 @@ namespace kda {
 constexpr int AF_THREADS = 256, AF_KEYS = 32, AF_BLOCK = kAttnBlockF32;
 
 // Rows of a tile of AF_KEYS keys, as float32: eight threads to a row.
-template <typename InT, int D, bool PAGED>
+template <int D, bool PAGED>
 struct KeyStage {
     static constexpr int PER = D / 8;     // values per thread
     float k[PER], v[PER];
     bool ok;
     // key: this thread's; len: keys that exist
-    __device__ __forceinline__ void load(const AttnKeys<InT, PAGED>& a, int32_t key, int32_t len) {
+    __device__ __forceinline__ void load(const AttnKeys<float, PAGED>& a, int32_t key, int32_t len) {
         int64_t ko = 0, vo = 0;
         ok = key < len && a.at(key, ko, vo);
         const int c = (threadIdx.x & 7) * 4;
@@ -50,7 +50,7 @@ struct KeyStage {
     }
 };
 
-template <typename InT, int D, bool PAGED>
+template <int D, bool PAGED>
 __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) {
     constexpr int PITCH = D + 4, S = D / 16;
     __shared__ __attribute__((aligned(16))) float ks[AF_KEYS * PITCH], vs[AF_KEYS * PITCH];
@@ -73,17 +73,17 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
     const int32_t t0 = (int32_t)((int64_t)tiles * split / p.splits), t1 = (int32_t)((int64_t)tiles * (split + 1) / p.splits);
 
     float q[S][4];
-    const InT* qrow = (const InT*)p.q + (b.start + t) * p.q_stride + (int64_t)head * D;
+    const float* qrow = (const float*)p.q + (b.start + t) * p.q_stride + (int64_t)head * D;
 #pragma unroll
     for (int s = 0; s < S; ++s) load4(qrow + 16 * s + 4 * grp, q[s]);
 
-    const AttnKeys<InT, PAGED> keys(p, b.n, b.start, pl.g);
+    const AttnKeys<float, PAGED> keys(p, b.n, b.start, pl.g);
     f32x4 o[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) o[s] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
     const float c = p.scale * kLog2e;
-    KeyStage<InT, D, PAGED> st;
+    KeyStage<D, PAGED> st;
     if (t0 < t1) st.load(keys, t0 * AF_KEYS + (tid >> 3), most);
     for (int32_t tile = t0; tile < t1; ++tile) {
         __syncthreads();
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
         return;
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    InT* orow = (InT*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
+    float* orow = (float*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const float y[4] = {o[s][0] * inv, o[s][1] * inv, o[s][2] * inv, o[s][3] * inv};
@@ -156,8 +156,9 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
 
 // The parts of a split block: o = sum_s e^{m_s - m} o_s / sum_s e^{m_s - m} l_s,
 // in the order of the parts.  A wave has a row.
-template <typename InT, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, int block) {
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
+    constexpr int block = AF_BLOCK;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t per = (uint32_t)block / 4;                 // workgroups of a block
     const uint32_t unit = blockIdx.x / per;
@@ -181,36 +182,23 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, int block)
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int row = b.r0 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
-    InT* orow = (InT*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
-    orow[lane] = (InT)(o0 * inv);
-    if constexpr (D == 128) orow[64 + lane] = (InT)(o1 * inv);
+    float* orow = (float*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
+    orow[lane] = o0 * inv;
+    if constexpr (D == 128) orow[64 + lane] = o1 * inv;
     if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-template <typename InT, int D>
+template <int D>
 static void run_fwd(const AttnParams& p, hipStream_t stream) {
     const dim3 grid((uint32_t)(p.slots * p.G * p.splits));
-    if (p.lengths) attn_fwd_f32_kernel<InT, D, true><<<grid, AF_THREADS, 0, stream>>>(p);
-    else attn_fwd_f32_kernel<InT, D, false><<<grid, AF_THREADS, 0, stream>>>(p);
+    if (p.lengths) attn_fwd_f32_kernel<D, true><<<grid, AF_THREADS, 0, stream>>>(p);
+    else attn_fwd_f32_kernel<D, false><<<grid, AF_THREADS, 0, stream>>>(p);
+    if (p.splits > 1) attn_join_kernel<D><<<dim3((uint32_t)(p.slots * p.G * (AF_BLOCK / 4))), 256, 0, stream>>>(p);
 }
 
 hipError_t launch_attn_fwd_f32(const AttnParams& p, hipStream_t stream) {
     if (p.slots == 0) return hipSuccess;
-    p.D == 64 ? run_fwd<float, 64>(p, stream) : run_fwd<float, 128>(p, stream);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    return launch_attn_join(p, false, AF_BLOCK, stream);
-}
-
-hipError_t launch_attn_join(const AttnParams& p, bool bf16_in, int block, hipStream_t stream) {
-    const dim3 grid((uint32_t)(p.slots * p.G * (block / 4)));
-    if (bf16_in) {
-        if (p.D == 64) attn_join_kernel<__bf16, 64><<<grid, 256, 0, stream>>>(p, block);
-        else attn_join_kernel<__bf16, 128><<<grid, 256, 0, stream>>>(p, block);
-    } else {
-        if (p.D == 64) attn_join_kernel<float, 64><<<grid, 256, 0, stream>>>(p, block);
-        else attn_join_kernel<float, 128><<<grid, 256, 0, stream>>>(p, block);
-    }
+    p.D == 64 ? run_fwd<64>(p, stream) : run_fwd<128>(p, stream);
     return hipGetLastError();
 }
 

@@ -20,30 +20,39 @@ namespace kda {
 
 constexpr int FW_THREADS = 256, FW_BLOCK = kAttnBlockBf16, FW_KEYS = 64;
 
+template <int D>
+struct FwdShared {
+    static constexpr int TILE = FW_KEYS * 2 * D;   // bytes
+    char tiles[4 * TILE];                          // keys, keys, values, values
+    int32_t there[2][4];                           // of each 16 keys: their page exists
+};
+
+// Steps of 64 keys that a block's rows see, and the position of its first token.
+template <bool PAGED>
+__device__ __forceinline__ int32_t fwd_steps(const AttnParams& p, const AttnBlock& b, int32_t& len, int32_t& most) {
+    len = PAGED ? attn_length(p, b.n) : b.tokens;
+    most = b.j < 0 ? 0 : p.causal ? len - b.tokens + (b.r1 - 1) / p.hpg + 1 : len;
+    return most > 0 ? (most + FW_KEYS - 1) / FW_KEYS : 0;
+}
+
+// A block's rows over the steps [t0, t1) of its keys: into o and lse, or with
+// `part` its sums, FW_BLOCK rows of D sums, the sum of weights, m and two unused floats.
 template <int D, bool PAGED>
-__global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams p) {
-    constexpr int ROWB = 2 * D, UNITS = D / 8, TILE = FW_KEYS * ROWB;   // bytes
+__device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh, const AttnBlock& b, int g, int32_t len,
+                                          int32_t most, int32_t t0, int32_t t1, float* part) {
+    constexpr int ROWB = 2 * D, UNITS = D / 8, TILE = FW_KEYS * ROWB;
     constexpr int LOADS = D / 32, RPL = 1024 / ROWB;                    // loads per wave and tile, rows of each
     constexpr int S = D / 16, O = D / 32;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];       // keys, keys, values, values
-    __shared__ int32_t there[2][4];                                     // of each 16 keys: their page exists
+    char* lds = sh.tiles;
+    auto& there = sh.there;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
-    const AttnPlace pl = attn_place(blockIdx.x, p.slots * p.splits, p.G);
-    const int64_t slot = p.slots - 1 - pl.item / p.splits;   // (later blocks see more keys)
-    const int split = (int)(pl.item % p.splits);
-    const AttnBlock b = attn_block(p, slot, p.hpg, FW_BLOCK);
-    if (b.j < 0) return;
-    const int32_t len = PAGED ? attn_length(p, b.n) : b.tokens;
     const int32_t first = len - b.tokens;                    // position of the first query token
     const int row = b.r0 + wave * 32 + col;
     const bool valid = row < b.r1;
-    const int32_t most = p.causal ? first + (b.r1 - 1) / p.hpg + 1 : len;
     const int32_t t = valid ? row / p.hpg : (b.r1 - 1) / p.hpg;
-    const int head = pl.g * p.hpg + (valid ? row - t * p.hpg : 0);
+    const int head = g * p.hpg + (valid ? row - t * p.hpg : 0);
     const int32_t sees = p.causal ? first + t + 1 : len;     // keys [0, sees)
-    const int32_t tiles = most > 0 ? (most + FW_KEYS - 1) / FW_KEYS : 0;
-    const int32_t t0 = (int32_t)((int64_t)tiles * split / p.splits), t1 = (int32_t)((int64_t)tiles * (split + 1) / p.splits);
     // rows come in order of their tokens
     const int32_t sees_least = __builtin_amdgcn_readfirstlane(sees), sees_most = __builtin_amdgcn_readlane(sees, 31);
 
@@ -64,7 +73,7 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
     const float c = scale * kLog2e;
 
     // this wave's 16 rows of each tile
-    const AttnKeys<__bf16, PAGED> keys(p, b.n, b.start, pl.g);
+    const AttnKeys<__bf16, PAGED> keys(p, b.n, b.start, g);
     const int64_t kstep = PAGED ? D : keys.k_stride, vstep = PAGED ? D : keys.v_stride;
     uint32_t koff[LOADS], voff[LOADS];
 #pragma unroll
@@ -81,13 +90,14 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
         }
         return 0;
     };
-    int32_t page = t0 < t1 ? page_of(t0) : 0;   // of the next tile to be requested
+    int32_t next_page = t0 < t1 ? page_of(t0) : 0;   // of the next tile to be requested
     auto request = [&](int32_t tile, int buf) {
         const int32_t key = tile * FW_KEYS + 16 * wave;
         const int32_t left = most - key < 16 ? most - key : 16;
         const __bf16 *kb, *vb;
         bool ok = left > 0;
         if constexpr (PAGED) {
+            const int32_t page = __builtin_amdgcn_readfirstlane(next_page);
             ok = ok && page >= 0 && page < keys.n_pages;
             const int64_t at = (int64_t)page * keys.k_stride + (int64_t)(key & ((1 << keys.shift) - 1)) * D;
             kb = keys.k + (ok ? at : 0);
@@ -97,6 +107,8 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
             kb = keys.k + (ok ? (int64_t)key : 0) * kstep;
             vb = keys.v + (ok ? (int64_t)key : 0) * vstep;
         }
+        kb = in_scalars(kb);
+        vb = in_scalars(vb);
         const auto krs = make_rsrc(kb, ok ? ((left - 1) * (int)kstep + D) * 2 : 0);
         const auto vrs = make_rsrc(vb, ok ? ((left - 1) * (int)vstep + D) * 2 : 0);
         const uint32_t to = lds0 + buf * TILE + wave * 16 * ROWB;
@@ -104,7 +116,7 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
         for (int i = 0; i < LOADS; ++i) load_to_lds(krs, koff[i], to + i * 1024);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) load_to_lds(vrs, voff[i], to + 2 * TILE + i * 1024);
-        if (PAGED && tile + 1 < t1) page = page_of(tile + 1);
+        if (PAGED && tile + 1 < t1) next_page = page_of(tile + 1);   // (arrives with the tile)
     };
 
     // where this lane reads its operands
@@ -181,15 +193,18 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
     }
     l += swap_halves(l);
     if (!valid) return;
-    if (p.splits > 1) {
-        float* to = p.part + (((slot * p.G + pl.g) * p.splits + split) * FW_BLOCK + (row - b.r0)) * (D + 2);
+    if (part) {
+        float* to = part + (row - b.r0) * (D + 4);
 #pragma unroll
         for (int i = 0; i < O; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) to[32 * i + 8 * (e >> 2) + 4 * half + (e & 3)] = o[i][e];
+            for (int k = 0; k < 4; ++k) {
+                const float y[4] = {o[i][4 * k], o[i][4 * k + 1], o[i][4 * k + 2], o[i][4 * k + 3]};
+                store4(to + 32 * i + 8 * k + 4 * half, y);
+            }
         if (half == 0) {
             to[D] = l;
-            to[D + 1] = l > 0.f ? m : -INFINITY;
+            to[D + 1] = m;
         }
         return;
     }
@@ -205,19 +220,167 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
     if (p.lse && half == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
+template <int D, bool PAGED>
+__global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams p) {
+    __shared__ __attribute__((aligned(1024))) FwdShared<D> sh;
+    const AttnPlace pl = attn_place(blockIdx.x, p.slots, p.G);
+    const AttnBlock b = attn_block(p, p.slots - 1 - pl.item, p.hpg, FW_BLOCK);   // (later blocks see more keys)
+    if (b.j < 0) return;
+    int32_t len, most;
+    const int32_t steps = fwd_steps<PAGED>(p, b, len, most);
+    fwd_block<D, PAGED>(p, sh, b, pl.g, len, most, 0, steps, nullptr);
+}
+
+// Few blocks over long requests: the steps of all of them, in the order of the
+// groups, then of the blocks, lie on one line that is cut into as many equal
+// pieces as workgroups run at once.  Each workgroup finds its piece, which may
+// hold the end of one block, some whole ones and the start of another; blocks
+// that are cut are joined by a second launch.  Neighbouring pieces go to one
+// XCD, for their common keys and values.
+//   (1024 new tokens in all of two requests of 8k to 32k tokens, 32 heads of 128
+// on 8: 435 us.  With the same number of parts for every block instead: 774 us
+// with 512 workgroups or more in all, 467 with 1024, 430 with 2048; but 256
+// tokens over 32k 165, 179 and 216, 163 here.)
+struct FwdLine {
+    int64_t per_group, quota;   // steps
+};
+__device__ __forceinline__ int64_t line_piece(uint32_t w, int32_t n) { return n % 8 == 0 ? (int64_t)(w % 8) * (n / 8) + w / 8 : w; }
+__device__ __forceinline__ int32_t* line_info(const AttnParams& p) { return reinterpret_cast<int32_t*>(p.part); }
+// Part of a piece's first block (goes on from the piece before) or of its last one (starts in it).
+template <int D>
+__device__ __forceinline__ float* line_part(const AttnParams& p, int64_t piece, bool starts) {
+    return p.part + ((2 * p.slots * p.G + 3) & ~(int64_t)3) + (2 * piece + starts) * (FW_BLOCK * (D + 4));
+}
+
+template <int D>
+__global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_line_kernel(AttnParams p) {
+    __shared__ __attribute__((aligned(1024))) FwdShared<D> sh;
+    __shared__ int64_t sums[FW_THREADS / 64], found[2];
+    const int tid = threadIdx.x, lane = tid & 63;
+    int32_t len, most;
+    // steps before this thread's slots, of one group
+    const int64_t each = (p.slots + FW_THREADS - 1) / FW_THREADS, s0 = tid * each, s1 = s0 + each < p.slots ? s0 + each : p.slots;
+    int64_t mine = 0;
+    for (int64_t s = s0; s < s1; ++s) mine += fwd_steps<true>(p, attn_block(p, s, p.hpg, FW_BLOCK), len, most);
+    int64_t up = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t y = __shfl_up(up, d);
+        if (lane >= d) up += y;
+    }
+    if (lane == 63) sums[tid >> 6] = up;
+    __syncthreads();
+    int64_t before = up - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < FW_THREADS / 64; ++w) {
+        if (w < (tid >> 6)) before += sums[w];
+        total += sums[w];
+    }
+    total = uniform(total);
+    const int64_t quota = (total * p.G + p.workgroups - 1) / p.workgroups;
+    const int64_t piece = line_piece(blockIdx.x, p.workgroups), begin = piece * quota;
+    const int64_t end = begin + quota < total * p.G ? begin + quota : total * p.G;
+    if (begin >= end) return;
+    int g = (int)(begin / total);
+    const int64_t within = begin - g * total;
+    if (within >= before && within < before + mine) {
+        int64_t at = before;
+        for (int64_t s = s0; s < s1; ++s) {
+            const int32_t x = fwd_steps<true>(p, attn_block(p, s, p.hpg, FW_BLOCK), len, most);
+            if (within < at + x) {
+                found[0] = s;
+                found[1] = at;
+                break;
+            }
+            at += x;
+        }
+    }
+    __syncthreads();
+    int64_t slot = uniform(found[0]), base = g * total + uniform(found[1]);   // first step of the block on the line
+    for (int64_t at = begin; at < end;) {
+        AttnBlock b = attn_block(p, slot, p.hpg, FW_BLOCK);
+        const int32_t steps = __builtin_amdgcn_readfirstlane(fwd_steps<true>(p, b, len, most));
+        if (steps > 0) {
+            // (all the same for every lane, which the compiler loses sight of)
+            b.start = uniform(b.start);
+            b.n = __builtin_amdgcn_readfirstlane(b.n);
+            b.tokens = __builtin_amdgcn_readfirstlane(b.tokens);
+            b.r0 = __builtin_amdgcn_readfirstlane(b.r0);
+            b.r1 = __builtin_amdgcn_readfirstlane(b.r1);
+            len = __builtin_amdgcn_readfirstlane(len);
+            most = __builtin_amdgcn_readfirstlane(most);
+            g = __builtin_amdgcn_readfirstlane(g);
+            const int32_t t0 = __builtin_amdgcn_readfirstlane((int32_t)(at - base));
+            const int32_t t1 = __builtin_amdgcn_readfirstlane((int32_t)(end - base < steps ? end - base : steps));
+            const bool whole = t0 == 0 && t1 == steps;
+            if (tid == 0) {   // for the joining: first piece (-1: nothing to join) and last
+                int32_t* info = line_info(p) + 2 * (g * p.slots + slot);
+                if (t0 == 0) info[0] = whole ? -1 : (int32_t)piece;
+                if (t1 == steps) info[1] = (int32_t)piece;
+            }
+            fwd_block<D, true>(p, sh, b, g, len, most, t0, t1, whole ? nullptr : line_part<D>(p, piece, t0 == 0));
+            tiles_barrier();   // (the tiles are the next block's)
+            at = base + t1;
+        }
+        if (at < end) {
+            base += steps;
+            if (++slot == p.slots) {
+                slot = 0;
+                ++g;
+            }
+        }
+    }
+}
+
+// Rows of the blocks that were cut, and of those that see no key.  A wave has a row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_fwd_line_join_kernel(AttnParams p) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t unit = blockIdx.x / (FW_BLOCK / 4);
+    const int64_t slot = unit % (uint32_t)p.slots;
+    const int g = (int)(unit / (uint32_t)p.slots), r = (int)(blockIdx.x % (FW_BLOCK / 4)) * 4 + wave;
+    const AttnBlock b = attn_block(p, slot, p.hpg, FW_BLOCK);
+    if (b.j < 0 || b.r0 + r >= b.r1) return;
+    int32_t len, most, w0 = 0, w1 = -1;
+    if (fwd_steps<true>(p, b, len, most) > 0) {
+        w0 = line_info(p)[2 * (g * p.slots + slot)];
+        w1 = line_info(p)[2 * (g * p.slots + slot) + 1];
+        if (w0 < 0) return;
+    }
+    float m = kAttnLowest, l = 0.f, o[D / 64] = {};
+    for (int32_t w = w0; w <= w1; ++w) {
+        const float* from = line_part<D>(p, w, w == w0) + r * (D + 4);
+        const float to = fmaxf(m, from[D + 1]), f0 = attn_exp2(m - to), f1 = attn_exp2(from[D + 1] - to);
+        m = to;
+        l = l * f0 + from[D] * f1;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) o[e] = o[e] * f0 + from[64 * e + lane] * f1;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int row = b.r0 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
+    __bf16* orow = (__bf16*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) orow[64 * e + lane] = (__bf16)(o[e] * inv);
+    if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+static void run_fwd(const AttnParams& p, hipStream_t stream) {
+    const dim3 grid((uint32_t)(p.slots * p.G));
+    if (p.workgroups > 0) {
+        attn_fwd_line_kernel<D><<<dim3((uint32_t)p.workgroups), FW_THREADS, 0, stream>>>(p);
+        attn_fwd_line_join_kernel<D><<<dim3((uint32_t)(p.slots * p.G * (FW_BLOCK / 4))), 256, 0, stream>>>(p);
+    } else if (p.lengths) {
+        attn_fwd_bf16_kernel<D, true><<<grid, FW_THREADS, 0, stream>>>(p);
+    } else {
+        attn_fwd_bf16_kernel<D, false><<<grid, FW_THREADS, 0, stream>>>(p);
+    }
+}
 hipError_t launch_attn_fwd_bf16(const AttnParams& p, hipStream_t stream) {
     if (p.slots == 0) return hipSuccess;
-    const dim3 grid((uint32_t)(p.slots * p.G * p.splits));
-    if (p.lengths) {
-        if (p.D == 64) attn_fwd_bf16_kernel<64, true><<<grid, FW_THREADS, 0, stream>>>(p);
-        else attn_fwd_bf16_kernel<128, true><<<grid, FW_THREADS, 0, stream>>>(p);
-    } else {
-        if (p.D == 64) attn_fwd_bf16_kernel<64, false><<<grid, FW_THREADS, 0, stream>>>(p);
-        else attn_fwd_bf16_kernel<128, false><<<grid, FW_THREADS, 0, stream>>>(p);
-    }
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    return launch_attn_join(p, true, FW_BLOCK, stream);
+    if (p.D == 64) run_fwd<64>(p, stream);
+    else run_fwd<128>(p, stream);
+    return hipGetLastError();
 }
 
 }  // namespace kda

@@ -30,20 +30,23 @@ struct AttnParams {
     int32_t n_seqs, H, G, D, hpg;
     int32_t n_pages, max_pages, page_shift;
     int32_t causal;
-    int32_t splits;          // parts of a block's keys, each its own workgroup (block kernels)
-    int32_t workgroups;      // of the step kernel
+    int32_t splits;          // parts of a block's keys, each its own workgroup (float32 block kernel)
+    int32_t workgroups;      // see the kernels below
     float scale;
 };
 
-// Block kernels.  With splits > 1, part s of block (slot, g) leaves for each
-// of its rows D sums of e^{s - m} v, then the sum of e^{s - m}, then m (base
-// 2), at part + (((slot * G + g) * splits + s) * block + row) * (D + 2).
+// Block kernels.  float32: with splits > 1, part s of block (slot, g) leaves
+// for each of its rows D sums of e^{s - m} v, then the sum of e^{s - m}, then m
+// (base 2), at part + (((slot * G + g) * splits + s) * block + row) * (D + 2).
+// bf16: with workgroups > 0, that many take equal pieces of all blocks' keys; at
+// `part`: two numbers for each (group, slot), then (from the next 16 bytes on)
+// two parts for each workgroup, of D sums, the sum of weights, m and two
+// unused floats for each row of a block.
 constexpr int kAttnBlockF32 = 64;    // rows of a block
 constexpr int kAttnBlockBf16 = 128;
 constexpr int kAttnBwdBlockF32 = 16;
 hipError_t launch_attn_fwd_f32(const AttnParams& p, hipStream_t stream);
 hipError_t launch_attn_fwd_bf16(const AttnParams& p, hipStream_t stream);
-hipError_t launch_attn_join(const AttnParams& p, bool bf16_in, int block, hipStream_t stream);
 
 // Step kernel, for (request, group) pairs of at most kAttnStepRows rows, with
 // step_row_tiles tiles of 16 rows.  At `part`: two numbers for each pair u = b *
@@ -61,6 +64,8 @@ struct AttnBwdParams {
     void* gk;
     void* gv;
     float* delta;            // [rows, H]: grad_o . o
+    float* part;             // parts > 1: [parts, rows, G, 2, D] sums of grad_k and grad_v
+    int32_t parts;           // of a block of keys' rows, each its own workgroup (bf16 kernel)
     int64_t gq_stride, gk_stride, gv_stride;
     int64_t key_slots;       // blocks of keys per group
     int32_t zero_rest;       // KDA_FRESH_*: these outputs' rows of no sequence become zero

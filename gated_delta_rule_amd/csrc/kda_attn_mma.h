@@ -32,6 +32,21 @@ __device__ __forceinline__ int tile_swap(int row) {
 
 #pragma clang diagnostic ignored "-Winline-asm"   // (m0 as a clobber)
 
+// A pointer that every lane has, in scalar registers: the compiler may know
+// that it is the same everywhere and still form it in vector registers, which
+// the buffers of the loads below cannot be given in.  Behind the reads come the
+// wait states that a buffer's words need after vector instructions wrote them
+// (the loads are assembly, so the compiler does not count them).
+template <typename T>
+__device__ __forceinline__ T* in_scalars(T* p) {
+    uint32_t lo = (uint32_t)(uint64_t)p, hi = (uint32_t)((uint64_t)p >> 32);
+    asm("" : "+v"(lo), "+v"(hi));
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    asm volatile("s_nop 4" : "+s"(lo), "+s"(hi));
+    return (T*)((uint64_t)hi << 32 | lo);
+}
+
 // 16 bytes per lane from a buffer to LDS at `to` + 16 lane.  Written out
 // because the compiler would wait for these before every LDS read.
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t to) {

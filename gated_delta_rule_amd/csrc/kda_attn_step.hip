@@ -42,11 +42,6 @@ __device__ __forceinline__ int32_t step_count(const AttnParams& p, int n, int st
     }
     return (attn_length(p, n) + step - 1) / step;
 }
-// A value that every lane has, where the compiler does not know that.
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)x >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
 // Sum of x over the workgroup's threads before this one, and over all.
 __device__ __forceinline__ int64_t step_before(int32_t x, int64_t* s, int64_t& total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;

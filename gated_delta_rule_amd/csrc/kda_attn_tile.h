@@ -126,6 +126,11 @@ __device__ __forceinline__ void store4(__bf16* p, const float (&x)[4]) {
     *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3])};
 }
 
+// A value that every lane has, where the compiler does not know that.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
 // Over the four 16-lane groups of a wave (lanes with equal l & 15).
 __device__ __forceinline__ float groups_max(float x) {
     x = fmaxf(x, __shfl_xor(x, 16));
