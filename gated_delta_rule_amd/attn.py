@@ -258,11 +258,41 @@ def attn_paged_fwd(q, k_pages, v_pages, table, lengths, cu_seqlens=None, *, scal
     return o, lse
 
 
+@functools.lru_cache(maxsize=256)
+def _page_layout(layouts):
+    """Bytes and strides of pages, as arrays for the library, from each tensor's
+    (shape, strides, element size)."""
+    size, step = [], []
+    for shape, strides, width in layouts:
+        elements = 1
+        for n, s in zip(reversed(shape[1:]), reversed(strides[1:])):
+            if n > 1 and s != elements:
+                raise KDAError("pages must be contiguous within a page")
+            elements *= n
+        size.append(elements * width)
+        step.append(strides[0] * width)
+    n = len(layouts)
+    return (ctypes.c_int64 * n)(*size), (ctypes.c_int64 * n)(*step)
+
+
 class _Pages:
     """Checked table, lengths and refs."""
 
+    __slots__ = ("dev", "n_slots", "max_pages", "n_pages")
+
     def __init__(self, table, lengths, refs):
         import torch
+        tensor, i32 = torch.Tensor, torch.int32
+        if table.__class__ is tensor and lengths.__class__ is tensor and refs.__class__ is tensor and table.is_cuda:   # the usual ones
+            i = table.get_device()
+            if table.dtype is i32 and lengths.dtype is i32 and refs.dtype is i32 and lengths.get_device() == i and \
+                    refs.get_device() == i and table.dim() == 2 and lengths.dim() == 1 and refs.dim() == 1 and \
+                    lengths.shape[0] == table.shape[0] and table.is_contiguous() and lengths.is_contiguous() and \
+                    refs.is_contiguous():
+                self.dev = table.device
+                self.n_slots, self.max_pages = table.shape
+                self.n_pages = refs.shape[0]
+                return
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise KDAError("table must be [n_slots, max_pages]")
         self.dev = table.device
@@ -277,21 +307,18 @@ class _Pages:
     def data(self, pages):
         """(pointers, bytes, strides, count) of the tensors that hold the pages."""
         import torch
-        tensors = [pages] if isinstance(pages, torch.Tensor) else list(pages)
+        tensors = (pages,) if isinstance(pages, torch.Tensor) else tuple(pages)
+        index, layouts = self.dev.index, []
         for t in tensors:
             if not isinstance(t, torch.Tensor) or t.dim() < 2:
                 raise KDAError("pages must be tensors [n_pages, ...]")
-            if not t.is_cuda or t.device != self.dev:
+            if not t.is_cuda or t.get_device() != index:
                 raise KDAError(f"pages must be on {self.dev}")
             if t.shape[0] != self.n_pages:
                 raise KDAError(f"pages must have {self.n_pages} pages, got {t.shape[0]}")
-            if t.numel() and not t[0].is_contiguous():
-                raise KDAError("pages must be contiguous within a page")
+            layouts.append((t.shape, t.stride(), t.element_size()))
         n = len(tensors)
-        size = [t.numel() // max(1, self.n_pages) * t.element_size() for t in tensors]
-        step = [t.stride(0) * t.element_size() for t in tensors]
-        return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int64 * n)(*size),
-                (ctypes.c_int64 * n)(*step), n)
+        return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),) + _page_layout(tuple(layouts)) + (n,)
 
 
 def kv_resize(table, lengths, refs, new_lengths, page_size):
@@ -316,6 +343,11 @@ def kv_resize(table, lengths, refs, new_lengths, page_size):
     return ok
 
 
+@functools.lru_cache(maxsize=256)
+def _fork_bytes(*sizes) -> int:
+    return int(load_library().kda_kv_fork_workspace_bytes(*sizes))
+
+
 def kv_fork(table, lengths, refs, src, dst, pages, page_size, *, workspace=None):
     """Makes slots dst branches of slots src, all at once: they share src's full
     pages and get a copy of an open last one (see kda_kv_fork in
@@ -328,14 +360,14 @@ def kv_fork(table, lengths, refs, src, dst, pages, page_size, *, workspace=None)
     import torch
     lib = load_library()
     a = _Pages(table, lengths, refs)
-    _check(src, "src", torch.int32, a.dev)
-    if src.dim() != 1:
+    if not isinstance(src, torch.Tensor) or src.dim() != 1:
         raise KDAError("src must be [n]")
+    _check_shape(src, "src", src.shape, a.dev, torch.int32)
     _check_shape(dst, "dst", src.shape, a.dev, torch.int32)
     ptrs, size, step, count = a.data(pages)
     ok = _like(src)
     n = src.shape[0]
-    ws = _workspace(workspace, int(lib.kda_kv_fork_workspace_bytes(n, a.n_slots, a.max_pages)), a.dev)
+    ws = _workspace(workspace, _fork_bytes(n, a.n_slots, a.max_pages), a.dev)
     with _on(a.dev):
         rc = lib.kda_kv_fork(_ptr(table), _ptr(lengths), _ptr(refs), _ptr(src), _ptr(dst), _ptr(ok), n, a.n_slots,
                              a.max_pages, a.n_pages, page_size, ptrs, size, step, count, _ptr(ws), _nbytes(ws),

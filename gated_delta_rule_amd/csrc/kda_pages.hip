@@ -3,7 +3,8 @@
 //
 // Who gets which page depends on everyone before, so one workgroup of 16
 // waves decides: prefix sums of what the slots need, then the free pages in
-// order of their numbers, 16384 counts at a time, until there are enough.
+// order of their numbers, 16384 counts at a time, until there are enough.  Its
+// time is that of a handful of reads in sequence.
 // Everything that needs no order (table rows, counts, the data of pages) runs
 // on the whole GPU in the launches behind it.  Counts of holders are changed
 // by integer atomics, whose order does not change the sum.
@@ -90,22 +91,62 @@ __device__ __forceinline__ int32_t block_before(int32_t x, int32_t* s, int32_t& 
 __device__ __forceinline__ int32_t fresh_load(const int32_t* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// Which of this thread's PG_EACH pages from `at` on are free, as bits.
-__device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int64_t at, int32_t n_pages) {
+// Which of the pages base + e * PG_THREADS + thread are free, as bits e.
+__device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int64_t base, int32_t n_pages) {
     uint32_t m = 0;
     int32_t r[PG_EACH];
 #pragma unroll
-    for (int e = 0; e < PG_EACH; ++e) r[e] = at + e < n_pages ? fresh_load(refs + at + e) : 1;
+    for (int e = 0; e < PG_EACH; ++e) {
+        const int64_t at = base + e * PG_THREADS + threadIdx.x;
+        r[e] = at < n_pages ? fresh_load(refs + at) : 1;
+    }
 #pragma unroll
     for (int e = 0; e < PG_EACH; ++e) m |= (r[e] <= 0 ? 1u : 0u) << e;
     return m;
+}
+// Calls put(e, rank) for the bits e that are set, ranked in the order of
+// e * PG_THREADS + thread over the workgroup; returns how many there are.
+// s: PG_EACH * PG_WAVES ints.
+template <typename F>
+__device__ __forceinline__ int32_t in_order(uint32_t bits, int32_t* s, F put) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    static_assert(PG_EACH == 16 && PG_WAVES == 16, "four counts per lane");
+    uint64_t b[PG_EACH];
+    __syncthreads();   // (s has been read)
+#pragma unroll
+    for (int e = 0; e < PG_EACH; ++e) {
+        b[e] = __ballot(bits >> e & 1);
+        if (lane == e) s[e * PG_WAVES + wave] = __popcll(b[e]);
+    }
+    __syncthreads();
+    int32_t c[4], mine = 0, up;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[i] = s[4 * lane + i];
+        mine += c[i];
+    }
+    up = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t y = __shfl_up(up, d);
+        if (lane >= d) up += y;
+    }
+    int32_t before = up - mine;   // this lane's four counts belong to waves 4 (lane & 3) .. + 3 of one e
+#pragma unroll
+    for (int i = 0; i < 3; ++i) before += i < (wave & 3) ? c[i] : 0;
+#pragma unroll
+    for (int e = 0; e < PG_EACH; ++e) {
+        const int32_t first = __builtin_amdgcn_readlane(before, 4 * e + (wave >> 2));
+        if (bits >> e & 1) put(e, first + (int32_t)__popcll(b[e] & ((1ull << lane) - 1)));
+    }
+    return __builtin_amdgcn_readlane(up, 63);
 }
 // Free pages, counted up to `enough`.
 __device__ int64_t count_free(const int32_t* refs, int32_t n_pages, int64_t enough, int32_t* s) {
     int64_t found = 0;
     for (int64_t base = 0; base < n_pages && found < enough; base += PG_STEP) {
         int32_t total;
-        block_before(__popc(free_bits(refs, base + threadIdx.x * PG_EACH, n_pages)), s, total);
+        block_before(__popc(free_bits(refs, base, n_pages)), s, total);
         found += total;
     }
     return found;
@@ -116,16 +157,12 @@ template <typename F>
 __device__ void give_out(int32_t* refs, int32_t n_pages, int32_t count, int32_t* s, F put) {
     int32_t done = 0;
     for (int64_t base = 0; base < n_pages && done < count; base += PG_STEP) {
-        const int64_t at = base + threadIdx.x * PG_EACH;
-        uint32_t m = free_bits(refs, at, n_pages);
-        int32_t total;
-        int32_t rank = done + block_before(__popc(m), s, total);
-        for (; m && rank < count; m &= m - 1, ++rank) {
-            const int32_t page = (int32_t)(at + __ffs(m) - 1);
+        done += in_order(free_bits(refs, base, n_pages), s, [&](int e, int32_t rank) {
+            if (done + rank >= count) return;
+            const int32_t page = (int32_t)(base + e * PG_THREADS + threadIdx.x);
             refs[page] = 1;
-            put(rank, page);
-        }
-        done += total;
+            put(done + rank, page);
+        });
     }
 }
 __device__ __forceinline__ int32_t pages_of(int32_t len, int shift) {
@@ -149,33 +186,32 @@ __device__ __forceinline__ int owner_of(const int32_t* off, int n, int32_t rank)
 // ----------------------------------------------------------------- resize
 
 __global__ __launch_bounds__(PG_THREADS) void kv_resize_kernel(PagesParams p) {
-    __shared__ int32_t s[PG_WAVES], off[PG_THREADS], held[PG_THREADS];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ int32_t s[PG_EACH * PG_WAVES], off[PG_THREADS], from[PG_THREADS];
+    const int tid = threadIdx.x;
     int32_t* refs = p.refs_out;
     int64_t need_all = 0;
-    for (int s0 = 0; s0 < p.n_slots; s0 += PG_THREADS) {
+    for (int s0 = 0; s0 < p.n_slots; s0 += PG_THREADS) {   // what is needed, and what is given up
         const int slot = s0 + tid;
-        int32_t need = 0;
+        int32_t d = 0, after = 0;
         if (slot < p.n_slots) {
-            const int32_t d = pages_of(clamp_length(p.want[slot], p), p.page_shift) -
-                              pages_of(clamp_length(p.lengths[slot], p), p.page_shift);
-            need = d > 0 ? d : 0;
+            after = pages_of(clamp_length(p.want[slot], p), p.page_shift);
+            d = after - pages_of(clamp_length(p.lengths[slot], p), p.page_shift);
         }
-        int32_t total;
-        block_before(need, s, total);   // (table entries: below 2^31 in all)
+        int32_t total, gone;
+        block_before(d > 0 ? d : 0, s, total);   // (table entries: below 2^31 in all)
         need_all += total;
-    }
-    for (int slot = wave; slot < p.n_slots; slot += PG_WAVES) {
-        const int32_t before = pages_of(clamp_length(p.lengths[slot], p), p.page_shift);
-        const int32_t after = pages_of(clamp_length(p.want[slot], p), p.page_shift);
-        int32_t* row = p.table_out + (int64_t)slot * p.max_pages;
-        for (int32_t col = after + lane; col < before; col += 64) {
-            const int32_t page = row[col];
+        off[tid] = block_before(d < 0 ? -d : 0, s, gone);
+        from[tid] = after;
+        __syncthreads();
+        for (int32_t i = tid; i < gone; i += PG_THREADS) {
+            const int o = owner_of(off, PG_THREADS, i);
+            int32_t* entry = p.table_out + (int64_t)(s0 + o) * p.max_pages + from[o] + i - off[o];
+            const int32_t page = *entry;
             if (page >= 0 && page < p.n_pages) atomicSub(refs + page, 1);
-            row[col] = -1;
+            *entry = -1;
         }
+        __syncthreads();
     }
-    __syncthreads();
     const int64_t n_free = need_all > 0 ? count_free(refs, p.n_pages, need_all, s) : 0;
     int64_t upto = 0;
     for (int s0 = 0; s0 < p.n_slots; s0 += PG_THREADS) {
@@ -188,19 +224,19 @@ __global__ __launch_bounds__(PG_THREADS) void kv_resize_kernel(PagesParams p) {
             const int32_t d = pages_of(want, p.page_shift) - before;
             need = d > 0 ? d : 0;
         }
-        int32_t total, served;
-        const int64_t at = upto + block_before(need, s, total);
-        const bool ok = need == 0 || at + need <= n_free;
-        upto += total;
-        const int32_t mine = block_before(ok ? need : 0, s, served);
-        off[tid] = mine;
-        held[tid] = before;
-        __syncthreads();
-        if (served > 0) {
+        bool ok = true;
+        if (need_all > 0) {
+            int32_t total, served;
+            const int64_t at = upto + block_before(need, s, total);
+            ok = need == 0 || at + need <= n_free;
+            upto += total;
+            off[tid] = block_before(ok ? need : 0, s, served);
+            from[tid] = before;
+            __syncthreads();
             // (slots without a need share the next one's offset: the last of equal ones has the page)
             give_out(refs, p.n_pages, served, s, [&](int32_t rank, int32_t page) {
                 const int i = owner_of(off, PG_THREADS, rank);
-                p.table_out[(int64_t)(s0 + i) * p.max_pages + held[i] + rank - off[i]] = page;
+                p.table_out[(int64_t)(s0 + i) * p.max_pages + from[i] + rank - off[i]] = page;
             });
             __syncthreads();
         }
@@ -208,7 +244,6 @@ __global__ __launch_bounds__(PG_THREADS) void kv_resize_kernel(PagesParams p) {
             p.lengths_out[slot] = ok ? want : len;
             if (p.ok) p.ok[slot] = ok;
         }
-        __syncthreads();
     }
 }
 
@@ -232,7 +267,7 @@ __device__ __forceinline__ int32_t* fork_rows(const PagesParams& p) {
 }
 
 __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p) {
-    __shared__ int32_t s[PG_WAVES], off[PG_THREADS];
+    __shared__ int32_t s[PG_EACH * PG_WAVES], off[PG_THREADS];
     const int tid = threadIdx.x;
     int32_t *refs = p.refs_out, *owner = p.ws;
     ForkPlan* plan = fork_plans(p);
@@ -315,7 +350,8 @@ __global__ __launch_bounds__(256) void kv_fork_count_kernel(PagesParams p, int32
 }
 
 // Bytes [piece * 16 KB, ...) of a page, all tensors in line.
-constexpr int64_t kCopyPiece = 16384;
+constexpr int kCopyLoads = 4;
+constexpr int64_t kCopyPiece = kCopyLoads * 4096;
 __device__ __forceinline__ void copy_piece(const PageData& d, int64_t from, int64_t to, int64_t piece) {
     for (int t = 0; t < d.n; ++t) {
         const int64_t pieces = (d.bytes[t] + kCopyPiece - 1) / kCopyPiece;
@@ -323,16 +359,19 @@ __device__ __forceinline__ void copy_piece(const PageData& d, int64_t from, int6
             piece -= pieces;
             continue;
         }
-        const char* a = d.base[t] + from * d.stride[t];
-        char* b = d.base[t] + to * d.stride[t];
-        u32x4 r[4];
-        const int64_t at = piece * kCopyPiece + threadIdx.x * 16;
+        const char* a = d.base[t] + from * d.stride[t] + piece * kCopyPiece;
+        char* b = d.base[t] + to * d.stride[t] + piece * kCopyPiece;
+        const int32_t at = threadIdx.x * 16;
+        if ((piece + 1) * kCopyPiece <= d.bytes[t]) {
+            u32x4 r[kCopyLoads];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (at + k * 4096 < d.bytes[t]) r[k] = *reinterpret_cast<const u32x4*>(a + at + k * 4096);
+            for (int k = 0; k < kCopyLoads; ++k) r[k] = *reinterpret_cast<const u32x4*>(a + at + k * 4096);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (at + k * 4096 < d.bytes[t]) *reinterpret_cast<u32x4*>(b + at + k * 4096) = r[k];
+            for (int k = 0; k < kCopyLoads; ++k) *reinterpret_cast<u32x4*>(b + at + k * 4096) = r[k];
+        } else {
+            const int32_t left = (int32_t)(d.bytes[t] - piece * kCopyPiece);
+            for (int32_t i = at; i < left; i += 4096) *reinterpret_cast<u32x4*>(b + i) = *reinterpret_cast<const u32x4*>(a + i);
+        }
         return;
     }
 }
@@ -376,34 +415,29 @@ hipError_t launch_kv_fork(const PagesParams& p, hipStream_t stream) {
 // Workspace: moves, pad; then [n_pages] each: pages that move, pages that
 // receive them, and the rank of each page that moves (-1: it stays).
 __global__ __launch_bounds__(PG_THREADS) void kv_compact_plan_kernel(PagesParams p) {
-    __shared__ int32_t s[PG_WAVES];
+    __shared__ int32_t s[PG_EACH * PG_WAVES];
     const int32_t N = p.n_pages;
     const int32_t n_live = N - (int32_t)count_free(p.refs, N, (int64_t)N + 1, s);
     int32_t *mov = p.ws + 4, *hol = mov + N, *rank_of = hol + N;
     int32_t moved = 0, holes = 0;
     for (int64_t base = 0; base < N; base += PG_STEP) {
-        const int64_t at = base + threadIdx.x * PG_EACH;
-        const uint32_t free = free_bits(p.refs, at, N);
+        const uint32_t free = free_bits(p.refs, base, N);
         uint32_t below = 0, exist = 0;   // pages < n_live, pages < N
 #pragma unroll
         for (int e = 0; e < PG_EACH; ++e) {
-            below |= (at + e < n_live ? 1u : 0u) << e;
-            exist |= (at + e < N ? 1u : 0u) << e;
+            const int64_t at = base + e * PG_THREADS + threadIdx.x;
+            below |= (at < n_live ? 1u : 0u) << e;
+            exist |= (at < N ? 1u : 0u) << e;
+            if (at < N && (at < n_live || free >> e & 1)) rank_of[at] = -1;   // (stays)
         }
-        const uint32_t mm = ~free & exist & ~below, hm = free & exist & below;
-        int32_t total;
-        int32_t r = moved + block_before(__popc(mm), s, total);
-        moved += total;
-#pragma unroll
-        for (int e = 0; e < PG_EACH; ++e) {
-            if (!(exist >> e & 1)) continue;
-            const bool moves = mm >> e & 1;
-            rank_of[at + e] = moves ? r : -1;
-            if (moves) mov[r++] = (int32_t)(at + e);
-        }
-        r = holes + block_before(__popc(hm), s, total);
-        holes += total;
-        for (uint32_t m = hm; m; m &= m - 1) hol[r++] = (int32_t)(at + __ffs(m) - 1);
+        const int64_t mine = base + threadIdx.x;
+        if (base + PG_STEP > n_live)
+            moved += in_order(~free & exist & ~below, s, [&](int e, int32_t rank) {
+                mov[moved + rank] = (int32_t)(mine + e * PG_THREADS);
+                rank_of[mine + e * PG_THREADS] = moved + rank;
+            });
+        if (base < n_live)
+            holes += in_order(free & below, s, [&](int e, int32_t rank) { hol[holes + rank] = (int32_t)(mine + e * PG_THREADS); });
     }
     if (threadIdx.x == 0) {
         p.ws[0] = moved;
