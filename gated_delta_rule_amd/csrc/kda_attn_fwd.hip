@@ -138,12 +138,11 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
         const char* ks = lds + buf * TILE;
         const char* vs = lds + 2 * TILE + buf * TILE;
         f32x16 x[2];
+        x[0] = x[1] = zero16();
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            x[kt] = zero16();
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int s = 0; s < S; ++s) x[kt] = mfma32x32(read_rows(ks + kt * 32 * ROWB, kat ^ (32 * s)), q[s], x[kt]);
-        }
+            for (int kt = 0; kt < 2; ++kt) x[kt] = mfma32x32(read_rows(ks + kt * 32 * ROWB, kat ^ (32 * s)), q[s], x[kt]);
         bool whole = key0 + FW_KEYS <= sees_least;
         if constexpr (PAGED) whole = whole && (there[buf][0] & there[buf][1] & there[buf][2] & there[buf][3]);
         if (!__builtin_amdgcn_readfirstlane(whole)) {

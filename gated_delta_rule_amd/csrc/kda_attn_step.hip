@@ -432,11 +432,19 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void attn_step_join_k
         for (int e = 0; e < E; ++e) o[e] *= fade;
         const int32_t here = n - i0 < 64 ? n - i0 : 64;
         const float* from = step_part<D, RT>(p, w0 + i0 + unit, r);
-#pragma unroll 8
-        for (int32_t i = 0; i < here; ++i) {
-            const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), i));
+        for (int32_t i = 0; i < here; i += 8) {   // (eight requests at once; behind the last part, its values with weight 0)
+            float y[8][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += w * from[i * (int64_t)(RT * 16) * (D + 4) + 64 * e + lane];
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    y[k][e] = from[(i + k < here ? i + k : here - 1) * (int64_t)(RT * 16) * (D + 4) + 64 * e + lane];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float w = i + k < here ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), i + k)) : 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] += w * y[k][e];
+            }
         }
     }
     if constexpr (WAVES > 1) {
