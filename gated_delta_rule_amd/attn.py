@@ -23,13 +23,19 @@ import ctypes
 import functools
 
 from . import KDA_BF16, KDA_F32, KDAError, _check, _in_dtype, _status, load_library
-from .ssm import _check_rows, _check_shape, _grad_like, _lead, _like, _nbytes, _on, _ptr, _stream, _workspace
+from .ssm import _NOTHING, _check_rows, _check_shape, _grad_like, _lead, _like, _nbytes, _ptr, _stream, _workspace
 
 __all__ = ["attn_fwd", "attn_bwd", "attn_paged_fwd", "kv_append", "kv_resize", "kv_fork", "kv_compact",
            "attn_bwd_workspace_bytes", "attn_paged_workspace_bytes"]
 
 # Gradients that a backward call makes itself, by their bits in csrc/kda_attn_launch.h.
 _FRESH_Q, _FRESH_K, _FRESH_V = 1, 2, 4
+
+
+def _on(dev):
+    """Makes `dev` the current device for the call's launches."""
+    import torch
+    return _NOTHING if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _of(q, name="q"):
@@ -54,6 +60,8 @@ def _scale(scale, D):
 
 class _Heads:
     """Checked q, k, v of a batch of sequences."""
+
+    __slots__ = ("dev", "dtype", "lead", "n_seqs", "T", "H", "D", "G", "q_tail", "k_tail", "qs", "ks", "vs")
 
     def __init__(self, q, k, v, cu_seqlens):
         import torch
@@ -97,18 +105,22 @@ def attn_fwd(q, k, v, cu_seqlens=None, *, scale=None, causal=True, o=None, lse=N
     a = _Heads(q, k, v, cu_seqlens)
     o, lse = _outputs(q, a.lead, a.H, a.dev, o, lse)
     with _on(a.dev):
-        rc = lib.kda_attn_fwd(_ptr(q), a.qs, _ptr(k), a.ks, _ptr(v), a.vs, a.dtype, _ptr(cu_seqlens), a.n_seqs, a.T,
-                              a.H, a.G, a.D, _scale(scale, a.D), int(bool(causal)), _ptr(o), _ptr(lse),
-                              _stream(a.dev))
+        rc = lib.kda_attn_fwd(q.data_ptr(), a.qs, k.data_ptr(), a.ks, v.data_ptr(), a.vs, a.dtype, _ptr(cu_seqlens),
+                              a.n_seqs, a.T, a.H, a.G, a.D, _scale(scale, a.D), int(bool(causal)), o.data_ptr(),
+                              lse.data_ptr(), _stream(a.dev))
     _status(rc, "kda_attn_fwd")
     return o, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _bwd_bytes(*sizes) -> int:
+    return int(load_library().kda_attn_bwd_workspace_bytes(*sizes))
 
 
 def attn_bwd_workspace_bytes(dtype, n_seqs, T, H, G, D, varlen) -> int:
     """Workspace of attn_bwd for q of this dtype."""
     import torch
-    return int(load_library().kda_attn_bwd_workspace_bytes(int(dtype == torch.float32), n_seqs, T, H, G, D,
-                                                           int(bool(varlen))))
+    return _bwd_bytes(int(dtype == torch.float32), n_seqs, T, H, G, D, int(bool(varlen)))
 
 
 def attn_bwd(q, k, v, o, lse, grad_o, cu_seqlens=None, *, scale=None, causal=True, grad_q=None, grad_k=None,
@@ -134,8 +146,7 @@ def attn_bwd(q, k, v, o, lse, grad_o, cu_seqlens=None, *, scale=None, causal=Tru
             fresh |= bit
         outs.append((t, _check_rows(t, name, a.lead, tail, q.dtype, a.dev)))
     (gq, gqs), (gk, gks), (gv, gvs) = outs
-    ws = _workspace(workspace, int(lib.kda_attn_bwd_workspace_bytes(a.dtype, a.n_seqs, a.T, a.H, a.G, a.D,
-                                                                    int(cu_seqlens is not None))), a.dev)
+    ws = _workspace(workspace, _bwd_bytes(a.dtype, a.n_seqs, a.T, a.H, a.G, a.D, int(cu_seqlens is not None)), a.dev)
     with _on(a.dev):
         rc = lib.kda_attn_bwd_fresh(_ptr(q), a.qs, _ptr(k), a.ks, _ptr(v), a.vs, a.dtype, _ptr(cu_seqlens), a.n_seqs,
                                     a.T, a.H, a.G, a.D, _scale(scale, a.D), int(bool(causal)), _ptr(o), _ptr(lse),
@@ -210,9 +221,9 @@ def kv_append(k, v, k_pages, v_pages, table, lengths, cu_seqlens=None):
     ks = _check_rows(k, "k", lead, (c.G, c.D), k.dtype, dev)
     vs = _check_rows(v, "v", lead, (c.G, c.D), k.dtype, dev)
     with _on(dev):
-        rc = lib.kda_kv_append(_ptr(k), ks, _ptr(v), vs, dt, _ptr(k_pages), _ptr(v_pages), c.stride, c.n_pages,
-                               c.page_size, _ptr(table), c.max_pages, _ptr(lengths), _ptr(cu_seqlens), n_seqs, T, c.G,
-                               c.D, _stream(dev))
+        rc = lib.kda_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, dt, k_pages.data_ptr(), v_pages.data_ptr(), c.stride,
+                               c.n_pages, c.page_size, table.data_ptr(), c.max_pages, lengths.data_ptr(),
+                               _ptr(cu_seqlens), n_seqs, T, c.G, c.D, _stream(dev))
     _status(rc, "kda_kv_append")
 
 
@@ -251,9 +262,10 @@ def attn_paged_fwd(q, k_pages, v_pages, table, lengths, cu_seqlens=None, *, scal
     ws = _workspace(workspace, _paged_bytes(dt, n_seqs, T, H, c.G, D, c.page_size, c.max_pages,
                                             int(cu_seqlens is not None)), dev)
     with _on(dev):
-        rc = lib.kda_attn_paged_fwd(_ptr(q), qs, dt, _ptr(k_pages), _ptr(v_pages), c.stride, c.n_pages, c.page_size,
-                                    _ptr(table), c.max_pages, _ptr(lengths), _ptr(cu_seqlens), n_seqs, T, H, c.G, D,
-                                    _scale(scale, D), _ptr(o), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(dev))
+        rc = lib.kda_attn_paged_fwd(q.data_ptr(), qs, dt, k_pages.data_ptr(), v_pages.data_ptr(), c.stride, c.n_pages,
+                                    c.page_size, table.data_ptr(), c.max_pages, lengths.data_ptr(), _ptr(cu_seqlens),
+                                    n_seqs, T, H, c.G, D, _scale(scale, D), o.data_ptr(), lse.data_ptr(), _ptr(ws),
+                                    _nbytes(ws), _stream(dev))
     _status(rc, "kda_attn_paged_fwd")
     return o, lse
 

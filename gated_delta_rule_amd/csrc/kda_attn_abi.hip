@@ -209,7 +209,7 @@ int kda_attn_bwd_fresh(const void* q, int64_t q_stride, const void* k, int64_t k
     if (!aligned(lse, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_MISALIGNED;
     const BwdPlan plan = bwd_plan(in_dtype == KDA_BF16, n_seqs, T, rows, H, G, D, varlen);
     if (plan.slots > kMaxWideGroups / G || plan.key_slots * plan.parts > kMaxWideGroups / G ||
-        rows * H / 8 >= kMaxWorkgroups || rows * G / 4 >= kMaxWorkgroups)
+        rows * G / 4 >= kMaxWorkgroups)
         return KDA_ERR_TOO_LARGE;
     if (!workspace || workspace_bytes < (size_t)plan.bytes) return KDA_ERR_WORKSPACE;
     const Span outs[] = {rows_span(grad_q, rows, grad_q_stride, HD, es), rows_span(grad_k, rows, grad_k_stride, GD, es),

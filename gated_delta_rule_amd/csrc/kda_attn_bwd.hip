@@ -215,7 +215,8 @@ __global__ __launch_bounds__(256) void attn_bwd_join_kernel(AttnBwdParams a) {
     }
 }
 
-// grad_q of 128 rows of one (sequence, group).
+// grad_q of 128 rows of one (sequence, group); leaves the rows' delta for the
+// blocks of keys, which run afterwards.
 template <int D>
 __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams a) {
     const AttnParams& p = a.f;
@@ -250,7 +251,21 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
             arrive(go[s]);
         }
     }
-    float lse2 = p.lse[at] * kLog2e, delta = a.delta[at];
+    float lse2 = p.lse[at] * kLog2e, delta = 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        float x[4], y[4];
+        const __bf16* o = (const __bf16*)p.o + at * D + 16 * s + 8 * half;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            load4(o + 4 * e, x);
+            load4((const __bf16*)a.go + at * D + 16 * s + 8 * half + 4 * e, y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) delta += x[k] * y[k];
+        }
+    }
+    delta += swap_halves(delta);
+    if (half == 0 && valid) a.delta[at] = delta;
     asm volatile("" : "+v"(lse2), "+v"(delta));   // (arrive, too)
     const float c = p.scale * kLog2e;
     f32x16 gq[O];
@@ -328,15 +343,15 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
 
 template <int D>
 static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
+    attn_bwd_q_kernel<D><<<dim3((uint32_t)(a.f.slots * a.f.G)), BW_THREADS, 0, stream>>>(a);
     attn_bwd_kv_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G * a.parts)), BW_THREADS, 0, stream>>>(a);
     if (a.parts > 1)
         attn_bwd_join_kernel<D><<<dim3((uint32_t)((a.f.rows * a.f.G * (D / 2) + 255) / 256)), 256, 0, stream>>>(a);
-    attn_bwd_q_kernel<D><<<dim3((uint32_t)(a.f.slots * a.f.G)), BW_THREADS, 0, stream>>>(a);
 }
 
 hipError_t launch_attn_bwd_bf16(const AttnBwdParams& a, hipStream_t stream) {
     if (a.f.rows == 0) return hipSuccess;
-    const hipError_t e = launch_attn_delta(a, true, stream);
+    const hipError_t e = launch_attn_bwd_rest(a, true, stream);
     if (e != hipSuccess) return e;
     if (a.f.D == 64) run_bwd<64>(a, stream);
     else run_bwd<128>(a, stream);

@@ -14,41 +14,27 @@ namespace kda {
 
 constexpr int AB_THREADS = 256, AB_BLOCK = kAttnBwdBlockF32;
 
-// delta of every row; rows of no sequence become zero in new gradients.
-template <typename InT, int D>
-__global__ __launch_bounds__(256) void attn_delta_kernel(AttnBwdParams a) {
+// Rows of no sequence become zero in new gradients of a packed batch.
+__global__ __launch_bounds__(256) void attn_bwd_rest_kernel(AttnBwdParams a, int32_t es) {
     const AttnParams& p = a.f;
-    constexpr int EV = 16 / (int)sizeof(InT), LANES = D / EV;   // lanes of a row
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
-    const int c = (threadIdx.x % LANES) * EV;
-    if (i >= p.rows * p.H) return;   // (whole rows: LANES divides 64)
-    const int64_t row = i / p.H;
-    const int h = (int)(i - row * p.H);
-    if (p.cu) {
-        const bool in = row >= attn_range(p.cu, p.rows, p.T, 0).start && row < attn_range(p.cu, p.rows, p.T, p.n_seqs - 1).end;
-        if (!in) {
-            const u32x4 z = {0, 0, 0, 0};
-            if (a.zero_rest & KDA_FRESH_Q) *reinterpret_cast<u32x4*>((InT*)a.gq + row * a.gq_stride + (int64_t)h * D + c) = z;
-            if (h % p.hpg == 0) {
-                const int64_t g = (int64_t)(h / p.hpg) * D + c;
-                if (a.zero_rest & KDA_FRESH_K) *reinterpret_cast<u32x4*>((InT*)a.gk + row * a.gk_stride + g) = z;
-                if (a.zero_rest & KDA_FRESH_V) *reinterpret_cast<u32x4*>((InT*)a.gv + row * a.gv_stride + g) = z;
-            }
-            return;
-        }
+    const int64_t first = attn_range(p.cu, p.rows, p.T, 0).start, last = attn_range(p.cu, p.rows, p.T, p.n_seqs - 1).end;
+    const int32_t qp = p.H * p.D * es / 16, kp = p.G * p.D * es / 16, per = qp + 2 * kp;   // 16-byte pieces of a row
+    const int64_t n = first + (p.rows - last);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t at = i / per, row = at < first ? at : last + at - first;
+        const int32_t c = (int32_t)(i - at * per);
+        const int which = c < qp ? KDA_FRESH_Q : c < qp + kp ? KDA_FRESH_K : KDA_FRESH_V;
+        if (!(a.zero_rest & which)) continue;
+        char* to = which == KDA_FRESH_Q ? (char*)a.gq + row * a.gq_stride * es + (int64_t)c * 16
+                 : which == KDA_FRESH_K ? (char*)a.gk + row * a.gk_stride * es + (int64_t)(c - qp) * 16
+                                        : (char*)a.gv + row * a.gv_stride * es + (int64_t)(c - qp - kp) * 16;
+        *reinterpret_cast<u32x4*>(to) = u32x4{0, 0, 0, 0};
     }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < EV; e += 4) {
-        float x[4], y[4];
-        load4((const InT*)p.o + i * D + c + e, x);
-        load4((const InT*)a.go + i * D + c + e, y);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s += x[k] * y[k];
-    }
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) s += __shfl_xor(s, d);
-    if (threadIdx.x % LANES == 0) a.delta[i] = s;
+}
+hipError_t launch_attn_bwd_rest(const AttnBwdParams& a, bool bf16_in, hipStream_t stream) {
+    if (!a.f.cu || !a.zero_rest) return hipSuccess;
+    attn_bwd_rest_kernel<<<kAttnRest, 256, 0, stream>>>(a, bf16_in ? 2 : 4);
+    return hipGetLastError();
 }
 
 // Tiles of 16 float32 rows in LDS, 16-byte unit u of row r in place u ^ (r & 15).
@@ -216,7 +202,8 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
     }
 }
 
-// grad_q of 16 rows, the waves taking 16 keys each in turn.
+// grad_q of 16 rows, the waves taking 16 keys each in turn; leaves the rows'
+// delta for the blocks of keys, which run afterwards.
 template <int D>
 __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_kernel(AttnBwdParams a) {
     const AttnParams& p = a.f;
@@ -241,7 +228,16 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_ke
         load4((const float*)p.q + (b.start + t) * p.q_stride + (int64_t)head * D + 16 * s + 4 * grp, q[s]);
         load4((const float*)a.go + at * D + 16 * s + 4 * grp, go[s]);
     }
-    float lse2 = p.lse[at] * kLog2e, delta = a.delta[at];
+    float lse2 = p.lse[at] * kLog2e, delta = 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        float o[4];
+        load4((const float*)p.o + at * D + 16 * s + 4 * grp, o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) delta += go[s][e] * o[e];
+    }
+    delta = groups_sum(delta);
+    if (wave == 0 && grp == 0 && valid) a.delta[at] = delta;
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -315,26 +311,15 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_ke
     }
 }
 
-template <typename InT, int D>
-static void run_delta(const AttnBwdParams& a, hipStream_t stream) {
-    constexpr int LANES = D / (16 / (int)sizeof(InT));
-    attn_delta_kernel<InT, D><<<dim3((uint32_t)((a.f.rows * a.f.H * LANES + 255) / 256)), 256, 0, stream>>>(a);
-}
-hipError_t launch_attn_delta(const AttnBwdParams& a, bool bf16_in, hipStream_t stream) {
-    if (bf16_in) a.f.D == 64 ? run_delta<__bf16, 64>(a, stream) : run_delta<__bf16, 128>(a, stream);
-    else a.f.D == 64 ? run_delta<float, 64>(a, stream) : run_delta<float, 128>(a, stream);
-    return hipGetLastError();
-}
-
 template <int D>
 static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
-    attn_bwd_kv_f32_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
     attn_bwd_q_f32_kernel<D><<<dim3((uint32_t)(a.f.slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
+    attn_bwd_kv_f32_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
 }
 
 hipError_t launch_attn_bwd_f32(const AttnBwdParams& a, hipStream_t stream) {
     if (a.f.rows == 0) return hipSuccess;
-    const hipError_t e = launch_attn_delta(a, false, stream);
+    const hipError_t e = launch_attn_bwd_rest(a, false, stream);
     if (e != hipSuccess) return e;
     a.f.D == 64 ? run_bwd<64>(a, stream) : run_bwd<128>(a, stream);
     return hipGetLastError();

@@ -107,8 +107,10 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
             kb = keys.k + (ok ? (int64_t)key : 0) * kstep;
             vb = keys.v + (ok ? (int64_t)key : 0) * vstep;
         }
-        kb = in_scalars(kb);
-        vb = in_scalars(vb);
+        if constexpr (PAGED) {
+            kb = in_scalars(kb);
+            vb = in_scalars(vb);
+        }
         const auto krs = make_rsrc(kb, ok ? ((left - 1) * (int)kstep + D) * 2 : 0);
         const auto vrs = make_rsrc(vb, ok ? ((left - 1) * (int)vstep + D) * 2 : 0);
         const uint32_t to = lds0 + buf * TILE + wave * 16 * ROWB;

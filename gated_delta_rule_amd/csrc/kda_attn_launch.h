@@ -70,7 +70,8 @@ struct AttnBwdParams {
     int64_t key_slots;       // blocks of keys per group
     int32_t zero_rest;       // KDA_FRESH_*: these outputs' rows of no sequence become zero
 };
-hipError_t launch_attn_delta(const AttnBwdParams& p, bool bf16_in, hipStream_t stream);
+constexpr int kAttnRest = 256;   // workgroups that see to the rows of no sequence
+hipError_t launch_attn_bwd_rest(const AttnBwdParams& p, bool bf16_in, hipStream_t stream);
 hipError_t launch_attn_bwd_f32(const AttnBwdParams& p, hipStream_t stream);
 hipError_t launch_attn_bwd_bf16(const AttnBwdParams& p, hipStream_t stream);
 
