@@ -266,7 +266,26 @@ __device__ __forceinline__ int32_t* fork_rows(const PagesParams& p) {
     return p.ws + (((int64_t)p.n_slots + 3) & ~3) + (int64_t)p.n * (sizeof(ForkPlan) / 4);
 }
 
-__global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p) {
+// Entry col of pair i: the counts, and the new row into the workspace (a source
+// may be another pair's destination).
+__device__ __forceinline__ void fork_count(const PagesParams& p, int64_t i, int32_t col) {
+    const ForkPlan f = fork_plans(p)[i];
+    if (!f.go || col >= f.cols) return;
+    const int32_t used = pages_of(f.length, p.page_shift), old = pages_of(clamp_length(p.lengths[p.dst[i]], p), p.page_shift);
+    int32_t page = -1;
+    if (col < used) {
+        page = p.table[(int64_t)p.src[i] * p.max_pages + col];
+        if (f.to >= 0 && col == used - 1) page = f.to;   // (its count is one already)
+        else if (page >= 0 && page < p.n_pages) atomicAdd(p.refs_out + page, 1);
+    }
+    if (col < old) {
+        const int32_t had = p.table[(int64_t)p.dst[i] * p.max_pages + col];
+        if (had >= 0 && had < p.n_pages) atomicSub(p.refs_out + had, 1);
+    }
+    fork_rows(p)[i * p.max_pages + col] = page;
+}
+
+__global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p, bool count) {
     __shared__ int32_t s[PG_EACH * PG_WAVES], off[PG_THREADS];
     const int tid = threadIdx.x;
     int32_t *refs = p.refs_out, *owner = p.ws;
@@ -327,26 +346,17 @@ __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p)
         }
         __syncthreads();
     }
+    if (!count) return;
+    const int32_t entries = p.n * p.max_pages;
+    for (int32_t k = tid; k < entries; k += PG_THREADS) {
+        const int32_t i = k / p.max_pages;
+        fork_count(p, i, k - i * p.max_pages);
+    }
 }
 
-// Counts, and the new rows into the workspace (a source may be another pair's destination).
 __global__ __launch_bounds__(256) void kv_fork_count_kernel(PagesParams p, int32_t chunks) {
     const int64_t i = blockIdx.x / (uint32_t)chunks;
-    const int32_t col = (int32_t)(blockIdx.x % (uint32_t)chunks) * 256 + threadIdx.x;
-    const ForkPlan f = fork_plans(p)[i];
-    if (!f.go || col >= f.cols) return;
-    const int32_t used = pages_of(f.length, p.page_shift), old = pages_of(clamp_length(p.lengths[p.dst[i]], p), p.page_shift);
-    int32_t page = -1;
-    if (col < used) {
-        page = p.table[(int64_t)p.src[i] * p.max_pages + col];
-        if (f.to >= 0 && col == used - 1) page = f.to;   // (its count is one already)
-        else if (page >= 0 && page < p.n_pages) atomicAdd(p.refs_out + page, 1);
-    }
-    if (col < old) {
-        const int32_t had = p.table[(int64_t)p.dst[i] * p.max_pages + col];
-        if (had >= 0 && had < p.n_pages) atomicSub(p.refs_out + had, 1);
-    }
-    fork_rows(p)[i * p.max_pages + col] = page;
+    fork_count(p, i, (int32_t)(blockIdx.x % (uint32_t)chunks) * 256 + threadIdx.x);
 }
 
 // Bytes [piece * 16 KB, ...) of a page, all tensors in line.
@@ -399,14 +409,18 @@ __global__ __launch_bounds__(256) void kv_fork_write_kernel(PagesParams p, int32
 }
 
 hipError_t launch_kv_fork(const PagesParams& p, hipStream_t stream) {
-    kv_fork_plan_kernel<<<1, PG_THREADS, 0, stream>>>(p);
+    // Few entries are counted by the planning workgroup, more of them by a launch
+    // of their own (2.5 us on the host, 2 to 4 on the GPU): 16 rounds of the
+    // workgroup take about as long.
+    const bool count = (int64_t)p.n * p.max_pages <= 16 * PG_THREADS;
+    kv_fork_plan_kernel<<<1, PG_THREADS, 0, stream>>>(p, count);
     const int32_t chunks = (p.max_pages + 255) / 256;
-    if (chunks > 0) kv_fork_count_kernel<<<dim3((uint32_t)p.n * chunks), 256, 0, stream>>>(p, chunks);
-    // (max_pages 0: lengths are 0, and stay so)
-    const int64_t pieces = copy_pieces(p.data);
-    const int32_t walkers = (int32_t)(pieces < 64 ? pieces : 64);
-    if (chunks > 0)
+    if (chunks > 0) {   // (max_pages 0: lengths are 0, and stay so)
+        if (!count) kv_fork_count_kernel<<<dim3((uint32_t)p.n * chunks), 256, 0, stream>>>(p, chunks);
+        const int64_t pieces = copy_pieces(p.data);
+        const int32_t walkers = (int32_t)(pieces < 64 ? pieces : 64);
         kv_fork_write_kernel<<<dim3((uint32_t)p.n * (uint32_t)(chunks + walkers)), 256, 0, stream>>>(p, chunks, walkers, pieces);
+    }
     return hipGetLastError();
 }
 
