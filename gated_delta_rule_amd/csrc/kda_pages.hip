@@ -141,26 +141,31 @@ __device__ __forceinline__ int32_t in_order(uint32_t bits, int32_t* s, F put) {
     }
     return __builtin_amdgcn_readlane(up, 63);
 }
-// Free pages, counted up to `enough`.
-__device__ int64_t count_free(const int32_t* refs, int32_t n_pages, int64_t enough, int32_t* s) {
+// Free pages, counted up to `enough`; bits: of the first step.
+__device__ __forceinline__ int64_t count_free(const int32_t* refs, int32_t n_pages, int64_t enough, int32_t* s, uint32_t& bits) {
     int64_t found = 0;
     for (int64_t base = 0; base < n_pages && found < enough; base += PG_STEP) {
+        const uint32_t m = free_bits(refs, base, n_pages);
+        if (base == 0) bits = m;
         int32_t total;
-        block_before(__popc(free_bits(refs, base, n_pages)), s, total);
+        block_before(__popc(m), s, total);
         found += total;
     }
     return found;
 }
 // Gives out `count` free pages in order: put(rank, page) for rank < count.
-// The pages become held once, so the next call goes on behind them.
+// The pages become held once, in refs and in `bits` (of the first step), so
+// that the next call goes on behind them.
 template <typename F>
-__device__ void give_out(int32_t* refs, int32_t n_pages, int32_t count, int32_t* s, F put) {
+__device__ __forceinline__ void give_out(int32_t* refs, int32_t n_pages, int32_t count, int32_t* s, uint32_t& bits, F put) {
     int32_t done = 0;
     for (int64_t base = 0; base < n_pages && done < count; base += PG_STEP) {
-        done += in_order(free_bits(refs, base, n_pages), s, [&](int e, int32_t rank) {
+        const uint32_t m = base == 0 ? bits : free_bits(refs, base, n_pages);
+        done += in_order(m, s, [&](int e, int32_t rank) {
             if (done + rank >= count) return;
             const int32_t page = (int32_t)(base + e * PG_THREADS + threadIdx.x);
             refs[page] = 1;
+            if (base == 0) bits &= ~(1u << e);
             put(done + rank, page);
         });
     }
@@ -212,7 +217,8 @@ __global__ __launch_bounds__(PG_THREADS) void kv_resize_kernel(PagesParams p) {
         }
         __syncthreads();
     }
-    const int64_t n_free = need_all > 0 ? count_free(refs, p.n_pages, need_all, s) : 0;
+    uint32_t bits = 0;
+    const int64_t n_free = need_all > 0 ? count_free(refs, p.n_pages, need_all, s, bits) : 0;
     int64_t upto = 0;
     for (int s0 = 0; s0 < p.n_slots; s0 += PG_THREADS) {
         const int slot = s0 + tid;
@@ -234,7 +240,7 @@ __global__ __launch_bounds__(PG_THREADS) void kv_resize_kernel(PagesParams p) {
             from[tid] = before;
             __syncthreads();
             // (slots without a need share the next one's offset: the last of equal ones has the page)
-            give_out(refs, p.n_pages, served, s, [&](int32_t rank, int32_t page) {
+            give_out(refs, p.n_pages, served, s, bits, [&](int32_t rank, int32_t page) {
                 const int i = owner_of(off, PG_THREADS, rank);
                 p.table_out[(int64_t)(s0 + i) * p.max_pages + from[i] + rank - off[i]] = page;
             });
@@ -254,7 +260,9 @@ hipError_t launch_kv_resize(const PagesParams& p, hipStream_t stream) {
 
 // ------------------------------------------------------------------- fork
 
-// Workspace: owner [n_slots], then per pair: what follows, then rows [n, max_pages].
+constexpr int FORK_NEAR = 8192;   // slots
+
+// Workspace: the first pair of each destination [n_slots], then per pair: what follows, then rows [n, max_pages].
 struct ForkPlan {
     int32_t go;        // the pair is carried out
     int32_t length;    // of the source
@@ -288,13 +296,19 @@ __device__ __forceinline__ void fork_count(const PagesParams& p, int64_t i, int3
 __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p, bool count) {
     __shared__ int32_t s[PG_EACH * PG_WAVES], off[PG_THREADS];
     const int tid = threadIdx.x;
-    int32_t *refs = p.refs_out, *owner = p.ws;
+    int32_t* refs = p.refs_out;
     ForkPlan* plan = fork_plans(p);
-    for (int i = tid; i < p.n_slots; i += PG_THREADS) owner[i] = INT32_MAX;
+    // the first pair of each destination, in LDS if it has room
+    __shared__ int32_t near[FORK_NEAR];
+    const bool in_lds = p.n_slots <= FORK_NEAR;
+    for (int i = tid; i < p.n_slots; i += PG_THREADS) (in_lds ? near : p.ws)[i] = INT32_MAX;
     __syncthreads();
     for (int i = tid; i < p.n; i += PG_THREADS) {
         const int32_t d = p.dst[i];
-        if (d >= 0 && d < p.n_slots) atomicMin(owner + d, i);
+        if (d >= 0 && d < p.n_slots) {
+            if (in_lds) atomicMin(near + d, i);
+            else atomicMin(p.ws + d, i);
+        }
     }
     __syncthreads();
     int64_t need_all = 0;
@@ -303,7 +317,7 @@ __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p,
         ForkPlan f = {0, 0, 0, -1, -1};
         if (i < p.n) {
             const int32_t a = p.src[i], d = p.dst[i];
-            if (a >= 0 && a < p.n_slots && d >= 0 && d < p.n_slots && fresh_load(owner + d) == i) {
+            if (a >= 0 && a < p.n_slots && d >= 0 && d < p.n_slots && (in_lds ? near[d] : fresh_load(p.ws + d)) == i) {
                 f.go = 1;
                 f.length = clamp_length(p.lengths[a], p);
                 const int32_t used = pages_of(f.length, p.page_shift), old = pages_of(clamp_length(p.lengths[d], p), p.page_shift);
@@ -319,7 +333,8 @@ __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p,
         block_before(f.from >= 0, s, total);
         need_all += total;
     }
-    const int64_t n_free = need_all > 0 ? count_free(refs, p.n_pages, need_all, s) : 0;
+    uint32_t bits = 0;
+    const int64_t n_free = need_all > 0 ? count_free(refs, p.n_pages, need_all, s, bits) : 0;
     int64_t upto = 0;
     for (int i0 = 0; i0 < p.n; i0 += PG_THREADS) {
         const int i = i0 + tid;
@@ -339,7 +354,7 @@ __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p,
         }
         __syncthreads();
         if (served > 0) {
-            give_out(refs, p.n_pages, served, s, [&](int32_t rank, int32_t page) {
+            give_out(refs, p.n_pages, served, s, bits, [&](int32_t rank, int32_t page) {
                 plan[i0 + owner_of(off, PG_THREADS, rank)].to = page;
             });
             __syncthreads();
@@ -431,11 +446,12 @@ hipError_t launch_kv_fork(const PagesParams& p, hipStream_t stream) {
 __global__ __launch_bounds__(PG_THREADS) void kv_compact_plan_kernel(PagesParams p) {
     __shared__ int32_t s[PG_EACH * PG_WAVES];
     const int32_t N = p.n_pages;
-    const int32_t n_live = N - (int32_t)count_free(p.refs, N, (int64_t)N + 1, s);
+    uint32_t bits = 0;
+    const int32_t n_live = N - (int32_t)count_free(p.refs, N, (int64_t)N + 1, s, bits);
     int32_t *mov = p.ws + 4, *hol = mov + N, *rank_of = hol + N;
     int32_t moved = 0, holes = 0;
     for (int64_t base = 0; base < N; base += PG_STEP) {
-        const uint32_t free = free_bits(p.refs, base, N);
+        const uint32_t free = base == 0 ? bits : free_bits(p.refs, base, N);
         uint32_t below = 0, exist = 0;   // pages < n_live, pages < N
 #pragma unroll
         for (int e = 0; e < PG_EACH; ++e) {
