@@ -84,7 +84,7 @@ def bounds(q, k, v, scale, half, first=0, causal=True, there=None):
         g = h // (H // G)
         P, lse = weights(q, k, h, scale, first, causal, there)
         # a score: D products and sums, the scale, its exponent's argument (values up to the score itself)
-        mag = scale * (np.abs(q[:, h]) @ np.abs(k[:, g]).T)
+        mag = abs(scale) * (np.abs(q[:, h]) @ np.abs(k[:, g]).T)
         s = np.where(P > 0, mag, 0.0).max(1, initial=0.0) * (D + 8) * U
         rel = 2 * s + (L + 32) * U          # a weight: its exponential, the sum below it, rescaling
         vh = np.abs(v[:, g])
@@ -102,7 +102,7 @@ def backward_bounds(q, k, v, gy, scale, half, causal=True):
         g = h // (H // G)
         P, _ = weights(q, k, h, scale, 0, causal)
         o = P @ v[:, g]
-        mag = scale * (np.abs(q[:, h]) @ np.abs(k[:, g]).T)
+        mag = abs(scale) * (np.abs(q[:, h]) @ np.abs(k[:, g]).T)
         s = np.where(P > 0, mag, 0.0).max(1, initial=0.0) * (D + 8) * U
         lse_err = s + (np.abs(np.log(np.maximum(P.max(1, initial=1e-30), 1e-30))) + T + 64) * U
         rel = (2 * s + lse_err + 64 * U)[:, None]
@@ -114,8 +114,8 @@ def backward_bounds(q, k, v, gy, scale, half, causal=True):
         eS = P * (half * (np.abs(gP - delta) + dmag) * 1.02 + (rel + (D + 8) * U) * (pmag + dmag))
         n = (T * (H // G) + 32) * U
         full = P * (np.abs(gP - delta) + half * dmag)
-        eq[:, h] = scale * ((eS + n * full) @ np.abs(k[:, g]))
-        ek[:, g] += scale * ((eS + n * full).T @ np.abs(q[:, h]))
+        eq[:, h] = abs(scale) * ((eS + n * full) @ np.abs(k[:, g]))
+        ek[:, g] += abs(scale) * ((eS + n * full).T @ np.abs(q[:, h]))
         ev[:, g] += (P * (half + rel + n)).T @ np.abs(gy[:, h])
     return eq, ek, ev
 
