@@ -24,7 +24,7 @@ template <int D>
 struct FwdShared {
     static constexpr int TILE = FW_KEYS * 2 * D;   // bytes
     char tiles[4 * TILE];                          // keys, keys, values, values
-    int32_t there[2][4];                           // of each 16 keys: their page exists
+    int32_t there[4][4];                           // of each 16 keys of four tiles: their page exists
 };
 
 // Steps of 64 keys that a block's rows see, and the position of its first token.
@@ -90,36 +90,42 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
         }
         return 0;
     };
-    int32_t next_page = t0 < t1 ? page_of(t0) : 0;   // of the next tile to be requested
-    auto request = [&](int32_t tile, int buf) {
-        const int32_t key = tile * FW_KEYS + 16 * wave;
-        const int32_t left = most - key < 16 ? most - key : 16;
-        const __bf16 *kb, *vb;
-        bool ok = left > 0;
-        if constexpr (PAGED) {
-            const int32_t page = __builtin_amdgcn_readfirstlane(next_page);
-            ok = ok && page >= 0 && page < keys.n_pages;
-            const int64_t at = (int64_t)page * keys.k_stride + (int64_t)(key & ((1 << keys.shift) - 1)) * D;
-            kb = keys.k + (ok ? at : 0);
-            vb = keys.v + (ok ? at : 0);
-            if (lane == 0) there[buf][wave] = ok;
-        } else {
-            kb = keys.k + (ok ? (int64_t)key : 0) * kstep;
-            vb = keys.v + (ok ? (int64_t)key : 0) * vstep;
-        }
-        if constexpr (PAGED) {
-            kb = in_scalars(kb);
-            vb = in_scalars(vb);
-        }
-        const auto krs = make_rsrc(kb, ok ? ((left - 1) * (int)kstep + D) * 2 : 0);
-        const auto vrs = make_rsrc(vb, ok ? ((left - 1) * (int)vstep + D) * 2 : 0);
-        const uint32_t to = lds0 + buf * TILE + wave * 16 * ROWB;
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(krs, koff[i], to + i * 1024);
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(vrs, voff[i], to + 2 * TILE + i * 1024);
-        if (PAGED && tile + 1 < t1) next_page = page_of(tile + 1);   // (arrives with the tile)
+    // A tile's keys are requested two steps before its weights are formed, its
+    // values one step before.
+    struct Source {
+        const __bf16* at;
+        bool ok;
     };
+    auto source = [&](const __bf16* base, int64_t step, int32_t tile, int32_t page) -> Source {
+        const int32_t key = tile * FW_KEYS + 16 * wave;
+        bool ok = key < most;
+        int64_t at;
+        if constexpr (PAGED) {
+            ok = ok && page >= 0 && page < keys.n_pages;
+            at = (int64_t)page * keys.k_stride + (int64_t)(key & ((1 << keys.shift) - 1)) * D;
+        } else {
+            at = (int64_t)key * step;
+        }
+        const __bf16* p0 = base + (ok ? at : 0);
+        if constexpr (PAGED) p0 = in_scalars(p0);
+        return Source{p0, ok};
+    };
+    auto request = [&](const Source& s, int64_t step, const uint32_t (&off)[LOADS], int32_t tile, int half_of) {
+        const int32_t left = most - (tile * FW_KEYS + 16 * wave);
+        const auto rs = make_rsrc(s.at, s.ok ? (((left < 16 ? left : 16) - 1) * (int)step + D) * 2 : 0);
+        const uint32_t to = lds0 + half_of * TILE + wave * 16 * ROWB;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load_to_lds(rs, off[i], to + i * 1024);
+    };
+    int32_t page_v = 0, page_raw = t0 < t1 ? page_of(t0) : 0;   // of the last keys requested; of the next ones
+    auto request_keys = [&](int32_t tile, int buf) {
+        page_v = PAGED ? __builtin_amdgcn_readfirstlane(page_raw) : 0;
+        const Source s = source(keys.k, kstep, tile, page_v);
+        if (PAGED && lane == 0) there[tile & 3][wave] = s.ok;
+        request(s, kstep, koff, tile, buf);
+        if (PAGED && tile + 1 < t1) page_raw = page_of(tile + 1);   // (arrives with the tile)
+    };
+    auto request_values = [&](int32_t tile, int buf) { request(source(keys.v, vstep, tile, page_v), vstep, voff, tile, 2 + buf); };
 
     // where this lane reads its operands
     const int kat = lane_rows<D>(lane);
@@ -130,30 +136,36 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
     for (int i = 0; i < O; ++i) o[i] = zero16();
     float m = kAttnLowest, l = 0.f;
 
-    if (t0 < t1) request(t0, 0);
-    for (int32_t tile = t0; tile < t1; ++tile) {
-        const int buf = (tile - t0) & 1;
+    f32x16 x[2], y[2];   // scores of this tile, of the next one
+    if (t0 < t1) {
+        request_keys(t0, 0);
         tiles_barrier();
-        if (tile + 1 < t1) request(tile + 1, buf ^ 1);
-        const int32_t key0 = tile * FW_KEYS;
-        if (key0 >= sees_most) continue;
-        const char* ks = lds + buf * TILE;
-        const char* vs = lds + 2 * TILE + buf * TILE;
-        f32x16 x[2];
+        request_values(t0, 0);
+        if (t0 + 1 < t1) request_keys(t0 + 1, 1);
         x[0] = x[1] = zero16();
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) x[kt] = mfma32x32(read_rows(ks + kt * 32 * ROWB, kat ^ (32 * s)), q[s], x[kt]);
+            for (int kt = 0; kt < 2; ++kt) x[kt] = mfma32x32(read_rows(lds + kt * 32 * ROWB, kat ^ (32 * s)), q[s], x[kt]);
+    }
+    auto step = [&](f32x16 (&x)[2], f32x16 (&y)[2], int32_t tile, int buf) {
+        tiles_barrier();
+        if (tile + 1 < t1) request_values(tile + 1, buf ^ 1);
+        if (tile + 2 < t1) request_keys(tile + 2, buf);
+        const int32_t key0 = tile * FW_KEYS;
+        if (key0 >= sees_most) return;
+        const char* ks = lds + (buf ^ 1) * TILE;   // the next tile's
+        const char* vs = lds + 2 * TILE + buf * TILE;
         bool whole = key0 + FW_KEYS <= sees_least;
-        if constexpr (PAGED) whole = whole && (there[buf][0] & there[buf][1] & there[buf][2] & there[buf][3]);
+        const int ring = tile & 3;
+        if constexpr (PAGED) whole = whole && (there[ring][0] & there[ring][1] & there[ring][2] & there[ring][3]);
         if (!__builtin_amdgcn_readfirstlane(whole)) {
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int key = 32 * kt + 8 * (e >> 2) + 4 * half + (e & 3);
-                    const bool seen = key0 + key < sees && (!PAGED || there[buf][2 * kt + (e >> 3)]);
+                    const bool seen = key0 + key < sees && (!PAGED || there[ring][2 * kt + (e >> 3)]);
                     x[kt][e] = seen ? x[kt][e] : -INFINITY;
                 }
         }
@@ -162,10 +174,9 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
         for (int e = 1; e < 16; ++e) top = fmaxf(top, x[0][e]);
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, x[1][e]);
-        top = fmaxf(top, swap_halves(top));
         top = fmaxf(top * c, kAttnLowest);
         if (__any(top > m + 8.f)) {
-            const float to = fmaxf(m, top), fade = attn_exp2(m - to);
+            const float to = fmaxf(m, fmaxf(top, swap_halves(top))), fade = attn_exp2(m - to);
             m = to;
             l *= fade;
 #pragma unroll
@@ -173,24 +184,32 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[i][e] *= fade;
         }
+        // This tile's weights, beside the next one's scores on the matrix cores.  Behind the last tile those are of
+        // whatever the memory holds, and nobody reads them: a branch around them cost 4% more than they do.
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        y[0] = y[1] = zero16();
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < S; ++s) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                x[kt][e] = attn_exp2(fmaf(x[kt][e], c, -m));
-                sum[e & 3] += x[kt][e];
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            for (int kt = 0; kt < 2; ++kt) y[kt] = mfma32x32(read_rows(ks + kt * 32 * ROWB, kat ^ (32 * s)), q[s], y[kt]);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const bf16x8 pw = as_operand(x[kt], s);
-                const int at = (2 * kt + s) * 16 * ROWB;
-#pragma unroll
-                for (int i = 0; i < O; ++i)
-                    o[i] = mfma32x32(read_cols(vs + at, vat, i), pw, o[i]);
+            for (int e = 32 / S * s; e < 32 / S * (s + 1); ++e) {
+                const float w = attn_exp2(fmaf(x[e >> 4][e & 15], c, -m));
+                x[e >> 4][e & 15] = w;
+                sum[e & 3] += w;
             }
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const bf16x8 pw = as_operand(x[s >> 1], s & 1);
+#pragma unroll
+            for (int i = 0; i < O; ++i) o[i] = mfma32x32(read_cols(vs + s * 16 * ROWB, vat, i), pw, o[i]);
+        }
+    };
+    for (int32_t tile = t0; tile < t1; tile += 2) {
+        step(x, y, tile, 0);
+        if (tile + 1 < t1) step(y, x, tile + 1, 1);
     }
     l += swap_halves(l);
     if (!valid) return;
