@@ -137,6 +137,13 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
     float m = kAttnLowest, l = 0.f;
 
     f32x16 x[2], y[2];   // scores of this tile, of the next one
+    float top = 0.f;     // the largest of x, of what nobody may see too
+    auto largest = [&](const f32x16 (&x)[2]) {
+        float top = x[0][0];
+#pragma unroll
+        for (int e = 1; e < 32; ++e) top = fmaxf(top, x[e >> 4][e & 15]);
+        return top;
+    };
     if (t0 < t1) {
         request_keys(t0, 0);
         tiles_barrier();
@@ -147,6 +154,7 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
         for (int s = 0; s < S; ++s)
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt) x[kt] = mfma32x32(read_rows(lds + kt * 32 * ROWB, kat ^ (32 * s)), q[s], x[kt]);
+        top = largest(x);
     }
     auto step = [&](f32x16 (&x)[2], f32x16 (&y)[2], int32_t tile, int buf) {
         tiles_barrier();
@@ -156,6 +164,9 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
         if (key0 >= sees_most) return;
         const char* ks = lds + (buf ^ 1) * TILE;   // the next tile's
         const char* vs = lds + 2 * TILE + buf * TILE;
+        bf16x8 kf[2][2], vf[2][O];   // operands of this product and of the next one
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) kf[0][kt] = read_rows(ks + kt * 32 * ROWB, kat);
         bool whole = key0 + FW_KEYS <= sees_least;
         const int ring = tile & 3;
         if constexpr (PAGED) whole = whole && (there[ring][0] & there[ring][1] & there[ring][2] & there[ring][3]);
@@ -168,12 +179,8 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
                     const bool seen = key0 + key < sees && (!PAGED || there[ring][2 * kt + (e >> 3)]);
                     x[kt][e] = seen ? x[kt][e] : -INFINITY;
                 }
+            top = largest(x);
         }
-        float top = x[0][0];
-#pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, x[0][e]);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, x[1][e]);
         top = fmaxf(top * c, kAttnLowest);
         if (__any(top > m + 8.f)) {
             const float to = fmaxf(m, fmaxf(top, swap_halves(top))), fade = attn_exp2(m - to);
@@ -186,26 +193,44 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
         }
         // This tile's weights, beside the next one's scores on the matrix cores.  Behind the last tile those are of
         // whatever the memory holds, and nobody reads them: a branch around them cost 4% more than they do.
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
         y[0] = y[1] = zero16();
 #pragma unroll
         for (int s = 0; s < S; ++s) {
+            if (s + 1 < S) {
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) y[kt] = mfma32x32(read_rows(ks + kt * 32 * ROWB, kat ^ (32 * s)), q[s], y[kt]);
+                for (int kt = 0; kt < 2; ++kt) kf[(s + 1) & 1][kt] = read_rows(ks + kt * 32 * ROWB, kat ^ (32 * (s + 1)));
+            } else {
 #pragma unroll
-            for (int e = 32 / S * s; e < 32 / S * (s + 1); ++e) {
-                const float w = attn_exp2(fmaf(x[e >> 4][e & 15], c, -m));
-                x[e >> 4][e & 15] = w;
-                sum[e & 3] += w;
+                for (int i = 0; i < O; ++i) vf[0][i] = read_cols(vs, vat, i);
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) y[kt] = mfma32x32(kf[s & 1][kt], q[s], y[kt]);
+#pragma unroll
+            for (int e = 32 / S * s; e < 32 / S * (s + 1); ++e) x[e >> 4][e & 15] = attn_exp2(fmaf(x[e >> 4][e & 15], c, -m));
+            __builtin_amdgcn_sched_barrier(0);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // The values' products, beside the sums of the weights and the largest of the next scores.
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        top = y[0][0];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
+            if (s < 3) {
+#pragma unroll
+                for (int i = 0; i < O; ++i) vf[(s + 1) & 1][i] = read_cols(vs + (s + 1) * 16 * ROWB, vat, i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             const bf16x8 pw = as_operand(x[s >> 1], s & 1);
 #pragma unroll
-            for (int i = 0; i < O; ++i) o[i] = mfma32x32(read_cols(vs + s * 16 * ROWB, vat, i), pw, o[i]);
+            for (int i = 0; i < O; ++i) o[i] = mfma32x32(vf[s & 1][i], pw, o[i]);
+#pragma unroll
+            for (int e = 8 * s; e < 8 * s + 8; ++e) {
+                sum[e & 3] += x[e >> 4][e & 15];
+                top = fmaxf(top, y[e >> 4][e & 15]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
     for (int32_t tile = t0; tile < t1; tile += 2) {
         step(x, y, tile, 0);
