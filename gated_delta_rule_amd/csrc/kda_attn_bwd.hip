@@ -65,7 +65,8 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
     const int32_t r_first = r_all + (int32_t)(steps * part / a.parts) * BW_STEP;
     const int32_t r_end = r_all + (int32_t)(steps * (part + 1) / a.parts) * BW_STEP, n_rows = r_end < all_rows ? r_end : all_rows;
     // key x is seen by the rows from x * hpg on
-    const int32_t from_least = p.causal ? key0 * p.hpg : 0, from_most = p.causal ? (key0 + 31) * p.hpg : 0;
+    // (a wave without keys only fetches)
+    const int32_t from_least = key0 >= b.r1 ? INT32_MAX : p.causal ? key0 * p.hpg : 0, from_most = p.causal ? (key0 + 31) * p.hpg : 0;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
     const int64_t gstride = (int64_t)p.H * D;
     const RowOf rows(p.hpg);
@@ -234,7 +235,8 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
     const int head = pl.g * p.hpg + (valid ? row - t * p.hpg : 0);
     const int64_t at = (b.start + t) * p.H + head;
     const int32_t sees = p.causal ? t + 1 : b.tokens, most = p.causal ? (b.r1 - 1) / p.hpg + 1 : b.tokens;
-    const int32_t sees_least = __builtin_amdgcn_readfirstlane(sees), sees_most = __builtin_amdgcn_readlane(sees, 31);
+    const int32_t sees_least = __builtin_amdgcn_readfirstlane(sees);
+    const int32_t sees_most = b.r0 + wave * 32 < b.r1 ? __builtin_amdgcn_readlane(sees, 31) : 0;   // (a wave without rows only fetches)
 
     bf16x8 q[S], go[S];
     {

@@ -53,8 +53,9 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
     const int32_t t = valid ? row / p.hpg : (b.r1 - 1) / p.hpg;
     const int head = g * p.hpg + (valid ? row - t * p.hpg : 0);
     const int32_t sees = p.causal ? first + t + 1 : len;     // keys [0, sees)
-    // rows come in order of their tokens
-    const int32_t sees_least = __builtin_amdgcn_readfirstlane(sees), sees_most = __builtin_amdgcn_readlane(sees, 31);
+    // rows come in order of their tokens; a wave without any only fetches its share of the tiles
+    const int32_t sees_least = __builtin_amdgcn_readfirstlane(sees);
+    const int32_t sees_most = b.r0 + wave * 32 < b.r1 ? __builtin_amdgcn_readlane(sees, 31) : 0;
 
     // scores are scale * q . k with scale > 0: its sign goes to q
     const float scale = p.scale < 0.f ? -p.scale : p.scale > 0.f ? p.scale : 1.f;
