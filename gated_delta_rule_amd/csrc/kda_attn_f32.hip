@@ -64,7 +64,7 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
     const int32_t len = PAGED ? attn_length(p, b.n) : b.tokens;
     const int32_t first = len - b.tokens;                    // position of the first query token
     const int row = b.r0 + wave * 16 + col;
-    const bool valid = row < b.r1;
+    const bool valid = row < b.r1, idle = b.r0 + __builtin_amdgcn_readfirstlane(wave) * 16 >= b.r1;   // (idle: only fetches)
     const int32_t t = valid ? row / p.hpg : 0;
     const int head = pl.g * p.hpg + (valid ? row - t * p.hpg : 0);
     const int32_t sees = !valid ? 0 : p.causal ? first + t + 1 : len;   // keys [0, sees)
@@ -91,6 +91,7 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
         if ((tid & 7) == 0) there[tid >> 3] = st.ok;
         __syncthreads();
         if (tile + 1 < t1) st.load(keys, (tile + 1) * AF_KEYS + (tid >> 3), most);
+        if (idle) continue;
         float x[2][4], top = m;
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
