@@ -131,6 +131,40 @@ def test_chunks_over_long_requests(case, dtype):
     run_paged(*case, dtype)
 
 
+MIXED = [([5000] + [700] * 20 + [90, 2000, 31], [1] * 21 + [0, 257, 5], 8, 2, 128, 64), ([300] * 70, [1] * 69 + [2], 4, 4, 64, 16),
+         ([9000, 9000, 40], [1, 130, 33], 32, 2, 64, 32)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", MIXED)
+def test_single_tokens_beside_chunks(case, dtype):
+    run_paged(*case, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,G,lens", [(200, 1, [37, 5]), (130, 2, [3, 0, 21])])
+def test_many_heads_to_a_group(H, G, lens, dtype):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    T, D = sum(lens), 64
+    q, k, v, go = (torch.randn(T, n, D, generator=g, device="cuda").to(dtype) for n in (H, G, G, H))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    o, lse = kda.attn_fwd(q, k, v, cu)
+    grads = kda.attn_bwd(q, k, v, o, lse, go, cu)
+    at = 0
+    for t in lens:
+        if t:
+            s = slice(at, at + t)
+            ref, eo, lref, el = exact(q[s], k[s], v[s], 0, D ** -0.5, dtype)
+            check("o", o[s], ref, eo, dtype)
+            check("lse", lse[s], lref, el, F32)
+            n = [x[s].double().cpu().numpy() for x in (q, k, v, go)]
+            refs, errs = O.attention_backward(*n, D ** -0.5), O.backward_bounds(*n, D ** -0.5, 2.0 ** -8 if dtype == BF16 else 0.0)
+            for x, r, e in zip(grads, refs, errs):
+                check("gradient", x[s], torch.from_numpy(r).cuda(), torch.from_numpy(e).cuda(), dtype)
+        at += t
+    run_paged([400, 70], [3, 70], H, G, D, 16, dtype)
+
+
 def test_many_blocks_are_not_cut():
     run_paged([1200] * 9, [900] * 9, 16, 8, 64, 16, BF16, look={0, 4, 8})
 
