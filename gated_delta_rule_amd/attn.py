@@ -341,7 +341,8 @@ def kv_resize(table, lengths, refs, new_lengths, page_size):
     table int32 [n_slots, max_pages], lengths int32 [n_slots], refs int32
     [n_pages] (holders of each page), all updated in place; new_lengths int32
     [n_slots].  Returns ok int32 [n_slots]: 0 where no pages were left, and the
-    slot is as it was.
+    slot is as it was.  A slot that is cut back into a page shared with a branch
+    still shares it: kv_fork it to another slot before appending.
     """
     import torch
     lib = load_library()

@@ -11,6 +11,13 @@
 //   rows: wave w has 32 rows and walks the keys:
 //     S^T = K Q^T, dP^T = V dO^T, then dQ^T += K^T dS^T.
 // P and dS go from product to product in registers, rounded to bf16 once.
+//   Bound by the matrix cores (0.52 and 0.62 busy) and by what stands between
+// their products: two sums and two operands fill 192 of 256 registers, so that
+// operands are read from LDS just before their turn and only the SIMD's other
+// wave covers that.  2 x 4096 causal tokens, 32 heads of 128 on 8: 571 us by the
+// keys, 393 by the rows, 26 to join the parts; 0.7 PFLOP/s of the formula's five
+// products.  Reading operands two to four products ahead, pinned there, took 4
+// to 11% longer.
 #include "kda_attn_mma.h"
 
 namespace kda {

@@ -9,6 +9,9 @@
 // O^T = V^T P^T, so weights go from product to product in registers, and a
 // row's maximum and sum are one lane's values and two exchanges.  The next
 // tile's rows are requested before the products of this one.
+//   Bound by the float32 matrix instructions and the LDS reads in front of them:
+// 72 TFLOP/s at 2048 causal tokens, 16 heads of 128, where a large product
+// reaches 153.
 #include "kda_attn_tile.h"
 
 namespace kda {

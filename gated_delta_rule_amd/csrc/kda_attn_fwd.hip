@@ -3,8 +3,9 @@
 //
 // One pass over the keys with each row's running maximum m and sum l.  A
 // workgroup has 128 rows of one (sequence, group), 32 per wave, and takes 64
-// keys at a time: while one tile is computed with, the next one comes from
-// memory straight into the other half of LDS (no registers in between).
+// keys at a time: while one tile is computed with, the next one's values and
+// the keys of the one behind it come from memory straight into the other half
+// of LDS (no registers in between).
 //   S^T = K Q^T leaves lane l with row l & 31 and keys 8 b + 4 (l >> 5) + i: the
 // place of P^T as an operand of O^T = V^T P^T, whose other operand the
 // transposing LDS reads give for any order of keys.  So the weights stay in
@@ -14,6 +15,14 @@
 // weights are then up to 2^8 instead of 1, which costs no precision (l and o
 // are float32, a bf16 weight has the same relative error), and the products
 // with e^{m - m'} are left out of nearly all tiles.
+//   Per tile and wave 32 products (1024 cycles of the matrix cores) stand beside
+// 32 exponentials and about 110 other vector instructions (about 1000 cycles),
+// so both have to run at once: the products of the next tile's scores beside
+// this tile's exponentials, those with the values beside the sums and the next
+// tile's maximum, and another wave's beside all of them (two waves per SIMD,
+// which 240 registers and 64 KB of LDS leave room for).  8192 causal tokens, 32
+// heads of 128 on 8: 522 us, 1.05 PFLOP/s; 2 x 4096: 261 us (286 with a tile's
+// scores, weights and sums one after the other).
 #include "kda_attn_mma.h"
 
 namespace kda {
@@ -284,9 +293,9 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
 // that are cut are joined by a second launch.  Neighbouring pieces go to one
 // XCD, for their common keys and values.
 //   (1024 new tokens in all of two requests of 8k to 32k tokens, 32 heads of 128
-// on 8: 435 us.  With the same number of parts for every block instead: 774 us
-// with 512 workgroups or more in all, 467 with 1024, 430 with 2048; but 256
-// tokens over 32k 165, 179 and 216, 163 here.)
+// on 8: 389 us and 21 to join.  When both took 435, the same number of parts for
+// every block took 774 us with 512 workgroups or more in all, 467 with 1024, 430
+// with 2048; but 256 tokens over 32k 165, 179 and 216, 163 here.)
 struct FwdLine {
     int64_t per_group, quota;   // steps
 };

@@ -21,7 +21,9 @@
  * synchronisation, deterministic results without atomics, `stream` on the
  * current device):
  *   - Sizes: head dimension D 64 or 128, H a multiple of G, H <=
- *     KDA_MAX_HEADS (anything else -> KDA_ERR_BAD_SHAPE / _TOO_LARGE).
+ *     KDA_MAX_HEADS, H * D <= KDA_ATTN_MAX_STRIDE, H / G times the tokens of
+ *     a sequence (packed: of the batch) at most 2^30 (anything else ->
+ *     KDA_ERR_BAD_SHAPE / _TOO_LARGE).
  *   - in_dtype (KDA_BF16 or KDA_F32) is the type of q, k, v, o and of their
  *     gradients; lse is float32.
  *   - Token rows: a `_stride` is the number of elements from one token row to
@@ -103,8 +105,9 @@ int kda_attn_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_strid
  * lengths[b] - T_b + t.  One with a negative position is not there.
  *
  * kda_kv_append writes the new tokens' k and v (rows with k_stride, v_stride)
- * into their pages.  No two of them may share a place (a page held by two
- * requests and open at its end): which is kept is undefined.
+ * into their pages.  No two of them may share a place: which is kept is
+ * undefined.  A page is written to whoever else holds it (kda_pages.h says when
+ * an open page can be shared).
  */
 int kda_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int in_dtype,
                   void* k_pages, void* v_pages, int64_t page_stride, int32_t n_pages,

@@ -7,7 +7,7 @@
  * State, all int32 on the device:
  *   table   [n_slots, max_pages]  the pages of each slot (request), in order
  *   lengths [n_slots]             tokens of each slot, in [0, max_pages * page_size]
- *   refs    [n_pages]             how many slots hold each page; 0: free
+ *   refs    [n_pages]             how many slots hold each page; 0 (or less): free
  * A slot holds the first ceil(lengths / page_size) entries of its row; the
  * calls set entries that a slot gives up to -1 and never read the others.
  * Several slots may hold one page (kda_kv_fork).  The calls keep refs equal
@@ -15,8 +15,10 @@
  * are passed over.  Lengths out of range are clamped.  page_size as in
  * kda_attn.h.  Free pages are given out lowest number first.
  *
- * Sizes: n_slots * max_pages < 2^31, n_pages < 2^31.  Tensors 4-byte aligned,
- * workspaces 16.  Results are deterministic.
+ * Sizes: n_slots * max_pages < 2^30, n_pages < 2^29, max_pages * page_size <
+ * 2^30 (else KDA_ERR_TOO_LARGE).  Tensors 4-byte aligned, workspaces 16.
+ * Results are deterministic: the counts are changed by integer atomics, whose
+ * order does not matter.
  */
 #ifndef KDA_PAGES_H_
 #define KDA_PAGES_H_
@@ -37,6 +39,9 @@ extern "C" {
  * first, then given out in the order of the slots.  ok[slot] is 1, or 0 for a
  * slot that wanted more pages than were left after those before it (the ones
  * that were refused included): it keeps its length and pages.
+ *   A slot that is cut back into a page that others hold, too, still shares it,
+ * and appending would write into theirs.  Fork it to another slot then: the
+ * branch has its own copy of such an open page.
  *   want, ok int32 [n_slots]; ok may be NULL.
  */
 int kda_kv_resize(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* want,

@@ -79,6 +79,17 @@ def test_by_hand():
     b.compact()
 
 
+def test_cut_back_into_a_shared_page():
+    b = Both(3, 4, 8, 16)
+    b.resize([32, 0, 0])
+    b.fork([0], [1])                    # both pages are shared
+    b.resize([32, 30, 0])               # the second one is open in the branch, and shared
+    assert b.plain.table[1][:2] == [0, 1] and b.plain.refs[1] == 2
+    b.fork([1], [2])                    # a branch of it has a copy
+    assert b.plain.table[2][:2] == [0, 2] and b.plain.data[2] == 1 and b.plain.refs[:3] == [3, 2, 1]
+    b.resize([32, 0, 40])
+
+
 @pytest.mark.parametrize("seed", range(6))
 def test_random_steps(seed):
     r = random.Random(seed)
