@@ -11,7 +11,7 @@
 //   rows: wave w has 32 rows and walks the keys:
 //     S^T = K Q^T, dP^T = V dO^T, then dQ^T += K^T dS^T.
 // P and dS go from product to product in registers, rounded to bf16 once.
-//   Bound by the matrix cores (0.52 and 0.62 busy) and by what stands between
+//   Bound by the matrix cores (0.46 and 0.53 busy, at 1.9 GHz) and by what stands between
 // their products: two sums and two operands fill 192 of 256 registers, so that
 // operands are read from LDS just before their turn and only the SIMD's other
 // wave covers that.  2 x 4096 causal tokens, 32 heads of 128 on 8: 571 us by the
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
     __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // keys, keys, values, values
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
-    const AttnPlace pl = attn_place(blockIdx.x, p.slots, p.G);
+    const AttnPlace pl = attn_place(attn_turned(blockIdx.x, gridDim.x, p.G), p.slots, p.G);
     const AttnBlock b = attn_block(p, p.slots - 1 - pl.item, p.hpg, BW_BLOCK);   // (later blocks see more keys)
     if (b.j < 0) return;
     const int row = b.r0 + wave * 32 + col;

@@ -10,8 +10,8 @@
 // row's maximum and sum are one lane's values and two exchanges.  The next
 // tile's rows are requested before the products of this one.
 //   Bound by the float32 matrix instructions and the LDS reads in front of them:
-// 72 TFLOP/s at 2048 causal tokens, 16 heads of 128, where a large product
-// reaches 153.
+// 88 TFLOP/s at 2048 causal tokens, 16 heads of 128, 101 at 4096, where a large
+// product reaches 153.
 #include "kda_attn_tile.h"
 
 namespace kda {
@@ -59,7 +59,8 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
     __shared__ __attribute__((aligned(16))) float ks[AF_KEYS * PITCH], vs[AF_KEYS * PITCH];
     __shared__ uint8_t there[AF_KEYS];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, grp = lane >> 4;
-    const AttnPlace pl = attn_place(blockIdx.x, p.slots * p.splits, p.G);
+    // (2048 tokens, 16 heads of 128: 196 us with every second round turned, 241 without; 4096: 677 and 707)
+    const AttnPlace pl = attn_place(attn_zigzag(blockIdx.x, gridDim.x, p.G), p.slots * p.splits, p.G);
     const int64_t slot = p.slots - 1 - pl.item / p.splits;   // (later blocks see more keys)
     const int split = (int)(pl.item % p.splits);
     const AttnBlock b = attn_block(p, slot, p.hpg, AF_BLOCK);

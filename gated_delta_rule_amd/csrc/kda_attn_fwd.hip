@@ -278,7 +278,7 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
 template <int D, bool PAGED>
 __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams p) {
     __shared__ __attribute__((aligned(1024))) FwdShared<D> sh;
-    const AttnPlace pl = attn_place(blockIdx.x, p.slots, p.G);
+    const AttnPlace pl = attn_place(attn_turned(blockIdx.x, gridDim.x, p.G), p.slots, p.G);
     const AttnBlock b = attn_block(p, p.slots - 1 - pl.item, p.hpg, FW_BLOCK);   // (later blocks see more keys)
     if (b.j < 0) return;
     int32_t len, most;

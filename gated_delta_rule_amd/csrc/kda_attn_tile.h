@@ -151,6 +151,14 @@ __device__ __forceinline__ uint32_t attn_zigzag(uint32_t w, uint32_t n, int32_t 
     return (2 * round * wide + wide - 1 - i) * step + x;
 }
 
+// The same for kernels of two workgroups per compute unit whose workgroups come
+// and go: turned if there are two rounds of them at most.  Causal prompts of
+// 2048 / 4096 / 8192 tokens, 32 heads of 128 on 8 (512 / 1024 / 2048
+// workgroups): 44, 138 and 496 us turned, 46, 140 and 488 as they are.
+__device__ __forceinline__ uint32_t attn_turned(uint32_t w, uint32_t n, int32_t G) {
+    return n <= 1024 ? attn_zigzag(w, n, G) : w;
+}
+
 // Workgroups of one (sequence, group) on one XCD (workgroup w starts on XCD w
 // mod 8), so that its keys and values stay in that L2: workgroup w works on
 // item `at` of group `g`.  Groups are dealt to the XCDs in turn; where they do
