@@ -286,9 +286,10 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
     fwd_block<D, PAGED>(p, sh, b, pl.g, len, most, 0, steps, nullptr);
 }
 
-// Few blocks over long requests: the steps of all of them, in the order of the
-// groups, then of the blocks, lie on one line that is cut into as many equal
-// pieces as workgroups run at once.  Each workgroup finds its piece, which may
+// Few blocks: short ones are taken whole, in turn (the lengths that decide are
+// on the device only).  Over long requests the steps of all of them, in the
+// order of the groups, then of the blocks, lie on one line that is cut into as
+// many equal pieces as workgroups run at once.  Each workgroup finds its piece, which may
 // hold the end of one block, some whole ones and the start of another; blocks
 // that are cut are joined by a second launch.  Neighbouring pieces go to one
 // XCD, for their common keys and values.
@@ -311,34 +312,61 @@ template <int D>
 __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_line_kernel(AttnParams p) {
     __shared__ __attribute__((aligned(1024))) FwdShared<D> sh;
     __shared__ int64_t sums[FW_THREADS / 64], found[2];
+    __shared__ int32_t most_steps[FW_THREADS / 64], counts[FW_THREADS / 64];
     const int tid = threadIdx.x, lane = tid & 63;
     int32_t len, most;
     // steps before this thread's slots, of one group
     const int64_t each = (p.slots + FW_THREADS - 1) / FW_THREADS, s0 = tid * each, s1 = s0 + each < p.slots ? s0 + each : p.slots;
     int64_t mine = 0;
-    for (int64_t s = s0; s < s1; ++s) mine += fwd_steps<true>(p, attn_block(p, s, p.hpg, FW_BLOCK), len, most);
+    int32_t longest = 0, count = 0;   // (count: blocks that have any)
+    for (int64_t s = s0; s < s1; ++s) {
+        const int32_t x = fwd_steps<true>(p, attn_block(p, s, p.hpg, FW_BLOCK), len, most);
+        mine += x;
+        longest = x > longest ? x : longest;
+        count += x > 0;
+    }
     int64_t up = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int64_t y = __shfl_up(up, d);
         if (lane >= d) up += y;
+        const int32_t z = __shfl_xor(longest, d);
+        longest = z > longest ? z : longest;
+        count += __shfl_xor(count, d);
     }
-    if (lane == 63) sums[tid >> 6] = up;
+    if (lane == 63) {
+        counts[tid >> 6] = count;
+        sums[tid >> 6] = up;
+        most_steps[tid >> 6] = longest;
+    }
     __syncthreads();
     int64_t before = up - mine, total = 0;
+    count = 0;
 #pragma unroll
     for (int w = 0; w < FW_THREADS / 64; ++w) {
         if (w < (tid >> 6)) before += sums[w];
         total += sums[w];
+        longest = most_steps[w] > longest ? most_steps[w] : longest;
+        count += counts[w];
     }
     total = uniform(total);
-    const int64_t quota = (total * p.G + p.workgroups - 1) / p.workgroups;
+    const int64_t units = p.slots * p.G, quota = (total * p.G + p.workgroups - 1) / p.workgroups;
+    // Whole blocks where that takes no longer, in steps of two workgroups on one compute unit (2.1 us; half a round of
+    // blocks takes half of that): rounds of average blocks, uneven by an eighth, or the longest one; cutting costs 30 us
+    // for more starts and the parts, and 0.04 per block to join.  One request's first 1024 / 2048 / 4096 tokens, 32 heads
+    // of 128 on 8: 33, 61 and 170 us whole, 56, 107 and 249 cut; 512 new tokens of each of 8 over 4096: 269 and 319; one
+    // of each of 64 over 4096, packed (a round and a few blocks): 296 and 230.
+    const int64_t rest = units % p.workgroups, halves = units / p.workgroups * 2 + (rest > p.workgroups / 2 ? 2 : rest > 0);
+    int64_t by_blocks = count > 0 ? total * halves * 9 / (16 * (int64_t)count) : 0;
+    const int64_t one = units <= p.workgroups / 2 ? longest / 2 : longest;
+    by_blocks = by_blocks > one ? by_blocks : one;
+    const bool cut = uniform(by_blocks) > quota + 14 + units / 50;
     const int64_t piece = line_piece(blockIdx.x, p.workgroups), begin = piece * quota;
     const int64_t end = begin + quota < total * p.G ? begin + quota : total * p.G;
-    if (begin >= end) return;
-    int g = (int)(begin / total);
+    if (cut && begin >= end) return;
+    int g = cut ? (int)(begin / total) : 0;
     const int64_t within = begin - g * total;
-    if (within >= before && within < before + mine) {
+    if (cut && within >= before && within < before + mine) {
         int64_t at = before;
         for (int64_t s = s0; s < s1; ++s) {
             const int32_t x = fwd_steps<true>(p, attn_block(p, s, p.hpg, FW_BLOCK), len, most);
@@ -351,8 +379,13 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_line_kernel(AttnParams
         }
     }
     __syncthreads();
-    int64_t slot = uniform(found[0]), base = g * total + uniform(found[1]);   // first step of the block on the line
-    for (int64_t at = begin; at < end;) {
+    int64_t slot = cut ? uniform(found[0]) : 0, base = cut ? g * total + uniform(found[1]) : 0;   // first step of the block on the line
+    for (int64_t at = cut ? begin : blockIdx.x; at < (cut ? end : units);) {   // (steps, or blocks)
+        if (!cut) {
+            const AttnPlace pl = attn_place(attn_zigzag((uint32_t)at, (uint32_t)units, p.G), p.slots, p.G);
+            slot = p.slots - 1 - pl.item;   // (later blocks see more keys)
+            g = pl.g;
+        }
         AttnBlock b = attn_block(p, slot, p.hpg, FW_BLOCK);
         const int32_t steps = __builtin_amdgcn_readfirstlane(fwd_steps<true>(p, b, len, most));
         if (steps > 0) {
@@ -365,8 +398,8 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_line_kernel(AttnParams
             len = __builtin_amdgcn_readfirstlane(len);
             most = __builtin_amdgcn_readfirstlane(most);
             g = __builtin_amdgcn_readfirstlane(g);
-            const int32_t t0 = __builtin_amdgcn_readfirstlane((int32_t)(at - base));
-            const int32_t t1 = __builtin_amdgcn_readfirstlane((int32_t)(end - base < steps ? end - base : steps));
+            const int32_t t0 = __builtin_amdgcn_readfirstlane(cut ? (int32_t)(at - base) : 0);
+            const int32_t t1 = __builtin_amdgcn_readfirstlane(cut && end - base < steps ? (int32_t)(end - base) : steps);
             const bool whole = t0 == 0 && t1 == steps;
             if (tid == 0) {   // for the joining: first piece (-1: nothing to join) and last
                 int32_t* info = line_info(p) + 2 * (g * p.slots + slot);
@@ -375,9 +408,11 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_line_kernel(AttnParams
             }
             fwd_block<D, true>(p, sh, b, g, len, most, t0, t1, whole ? nullptr : line_part<D>(p, piece, t0 == 0));
             tiles_barrier();   // (the tiles are the next block's)
-            at = base + t1;
+            if (cut) at = base + t1;
         }
-        if (at < end) {
+        if (!cut) {
+            at += p.workgroups;
+        } else if (at < end) {
             base += steps;
             if (++slot == p.slots) {
                 slot = 0;
@@ -387,36 +422,40 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_line_kernel(AttnParams
     }
 }
 
-// Rows of the blocks that were cut, and of those that see no key.  A wave has a row.
+// Rows of the blocks that were cut, and of those that see no key.  A wave has
+// FW_BLOCK / 4 / LINE_JOIN rows, one after the other.
+constexpr int LINE_JOIN = 8;   // workgroups per block
 template <int D>
 __global__ __launch_bounds__(256) void attn_fwd_line_join_kernel(AttnParams p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t unit = blockIdx.x / (FW_BLOCK / 4);
+    const uint32_t unit = blockIdx.x / LINE_JOIN;
     const int64_t slot = unit % (uint32_t)p.slots;
-    const int g = (int)(unit / (uint32_t)p.slots), r = (int)(blockIdx.x % (FW_BLOCK / 4)) * 4 + wave;
+    const int g = (int)(unit / (uint32_t)p.slots);
     const AttnBlock b = attn_block(p, slot, p.hpg, FW_BLOCK);
-    if (b.j < 0 || b.r0 + r >= b.r1) return;
+    if (b.j < 0) return;
     int32_t len, most, w0 = 0, w1 = -1;
     if (fwd_steps<true>(p, b, len, most) > 0) {
         w0 = line_info(p)[2 * (g * p.slots + slot)];
         w1 = line_info(p)[2 * (g * p.slots + slot) + 1];
         if (w0 < 0) return;
     }
-    float m = kAttnLowest, l = 0.f, o[D / 64] = {};
-    for (int32_t w = w0; w <= w1; ++w) {
-        const float* from = line_part<D>(p, w, w == w0) + r * (D + 4);
-        const float to = fmaxf(m, from[D + 1]), f0 = attn_exp2(m - to), f1 = attn_exp2(from[D + 1] - to);
-        m = to;
-        l = l * f0 + from[D] * f1;
+    for (int r = (int)(blockIdx.x % LINE_JOIN) * 4 + wave; b.r0 + r < b.r1; r += 4 * LINE_JOIN) {
+        float m = kAttnLowest, l = 0.f, o[D / 64] = {};
+        for (int32_t w = w0; w <= w1; ++w) {
+            const float* from = line_part<D>(p, w, w == w0) + r * (D + 4);
+            const float to = fmaxf(m, from[D + 1]), f0 = attn_exp2(m - to), f1 = attn_exp2(from[D + 1] - to);
+            m = to;
+            l = l * f0 + from[D] * f1;
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e) o[e] = o[e] * f0 + from[64 * e + lane] * f1;
+            for (int e = 0; e < D / 64; ++e) o[e] = o[e] * f0 + from[64 * e + lane] * f1;
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int row = b.r0 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
+        __bf16* orow = (__bf16*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) orow[64 * e + lane] = (__bf16)(o[e] * inv);
+        if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int row = b.r0 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
-    __bf16* orow = (__bf16*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e) orow[64 * e + lane] = (__bf16)(o[e] * inv);
-    if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <int D>
@@ -424,7 +463,7 @@ static void run_fwd(const AttnParams& p, hipStream_t stream) {
     const dim3 grid((uint32_t)(p.slots * p.G));
     if (p.workgroups > 0) {
         attn_fwd_line_kernel<D><<<dim3((uint32_t)p.workgroups), FW_THREADS, 0, stream>>>(p);
-        attn_fwd_line_join_kernel<D><<<dim3((uint32_t)(p.slots * p.G * (FW_BLOCK / 4))), 256, 0, stream>>>(p);
+        attn_fwd_line_join_kernel<D><<<dim3((uint32_t)(p.slots * p.G * LINE_JOIN)), 256, 0, stream>>>(p);
     } else if (p.lengths) {
         attn_fwd_bf16_kernel<D, true><<<grid, FW_THREADS, 0, stream>>>(p);
     } else {
