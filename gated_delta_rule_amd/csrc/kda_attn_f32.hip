@@ -10,7 +10,8 @@
 // row's maximum and sum are one lane's values and two exchanges.  The next
 // tile's rows are requested before the products of this one.
 //   Bound by the float32 matrix instructions and the LDS reads in front of them:
-// 88 TFLOP/s at 2048 causal tokens, 16 heads of 128, 101 at 4096, where a large
+// 94 TFLOP/s at 2048 causal tokens, 16 heads of 128 (182 us; 195 with operands
+// read as they are needed), where a large
 // product reaches 153.
 #include "kda_attn_tile.h"
 
@@ -96,23 +97,38 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
         __syncthreads();
         if (tile + 1 < t1) st.load(keys, (tile + 1) * AF_KEYS + (tid >> 3), most);
         if (idle) continue;
+        // operands are read one product (of 16 keys or values) ahead, where the fences keep them
+        float kf[2][2][4], vf[2][4];
+        auto key_rows = [&](int s, float (&a)[2][4]) {
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) load4(ks + (16 * kt + col) * PITCH + 16 * s + 4 * grp, a[kt]);
+        };
+        auto value_cols = [&](int i, float (&a)[4]) {   // i = kt S + s
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = vs[(16 * (i / S) + 4 * grp + e) * PITCH + 16 * (i % S) + col];
+        };
+        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        key_rows(0, kf[0]);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            if (s + 1 < S) key_rows(s + 1, kf[(s + 1) & 1]);
+            else value_cols(0, vf[0]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) acc[kt] = mfma4f(kf[s & 1][kt][e], q[s][e], acc[kt]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         float x[2][4], top = m;
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float a[4];
-                load4(ks + (16 * kt + col) * PITCH + 16 * s + 4 * grp, a);
-                mma_k16<true, PLAIN>(acc, a, q[s]);
-            }
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = 16 * kt + 4 * grp + i;
-                x[kt][i] = tile * AF_KEYS + key < sees && (!PAGED || there[key]) ? acc[i] * c : -INFINITY;
+                x[kt][i] = tile * AF_KEYS + key < sees && (!PAGED || there[key]) ? acc[kt][i] * c : -INFINITY;
                 top = fmaxf(top, x[kt][i]);
             }
-        }
         top = groups_max(top);
         const float base = top == -INFINITY ? 0.f : top, fade = attn_exp2(m - base);
         m = top;
@@ -120,19 +136,18 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
 #pragma unroll
         for (int s = 0; s < S; ++s) o[s] *= fade;
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[kt][i] = attn_exp2(x[kt][i] - base);
                 l += x[kt][i];
             }
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                float a[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) a[e] = vs[(16 * kt + 4 * grp + e) * PITCH + 16 * s + col];
-                mma_k16<true, PLAIN>(o[s], a, x[kt]);
-            }
+        for (int i = 0; i < 2 * S; ++i) {
+            if (i + 1 < 2 * S) value_cols(i + 1, vf[(i + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            mma_k16<true, PLAIN>(o[i % S], vf[i & 1], x[i / S]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     l = groups_sum(l);
