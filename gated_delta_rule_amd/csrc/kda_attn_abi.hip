@@ -126,6 +126,10 @@ PagedPlan paged_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t
 // sums are added by another launch.  32 heads of 128 on 8, with 1 / 2 / 4 / 8 / 16
 // parts, us: 512 tokens 112 / 77 / 60 / 51 / 51, 2048 tokens 407 / 256 / 189 / 186 / 246,
 // 4096 tokens 878 / 611 / 542 / 585 / 681, 2 x 4096 1150 / 1013 / 1034 / 1138 / 1352.
+// In float32, whose blocks have 16 keys, about 512 workgroups: 1024 tokens, 16
+// heads of 128 on 4, 196 us, 206 and 232 with twice and four times as many; 385
+// of each of 2, 32 heads on 4, 158, 162 and 183; before blocks were cut 279 and
+// 224 (operands read one product ahead included).
 struct BwdPlan {
     int64_t slots, key_slots, parts, delta, bytes;   // delta: bytes before the parts' sums
 };
@@ -136,13 +140,11 @@ BwdPlan bwd_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, 
     b.key_slots = block_slots(rows, n_seqs, T, 1, block, varlen);
     b.delta = (rows * H * 4 + 15) / 16 * 16;
     b.parts = 1;
-    if (bf16) {
-        // (the same for a packed batch of equal lengths)
-        const int64_t most = rows * (H / G) / kMinPartRows, blocks = block_slots(rows, n_seqs, T, 1, block, true) * G;
-        b.parts = blocks > 0 ? (2 * kFill + blocks / 2) / blocks : 1;
-        if (b.parts > most) b.parts = most;
-        if (b.parts < 1) b.parts = 1;
-    }
+    // (the same for a packed batch of equal lengths)
+    const int64_t most = rows * (H / G) / kMinPartRows, blocks = block_slots(rows, n_seqs, T, 1, block, true) * G;
+    b.parts = blocks > 0 ? ((bf16 ? 2 : 1) * kFill + blocks / 2) / blocks : 1;
+    if (b.parts > most) b.parts = most;
+    if (b.parts < 1) b.parts = 1;
     b.bytes = b.delta + (b.parts > 1 ? b.parts * rows * G * 2 * D * 4 : 0);
     return b;
 }

@@ -198,31 +198,6 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
         }
 }
 
-// grad_k and grad_v from their parts, in order.
-template <int D>
-__global__ __launch_bounds__(256) void attn_bwd_join_kernel(AttnBwdParams a) {
-    const AttnParams& p = a.f;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, item = i / (D / 2);   // (row, group); four values per thread
-    if (item >= p.rows * p.G) return;
-    const int64_t row = item / p.G;
-    const int g = (int)(item - row * p.G), d = (int)(i % (D / 2)) * 4;
-    if (p.cu && (row < attn_range(p.cu, p.rows, p.T, 0).start || row >= attn_range(p.cu, p.rows, p.T, p.n_seqs - 1).end)) return;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int part = 0; part < a.parts; ++part) {
-        float x[4];
-        load4(a.part + ((part * p.rows * p.G + item) * 2) * D + d, x);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += x[e];
-    }
-    if (d < D) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] *= p.scale;
-        store4((__bf16*)a.gk + row * a.gk_stride + (int64_t)g * D + d, s);
-    } else {
-        store4((__bf16*)a.gv + row * a.gv_stride + (int64_t)g * D + d - D, s);
-    }
-}
-
 // grad_q of 128 rows of one (sequence, group); leaves the rows' delta for the
 // blocks of keys, which run afterwards.
 template <int D>
@@ -355,7 +330,7 @@ static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
     attn_bwd_q_kernel<D><<<dim3((uint32_t)(a.f.slots * a.f.G)), BW_THREADS, 0, stream>>>(a);
     attn_bwd_kv_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G * a.parts)), BW_THREADS, 0, stream>>>(a);
     if (a.parts > 1)
-        attn_bwd_join_kernel<D><<<dim3((uint32_t)((a.f.rows * a.f.G * (D / 2) + 255) / 256)), 256, 0, stream>>>(a);
+        attn_bwd_join_kernel<__bf16, D><<<dim3((uint32_t)((a.f.rows * a.f.G * (D / 2) + 255) / 256)), 256, 0, stream>>>(a);
 }
 
 hipError_t launch_attn_bwd_bf16(const AttnBwdParams& a, hipStream_t stream) {

@@ -3,13 +3,15 @@
 //
 // P and dP are formed again from q, k, v, lse and grad_o, once by the blocks
 // of keys (grad_k, grad_v) and once by the blocks of rows (grad_q), so that
-// every sum stays in the registers of one wave: no atomics, no arrays of
-// partial sums, seven products where five would do.  Products that sum over
+// every sum stays in the registers of one wave: no atomics, seven products
+// where five would do.  Blocks of keys walk their rows in parts where there are
+// few of them; a third launch adds those in order.  Products that sum over
 // the rows take S = Q K^T, whose place in registers (key l & 15, rows
 // 4 (l >> 4) + i) is that of P^T as an operand of P^T dO; the one that sums
 // over the keys takes S^T = K Q^T.
-//   Bound as the forward pass is: 60 TFLOP/s of the formula's five products at
-// 2048 causal tokens, 16 heads of 128.
+//   Bound as the forward pass is: 63 TFLOP/s of the formula's five products (88
+// of the seven done) at 2048 causal tokens, 16 heads of 128: 390 us by the keys,
+// 290 by the rows.
 #include "kda_attn_mma.h"
 
 namespace kda {
@@ -96,11 +98,21 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
     __shared__ __attribute__((aligned(1024))) char lds[4 * 2 * HALF];
     static_assert(4 * 2 * 16 * (D + 4) * 4 <= (int)sizeof(lds), "");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, grp = lane >> 4;
-    const AttnPlace pl = attn_place(blockIdx.x, a.key_slots, p.G);
-    const AttnBlock b = attn_block(p, pl.item, 1, AB_BLOCK);
+    const AttnPlace pl = attn_place(blockIdx.x, a.key_slots * a.parts, p.G);
+    int64_t slot = pl.item / a.parts;
+    const int part = (int)(pl.item % a.parts);
+    if (!p.cu && p.causal) {   // the first blocks of all sequences, then the second ones: they have the most rows
+        const int64_t each = a.key_slots / p.n_seqs;
+        slot = (slot % p.n_seqs) * each + slot / p.n_seqs;
+    }
+    const AttnBlock b = attn_block(p, slot, 1, AB_BLOCK);
     if (b.j < 0) return;
     const int key = b.r0 + col;
-    const int32_t n_rows = b.tokens * p.hpg;
+    // rows [r_first, n_rows), of which this part takes whole steps of the four waves
+    const int32_t all_rows = b.tokens * p.hpg, r_all = p.causal ? (int32_t)((int64_t)b.r0 * p.hpg / 16 * 16) : 0;
+    const int64_t steps = ((int64_t)all_rows - r_all + 63) / 64;
+    const int32_t r_first = r_all + (int32_t)(steps * part / a.parts) * 64;
+    const int32_t r_end = r_all + (int32_t)(steps * (part + 1) / a.parts) * 64, n_rows = r_end < all_rows ? r_end : all_rows;
     const int64_t krow = b.start + (key < b.r1 ? key : b.r0);
     float k[S][4], v[S][4];
 #pragma unroll
@@ -145,7 +157,7 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
     for (int s = 0; s < S; ++s) g[0][s] = g[1][s] = f32x4{0.f, 0.f, 0.f, 0.f};
     const float c = p.scale * kLog2e;
     const int32_t from = p.causal ? key * p.hpg : 0, from_most = p.causal ? (b.r0 + 15) * p.hpg : 0;
-    const int32_t first = (p.causal ? (int32_t)((int64_t)b.r0 * p.hpg / 16 * 16) : 0) + 16 * wave;
+    const int32_t first = r_first + 16 * wave;
     if (first < n_rows) request(first, 0);
     for (int32_t r0 = first; r0 < n_rows; r0 += 64) {
         const int buf = ((r0 - first) >> 6) & 1;
@@ -159,13 +171,26 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
         const char *qs = own + buf * HALF, *gs = qs + Tile::BYTES;
         const float* stat = reinterpret_cast<const float*>(gs + Tile::BYTES);
         f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
+        // operands are read one product ahead, where the fences keep them
+        float zq[2][4], zg[2][4];
+        Tile::rows(qs, col, grp, 0, zq[0]);
+        Tile::rows(gs, col, grp, 0, zg[0]);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float z[4];
-            Tile::rows(qs, col, grp, s, z);
-            mma_k16<true, PLAIN>(x, z, k[s]);
-            Tile::rows(gs, col, grp, s, z);
-            mma_k16<true, PLAIN>(y, z, v[s]);
+            if (s + 1 < S) {
+                Tile::rows(qs, col, grp, s + 1, zq[(s + 1) & 1]);
+                Tile::rows(gs, col, grp, s + 1, zg[(s + 1) & 1]);
+            } else {
+                Tile::cols(qs, col, grp, 0, zq[0]);
+                Tile::cols(gs, col, grp, 0, zg[0]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x = mfma4f(zq[s & 1][e], k[s][e], x);
+                y = mfma4f(zg[s & 1][e], v[s][e], y);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         float lse[4], delta[4], w[4], ds[4];
         load4(stat + 4 * grp, lse);
@@ -180,11 +205,17 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
         }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float z[4];
-            Tile::cols(qs, col, grp, s, z);
-            mma_k16<true, PLAIN>(g[0][s], z, ds);
-            Tile::cols(gs, col, grp, s, z);
-            mma_k16<true, PLAIN>(g[1][s], z, w);
+            if (s + 1 < S) {
+                Tile::cols(qs, col, grp, s + 1, zq[(s + 1) & 1]);
+                Tile::cols(gs, col, grp, s + 1, zg[(s + 1) & 1]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[0][s] = mfma4f(zq[s & 1][e], ds[e], g[0][s]);
+                g[1][s] = mfma4f(zg[s & 1][e], w[e], g[1][s]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     const float* joint = join_waves<D, 2>(lds, g);
@@ -192,12 +223,18 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
     if (b.r0 + mine >= b.r1) return;
     float* tk = (float*)a.gk + (b.start + b.r0 + mine) * a.gk_stride + (int64_t)pl.g * D;
     float* tv = (float*)a.gv + (b.start + b.r0 + mine) * a.gv_stride + (int64_t)pl.g * D;
+    float scale = p.scale;
+    if (a.parts > 1) {
+        tk = a.part + (((part * p.rows + b.start + b.r0 + mine) * p.G + pl.g) * 2) * D;
+        tv = tk + D;
+        scale = 1.f;
+    }
 #pragma unroll
     for (int n = 0; n < D / 64; ++n) {
         float z[4];
         joint_sum<D, 2>(joint, 0, mine, 64 * n + d0, z);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] *= p.scale;
+        for (int e = 0; e < 4; ++e) z[e] *= scale;
         store4(tk + 64 * n + d0, z);
         joint_sum<D, 2>(joint, 1, mine, 64 * n + d0, z);
         store4(tv + 64 * n + d0, z);
@@ -277,13 +314,25 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_ke
         }
         const char *ks = own + buf * HALF, *vs = ks + Tile::BYTES;
         f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
+        // (operands one product ahead, as above)
+        float zk[2][4], zv[2][4];
+        Tile::rows(ks, col, grp, 0, zk[0]);
+        Tile::rows(vs, col, grp, 0, zv[0]);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float z[4];
-            Tile::rows(ks, col, grp, s, z);
-            mma_k16<true, PLAIN>(x, z, q[s]);
-            Tile::rows(vs, col, grp, s, z);
-            mma_k16<true, PLAIN>(y, z, go[s]);
+            if (s + 1 < S) {
+                Tile::rows(ks, col, grp, s + 1, zk[(s + 1) & 1]);
+                Tile::rows(vs, col, grp, s + 1, zv[(s + 1) & 1]);
+            } else {
+                Tile::cols(ks, col, grp, 0, zk[0]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x = mfma4f(zk[s & 1][e], q[s][e], x);
+                y = mfma4f(zv[s & 1][e], go[s][e], y);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         float ds[4];
 #pragma unroll
@@ -293,9 +342,10 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_ke
         }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float z[4];
-            Tile::cols(ks, col, grp, s, z);
-            mma_k16<true, PLAIN>(g[0][s], z, ds);
+            if (s + 1 < S) Tile::cols(ks, col, grp, s + 1, zk[(s + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            mma_k16<true, PLAIN>(g[0][s], zk[s & 1], ds);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     const float* joint = join_waves<D, 1>(lds, g);
@@ -316,7 +366,9 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_ke
 template <int D>
 static void run_bwd(const AttnBwdParams& a, hipStream_t stream) {
     attn_bwd_q_f32_kernel<D><<<dim3((uint32_t)(a.f.slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
-    attn_bwd_kv_f32_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G)), AB_THREADS, 0, stream>>>(a);
+    attn_bwd_kv_f32_kernel<D><<<dim3((uint32_t)(a.key_slots * a.f.G * a.parts)), AB_THREADS, 0, stream>>>(a);
+    if (a.parts > 1)
+        attn_bwd_join_kernel<float, D><<<dim3((uint32_t)((a.f.rows * a.f.G * (D / 2) + 255) / 256)), 256, 0, stream>>>(a);
 }
 
 hipError_t launch_attn_bwd_f32(const AttnBwdParams& a, hipStream_t stream) {

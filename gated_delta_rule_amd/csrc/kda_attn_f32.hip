@@ -11,8 +11,7 @@
 // tile's rows are requested before the products of this one.
 //   Bound by the float32 matrix instructions and the LDS reads in front of them:
 // 94 TFLOP/s at 2048 causal tokens, 16 heads of 128 (182 us; 195 with operands
-// read as they are needed), where a large
-// product reaches 153.
+// read as they are needed), where a large product reaches 153.
 #include "kda_attn_tile.h"
 
 namespace kda {

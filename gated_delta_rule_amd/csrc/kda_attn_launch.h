@@ -65,7 +65,7 @@ struct AttnBwdParams {
     void* gv;
     float* delta;            // [rows, H]: grad_o . o
     float* part;             // parts > 1: [parts, rows, G, 2, D] sums of grad_k and grad_v
-    int32_t parts;           // of a block of keys' rows, each its own workgroup (bf16 kernel)
+    int32_t parts;           // of a block of keys' rows, each its own workgroup
     int64_t gq_stride, gk_stride, gv_stride;
     int64_t key_slots;       // blocks of keys per group
     int32_t zero_rest;       // KDA_FRESH_*: these outputs' rows of no sequence become zero

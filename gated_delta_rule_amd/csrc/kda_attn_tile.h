@@ -180,4 +180,29 @@ __device__ __forceinline__ AttnPlace attn_place(uint32_t w, int64_t items, int32
     return a;
 }
 
+// grad_k and grad_v from their parts, in order.
+template <typename OutT, int D>
+__global__ __launch_bounds__(256) void attn_bwd_join_kernel(AttnBwdParams a) {
+    const AttnParams& p = a.f;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, item = i / (D / 2);   // (row, group); four values per thread
+    if (item >= p.rows * p.G) return;
+    const int64_t row = item / p.G;
+    const int g = (int)(item - row * p.G), d = (int)(i % (D / 2)) * 4;
+    if (p.cu && (row < attn_range(p.cu, p.rows, p.T, 0).start || row >= attn_range(p.cu, p.rows, p.T, p.n_seqs - 1).end)) return;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int part = 0; part < a.parts; ++part) {
+        float x[4];
+        load4(a.part + ((part * p.rows * p.G + item) * 2) * D + d, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += x[e];
+    }
+    if (d < D) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] *= p.scale;
+        store4((OutT*)a.gk + row * a.gk_stride + (int64_t)g * D + d, s);
+    } else {
+        store4((OutT*)a.gv + row * a.gv_stride + (int64_t)g * D + d - D, s);
+    }
+}
+
 }  // namespace kda

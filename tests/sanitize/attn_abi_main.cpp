@@ -103,7 +103,7 @@ static void backward(const AttnBwdParams& a, bool bf16) {
     const big block = bf16 ? kAttnBlockBf16 : kAttnBwdBlockF32;
     blocks(p, p.slots, p.hpg, block);
     blocks(p, a.key_slots, 1, block);
-    CHECK(a.parts >= 1 && (bf16 || a.parts == 1));
+    CHECK(a.parts >= 1);
     in_ws(a.delta, (big)p.rows * p.H * 4);
     threads((big)p.slots * p.G, 256);
     threads((big)a.key_slots * p.G * a.parts, 256);
