@@ -122,11 +122,13 @@ PagedPlan paged_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t
 
 // The backward pass cuts the rows that a block of keys walks into parts, so
 // that there are about 1024 workgroups (twice as many as run at once: the
-// first keys' blocks walk the most rows) of at least 256 rows each; the parts'
+// first keys' blocks walk the most rows) of at least 256 rows of an average
+// sequence each (4 x 200 tokens 43 us, 53 with 256 of the whole batch); the parts'
 // sums are added by another launch.  32 heads of 128 on 8, with 1 / 2 / 4 / 8 / 16
 // parts, us: 512 tokens 112 / 77 / 60 / 51 / 51, 2048 tokens 407 / 256 / 189 / 186 / 246,
 // 4096 tokens 878 / 611 / 542 / 585 / 681, 2 x 4096 1150 / 1013 / 1034 / 1138 / 1352.
-// In float32, whose blocks have 16 keys, about 512 workgroups: 1024 tokens, 16
+// In float32, whose blocks have 16 keys, about 512 workgroups of at least 512
+// rows (a launch more costs as much as it saves below): 1024 tokens, 16
 // heads of 128 on 4, 196 us, 206 and 232 with twice and four times as many; 385
 // of each of 2, 32 heads on 4, 158, 162 and 183; before blocks were cut 279 and
 // 224 (operands read one product ahead included).
@@ -141,7 +143,8 @@ BwdPlan bwd_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t H, 
     b.delta = (rows * H * 4 + 15) / 16 * 16;
     b.parts = 1;
     // (the same for a packed batch of equal lengths)
-    const int64_t most = rows * (H / G) / kMinPartRows, blocks = block_slots(rows, n_seqs, T, 1, block, true) * G;
+    const int64_t least = (bf16 ? 1 : 2) * kMinPartRows, most = rows * (H / G) / (least * (n_seqs > 0 ? n_seqs : 1));
+    const int64_t blocks = block_slots(rows, n_seqs, T, 1, block, true) * G;
     b.parts = blocks > 0 ? ((bf16 ? 2 : 1) * kFill + blocks / 2) / blocks : 1;
     if (b.parts > most) b.parts = most;
     if (b.parts < 1) b.parts = 1;
