@@ -135,6 +135,8 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
         const auto grs = make_rsrc((const float*)a.go + (b.start + t0) * gstride + head * D, 0x40000000);
         const auto lrs = make_rsrc(p.lse + (b.start + t0) * p.H + head, 0x40000000);
         const auto drs = make_rsrc(a.delta + (b.start + t0) * p.H + head, 0x40000000);
+        settle(qrs, grs);
+        settle(lrs, drs);
         const uint32_t to = lds0 + buf * HALF;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
@@ -290,6 +292,7 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_ke
         const int32_t left = most - key < 16 ? most - key : 16;
         const auto krs = make_rsrc(keys.k + key * keys.k_stride, ((left - 1) * (int)keys.k_stride + D) * 4);
         const auto vrs = make_rsrc(keys.v + key * keys.v_stride, ((left - 1) * (int)keys.v_stride + D) * 4);
+        settle(krs, vrs);
         const uint32_t to = lds0 + buf * HALF;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {

@@ -47,6 +47,13 @@ __device__ __forceinline__ T* in_scalars(T* p) {
     return (T*)((uint64_t)hi << 32 | lo);
 }
 
+// The same wait states before a buffer's first load: its words may have just
+// come out of vector registers that the compiler keeps scalars in.
+__device__ __forceinline__ void settle(__amdgpu_buffer_rsrc_t a) { asm volatile("s_nop 4" :: "s"(a) : "memory"); }
+__device__ __forceinline__ void settle(__amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b) {
+    asm volatile("s_nop 4" :: "s"(a), "s"(b) : "memory");
+}
+
 // 16 bytes per lane from a buffer to LDS at `to` + 16 lane.  Written out
 // because the compiler would wait for these before every LDS read.
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t to) {
