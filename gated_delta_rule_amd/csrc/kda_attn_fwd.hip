@@ -295,7 +295,7 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
 // that are cut are joined by a second launch.  Neighbouring pieces go to one
 // XCD, for their common keys and values.
 //   (1024 new tokens in all of two requests of 8k to 32k tokens, 32 heads of 128
-// on 8: 389 us and 21 to join.  When both took 435, the same number of parts for
+// on 8: 391 us and 17 to join.  When both took 435, the same number of parts for
 // every block took 774 us with 512 workgroups or more in all, 467 with 1024, 430
 // with 2048; but 256 tokens over 32k 165, 179 and 216, 163 here.)
 struct FwdLine {
