@@ -119,6 +119,12 @@ def test_paged_refusals(lib):
     assert lib.kda_attn_paged_workspace_bytes(0, 2, 3, 4, 2, 64, 17, 1000, 0) == 0
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_a_scale_that_is_no_number_is_refused(lib, scale):
+    for f in (fwd, bwd, paged):
+        assert f(lib, sc=scale) == SHAPE
+
+
 def append(lib, **kw):
     d = dict(k=ptr("k"), ks=128, v=ptr("v"), vs=128, dt=0, kp=ptr("kp"), vp=ptr("vp"), ps=2 * 16 * 64, np=9, pg=16,
              tab=ptr("table"), mp=4, len=ptr("len"), cu=None, n=2, T=3, G=2, D=64, st=None)
