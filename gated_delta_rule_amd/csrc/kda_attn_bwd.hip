@@ -31,7 +31,7 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
     constexpr int ROWB = 2 * D, UNITS = D / 8, TILE = BW_STEP * ROWB, LOADS = D / 32, RPL = 1024 / ROWB;
     constexpr int S = D / 16, O = D / 32;
     __shared__ __attribute__((aligned(1024))) char lds[4 * TILE];   // q, q, grad_o, grad_o
-    __shared__ __attribute__((aligned(16))) float stat[2][2][BW_STEP];   // of each row: lse in base 2, delta
+    __shared__ __attribute__((aligned(16))) float stat[2][2][BW_STEP];   // of each row: lse in base 2, -delta
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const AttnPlace pl = attn_place(attn_zigzag(blockIdx.x, gridDim.x, p.G), a.key_slots * a.parts, p.G);
     int64_t slot = pl.item / a.parts;
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
         const int buf = ((r0 - r_first) / BW_STEP) & 1;
         if (tid < 2 * BW_STEP) {   // (a row that is not there has weight e^{-inf})
             const int r = tid & (BW_STEP - 1);
-            stat[buf][tid / BW_STEP][r] = tid < BW_STEP ? (r0 + r < n_rows ? mine * kLog2e : INFINITY) : mine;
+            stat[buf][tid / BW_STEP][r] = tid < BW_STEP ? (r0 + r < n_rows ? mine * kLog2e : INFINITY) : -mine;
         }
         tiles_barrier();
         if (r0 + BW_STEP < n_rows) request(r0 + BW_STEP, buf ^ 1);
@@ -145,18 +145,20 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
                 for (int i = 0; i < O; ++i) gv[i] = mfma32x32(read_cols(gt + s * 16 * ROWB, cat, i), pw, gv[i]);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            f32x16 y = zero16();
+            f32x16 y;   // dP - delta
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) {
+                const f32x4 less = *reinterpret_cast<const f32x4*>(&stat[buf][1][32 * rt + 8 * e4 + 4 * half]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[4 * e4 + i] = less[i];
+            }
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 y = mfma32x32(read_rows(gt, rat ^ (32 * s)), v[s], y);
                 if (s % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-                const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[buf][1][32 * rt + 8 * e4 + 4 * half]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 * e4 + i] *= y[4 * e4 + i] - delta[i];
-            }
+            for (int e = 0; e < 16; ++e) x[e] *= y[e];
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
