@@ -202,7 +202,11 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
 }
 
 // grad_q of 128 rows of one (sequence, group); leaves the rows' delta for the
-// blocks of keys, which run afterwards.
+// blocks of keys, which run afterwards.  A row's dS add up to 0 with the exact
+// delta; with the one from o, which is rounded, to the difference.  So the
+// blocks of keys get delta + sum_j dS_ij: grad_k is off by 2.4e-3 of its norm
+// instead of 2.8e-3 for sequences of 64 tokens (the rounding of dS and its own
+// make up 2.35e-3), for 1.3% of the backward pass's time.
 template <int D>
 __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams a) {
     const AttnParams& p = a.f;
@@ -252,10 +256,10 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
         }
     }
     delta += swap_halves(delta);
-    if (half == 0 && valid) a.delta[at] = delta;
     asm volatile("" : "+v"(lse2), "+v"(delta));   // (arrive, too)
     const float c = p.scale * kLog2e;
     f32x16 gq[O];
+    float rest[4] = {0.f, 0.f, 0.f, 0.f};   // sums of the row's dS
 #pragma unroll
     for (int i = 0; i < O; ++i) gq[i] = zero16();
 
@@ -309,6 +313,8 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
                     x[e] = key0 + 32 * kt + 8 * (e >> 2) + 4 * half + (e & 3) < sees ? x[e] : 0.f;
             }
 #pragma unroll
+            for (int e = 0; e < 16; ++e) rest[e & 3] += x[e];
+#pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const bf16x8 ds = as_operand(x, s);
 #pragma unroll
@@ -316,7 +322,10 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
             }
         }
     }
+    float off = (rest[0] + rest[1]) + (rest[2] + rest[3]);
+    off += swap_halves(off);
     if (!valid) return;
+    if (half == 0) a.delta[at] = delta + off;
     __bf16* to = (__bf16*)a.gq + (b.start + t) * a.gq_stride + (int64_t)head * D + 4 * half;
 #pragma unroll
     for (int i = 0; i < O; ++i)

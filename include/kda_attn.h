@@ -45,7 +45,8 @@
  *   - Numerics: scores, softmax statistics and sums in float32.  With
  *     KDA_BF16 the weights (and in the backward pass the score gradients)
  *     are rounded to bf16 once, as operands of the matrix cores: a half step
- *     of the output's own type.  With KDA_F32 nothing is rounded below
+ *     of the output's own type.  grad_q's delta is that of o as it was rounded,
+ *     grad_k's is exact to float32.  With KDA_F32 nothing is rounded below
  *     float32.
  */
 #ifndef KDA_ATTN_H_

@@ -191,6 +191,28 @@ def test_scales_of_prompts(scale, dtype):
         check("gradient", x[0], torch.from_numpy(r).cuda(), torch.from_numpy(e).cuda(), dtype)
 
 
+@pytest.mark.parametrize("T", [8, 50, 150])
+def test_grad_k_does_not_depend_on_the_rounding_of_o(T):
+    # values of 128 and a little: bf16 holds o to 0.5 only, and delta = grad_o . o to about 0.15 |grad_o|
+    g = torch.Generator(device="cuda").manual_seed(T)
+    D = 64
+    q, k, go = (torch.randn(1, T, 1, D, generator=g, device="cuda").to(BF16) for _ in range(3))
+    v = (128 + torch.randint(0, 4, (1, T, 1, D), generator=g, device="cuda")).to(BF16)
+    o, lse = kda.attn_fwd(q, k, v)
+    gk = kda.attn_bwd(q, k, v, o, lse, go)[1][0, :, 0].double()
+    q, k, v, go = (t[0, :, 0].double() for t in (q, k, v, go))
+    late = torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1)
+    x = (q @ k.T.contiguous() * D ** -0.5).masked_fill(late, -float("inf"))
+    P, dP = torch.softmax(x, 1), go @ v.T.contiguous()
+    dS = P * (dP - (P * dP).sum(1, keepdim=True))
+    # P: errors of scores and lse in float32; dP and the sum of dS: of products of 64 float32 terms and sums over the row
+    score = D ** -0.5 * (q.abs() @ k.abs().T.contiguous()).amax(1) * (D + 8) * U
+    part = (go.abs() @ v.abs().T.contiguous()).amax(1) * (2 * D + T + 16) * U
+    err = dS.abs() * (2.0 ** -8 + (4 * score + (T + 40) * U)[:, None]) + 2 * P * part[:, None]
+    ref = D ** -0.5 * (dS.T.contiguous() @ q)
+    check("grad_k", gk, ref, D ** -0.5 * (err.T.contiguous() @ q.abs()), BF16)
+
+
 @pytest.mark.parametrize("dtype,n,T,H,G,D", [(BF16, 1, 5000, 4, 1, 128), (BF16, 3, 1111, 8, 8, 64), (F32, 1, 2100, 4, 2, 128)])
 def test_long_prompts(dtype, n, T, H, G, D):
     g = torch.Generator(device="cuda").manual_seed(1)
