@@ -346,7 +346,7 @@ __global__ __launch_bounds__(PG_THREADS) void kv_fork_plan_kernel(PagesParams p,
         const int32_t need = f.from >= 0;
         int32_t total, served;
         const int64_t at = upto + block_before(need, s, total);
-        const bool ok = f.go && at + need <= n_free;
+        const bool ok = f.go && (need == 0 || at + need <= n_free);
         upto += total;
         off[tid] = block_before(ok ? need : 0, s, served);
         if (!ok || !need) f.from = -1;

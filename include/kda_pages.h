@@ -55,8 +55,9 @@ int kda_kv_resize(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t
  * not full is copied, so that both can be appended to.  Copies go to pages
  * that were free before the call, in the order of i.  ok[i] is 1, or 0 where
  * src[i] or dst[i] is no slot, an earlier i has the same dst, or no free page
- * was left for the copy (counting those before it that needed one): dst then
- * stays as it is.  src[i] == dst[i] changes nothing.
+ * was left for the copy: dst then stays as it is.  A pair without a copy (its
+ * source ends with a full page or holds nothing) needs no free page.  src[i] ==
+ * dst[i] changes nothing.
  *   src, dst, ok int32 [n]; ok may be NULL.  n <= KDA_PAGES_MAX_SLOTS.
  *   pages[t], page_bytes[t], page_stride_bytes[t], t < n_tensors <=
  *   KDA_PAGES_MAX_TENSORS: host arrays of the tensors that hold the pages'

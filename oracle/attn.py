@@ -180,7 +180,7 @@ class Pool:
             row = self.table[a][:self.used(length)]
             copy = a != d and length % self.page != 0 and self._real(row[-1])
             needed += copy
-            ok.append(int(needed <= n_free))
+            ok.append(int(not copy or needed <= n_free))
             if ok[-1] and a != d:
                 if copy:
                     todo.append((d, length, row[:-1], row[-1], free.pop(0)))

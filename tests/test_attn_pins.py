@@ -102,3 +102,14 @@ def test_pool_by_hand():
     assert p.resize([0, 40, 17]) == [1, 1, 1] and p.table[1] == [2, 1, 4] and p.refs == [1, 1, 1, 1, 1]
     assert p.resize([0, 0, 17]) == [1, 1, 1]
     assert p.compact() == ([[-1] * 3, [-1] * 3, [0, 1, -1]], [1, 1, 0, 0, 0], 2) and p.data[1] == "b"
+
+
+def test_pairs_that_copy_nothing_need_no_page():
+    table = [[0, -1], [1, -1], [2, 3], [-1, -1], [-1, -1], [4, 5]]
+    p = O.Pool(table, [10, 16, 32, 0, 0, 20], [1] * 6, 16, "abcdef")
+    assert p.fork([0, 1, 0, 5, 3], [3, 4, 5, 5, 2]) == [0, 1, 0, 0, 1]
+    assert p.table == [[0, -1], [1, -1], [-1, -1], [-1, -1], [1, -1], [4, 5]]
+    assert p.lengths == [10, 16, 0, 0, 16, 20] and p.refs == [1, 2, 0, 0, 1, 1] and p.data == list("abcdef")
+    assert p.fork([0, 5, 0, 5, 1], [2, 3, 4, 5, 1]) == [1, 1, 0, 1, 1]
+    assert p.table == [[0, -1], [1, -1], [2, -1], [4, 3], [1, -1], [4, 5]]
+    assert p.lengths == [10, 16, 10, 20, 16, 20] and p.refs == [1, 2, 1, 1, 2, 1] and p.data == list("abafef")

@@ -177,3 +177,24 @@ def test_data_with_strides_and_odd_sizes():
         want[h, 0] = want[p, 0]
         want[h, 1, :4104] = want[p, 1, :4104]
     assert torch.equal(pool, want) and t.tolist() == [[1, 2], [1, 0]] and r.tolist() == [1, 2, 1, 0, 0, 0]
+
+
+def test_pairs_that_copy_nothing_need_no_page():
+    # all pages are held: one open source, one that ends with its page, one without tokens
+    table = ints([[0, -1], [1, -1], [2, 3], [-1, -1], [-1, -1], [4, 5]])
+    lengths, refs = ints([10, 16, 32, 0, 0, 20]), ints([1] * 6)
+    pages = torch.arange(6 * 4, device="cuda", dtype=torch.float32).view(6, 4)
+    before = pages.clone()
+    ok = kda.kv_fork(table, lengths, refs, ints([0, 1, 0, 5, 3]), ints([3, 4, 5, 5, 2]), pages, 16)
+    # the copy of page 0 finds none left, twice (the second time for slot 5); the full page is shared; slot 2 becomes empty
+    assert ok.tolist() == [0, 1, 0, 0, 1]
+    assert table.tolist() == [[0, -1], [1, -1], [-1, -1], [-1, -1], [1, -1], [4, 5]]
+    assert lengths.tolist() == [10, 16, 0, 0, 16, 20] and refs.tolist() == [1, 2, 0, 0, 1, 1]
+    assert torch.equal(pages, before)
+    # two pages are free now: one copy, a slot onto itself behind the one that finds none
+    ok = kda.kv_fork(table, lengths, refs, ints([0, 5, 0, 5, 1]), ints([2, 3, 4, 5, 1]), pages, 16)
+    assert ok.tolist() == [1, 1, 0, 1, 1]
+    assert table.tolist() == [[0, -1], [1, -1], [2, -1], [4, 3], [1, -1], [4, 5]]
+    assert lengths.tolist() == [10, 16, 10, 20, 16, 20] and refs.tolist() == [1, 2, 1, 1, 2, 1]
+    before[2], before[3] = before[0], before[5]
+    assert torch.equal(pages, before)
