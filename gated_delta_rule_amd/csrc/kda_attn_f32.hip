@@ -163,14 +163,14 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
         }
         return;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = attn_inverse(l);
     float* orow = (float*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const float y[4] = {o[s][0] * inv, o[s][1] * inv, o[s][2] * inv, o[s][3] * inv};
         store4(orow + 16 * s + 4 * grp, y);
     }
-    if (p.lse && grp == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && grp == 0) p.lse[(b.start + t) * p.H + head] = attn_lse(m, l);
 }
 
 // The parts of a split block: o = sum_s e^{m_s - m} o_s / sum_s e^{m_s - m} l_s,
@@ -199,12 +199,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
         o0 += w * at[lane];
         if constexpr (D == 128) o1 += w * at[64 + lane];
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = attn_inverse(l);
     const int row = b.r0 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
     float* orow = (float*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
     orow[lane] = o0 * inv;
     if constexpr (D == 128) orow[64 + lane] = o1 * inv;
-    if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = attn_lse(m, l);
 }
 
 template <int D>

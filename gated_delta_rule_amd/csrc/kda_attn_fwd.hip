@@ -264,7 +264,7 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
         }
         return;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = attn_inverse(l);
     __bf16* orow = (__bf16*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
 #pragma unroll
     for (int i = 0; i < O; ++i)
@@ -273,7 +273,7 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
             const float y[4] = {o[i][4 * k] * inv, o[i][4 * k + 1] * inv, o[i][4 * k + 2] * inv, o[i][4 * k + 3] * inv};
             store4(orow + 32 * i + 8 * k + 4 * half, y);
         }
-    if (p.lse && half == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && half == 0) p.lse[(b.start + t) * p.H + head] = attn_lse(m, l);
 }
 
 template <int D, bool PAGED>
@@ -450,12 +450,12 @@ __global__ __launch_bounds__(256) void attn_fwd_line_join_kernel(AttnParams p) {
 #pragma unroll
             for (int e = 0; e < D / 64; ++e) o[e] = o[e] * f0 + from[64 * e + lane] * f1;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = attn_inverse(l);
         const int row = b.r0 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
         __bf16* orow = (__bf16*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
 #pragma unroll
         for (int e = 0; e < D / 64; ++e) orow[64 * e + lane] = (__bf16)(o[e] * inv);
-        if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (p.lse && lane == 0) p.lse[(b.start + t) * p.H + head] = attn_lse(m, l);
     }
 }
 

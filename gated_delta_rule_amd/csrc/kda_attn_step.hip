@@ -368,7 +368,7 @@ __global__ __launch_bounds__(SP_THREADS, (StepTile<InT, D>::PER_UNIT)) void attn
                 sl += w[v] * ml[v][r][0];
             }
             const StepRow x = step_row(p, qr, len, g, 16 * rt + r);
-            const float inv = !whole ? 1.f : sl > 0.f ? 1.f / sl : 0.f;
+            const float inv = !whole ? 1.f : attn_inverse(sl);
             float* part = step_part<D, RT>(p, blockIdx.x + unit, 16 * rt + r);
 #pragma unroll
             for (int k = 0; k < D / 64; ++k) {
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(SP_THREADS, (StepTile<InT, D>::PER_UNIT)) void attn
                     part[D] = sl;
                     part[D + 1] = top;
                 } else if (p.lse) {
-                    p.lse[x.at * p.H + x.head] = sl > 0.f ? (top + log2f(sl)) * kLn2 : -INFINITY;
+                    p.lse[x.at * p.H + x.head] = attn_lse(top, sl);
                 }
             }
         }
@@ -475,11 +475,11 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void attn_step_join_k
             for (int e = 0; e < E; ++e) o[e] += f * joint[v][64 * e + lane];
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = attn_inverse(l);
     InT* orow = (InT*)p.o + (x.at * p.H + x.head) * D;
 #pragma unroll
     for (int e = 0; e < E; ++e) orow[64 * e + lane] = (InT)(o[e] * inv);
-    if (p.lse && lane == 0) p.lse[x.at * p.H + x.head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[x.at * p.H + x.head] = attn_lse(m, l);
 }
 
 // Waves for a row's parts: by how many parts a unit has, at the most.

@@ -131,6 +131,10 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)x >> 32));
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
+// 1 / l and lse of a row with the sum of weights l over its maximum m (base 2); a
+// row that sees nothing has l = 0, and a NaN (from q or k) stays one.
+__device__ __forceinline__ float attn_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 // Over the four 16-lane groups of a wave (lanes with equal l & 15).
 __device__ __forceinline__ float groups_max(float x) {
     x = fmaxf(x, __shfl_xor(x, 16));

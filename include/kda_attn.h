@@ -13,7 +13,8 @@
  *     o_i   = sum_j e^{s_ij - lse_i} v_j
  *
  * With causal != 0 a row sees the tokens of its sequence up to its own; with
- * 0 all of them.  A row that sees no token has o = 0 and lse = -infinity.
+ * 0 all of them.  A row that sees no token has o = 0 and lse = -infinity; one
+ * whose query, or a key that it sees, holds a NaN has NaN in both.
  *
  * Common contract (beside that of kda.h, which holds here too: device
  * pointers, 16-byte alignment (lse, cu_seqlens, table, lengths 4-byte),

@@ -482,3 +482,44 @@ def test_empty_batches(dtype):
     assert (o == 0).all() and torch.isneginf(lse).all()
     o, lse = kda.attn_paged_fwd(torch.ones(5, 40, 4, 64, dtype=dtype, device="cuda"), c.kp, c.vp, c.table, c.lengths)
     assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+# held, new, H, G, D, page: steps in one piece and cut, chunks taken whole, cut and in parts
+NAN_ROWS = [([40, 7], [2, 2], 4, 2, 64, 16), ([9000], [1], 8, 2, 128, 64), ([9000, 300], [4, 4], 64, 4, 64, 64), ([300, 80], [70, 70], 4, 2, 64, 16),
+            ([20000], [150], 8, 2, 128, 16)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", NAN_ROWS)
+def test_lse_says_nan_beside_a_nan(case, dtype):
+    """A NaN in a query, or in a key that it sees, is no row that sees nothing."""
+    held, new, H, G, D, page = case
+    c, n, T = Cache(held, G, D, page, dtype), len(held), new[0]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    q = torch.randn(n, T, H, D, generator=g, device="cuda").to(dtype)
+    bad = torch.zeros(n, T, H, dtype=torch.bool, device="cuda")
+    bad[0, T // 2, H - 1] = bad[n - 1, T - 1, 0] = True
+    refs = [exact(q[b], *c.keys(b), held[b] - T, D ** -0.5, dtype) for b in range(n)]
+    q[bad] = float("nan")
+    o, lse = kda.attn_paged_fwd(q, c.kp, c.vp, c.table, c.lengths)
+    assert torch.equal(torch.isnan(lse), bad) and torch.equal(torch.isnan(o).all(-1), bad)
+    for b, (ref, eo, lref, el) in enumerate(refs):
+        check("o", o[b][~bad[b]], ref[~bad[b]], eo[~bad[b]], dtype)
+        check("lse", lse[b][~bad[b]], lref[~bad[b]], el[~bad[b]], F32)
+    # one value of the first key of request 0, group 0
+    c.kp[c.table[0, 0].long(), 0, 0, D - 1] = float("nan")
+    o, lse = kda.attn_paged_fwd(q, c.kp, c.vp, c.table, c.lengths)
+    bad[0, :, :H // G] = True
+    assert torch.equal(torch.isnan(lse), bad) and torch.equal(torch.isnan(o).all(-1), bad)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_lse_of_a_prompt_says_nan_beside_a_nan(dtype):
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q, k, v = (torch.randn(2, 150, n, 64, generator=g, device="cuda").to(dtype) for n in (4, 2, 2))
+    q[0, 30, 1, 5], k[1, 100, 1, 9] = float("nan"), float("nan")
+    bad = torch.zeros(2, 150, 4, dtype=torch.bool, device="cuda")
+    bad[0, 30, 1] = bad[1, 100:, 2:] = True
+    o, lse = kda.attn_fwd(q, k, v)
+    assert torch.equal(torch.isnan(lse), bad) and torch.equal(torch.isnan(o).all(-1), bad)
+    assert not torch.isinf(lse).any()
