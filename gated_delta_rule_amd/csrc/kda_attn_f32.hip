@@ -53,8 +53,38 @@ struct KeyStage {
     }
 };
 
+// The rows of this wave that `odds` names (by their lanes) once more (attn_row_again), over what has been written of them.
 template <int D, bool PAGED>
-__global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) {
+__device__ __forceinline__ void f32_again(const AttnBlock& b, int g, uint64_t odds, int64_t slot, int split) {
+    const AttnParams& p = attn_params_again();
+    if (!p.causal) return;
+    const int lane = thread_again() & 63, wave = thread_again() >> 6;
+    const int32_t len = PAGED ? attn_length(p, b.n) : b.tokens, first = len - b.tokens, most = first + (b.r1 - 1) / p.hpg + 1;
+    const int32_t tiles = most > 0 ? (most + AF_KEYS - 1) / AF_KEYS : 0;
+    const int32_t t0 = (int32_t)((int64_t)tiles * split / p.splits), t1 = (int32_t)((int64_t)tiles * (split + 1) / p.splits);
+    const int32_t k1 = t1 * AF_KEYS < most ? t1 * AF_KEYS : most;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (written)
+    odds |= odds >> 32;
+    for (uint32_t left = (uint32_t)(odds | odds >> 16) & 0xffff; left; left &= left - 1) {
+        const int r = __builtin_ctz(left), row = b.r0 + wave * 16 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
+        float y[D / 64], m, l;
+        if (!attn_row_again<float, D, PAGED>(p, b.n, b.start, g, b.start + t, head, t0 * AF_KEYS, first + t + 1, k1, y, m, l)) continue;
+        const float inv = attn_inverse(l);
+        float* to = p.part + (((slot * p.G + g) * p.splits + split) * AF_BLOCK + wave * 16 + r) * (D + 2);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+            if (p.splits > 1) to[64 * e + lane] = y[e];
+            else ((float*)p.o)[((b.start + t) * p.H + head) * D + 64 * e + lane] = y[e] * inv;
+        }
+        if (p.splits > 1 && lane == 0) {
+            to[D] = l;
+            to[D + 1] = m;
+        }
+    }
+}
+
+template <int D, bool PAGED>
+__global__ __launch_bounds__(AF_THREADS, D == 64 ? 4 : 1) void attn_fwd_f32_kernel(AttnParams p) {
     constexpr int PITCH = D + 4, S = D / 16;
     __shared__ __attribute__((aligned(16))) float ks[AF_KEYS * PITCH], vs[AF_KEYS * PITCH];
     __shared__ uint8_t there[AF_KEYS];
@@ -150,8 +180,13 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
         }
     }
     l = groups_sum(l);
-    if (!valid) return;
-    if (p.splits > 1) {
+    float odd = 0.f;   // NaN if a sum is not finite
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd = fmaf(o[s][i], 0.f, odd);
+    const uint64_t odds = __ballot(valid && odd != 0.f && l - l == 0.f);
+    if (valid && p.splits > 1) {
         float* to = p.part + (((slot * p.G + pl.g) * p.splits + split) * AF_BLOCK + (row - b.r0)) * (D + 2);
 #pragma unroll
         for (int s = 0; s < S; ++s)
@@ -161,16 +196,17 @@ __global__ __launch_bounds__(AF_THREADS) void attn_fwd_f32_kernel(AttnParams p) 
             to[D] = l;
             to[D + 1] = m;
         }
-        return;
-    }
-    const float inv = attn_inverse(l);
-    float* orow = (float*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
+    } else if (valid) {
+        const float inv = attn_inverse(l);
+        float* orow = (float*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const float y[4] = {o[s][0] * inv, o[s][1] * inv, o[s][2] * inv, o[s][3] * inv};
-        store4(orow + 16 * s + 4 * grp, y);
+        for (int s = 0; s < S; ++s) {
+            const float y[4] = {o[s][0] * inv, o[s][1] * inv, o[s][2] * inv, o[s][3] * inv};
+            store4(orow + 16 * s + 4 * grp, y);
+        }
+        if (p.lse && grp == 0) p.lse[(b.start + t) * p.H + head] = attn_lse(m, l);
     }
-    if (p.lse && grp == 0) p.lse[(b.start + t) * p.H + head] = attn_lse(m, l);
+    if (odds) f32_again<D, PAGED>(b, pl.g, odds, slot, split);
 }
 
 // The parts of a split block: o = sum_s e^{m_s - m} o_s / sum_s e^{m_s - m} l_s,

@@ -44,6 +44,36 @@ __device__ __forceinline__ int32_t fwd_steps(const AttnParams& p, const AttnBloc
     return most > 0 ? (most + FW_KEYS - 1) / FW_KEYS : 0;
 }
 
+// The rows of this wave that `odds` names once more (attn_row_again), over what has been written of them.
+template <int D, bool PAGED>
+__device__ __forceinline__ void fwd_again(const AttnBlock& b, int g, uint32_t odds, int32_t t0, int32_t t1, float* part) {
+    const AttnParams& p = attn_params_again();
+    if (!p.causal) return;
+    const int lane = thread_again() & 63, wave = thread_again() >> 6;
+    int32_t len, most;
+    fwd_steps<PAGED>(p, b, len, most);
+    const int32_t k1 = t1 * FW_KEYS < most ? t1 * FW_KEYS : most;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (written)
+    for (; odds; odds &= odds - 1) {
+        const int r = __builtin_ctz(odds), row = b.r0 + wave * 32 + r, t = row / p.hpg, head = g * p.hpg + row - t * p.hpg;
+        float y[D / 64], m, l;
+        if (!attn_row_again<__bf16, D, PAGED>(p, b.n, b.start, g, b.start + t, head, t0 * FW_KEYS, len - b.tokens + t + 1, k1, y,
+                                              m, l))
+            continue;
+        const float inv = attn_inverse(l);
+        float* to = part + (wave * 32 + r) * (D + 4);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+            if (part) to[64 * e + lane] = y[e];
+            else ((__bf16*)p.o)[((b.start + t) * p.H + head) * D + 64 * e + lane] = (__bf16)(y[e] * inv);
+        }
+        if (part && lane == 0) {
+            to[D] = l;
+            to[D + 1] = m;
+        }
+    }
+}
+
 // A block's rows over the steps [t0, t1) of its keys: into o and lse, or with
 // `part` its sums, FW_BLOCK rows of D sums, the sum of weights, m and two unused floats.
 template <int D, bool PAGED>
@@ -248,8 +278,13 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
         if (tile + 1 < t1) step(y, x, tile + 1, 1);
     }
     l += swap_halves(l);
-    if (!valid) return;
-    if (part) {
+    float odd = 0.f;   // NaN if a sum is not finite
+#pragma unroll
+    for (int i = 0; i < O; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) odd = fmaf(o[i][e], 0.f, odd);
+    const uint64_t odds = __ballot(valid && odd != 0.f && l - l == 0.f);
+    if (valid && part) {
         float* to = part + (row - b.r0) * (D + 4);
 #pragma unroll
         for (int i = 0; i < O; ++i)
@@ -262,18 +297,19 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
             to[D] = l;
             to[D + 1] = m;
         }
-        return;
+    } else if (valid) {
+        const float inv = attn_inverse(l);
+        __bf16* orow = (__bf16*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
+#pragma unroll
+        for (int i = 0; i < O; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float y[4] = {o[i][4 * k] * inv, o[i][4 * k + 1] * inv, o[i][4 * k + 2] * inv, o[i][4 * k + 3] * inv};
+                store4(orow + 32 * i + 8 * k + 4 * half, y);
+            }
+        if (p.lse && half == 0) p.lse[(b.start + t) * p.H + head] = attn_lse(m, l);
     }
-    const float inv = attn_inverse(l);
-    __bf16* orow = (__bf16*)p.o + ((b.start + t) * p.H + head) * (int64_t)D;
-#pragma unroll
-    for (int i = 0; i < O; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float y[4] = {o[i][4 * k] * inv, o[i][4 * k + 1] * inv, o[i][4 * k + 2] * inv, o[i][4 * k + 3] * inv};
-            store4(orow + 32 * i + 8 * k + 4 * half, y);
-        }
-    if (p.lse && half == 0) p.lse[(b.start + t) * p.H + head] = attn_lse(m, l);
+    if (odds) fwd_again<D, PAGED>(b, g, (uint32_t)(odds | odds >> 32), t0, t1, part);
 }
 
 template <int D, bool PAGED>

@@ -400,8 +400,24 @@ __global__ __launch_bounds__(SP_THREADS, (StepTile<InT, D>::PER_UNIT)) void attn
     }
 }
 
+// Row r of request b's new tokens once more, by one wave (attn_row_again).
+template <typename InT, int D>
+__device__ __forceinline__ bool step_again(const AttnParams& p, int b, int g, int64_t at, int head, const AttnRange& qr, int r,
+                                           bool anyway) {
+    const int lane = threadIdx.x & 63;
+    const int32_t len = attn_length(p, b), sees = step_row(p, qr, len, g, r).sees;
+    float y[D / 64], m, l;
+    if (!attn_row_again<InT, D, true>(p, b, 0, g, at, head, 0, sees, len, y, m, l, anyway)) return false;
+    const float inv = attn_inverse(l);
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) ((InT*)p.o)[(at * p.H + head) * D + 64 * e + lane] = (InT)(y[e] * inv);
+    if (p.lse && lane == 0) p.lse[at * p.H + head] = attn_lse(m, l);
+    return true;
+}
+
 // A row of a unit that several workgroups hold: o = sum_s e^{m_s - m} o_s / sum_s e^{m_s - m} l_s;
-// and of one that nobody holds (a request without tokens).  WAVES waves share a
+// of one that nobody holds (a request without tokens); and any that is not finite because of a key that it does not see,
+// or of the joining's own products with zero.  WAVES waves share a
 // row's parts, lane i first takes the sums and maxima of parts i, i + 64, ...
 template <typename InT, int D, int RT, int WAVES>
 __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void attn_step_join_kernel(AttnParams p, int32_t max_rows) {
@@ -420,7 +436,17 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void attn_step_join_k
         w0 = step_info(p)[2 * unit];
         w1 = step_info(p)[2 * unit + 1];
     }
-    if (!x.valid || w0 < 0) return;   // (the whole workgroup where its waves share a row)
+    if (!x.valid) return;   // (the whole workgroup where its waves share a row)
+    InT* orow = (InT*)p.o + (x.at * p.H + x.head) * D;
+    float odd = 0.f;   // NaN if a value is not finite
+    if (w0 < 0) {
+        if (share == 0 && x.at + 1 < qr.end) {   // (the last token sees every key)
+#pragma unroll
+            for (int e = 0; e < E; ++e) odd = fmaf(to_f32(orow[64 * e + lane]), 0.f, odd);
+            if (__any(odd != 0.f)) step_again<InT, D>(p, b, g, x.at, x.head, qr, r, false);
+        }
+        return;
+    }
     const int32_t n = w1 - w0 + 1;
     float m = kAttnLowest, l = 0.f, o[E] = {};
     for (int32_t i0 = 64 * share; i0 < n; i0 += 64 * WAVES) {
@@ -475,8 +501,10 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void attn_step_join_k
             for (int e = 0; e < E; ++e) o[e] += f * joint[v][64 * e + lane];
         }
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) odd = fmaf(o[e], 0.f, odd);
+    if (__any(odd != 0.f) && l - l == 0.f && step_again<InT, D>(p, b, g, x.at, x.head, qr, r, true)) return;
     const float inv = attn_inverse(l);
-    InT* orow = (InT*)p.o + (x.at * p.H + x.head) * D;
 #pragma unroll
     for (int e = 0; e < E; ++e) orow[64 * e + lane] = (InT)(o[e] * inv);
     if (p.lse && lane == 0) p.lse[x.at * p.H + x.head] = attn_lse(m, l);

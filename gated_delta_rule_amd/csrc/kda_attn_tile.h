@@ -145,6 +145,88 @@ __device__ __forceinline__ float groups_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
+// The kernel's AttnParams (its first argument), read anew: what only the rare path
+// below needs is not to be held in registers through the loops before it.
+__device__ __forceinline__ const AttnParams& attn_params_again() {
+    const char* at = (const char*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+    return *reinterpret_cast<const AttnParams*>(at);
+}
+
+// (and the thread's number, so that nothing is formed from it ahead of the path)
+__device__ __forceinline__ int thread_again() {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    return tid;
+}
+
+// A row once more, key by key.  The products of a tile take every key's values
+// with the row's weight, which is zero for a key that the row does not see, and
+// zero times a NaN or an infinity is NaN.  So a row whose sums are not finite,
+// though its weights are, comes here: false if no key in [sees, k1), which its
+// tiles held beside those that it sees, has such a value (the sums are right
+// then, unless `anyway`); else of its keys in [k0, sees) the largest score m (base 2), l = sum of
+// e^{s - m} and y = sum of e^{s - m} v, value 64 e + lane in y[e].  All lanes of a
+// wave share one row.
+template <typename InT, int D, bool PAGED>
+__device__ __forceinline__ bool attn_row_again(const AttnParams& p, int n, int64_t start, int g, int64_t row, int head, int32_t k0,
+                                               int32_t sees, int32_t k1, float (&y)[D / 64], float& m, float& l, bool anyway = false) {
+    const AttnKeys<InT, PAGED> keys(p, n, start, g);
+    const InT* q = (const InT*)p.q + row * p.q_stride + (int64_t)head * D;
+    const float c = p.scale * kLog2e;
+    const int lane = thread_again() & 63;
+    int64_t ko, vo;
+    bool odd = anyway;
+    for (int32_t j = (sees > k0 ? sees : k0) + lane; j < k1; j += 64)
+        if (keys.at(j, ko, vo))
+#pragma unroll 1
+            for (int d = 0; d < D; d += 4) {
+                float x[4];
+                load4(keys.v + vo + d, x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) odd = odd || x[e] - x[e] != 0.f;
+            }
+    if (!__any(odd)) return false;
+    m = kAttnLowest;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) y[e] = 0.f;
+    const int32_t end = sees < k1 ? sees : k1;
+    for (int32_t j0 = k0; j0 < end; j0 += 64) {
+        const bool there = j0 + lane < end && keys.at(j0 + lane, ko, vo);
+        float s = 0.f;
+        if (there)
+#pragma unroll 1
+            for (int d = 0; d < D; d += 4) {
+                float a[4], b[4];
+                load4(q + d, a);
+                load4(keys.k + ko + d, b);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s = fmaf(a[e], b[e], s);
+            }
+        float top = there ? s * c : kAttnLowest;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+        const float to = fmaxf(m, top), fade = attn_exp2(m - to);
+        m = to;
+        const float w = there ? attn_exp2(fmaf(s, c, -m)) : 0.f;
+        float sum = w;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+        l = l * fade + sum;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) y[e] *= fade;
+        for (uint64_t left = __ballot(there); left; left &= left - 1) {
+            const int i = __builtin_ctzll(left);
+            const float wi = __shfl(w, i);
+            keys.at(j0 + i, ko, vo);
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) y[e] = fmaf(wi, to_f32(keys.v[vo + 64 * e + lane]), y[e]);
+        }
+    }
+    return true;
+}
+
 // Workgroup numbers for work that shrinks from the first workgroup to the last:
 // every second round of one workgroup per compute unit (32 of each XCD) is
 // turned round, so that the units' shares are alike.

@@ -37,12 +37,15 @@
  *     cu_seqlens[n_seqs] on belong to no sequence: they affect nothing and
  *     their outputs keep what they held.  The device clamps each range into
  *     [0, T].  Sequences may be empty.
- *   - q, k and v must be finite, and scores within float32.  Keys are taken
- *     up to 64 at a time and a masked score has weight zero, so a NaN or
- *     infinity in v (gradients: in any input) of a token can reach rows up to
- *     63 tokens before it, in its own sequence and group.  What lies outside
- *     a sequence, behind a request's length or in pages that it does not hold
- *     is never part of a product.
+ *   - Scores (times log2 e) must be within float32.  A NaN or an infinity in q
+ *     reaches its own row only, one in k or v the rows that see its token:
+ *     rows that do not, but share a tile of keys with it, are computed once
+ *     more key by key.  In the backward pass a masked weight of zero is
+ *     multiplied with whatever stands there: a NaN or an infinity in any input
+ *     can also reach gradients of tokens up to 94 away in its own sequence and
+ *     group, on the side that does not see it.  What lies outside a sequence,
+ *     behind a request's length or in pages that it does not hold is never
+ *     part of a product.
  *   - Numerics: scores, softmax statistics and sums in float32.  With
  *     KDA_BF16 the weights (and in the backward pass the score gradients)
  *     are rounded to bf16 once, as operands of the matrix cores: a half step

@@ -523,3 +523,67 @@ def test_lse_of_a_prompt_says_nan_beside_a_nan(dtype):
     o, lse = kda.attn_fwd(q, k, v)
     assert torch.equal(torch.isnan(lse), bad) and torch.equal(torch.isnan(o).all(-1), bad)
     assert not torch.isinf(lse).any()
+
+
+def unseen(o, lse, q, K, V, first, dtype, at, d, what):
+    """Rows before key `at` are as if it held no `what` in value d; from it on that value is `what`."""
+    D = q.shape[-1]
+    ref, eo, lref, el = exact(q, K, V.nan_to_num(0.0, 0.0, 0.0), first, D ** -0.5, dtype)
+    H, G = q.shape[1], K.shape[1]
+    bad = torch.zeros(ref.shape, dtype=torch.bool, device="cuda")
+    bad[max(0, at - first):, -(H // G):, d] = True       # (the last group)
+    got = o.masked_select(bad)
+    assert torch.isnan(got).all() if what != what else (got == what).all()
+    check("o", o.masked_fill(bad, 0.0), ref.masked_fill(bad, 0.0), eo, dtype)
+    check("lse", lse, lref, el, F32)
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens,at,H,G,D", [([5], 4, 2, 1, 64), ([70, 300], 250, 8, 2, 128), ([64, 129], 1, 3, 3, 64), ([600], 599, 4, 1, 64),
+                                           ([300, 200, 90], 63, 4, 4, 128)])
+def test_a_value_that_is_not_finite_reaches_no_earlier_row(lens, at, H, G, D, dtype, what):
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q, k, v = (torch.randn(sum(lens), n, D, generator=g, device="cuda").to(dtype) for n in (H, G, G))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    last = slice(sum(lens[:-1]), sum(lens))
+    v[last][at, G - 1, 7] = what
+    o, lse = kda.attn_fwd(q, k, v, cu)
+    for n, s in zip(lens, cu.tolist()):
+        x = slice(s, s + n)
+        unseen(o[x], lse[x], q[x], k[x], v[x], 0, dtype, at if x == last else n, 7, what)
+
+
+@pytest.mark.parametrize("what", [float("nan"), -float("inf")])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", [([40, 7], [3, 3], 4, 2, 64, 16), ([9000], [5], 8, 2, 128, 64), ([9000, 300], [4, 4], 64, 4, 64, 64),
+                                  ([300, 80], [70, 70], 4, 2, 64, 16), ([20000], [150], 8, 2, 128, 16), ([700, 900], [200, 30], 8, 2, 128, 32)])
+def test_a_new_value_that_is_not_finite_reaches_no_earlier_row(case, dtype, what):
+    held, new, H, G, D, page = case
+    c, n = Cache(held, G, D, page, dtype), len(held)
+    g = torch.Generator(device="cuda").manual_seed(10)
+    q = torch.randn(sum(new), H, D, generator=g, device="cuda").to(dtype)
+    x = held[-1] - new[-1] // 2
+    c.vp[c.table[n - 1, x // page].long(), G - 1, x % page, D - 1] = what
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    o, lse = kda.attn_paged_fwd(q, c.kp, c.vp, c.table, c.lengths, cu)
+    for b in range(n):
+        s = slice(int(cu[b]), int(cu[b + 1]))
+        unseen(o[s], lse[s], q[s], *c.keys(b), held[b] - new[b], dtype, x if b == n - 1 else held[b], D - 1, what)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_padding_may_hold_anything(dtype):
+    # equal lengths, of which the batch's sequences fill less: their tokens see no padding
+    g = torch.Generator(device="cuda").manual_seed(11)
+    lens, T, H, G, D = [200, 1, 131, 64], 200, 6, 2, 64
+    q, k, v = (torch.randn(len(lens), T, n, D, generator=g, device="cuda").to(dtype) for n in (H, G, G))
+    for b, n in enumerate(lens):
+        for t in (q, k, v):
+            t[b, n:] = float("nan")
+    o, lse = kda.attn_fwd(q, k, v)
+    for b, n in enumerate(lens):
+        ref, eo, lref, el = exact(q[b, :n], k[b, :n], v[b, :n], 0, D ** -0.5, dtype)
+        check("o", o[b, :n], ref, eo, dtype)
+        check("lse", lse[b, :n], lref, el, F32)
+        assert torch.isnan(o[b, n:]).all() and torch.isnan(lse[b, n:]).all()
