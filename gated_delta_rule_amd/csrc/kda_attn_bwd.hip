@@ -82,7 +82,6 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
         const int32_t t0 = r0 / p.hpg, h0 = r0 - t0 * p.hpg;                  // first row of the tile
         const auto qrs = make_rsrc((const __bf16*)p.q + (b.start + t0) * p.q_stride + (int64_t)pl.g * p.hpg * D, 0x40000000);
         const auto grs = make_rsrc((const __bf16*)a.go + (b.start + t0) * gstride + (int64_t)pl.g * p.hpg * D, 0x40000000);
-        settle(qrs, grs);
         const uint32_t to = lds0 + buf * TILE + wave * 16 * ROWB;
         int ln = lane;
         hide(ln);   // (offsets are formed anew: there are no registers to keep them)
@@ -93,8 +92,8 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_kv_kernel(AttnBwdParam
             rows.of((uint32_t)(h0 + r), t, hh);
             const uint32_t at = hh * (2 * D) + u * 16;
             const bool in = r0 + r < n_rows;                                  // rows behind the last one read as zero
-            load_to_lds(qrs, in ? t * (uint32_t)(p.q_stride * 2) + at : 0x80000000u, to + i * 1024);
-            load_to_lds(grs, in ? t * (uint32_t)(gstride * 2) + at : 0x80000000u, to + 2 * TILE + i * 1024);
+            load_pair_to_lds(qrs, in ? t * (uint32_t)(p.q_stride * 2) + at : 0x80000000u,
+                             grs, in ? t * (uint32_t)(gstride * 2) + at : 0x80000000u, to + i * 1024, 2 * TILE);
         }
         if (tid < 2 * BW_STEP) {
             const int r = tid & (BW_STEP - 1);
@@ -278,8 +277,8 @@ __global__ __launch_bounds__(BW_THREADS, 2) void attn_bwd_q_kernel(AttnBwdParams
         const int64_t first = left > 0 ? key : 0;
         const auto krs = make_rsrc(keys.k + first * keys.k_stride, left > 0 ? ((left - 1) * (int)keys.k_stride + D) * 2 : 0);
         const auto vrs = make_rsrc(keys.v + first * keys.v_stride, left > 0 ? ((left - 1) * (int)keys.v_stride + D) * 2 : 0);
-        settle(krs, vrs);
         const uint32_t to = lds0 + buf * TILE + wave * 16 * ROWB;
+        // (single loads: 411 us at 2 x 4096 tokens, 32 heads of 128 on 8; as two blocks 419, the compiler puts products between these)
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) load_to_lds(krs, koff[i], to + i * 1024);
 #pragma unroll

@@ -153,10 +153,7 @@ __device__ __forceinline__ void fwd_block(const AttnParams& p, FwdShared<D>& sh,
     auto request = [&](const Source& s, int64_t step, const uint32_t (&off)[LOADS], int32_t tile, int half_of) {
         const int32_t left = most - (tile * FW_KEYS + 16 * wave);
         const auto rs = make_rsrc(s.at, s.ok ? (((left < 16 ? left : 16) - 1) * (int)step + D) * 2 : 0);
-        settle(rs);
-        const uint32_t to = lds0 + half_of * TILE + wave * 16 * ROWB;
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) load_to_lds(rs, off[i], to + i * 1024);
+        load_to_lds(rs, off, lds0 + half_of * TILE + wave * 16 * ROWB);
     };
     int32_t page_v = 0, page_raw = t0 < t1 ? page_of(t0) : 0;   // of the last keys requested; of the next ones
     auto request_keys = [&](int32_t tile, int buf) {

@@ -34,35 +34,56 @@ __device__ __forceinline__ int tile_swap(int row) {
 
 // A pointer that every lane has, in scalar registers: the compiler may know
 // that it is the same everywhere and still form it in vector registers, which
-// the buffers of the loads below cannot be given in.  Behind the reads come the
-// wait states that a buffer's words need after vector instructions wrote them
-// (the loads are assembly, so the compiler does not count them).
+// the buffers of the loads below cannot be given in.
 template <typename T>
 __device__ __forceinline__ T* in_scalars(T* p) {
     uint32_t lo = (uint32_t)(uint64_t)p, hi = (uint32_t)((uint64_t)p >> 32);
     asm("" : "+v"(lo), "+v"(hi));
     lo = __builtin_amdgcn_readfirstlane(lo);
     hi = __builtin_amdgcn_readfirstlane(hi);
-    asm volatile("s_nop 4" : "+s"(lo), "+s"(hi));
+    asm volatile("" : "+s"(lo), "+s"(hi));
     return (T*)((uint64_t)hi << 32 | lo);
 }
 
-// The same wait states before a buffer's first load: its words may have just
-// come out of vector registers that the compiler keeps scalars in.
-__device__ __forceinline__ void settle(__amdgpu_buffer_rsrc_t a) { asm volatile("s_nop 4" :: "s"(a) : "memory"); }
-__device__ __forceinline__ void settle(__amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b) {
-    asm volatile("s_nop 4" :: "s"(a), "s"(b) : "memory");
+// Loads from a buffer to LDS, 16 bytes per lane, written out because the
+// compiler would wait for them before every LDS read.  It counts no wait states
+// in front of assembly either, and may form a buffer's words, or bring them
+// back, with vector instructions at any place: so every block begins with the
+// five that a load needs behind such a write (a move to m0 and s_nop 3), and
+// within a block nothing can come between.  A load needs one behind m0's write.
+#define KDA_LDS_FIRST "s_mov_b32 m0, %0\n\ts_nop 3\n\t"
+#define KDA_LDS_NEXT "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+#define KDA_LDS_LOAD(off, rs) "buffer_load_dwordx4 %" #off ", %" #rs ", 0 offen lds\n\t"
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t to) {   // to `to` + 16 lane
+    asm volatile(KDA_LDS_FIRST KDA_LDS_LOAD(1, 2) :: "s"(to), "v"(off), "s"(rs) : "memory", "m0");
 }
-
-// 16 bytes per lane from a buffer to LDS at `to` + 16 lane.  Written out
-// because the compiler would wait for these before every LDS read.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(to), "v"(off), "s"(rs) : "memory", "m0");
+// Load n to `to` + 1024 n + 16 lane.
+template <int N>
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, const uint32_t (&off)[N], uint32_t to) {
+    static_assert(N == 2 || N == 4 || N == 8, "");
+    if constexpr (N == 8) {
+        load_to_lds<4>(rs, {off[0], off[1], off[2], off[3]}, to);
+        load_to_lds<4>(rs, {off[4], off[5], off[6], off[7]}, to + 4096);
+    } else if constexpr (N == 2) {
+        asm volatile(KDA_LDS_FIRST KDA_LDS_LOAD(1, 3) KDA_LDS_NEXT KDA_LDS_LOAD(2, 3)
+                     :: "s"(to), "v"(off[0]), "v"(off[1]), "s"(rs) : "memory", "m0", "scc");
+    } else {
+        asm volatile(KDA_LDS_FIRST KDA_LDS_LOAD(1, 5) KDA_LDS_NEXT KDA_LDS_LOAD(2, 5) KDA_LDS_NEXT KDA_LDS_LOAD(3, 5)
+                     KDA_LDS_NEXT KDA_LDS_LOAD(4, 5)
+                     :: "s"(to), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(rs) : "memory", "m0", "scc");
+    }
 }
-__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t to) {   // 4 bytes per lane
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :: "s"(to), "v"(off), "s"(rs) : "memory", "m0");
+// One load of each of two buffers, to `to` + 16 lane and `to` + `apart` + 16 lane.
+__device__ __forceinline__ void load_pair_to_lds(__amdgpu_buffer_rsrc_t a, uint32_t aoff, __amdgpu_buffer_rsrc_t b, uint32_t boff,
+                                                 uint32_t to, uint32_t apart) {
+    asm volatile(KDA_LDS_FIRST KDA_LDS_LOAD(2, 4) "s_add_u32 m0, m0, %1\n\ts_nop 0\n\t" KDA_LDS_LOAD(3, 5)
+                 :: "s"(to), "s"(apart), "v"(aoff), "v"(boff), "s"(a), "s"(b) : "memory", "m0", "scc");
+}
+// The same with 4 bytes per lane, the second load to `to` + 256 + 4 lane.
+__device__ __forceinline__ void load4_pair_to_lds(__amdgpu_buffer_rsrc_t a, __amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t to) {
+    asm volatile(KDA_LDS_FIRST "buffer_load_dword %1, %2, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, 0x100\n\ts_nop 0\n\tbuffer_load_dword %1, %3, 0 offen lds\n\t"
+                 :: "s"(to), "v"(off), "s"(a), "s"(b) : "memory", "m0", "scc");
 }
 // All of this wave's loads to LDS have arrived and its LDS reads are done; then the workgroup's barrier.
 __device__ __forceinline__ void tiles_barrier() {

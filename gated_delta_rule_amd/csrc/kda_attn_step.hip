@@ -230,12 +230,9 @@ __global__ __launch_bounds__(SP_THREADS, (StepTile<InT, D>::PER_UNIT)) void attn
                 const int32_t left = len - key < 16 ? len - key : 16;
                 const auto krs = make_rsrc(keys.k + from, ok[n] ? left * ROWB : 0);
                 const auto vrs = make_rsrc(keys.v + from, ok[n] ? left * ROWB : 0);
-                settle(krs, vrs);
                 const uint32_t to = lds0 + buf * Tile::BUF + n * GROUP;
-#pragma unroll
-                for (int i = 0; i < LOADS; ++i) load_to_lds(krs, off[i], to + i * 1024);
-#pragma unroll
-                for (int i = 0; i < LOADS; ++i) load_to_lds(vrs, off[i], to + NG * GROUP + i * 1024);
+                load_to_lds(krs, off, to);
+                load_to_lds(vrs, off, to + NG * GROUP);
             }
         };
 
