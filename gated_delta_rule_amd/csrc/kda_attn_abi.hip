@@ -31,7 +31,11 @@ int attn_shape(int in_dtype, int32_t n_seqs, int64_t T, int32_t H, int32_t G, in
     return *rows <= kMaxRows / H ? KDA_OK : KDA_ERR_TOO_LARGE;
 }
 
-bool finite(float x) { return x - x == 0.f; }
+// The kernels take scores in base 2: scale log2 e has to be a number, too.
+bool scale_ok(float x) {
+    const float c = x * 1.44269504f;
+    return c - c == 0.f;
+}
 
 // A row stride: at least the row, whole 16-byte pieces, small enough for
 // 32-bit offsets within a tile of rows.
@@ -166,7 +170,7 @@ int kda_attn_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_strid
     int64_t rows = 0;
     int rc = attn_shape(in_dtype, n_seqs, T, H, G, D, cu_seqlens != nullptr, &rows);
     if (rc) return rc;
-    if (!finite(scale)) return KDA_ERR_BAD_SHAPE;
+    if (!scale_ok(scale)) return KDA_ERR_BAD_SHAPE;
     if (rows == 0) return KDA_OK;
     if (!q || !k || !v || !o) return KDA_ERR_NULL_POINTER;
     const int64_t es = elem_size(in_dtype), HD = (int64_t)H * D, GD = (int64_t)G * D;
@@ -208,7 +212,7 @@ int kda_attn_bwd_fresh(const void* q, int64_t q_stride, const void* k, int64_t k
     int64_t rows = 0;
     int rc = attn_shape(in_dtype, n_seqs, T, H, G, D, varlen, &rows);
     if (rc) return rc;
-    if (!finite(scale)) return KDA_ERR_BAD_SHAPE;
+    if (!scale_ok(scale)) return KDA_ERR_BAD_SHAPE;
     if (rows == 0) return KDA_OK;
     if (!q || !k || !v || !o || !lse || !grad_o || !grad_q || !grad_k || !grad_v) return KDA_ERR_NULL_POINTER;
     const int64_t es = elem_size(in_dtype), HD = (int64_t)H * D, GD = (int64_t)G * D;
@@ -345,7 +349,7 @@ int kda_attn_paged_fwd(const void* q, int64_t q_stride, int in_dtype, const void
     int64_t rows = 0;
     int rc = attn_shape(in_dtype, n_seqs, T, H, G, D, varlen, &rows);
     if (rc) return rc;
-    if (!finite(scale)) return KDA_ERR_BAD_SHAPE;
+    if (!scale_ok(scale)) return KDA_ERR_BAD_SHAPE;
     const int64_t es = elem_size(in_dtype), HD = (int64_t)H * D, GD = (int64_t)G * D;
     if (n_seqs > 0 && (rc = check_cache(k_pages, v_pages, page_stride, n_pages, page_size, table, max_pages, lengths,
                                         cu_seqlens, GD, es)))

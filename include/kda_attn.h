@@ -23,8 +23,8 @@
  * current device):
  *   - Sizes: head dimension D 64 or 128, H a multiple of G, H <=
  *     KDA_MAX_HEADS, H * D <= KDA_ATTN_MAX_STRIDE, H / G times the tokens of
- *     a sequence (packed: of the batch) at most 2^30, scale finite (anything
- *     else -> KDA_ERR_BAD_SHAPE / _TOO_LARGE).
+ *     a sequence (packed: of the batch) at most 2^30, scale log2 e within
+ *     float32 (anything else -> KDA_ERR_BAD_SHAPE / _TOO_LARGE).
  *   - in_dtype (KDA_BF16 or KDA_F32) is the type of q, k, v, o and of their
  *     gradients; lse is float32.
  *   - Token rows: a `_stride` is the number of elements from one token row to

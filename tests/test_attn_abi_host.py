@@ -125,6 +125,12 @@ def test_a_scale_that_is_no_number_is_refused(lib, scale):
         assert f(lib, sc=scale) == SHAPE
 
 
+def test_a_scale_whose_base_2_form_overflows_is_refused(lib):
+    for f in (fwd, bwd, paged):
+        assert f(lib, sc=3e38) == SHAPE and f(lib, sc=-2.4e38) == SHAPE
+        assert f(lib, sc=2.3e38, T=0) == OK and f(lib, sc=-2.3e38, T=0) == OK and f(lib, sc=1e-45, T=0) == OK
+
+
 def append(lib, **kw):
     d = dict(k=ptr("k"), ks=128, v=ptr("v"), vs=128, dt=0, kp=ptr("kp"), vp=ptr("vp"), ps=2 * 16 * 64, np=9, pg=16,
              tab=ptr("table"), mp=4, len=ptr("len"), cu=None, n=2, T=3, G=2, D=64, st=None)
