@@ -587,3 +587,52 @@ def test_padding_may_hold_anything(dtype):
         check("o", o[b, :n], ref, eo, dtype)
         check("lse", lse[b, :n], lref, el, F32)
         assert torch.isnan(o[b, n:]).all() and torch.isnan(lse[b, n:]).all()
+
+
+@pytest.mark.parametrize("held,new", [
+    # uneven lengths, cut into pieces: single tokens, a chunk, requests without new tokens
+    ([100 + 37 * (b % 11) for b in range(150)] + [20000] + [60] * 110 + [9000, 300] + [500] * 60, [1] * 100 + [0, 1] * 25 + [150] + [1] * 170 + [0, 2]),
+    # short ones, taken whole
+    ([40 + b % 7 for b in range(330)], [1] * 329 + [9])])
+def test_more_blocks_than_threads(held, new):
+    """More than 256 blocks per group: a thread of the piece finding has several."""
+    cu = np.concatenate([[0], np.cumsum(new)])
+    slots = cu[:-1] * 8 // 128 + np.arange(len(new))      # first block of each request
+    assert slots[-1] > 256 and (cu[-1] * 8 // 128 + len(new)) * 4 < 2048
+    look = {0, 1, 99, 149, 150, 151, 200, 261, 262, len(new) - 2, len(new) - 1} | set(np.nonzero((slots >= 250) & (slots < 262))[0].tolist())
+    run_paged(held, new, 32, 4, 64, 16, BF16, look=look)
+
+
+@pytest.mark.parametrize("dtype,n,T,H,G,D", [(BF16, 1, 2100, 4, 2, 128), (BF16, 2, 1111, 6, 2, 64), (F32, 1, 1300, 4, 2, 128), (F32, 2, 700, 3, 3, 64)])
+def test_long_sequences_that_see_all(dtype, n, T, H, G, D):
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q, k, v, go = (torch.randn(n, T, m, D, generator=g, device="cuda").to(dtype) for m in (H, G, G, H))
+    o, lse = kda.attn_fwd(q, k, v, causal=False)
+    grads = kda.attn_bwd(q, k, v, o, lse, go, causal=False)
+    half, scale = 2.0 ** -8 if dtype == BF16 else 0.0, D ** -0.5
+    for b in range(n):
+        ref, eo, lref, el = exact(q[b], k[b], v[b], 0, scale, dtype, causal=False)
+        check("o", o[b], ref, eo, dtype)
+        check("lse", lse[b], lref, el, F32)
+        refs = [torch.zeros(t.shape[1:], dtype=torch.float64, device="cuda") for t in (q, k, v)]
+        errs = [torch.zeros_like(t) for t in refs]
+        for h in range(H):   # as oracle/attn.py: attention_backward and backward_bounds
+            i = h // (H // G)
+            Q, K, V, Y = q[b, :, h].double(), k[b, :, i].double(), v[b, :, i].double(), go[b, :, h].double()
+            P = torch.exp((Q @ K.T.contiguous()) * scale - lref[:, h:h + 1])
+            gP, out = Y @ V.T.contiguous(), P @ V
+            delta, dmag = (Y * out).sum(1, keepdim=True), (Y.abs() * out.abs()).sum(1, keepdim=True)
+            gS = P * (gP - delta)
+            refs[0][:, h] = scale * gS @ K
+            refs[1][:, i] += scale * gS.T.contiguous() @ Q
+            refs[2][:, i] += P.T.contiguous() @ Y
+            s = (scale * (Q.abs() @ K.abs().T.contiguous())).amax(1) * (D + 8) * U
+            rel = (3 * s + (P.amax(1).log().abs() + T + 128) * U)[:, None]
+            n_sum = (T * (H // G) + 32) * U
+            eS = P * (half * ((gP - delta).abs() + dmag) * 1.02 + (rel + (D + 8) * U) * (Y.abs() @ V.abs().T.contiguous() + dmag))
+            eS = eS + n_sum * P * ((gP - delta).abs() + half * dmag)
+            errs[0][:, h] = scale * eS @ K.abs()
+            errs[1][:, i] += scale * eS.T.contiguous() @ Q.abs()
+            errs[2][:, i] += (P * (half + rel + n_sum)).T.contiguous() @ Y.abs()
+        w = [check(name, x[b], r, e, dtype) for name, x, r, e in zip(("gq", "gk", "gv"), grads, refs, errs)]
+    say(f"[all] {n} x {T}, {H}/{G} x {D} {dtype}: gradients at {max(w):.2g} of the tolerance")

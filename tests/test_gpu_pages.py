@@ -198,3 +198,36 @@ def test_pairs_that_copy_nothing_need_no_page():
     assert lengths.tolist() == [10, 16, 10, 20, 16, 20] and refs.tolist() == [1, 2, 1, 1, 2, 1]
     before[2], before[3] = before[0], before[5]
     assert torch.equal(pages, before)
+
+
+@pytest.mark.parametrize("n", [20, 45])
+def test_rows_of_several_column_blocks(n):
+    # 600 columns: counts and rows in blocks of 256; 12000 and 27000 entries, counted by one workgroup and by many
+    r = random.Random(n)
+    b = Both(60, 600, 12000, 16, shape=(4,))
+    b.resize([r.choice([0, 255 * 16, 256 * 16, 256 * 16 + 1, 512 * 16, 513 * 16, r.randint(4100, 9600), 9599, 9600]) if s < 20 else
+              r.randint(0, 600) for s in range(60)])
+    b.fork([r.randrange(20) for _ in range(n)], r.sample(range(60), n))
+    b.resize([r.choice([w, w // 2, 0]) for w in b.plain.lengths])
+    b.fork([r.randrange(60) for _ in range(n)], [r.randrange(60) for _ in range(n)])
+    b.compact()
+
+
+def test_more_slots_than_lds_holds():
+    r = random.Random(5)
+    b = Both(9000, 3, 24000, 16, shape=(4,))
+    b.resize([r.randint(0, 40) for _ in range(9000)])
+    n = 10000   # destinations twice and thrice, no slots among them
+    b.fork([r.randint(-1, 9000) for _ in range(n)], [r.choice([0, 4095, 8191, 8192, 8999, -1, 9000, r.randrange(9000)]) for _ in range(n)])
+    b.resize([r.randint(0, 48) for _ in range(9000)])
+    b.fork(list(range(9000)), [(i * 7 + 1) % 9000 for i in range(9000)])
+    b.compact(in_place=True)
+
+
+def test_pages_above_a_megabyte():
+    # 66 pieces of 16 KB and a rest, more than the workgroups that share a copy
+    b = Both(4, 3, 10, 16, shape=(270340,), tensors=2)
+    b.resize([20, 5, 48, 0])
+    b.fork([0, 1, 0], [3, 2, 1])
+    b.resize([0, 20, 5, 20])
+    b.compact()
