@@ -135,6 +135,7 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
         const auto grs = make_rsrc((const float*)a.go + (b.start + t0) * gstride + head * D, 0x40000000);
         const auto lrs = make_rsrc(p.lse + (b.start + t0) * p.H + head, 0x40000000);
         const auto drs = make_rsrc(a.delta + (b.start + t0) * p.H + head, 0x40000000);
+        uint32_t qoff[LOADS], goff[LOADS];
         const uint32_t to = lds0 + buf * HALF;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
@@ -143,9 +144,11 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_kv_f32_k
             rows.of((uint32_t)(h0 + r), t, hh);
             const uint32_t at = hh * (4 * D) + u * 16;
             const bool in = r0 + r < n_rows;                  // rows behind the last one read as zero
-            load_pair_to_lds(qrs, in ? t * (uint32_t)(p.q_stride * 4) + at : 0x80000000u,
-                             grs, in ? t * (uint32_t)(gstride * 4) + at : 0x80000000u, to + i * 1024, Tile::BYTES);
+            qoff[i] = in ? t * (uint32_t)(p.q_stride * 4) + at : 0x80000000u;
+            goff[i] = in ? t * (uint32_t)(gstride * 4) + at : 0x80000000u;
         }
+        load_to_lds(qrs, qoff, to);
+        load_to_lds(grs, goff, to + Tile::BYTES);
         uint32_t t, hh;
         rows.of((uint32_t)(h0 + col), t, hh);
         const uint32_t at = r0 + col < n_rows ? (t * (uint32_t)p.H + hh) * 4 : 0x80000000u;
@@ -289,13 +292,16 @@ __global__ __launch_bounds__(AB_THREADS, D == 64 ? 2 : 1) void attn_bwd_q_f32_ke
         const int32_t left = most - key < 16 ? most - key : 16;
         const auto krs = make_rsrc(keys.k + key * keys.k_stride, ((left - 1) * (int)keys.k_stride + D) * 4);
         const auto vrs = make_rsrc(keys.v + key * keys.v_stride, ((left - 1) * (int)keys.v_stride + D) * 4);
+        uint32_t koff[LOADS], voff[LOADS];
         const uint32_t to = lds0 + buf * HALF;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int r = i * Tile::RPL + lane / Tile::UNITS, u = (lane % Tile::UNITS) ^ r;
-            load_pair_to_lds(krs, (uint32_t)(r * (int)keys.k_stride * 4 + u * 16),
-                             vrs, (uint32_t)(r * (int)keys.v_stride * 4 + u * 16), to + i * 1024, Tile::BYTES);
+            koff[i] = (uint32_t)(r * (int)keys.k_stride * 4 + u * 16);
+            voff[i] = (uint32_t)(r * (int)keys.v_stride * 4 + u * 16);
         }
+        load_to_lds(krs, koff, to);
+        load_to_lds(vrs, voff, to + Tile::BYTES);
     };
     f32x4 g[1][S];
 #pragma unroll

@@ -62,8 +62,11 @@ template <int N>
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, const uint32_t (&off)[N], uint32_t to) {
     static_assert(N == 2 || N == 4 || N == 8, "");
     if constexpr (N == 8) {
-        load_to_lds<4>(rs, {off[0], off[1], off[2], off[3]}, to);
-        load_to_lds<4>(rs, {off[4], off[5], off[6], off[7]}, to + 4096);
+        asm volatile(KDA_LDS_FIRST KDA_LDS_LOAD(1, 9) KDA_LDS_NEXT KDA_LDS_LOAD(2, 9) KDA_LDS_NEXT KDA_LDS_LOAD(3, 9)
+                     KDA_LDS_NEXT KDA_LDS_LOAD(4, 9) KDA_LDS_NEXT KDA_LDS_LOAD(5, 9) KDA_LDS_NEXT KDA_LDS_LOAD(6, 9)
+                     KDA_LDS_NEXT KDA_LDS_LOAD(7, 9) KDA_LDS_NEXT KDA_LDS_LOAD(8, 9)
+                     :: "s"(to), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "v"(off[4]), "v"(off[5]), "v"(off[6]),
+                        "v"(off[7]), "s"(rs) : "memory", "m0", "scc");
     } else if constexpr (N == 2) {
         asm volatile(KDA_LDS_FIRST KDA_LDS_LOAD(1, 3) KDA_LDS_NEXT KDA_LDS_LOAD(2, 3)
                      :: "s"(to), "v"(off[0]), "v"(off[1]), "s"(rs) : "memory", "m0", "scc");
