@@ -163,11 +163,12 @@ __device__ __forceinline__ int thread_again() {
 // A row once more, key by key.  The products of a tile take every key's values
 // with the row's weight, which is zero for a key that the row does not see, and
 // zero times a NaN or an infinity is NaN.  So a row whose sums are not finite,
-// though its weights are, comes here: false if no key in [sees, k1), which its
-// tiles held beside those that it sees, has such a value (the sums are right
-// then, unless `anyway`); else of its keys in [k0, sees) the largest score m (base 2), l = sum of
-// e^{s - m} and y = sum of e^{s - m} v, value 64 e + lane in y[e].  All lanes of a
-// wave share one row.
+// though its weights are, comes here: false if those sums stand (unless
+// `anyway`), which is where no key in [sees, k1), which its tiles held beside
+// those that it sees, has such a value at the same place, or one that it sees
+// has, too; else of its keys in [k0, sees) the largest score m (base 2), l = sum
+// of e^{s - m} and y = sum of e^{s - m} v, value 64 e + lane in y[e].  All lanes
+// of a wave share one row.
 template <typename InT, int D, bool PAGED>
 __device__ __forceinline__ bool attn_row_again(const AttnParams& p, int n, int64_t start, int g, int64_t row, int head, int32_t k0,
                                                int32_t sees, int32_t k1, float (&y)[D / 64], float& m, float& l, bool anyway = false) {
@@ -175,28 +176,41 @@ __device__ __forceinline__ bool attn_row_again(const AttnParams& p, int n, int64
     const InT* q = (const InT*)p.q + row * p.q_stride + (int64_t)head * D;
     const float c = p.scale * kLog2e;
     const int lane = thread_again() & 63;
+    const int32_t end = sees < k1 ? sees : k1;
     int64_t ko, vo;
-    bool odd = anyway;
-    for (int32_t j = (sees > k0 ? sees : k0) + lane; j < k1; j += 64)
-        if (keys.at(j, ko, vo))
-#pragma unroll 1
-            for (int d = 0; d < D; d += 4) {
-                float x[4];
-                load4(keys.v + vo + d, x);
+    if (!anyway) {
+        auto not_finite = [&](int32_t j) {   // bit e: value 64 e + lane of key j
+            uint32_t bits = 0;
+            if (j >= k0 && keys.at(j, ko, vo)) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) odd = odd || x[e] - x[e] != 0.f;
+                for (int e = 0; e < D / 64; ++e) {
+                    const float x = to_f32(keys.v[vo + 64 * e + lane]);
+                    bits |= (x - x == 0.f ? 0u : 1u) << e;
+                }
             }
-    if (!__any(odd)) return false;
+            return bits;
+        };
+        uint32_t odd = 0;
+#pragma unroll 1
+        for (int32_t j = sees > k0 ? sees : k0; j < k1; ++j) odd |= not_finite(j);
+        for (int32_t j = end - 1; j >= k0 && __any(odd); j -= 8) {
+            uint32_t had = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) had |= not_finite(j - i);
+            odd &= ~had;
+        }
+        if (!__any(odd)) return false;
+    }
     m = kAttnLowest;
     l = 0.f;
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) y[e] = 0.f;
-    const int32_t end = sees < k1 ? sees : k1;
     for (int32_t j0 = k0; j0 < end; j0 += 64) {
         const bool there = j0 + lane < end && keys.at(j0 + lane, ko, vo);
+        if (!there) ko = vo = 0;
         float s = 0.f;
         if (there)
-#pragma unroll 1
+#pragma unroll 4
             for (int d = 0; d < D; d += 4) {
                 float a[4], b[4];
                 load4(q + d, a);
@@ -216,12 +230,22 @@ __device__ __forceinline__ bool attn_row_again(const AttnParams& p, int n, int64
         l = l * fade + sum;
 #pragma unroll
         for (int e = 0; e < D / 64; ++e) y[e] *= fade;
-        for (uint64_t left = __ballot(there); left; left &= left - 1) {
-            const int i = __builtin_ctzll(left);
-            const float wi = __shfl(w, i);
-            keys.at(j0 + i, ko, vo);
+        const uint64_t some = __ballot(there);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 64; i0 += 8) {
+            float x[8][D / 64];
 #pragma unroll
-            for (int e = 0; e < D / 64; ++e) y[e] = fmaf(wi, to_f32(keys.v[vo + 64 * e + lane]), y[e]);
+            for (int i = 0; i < 8; ++i) {
+                const InT* at = keys.v + (((int64_t)__shfl((int32_t)(vo >> 32), i0 + i) << 32) | (uint32_t)__shfl((int32_t)vo, i0 + i));
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) x[i][e] = some >> (i0 + i) & 1 ? to_f32(at[64 * e + lane]) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float wi = __shfl(w, i0 + i);
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) y[e] = fmaf(wi, x[i][e], y[e]);
+            }
         }
     }
     return true;

@@ -38,9 +38,9 @@
  *     their outputs keep what they held.  The device clamps each range into
  *     [0, T].  Sequences may be empty.
  *   - Scores (times log2 e) must be within float32.  A NaN or an infinity in q
- *     reaches its own row only, one in k or v the rows that see its token:
- *     rows that do not, but share a tile of keys with it, are computed once
- *     more key by key.  In the backward pass a masked weight of zero is
+ *     reaches its own row only, one in k or v the rows that see its token (an
+ *     infinity perhaps as a NaN): rows that do not, but share a tile of keys
+ *     with it, are computed once more key by key.  In the backward pass a masked weight of zero is
  *     multiplied with whatever stands there: a NaN or an infinity in any input
  *     can also reach gradients of tokens up to 94 away in its own sequence and
  *     group, on the side that does not see it.  What lies outside a sequence,

@@ -636,3 +636,31 @@ def test_long_sequences_that_see_all(dtype, n, T, H, G, D):
             errs[2][:, i] += (P * (half + rel + n_sum)).T.contiguous() @ Y.abs()
         w = [check(name, x[b], r, e, dtype) for name, x, r, e in zip(("gq", "gk", "gv"), grads, refs, errs)]
     say(f"[all] {n} x {T}, {H}/{G} x {D} {dtype}: gradients at {max(w):.2g} of the tolerance")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,H,G,D,share", [(400, 6, 2, 64, 0.002), (333, 4, 4, 128, 0.0005), (700, 8, 1, 128, 0.00005), (200, 3, 1, 64, 0.2)])
+def test_values_that_are_not_finite_here_and_there(T, H, G, D, share, dtype):
+    """Each value of a row is a NaN if a token that it sees has one there, else as if there was none: of a prompt, and of its
+    last tokens over a cache."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    q, k, v = (torch.randn(T, n, D, generator=g, device="cuda").to(dtype) for n in (H, G, G))
+    v[torch.rand(T, G, D, generator=g, device="cuda") < share] = float("nan")
+    v[T - 1, 0, 1] = v[T - 30, G - 1, D - 2] = float("nan")
+    ref, eo, lref, el = exact(q, k, v.nan_to_num(0.0), 0, D ** -0.5, dtype)
+    had = torch.isnan(v).cumsum(0).bool().repeat_interleave(H // G, 1)
+    o, lse = kda.attn_fwd(q[None], k[None], v[None])
+    assert torch.equal(torch.isnan(o[0]), had)
+    check("o", o[0].nan_to_num(0.0), ref.masked_fill(had, 0.0), eo, dtype)
+    check("lse", lse[0], lref, el, F32)
+    page = 16
+    n_pages = -(-T // page)
+    kp, vp = (torch.full((n_pages, G, page, D), 3.0, dtype=dtype, device="cuda") for _ in range(2))
+    table = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)[None]
+    lengths = torch.tensor([T], dtype=torch.int32, device="cuda")
+    kda.kv_append(k[None], v[None], kp, vp, table, lengths)
+    for new in (2, 7, 60, T):
+        o, lse = kda.attn_paged_fwd(q[None, T - new:], kp, vp, table, lengths)
+        assert torch.equal(torch.isnan(o[0]), had[T - new:]), new
+        check("o", o[0].nan_to_num(0.0), ref[T - new:].masked_fill(had[T - new:], 0.0), eo[T - new:], dtype)
+        check("lse", lse[0], lref[T - new:], el[T - new:], F32)
