@@ -368,7 +368,8 @@ def kv_fork(table, lengths, refs, src, dst, pages, page_size, *, workspace=None)
 
     table, lengths, refs as for kv_resize, updated in place; src, dst int32
     [n]; pages the tensor [n_pages, ...], or up to 16 of them, that hold the
-    pages' data.  Returns ok int32 [n]: 0 where dst stays as it was.
+    pages' data.  Returns ok int32 [n]: 0 where dst stays as it was.  With too
+    few free pages only pairs that copy one are refused, the later ones.
     """
     import torch
     lib = load_library()

@@ -117,8 +117,8 @@ PagedPlan paged_plan(bool bf16, int32_t n_seqs, int64_t T, int64_t rows, int32_t
         return a;
     }
     // A packed batch's requests may differ by much, so it gets four times the parts.  A chunk of 512 tokens and 7 single
-    // ones over 16384 keys, 32 heads of 128 on 8: 1696 us instead of 2692 (63 single ones over 4096: 836 and 1032, 64 single
-    // ones: 502 and 462); 64 tokens of each of 16 requests over 1024 the other way round: 201 us, 176 with the fewer parts.
+    // ones over 16384 keys, 32 heads of 128 on 8: 1642 us instead of 2606 (63 single ones over 4096: 961 and 976, 64 single
+    // ones: 601 and 838); 64 tokens of each of 16 requests over 1024 the other way round: 227 us, 172 with the fewer parts.
     const int64_t want = units > 0 ? (varlen ? 4 : 1) * kFill / units : 1, most = max_tokens / kMinSplitKeys;
     a.splits = want < most ? want : most;
     if (a.splits < 1) a.splits = 1;

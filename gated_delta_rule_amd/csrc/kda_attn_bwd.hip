@@ -11,12 +11,12 @@
 //   rows: wave w has 32 rows and walks the keys:
 //     S^T = K Q^T, dP^T = V dO^T, then dQ^T += K^T dS^T.
 // P and dS go from product to product in registers, rounded to bf16 once.
-//   Bound by the matrix cores (0.46 and 0.53 busy, at 1.9 GHz) and by what stands between
+//   Bound by the matrix cores (0.46 and 0.50 busy, at 2.0 and 1.9 GHz) and by what stands between
 // their products: two sums and two operands fill 192 of 256 registers, so that
 // operands are read from LDS just before their turn and only the SIMD's other
-// wave covers that.  2 x 4096 causal tokens, 32 heads of 128 on 8: 552 us by the
-// keys, 394 by the rows, 26 to join the parts; 0.7 PFLOP/s of the formula's five
-// products.  Reading operands two to four products ahead, pinned there, took 4
+// wave covers that.  2 x 4096 causal tokens, 32 heads of 128 on 8: 552 to 572 us
+// by the keys, 394 to 411 by the rows on different machines, 26 to join the
+// parts; 0.7 PFLOP/s of the formula's five products.  Reading operands two to four products ahead, pinned there, took 4
 // to 11% longer.
 #include "kda_attn_mma.h"
 

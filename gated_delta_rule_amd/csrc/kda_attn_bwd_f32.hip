@@ -9,9 +9,9 @@
 // the rows take S = Q K^T, whose place in registers (key l & 15, rows
 // 4 (l >> 4) + i) is that of P^T as an operand of P^T dO; the one that sums
 // over the keys takes S^T = K Q^T.
-//   Bound as the forward pass is: 63 TFLOP/s of the formula's five products (88
-// of the seven done) at 2048 causal tokens, 16 heads of 128: 390 us by the keys,
-// 290 by the rows.
+//   Bound as the forward pass is: 64 TFLOP/s of the formula's five products (90
+// of the seven done) at 2048 causal tokens, 16 heads of 128: 382 us by the keys,
+// 288 by the rows.
 #include "kda_attn_mma.h"
 
 namespace kda {

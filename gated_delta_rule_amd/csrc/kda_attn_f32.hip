@@ -11,7 +11,10 @@
 // tile's rows are requested before the products of this one.
 //   Bound by the float32 matrix instructions and the LDS reads in front of them:
 // 94 TFLOP/s at 2048 causal tokens, 16 heads of 128 (182 us; 195 with operands
-// read as they are needed), where a large product reaches 153.
+// read as they are needed), where a large product reaches 153.  Heads of 64 are
+// held to four waves per SIMD: with three, which the compiler takes by itself,
+// chunks of 2 x 1000 tokens over 8000 and 5000, 32 heads on 8, took 1292 us, and
+// 1103 with four.
 #include "kda_attn_tile.h"
 
 namespace kda {

@@ -21,8 +21,9 @@
 // this tile's exponentials, those with the values beside the sums and the next
 // tile's maximum, and another wave's beside all of them (two waves per SIMD,
 // which 240 registers and 64 KB of LDS leave room for).  8192 causal tokens, 32
-// heads of 128 on 8: 522 us, 1.05 PFLOP/s; 2 x 4096: 261 us (286 with a tile's
-// scores, weights and sums one after the other).
+// heads of 128 on 8: 495 to 525 us on different machines (1.05 to 1.11 PFLOP/s);
+// 2 x 4096: 261 to 272 (3% less than with a tile's scores, weights and sums one
+// after the other).
 #include "kda_attn_mma.h"
 
 namespace kda {
@@ -328,7 +329,8 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_bf16_kernel(AttnParams
 // that are cut are joined by a second launch.  Neighbouring pieces go to one
 // XCD, for their common keys and values.
 //   (1024 new tokens in all of two requests of 8k to 32k tokens, 32 heads of 128
-// on 8: 391 us and 17 to join.  When both took 435, the same number of parts for
+// on 8: 0.81 to 0.87 PFLOP/s with the append and the joining, 309 us for 251
+// GFLOP and 433 for 379.  When an input took 435, the same number of parts for
 // every block took 774 us with 512 workgroups or more in all, 467 with 1024, 430
 // with 2048; but 256 tokens over 32k 165, 179 and 216, 163 here.)
 struct FwdLine {
@@ -388,8 +390,8 @@ __global__ __launch_bounds__(FW_THREADS, 2) void attn_fwd_line_kernel(AttnParams
     // Whole blocks where that takes no longer, in steps of two workgroups on one compute unit (2.1 us; half a round of
     // blocks takes half of that): rounds of average blocks, uneven by an eighth, or the longest one; cutting costs 30 us
     // for more starts and the parts, and 0.04 per block to join.  One request's first 1024 / 2048 / 4096 tokens, 32 heads
-    // of 128 on 8: 33, 61 and 170 us whole, 56, 107 and 249 cut; 512 new tokens of each of 8 over 4096: 269 and 319; one
-    // of each of 64 over 4096, packed (a round and a few blocks): 296 and 230.
+    // of 128 on 8: 35, 63 and 171 us whole, 57, 102 and 232 cut; 512 new tokens of each of 8 over 4096: 266 and 305; one
+    // of each of 64 over 4096, packed (a round and a few blocks): 293 and 198.
     const int64_t rest = units % p.workgroups, halves = units / p.workgroups * 2 + (rest > p.workgroups / 2 ? 2 : rest > 0);
     int64_t by_blocks = count > 0 ? total * halves * 9 / (16 * (int64_t)count) : 0;
     const int64_t one = units <= p.workgroups / 2 ? longest / 2 : longest;

@@ -16,10 +16,11 @@
 // barriers, only counts of loads.  S^T = K Q^T leaves lane l with row l & 15 and
 // keys 4 (l >> 4) + i, the place of P^T as an operand of O^T = V^T P^T.  The
 // waves' sums are joined when the unit or the piece ends.
-//   One token of each of 64 requests of 8192, 32 heads of 128 on 8, bf16: 233 us,
-// 5.7 TB/s (a copy of 1 GiB: 5.2); 4, 6 and 8 tokens of 64 requests of 4096, 64
-// heads of 128 on 8: 194, 202 and 225 us (with four tiles of 16 rows 31 registers
-// are in memory).
+//   One token of each of 64 requests, 32 heads of 128 on 8, bf16: 233 us where
+// they hold 2048 to 8192 tokens (1.34 GB, 5.7 TB/s), 363 with 8192 each (2.15 GB,
+// 5.9; a copy of 1 GiB: 5.2); 4, 6 and 8 tokens of 64 requests of 4096, 64 heads
+// of 128 on 8: 195, 203 and 228 us (with four tiles of 16 rows 31 registers are
+// in memory).
 #include "kda_attn_mma.h"
 
 namespace kda {

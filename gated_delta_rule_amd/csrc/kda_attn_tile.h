@@ -264,7 +264,8 @@ __device__ __forceinline__ uint32_t attn_zigzag(uint32_t w, uint32_t n, int32_t 
 // The same for kernels of two workgroups per compute unit whose workgroups come
 // and go: turned if there are two rounds of them at most.  Causal prompts of
 // 2048 / 4096 / 8192 tokens, 32 heads of 128 on 8 (512 / 1024 / 2048
-// workgroups): 44, 138 and 496 us turned, 46, 140 and 488 as they are.
+// workgroups), on one machine: 47, 145 and 522 us turned, 49, 147 and 514 as
+// they are.
 __device__ __forceinline__ uint32_t attn_turned(uint32_t w, uint32_t n, int32_t G) {
     return n <= 1024 ? attn_zigzag(w, n, G) : w;
 }

@@ -1,9 +1,10 @@
 /*
- * kda_attn.h -- C ABI of softmax attention on MI355X (gfx950): the full
- * attention layers that stand between the layers of kda.h and kda_ssm.h, in
- * the same library, with the same conventions.  Whole prompts with their
- * gradients, and new tokens of requests over a paged cache of keys and values
- * (whose pages kda_pages.h looks after).
+ * kda_attn.h -- C ABI of softmax attention on MI355X (gfx950): full
+ * attention layers with grouped heads, one width of 64 or 128 for queries, keys
+ * and values, beside the layers of kda.h and kda_ssm.h, in the same library,
+ * with the same conventions.  Whole prompts with their gradients, and new
+ * tokens of requests over a paged cache of keys and values (whose pages
+ * kda_pages.h looks after).
  *
  * Row i is a token with a query head h; group g = h / (H / G) holds the keys
  * and values that the H / G consecutive heads of the group share:
@@ -40,12 +41,12 @@
  *   - Scores (times log2 e) must be within float32.  A NaN or an infinity in q
  *     reaches its own row only, one in k or v the rows that see its token (an
  *     infinity perhaps as a NaN): rows that do not, but share a tile of keys
- *     with it, are computed once more key by key.  In the backward pass a masked weight of zero is
- *     multiplied with whatever stands there: a NaN or an infinity in any input
- *     can also reach gradients of tokens up to 94 away in its own sequence and
- *     group, on the side that does not see it.  What lies outside a sequence,
- *     behind a request's length or in pages that it does not hold is never
- *     part of a product.
+ *     with it, are computed once more key by key.  In the backward pass a
+ *     masked weight of zero is multiplied with whatever stands there: a NaN or
+ *     an infinity in any input can also reach gradients of tokens up to 94 away
+ *     in its own sequence and group, on the side that does not see it.  What
+ *     lies outside a sequence, behind a request's length or in pages that it
+ *     does not hold is never part of a product.
  *   - Numerics: scores, softmax statistics and sums in float32.  With
  *     KDA_BF16 the weights (and in the backward pass the score gradients)
  *     are rounded to bf16 once, as operands of the matrix cores: a half step
